@@ -16,10 +16,21 @@ from . import build as _build
 
 STATUS = {0: "DFL2_OK", 1: "DFL2_ERR_INVALID_ARG", 2: "DFL2_ERR_UNSUPPORTED",
           3: "DFL2_ERR_WORKSPACE", 4: "DFL2_ERR_CUDA", 5: "DFL2_ERR_TIMEOUT"}
-DFL2_F32, DFL2_BF16 = 0, 1
+DFL2_F32, DFL2_BF16, DFL2_F16 = 0, 1, 2
 NCAND, RANK = 16, 256
 
 _lib = None
+
+
+class _CacheStruct(ctypes.Structure):
+    """struct dfl2_cache of include/dfl2.h."""
+    _fields_ = ([("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] +
+                [(n, ctypes.c_int32) for n in ("dtype", "layers", "pages", "kv_heads",
+                                               "page_size", "head_dim")] +
+                [(n, ctypes.c_int64) for n in ("layer_stride", "page_stride", "head_stride",
+                                               "slot_stride")] +
+                [("table", ctypes.c_void_p), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                 ("refs", ctypes.c_void_p), ("free_bits", ctypes.c_void_p)])
 
 
 class Dfl2Error(RuntimeError):
@@ -82,6 +93,22 @@ def load():
     L.dfl2_verify_workspace_size.argtypes = [I, I, I]
     L.dfl2_verify_workspace_size.restype = SZ
     L.dfl2_verify.argtypes = [P, P, P, P, P, I, I, I, I, P, U64, P, P, P, SZ, P]
+    C = ctypes.POINTER(_CacheStruct)
+    S = ctypes.POINTER(ctypes.c_int64)
+    L.dfl2_cache_reserve.argtypes = [C, I, I, P, P, P, P, P]
+    L.dfl2_cache_write.argtypes = [C, I, I, P, P, S, I, I, P, P, P, P]
+    L.dfl2_cache_compact.argtypes = [C, I, I, P, P, P, P, P, P, P]
+    L.dfl2_cache_fork.argtypes = [C, I, P, P, P, P, P]
+    L.dfl2_cache_free.argtypes = [C, I, P, P]
+    L.dfl2_tree_mask.argtypes = [P, I, I, P, P, P, P]
+    L.dfl2_tree_accept.argtypes = [P, P, P, I, I, P, P, P, P, P]
+    L.dfl2_tree_attn_workspace_size.argtypes = [I, I, I, I, I, I]
+    L.dfl2_tree_attn_workspace_size.restype = SZ
+    L.dfl2_tree_attn.argtypes = [P, S, C, I, I, I, I, P, P, P, P, F, P, S, P, P, SZ, P]
+    for name in ("dfl2_cache_reserve", "dfl2_cache_write", "dfl2_cache_compact",
+                 "dfl2_cache_fork", "dfl2_cache_free", "dfl2_tree_mask", "dfl2_tree_accept",
+                 "dfl2_tree_attn"):
+        getattr(L, name).restype = I
     for name in ("dfl2_workspace_init", "dfl2_device_error", "dfl2_topk", "dfl2_select",
                  "dfl2_walk", "dfl2_conv2", "dfl2_conv2_ws", "dfl2_tail", "dfl2_verify", "dfl2_tables_build",
                  "dfl2_select_tables", "dfl2_tail_tables"):
@@ -338,3 +365,190 @@ def dfl2_tail_tables(logits, verified_tok, hidden, W_H, P_A, P_B, temperature: f
                                    _ptr(seeds), int(cycle_offset), _ptr(tokens), _ptr(slots),
                                    _ptr(q), _ptr(cand_idx), _ptr(cand_val), _ptr(scores),
                                    _ptr(ws), wb, _stream(stream)))
+
+
+# ---- the paged cache and trees of drafted tokens ---------------------------------
+def _i32(t, name, shape=None):
+    """An int32 device array's address; None stays None.  The C side cannot see
+    types, so a wrong one is an error here."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    return t.data_ptr()
+
+
+def _strides(t):
+    """Element strides; that of a dimension of one entry, which torch leaves open, is 0."""
+    return tuple(0 if n == 1 else s for n, s in zip(t.shape, t.stride()))
+
+
+class Cache:
+    """A dfl2_cache over the caller's tensors, which it keeps alive.
+
+    k, v [layers, pages, kv_heads, page_size, head_dim] float32, bf16 or fp16: any
+    strides (the same for both) with the last dimension's 1, so a cache laid out
+    [layers, pages, page_size, kv_heads, head_dim] is passed transposed.
+    table int32 [rows, cols], refs int32 [pages], free_bits int32 [ceil(pages/32)]."""
+
+    def __init__(self, k, v, table, refs, free_bits):
+        import torch
+        codes = {torch.float32: DFL2_F32, torch.bfloat16: DFL2_BF16, torch.float16: DFL2_F16}
+        if k.dtype not in codes or v.dtype != k.dtype:
+            raise TypeError(f"k and v must both be float32, bf16 or fp16, not {k.dtype}, {v.dtype}")
+        st = _strides(k)
+        if k.dim() != 5 or v.shape != k.shape or _strides(v) != st or k.stride(4) != 1:
+            raise ValueError("k and v must be [layers, pages, kv_heads, page_size, head_dim] with "
+                             "the same strides, the last of them 1")
+        layers, pages, heads, page_size, dim = k.shape
+        if table.dim() != 2:
+            raise ValueError("table must be [rows, cols]")
+        _i32(table, "table")
+        _i32(refs, "refs", (pages,))
+        _i32(free_bits, "free_bits", ((pages + 31) // 32,))
+        self.k, self.v, self.table, self.refs, self.free_bits = k, v, table, refs, free_bits
+        self.dtype = k.dtype
+        self._s = _CacheStruct(
+            k.data_ptr(), v.data_ptr(), codes[k.dtype], layers, pages, heads, page_size, dim,
+            st[0], st[1], st[2], st[3], table.data_ptr(), table.shape[0],
+            table.shape[1], refs.data_ptr(), free_bits.data_ptr())
+        self._ref = ctypes.byref(self._s)
+
+
+def cache(layers: int, pages: int, kv_heads: int, page_size: int, head_dim: int, rows: int,
+          cols: int, dtype=None, device="cuda") -> Cache:
+    """A new, empty Cache (torch allocation; plumbing only)."""
+    import torch
+    shape = (layers, pages, kv_heads, page_size, head_dim)
+    dtype = dtype or torch.bfloat16
+    bits = torch.full(((pages + 31) // 32,), -1, dtype=torch.int32, device=device)
+    if pages % 32:
+        bits[-1] = (1 << pages % 32) - 1
+    return Cache(torch.zeros(shape, dtype=dtype, device=device),
+                 torch.zeros(shape, dtype=dtype, device=device),
+                 torch.full((rows, cols), -1, dtype=torch.int32, device=device),
+                 torch.zeros(pages, dtype=torch.int32, device=device), bits)
+
+
+def _count(count, T, B):
+    """(T, address of the counts): a plain number is every sequence's count."""
+    if isinstance(count, int):
+        return count, None
+    return T, _i32(count, "count", (B,))
+
+
+def dfl2_cache_reserve(cache, length, count, served, rows=None, stream=None) -> None:
+    """Pages for positions length .. length+count-1; served int32 [B] out.  count: int or [B]."""
+    B = length.shape[0]
+    T, n = _count(count, 1 << 30, B)
+    _check(load().dfl2_cache_reserve(cache._ref, B, T, _i32(rows, "rows", (B,)),
+                                     _i32(length, "length", (B,)), n,
+                                     _i32(served, "served", (B,)), _stream(stream)))
+
+
+def dfl2_cache_write(cache, k_new, v_new, length, count=None, rows=None, layer: int = 0,
+                     stream=None) -> None:
+    """k_new, v_new [n_layers, B, T, kv_heads, head_dim] (one layer: without the first
+    dimension) into layers layer .. of the cache, positions length .. length+count-1."""
+    s = cache._s
+    if k_new.dim() == 4:
+        k_new, v_new = k_new[None], v_new[None]
+    N, B, T = k_new.shape[:3]
+    if (k_new.dtype != cache.dtype or v_new.dtype != cache.dtype or v_new.shape != k_new.shape
+            or tuple(k_new.shape[3:]) != (s.kv_heads, s.head_dim)):
+        raise ValueError("k_new and v_new must be [n_layers, B, T, kv_heads, head_dim] of the "
+                         "cache's type")
+    st = _strides(k_new)
+    if _strides(v_new) != st or k_new.stride(4) != 1:
+        raise ValueError("k_new and v_new must have the same strides, the last of them 1")
+    T, n = _count(count, T, B) if not isinstance(count, int) else (min(T, count), None)
+    _check(load().dfl2_cache_write(cache._ref, layer, N, k_new.data_ptr(), v_new.data_ptr(),
+                                   (ctypes.c_int64 * 4)(*st[:4]), B, T, _i32(rows, "rows", (B,)),
+                                   _i32(length, "length", (B,)), n, _stream(stream)))
+
+
+def dfl2_cache_compact(cache, length, count, path, n_path, new_length, rows=None,
+                       stream=None) -> None:
+    """The rows of nodes path[b,:n_path] to positions length .., the pages behind them
+    given back, new_length = length + n_path (may be length).  count: int or [B]."""
+    B, T = path.shape
+    if isinstance(count, int) and count != T:
+        raise ValueError(f"path has room for {T} nodes, not {count}")
+    _, n = _count(count, T, B)
+    _check(load().dfl2_cache_compact(cache._ref, B, T, _i32(rows, "rows", (B,)),
+                                     _i32(length, "length", (B,)), n, _i32(path, "path"),
+                                     _i32(n_path, "n_path", (B,)),
+                                     _i32(new_length, "new_length", (B,)), _stream(stream)))
+
+
+def dfl2_cache_fork(cache, src, dst, length, served, stream=None) -> None:
+    """Table rows dst become copies of the first length positions of rows src."""
+    n = src.shape[0]
+    _check(load().dfl2_cache_fork(cache._ref, n, _i32(src, "src", (n,)), _i32(dst, "dst", (n,)),
+                                  _i32(length, "length", (n,)), _i32(served, "served", (n,)),
+                                  _stream(stream)))
+
+
+def dfl2_cache_free(cache, rows, stream=None) -> None:
+    """Every page of the table rows given back."""
+    _check(load().dfl2_cache_free(cache._ref, rows.shape[0], _i32(rows, "rows"), _stream(stream)))
+
+
+def dfl2_tree_mask(parents, mask, depth=None, count=None, stream=None) -> None:
+    """parents [B,T] -> mask int32 [B,T,ceil(T/32)] (bit j: node i sees node j), depth [B,T]."""
+    B, T = parents.shape
+    _check(load().dfl2_tree_mask(_i32(parents, "parents"), B, T, _i32(count, "count", (B,)),
+                                 _i32(mask, "mask", (B, T, (T + 31) // 32)),
+                                 _i32(depth, "depth", (B, T)), _stream(stream)))
+
+
+def dfl2_tree_accept(tokens, parents, target, path, n_path, next_token, count=None,
+                     stream=None) -> None:
+    """The path of the target's tokens through each tree: path [B,T], n_path [B], next_token [B]."""
+    B, T = tokens.shape
+    _check(load().dfl2_tree_accept(_i32(tokens, "tokens"), _i32(parents, "parents", (B, T)),
+                                   _i32(target, "target", (B, T)), B, T,
+                                   _i32(count, "count", (B,)), _i32(path, "path", (B, T)),
+                                   _i32(n_path, "n_path", (B,)),
+                                   _i32(next_token, "next_token", (B,)), _stream(stream)))
+
+
+def _attn_dtype(dtype) -> int:
+    import torch
+    return {torch.float32: DFL2_F32, torch.bfloat16: DFL2_BF16, torch.float16: DFL2_F16}.get(
+        dtype, dtype)
+
+
+def dfl2_tree_attn_workspace_size(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int,
+                                  dtype) -> int:
+    """dtype: a torch dtype or DFL2_BF16 / DFL2_F16."""
+    return int(load().dfl2_tree_attn_workspace_size(B, T, q_heads, kv_heads, head_dim,
+                                                    _attn_dtype(dtype)))
+
+
+def dfl2_tree_attn(q, cache, layer: int, length, mask, out, ws, rows=None, count=None, lse=None,
+                   scale=None, stream=None) -> None:
+    """q [B,T,q_heads,head_dim] over layer `layer` of the cache -> out (as q), lse float32
+    [B,T,q_heads].  mask int32 [B,T,ceil(T/32)], None for a chain; scale: head_dim ** -0.5."""
+    B, T, H, D = q.shape
+    s = cache._s
+    if q.dtype != cache.dtype or out.dtype != cache.dtype or out.shape != q.shape:
+        raise ValueError("q and out must be [B, T, q_heads, head_dim] of the cache's type")
+    qs, os_ = _strides(q), _strides(out)
+    if D != s.head_dim or q.stride(3) != 1 or out.stride(3) != 1:
+        raise ValueError(f"head_dim {D} against the cache's {s.head_dim}, strides {qs}, {os_}")
+    if lse is not None:
+        import torch
+        if lse.dtype != torch.float32 or lse.shape != (B, T, H) or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous float32 [B, T, q_heads]")
+    _check(load().dfl2_tree_attn(
+        q.data_ptr(), (ctypes.c_int64 * 3)(*qs[:3]), cache._ref, layer, B, T, H,
+        _i32(rows, "rows", (B,)), _i32(length, "length", (B,)), _i32(count, "count", (B,)),
+        _i32(mask, "mask", (B, T, (T + 31) // 32)), D ** -0.5 if scale is None else float(scale),
+        out.data_ptr(), (ctypes.c_int64 * 3)(*os_[:3]), _ptr(lse), _ptr(ws), _nbytes(ws),
+        _stream(stream)))

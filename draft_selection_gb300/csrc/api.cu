@@ -14,6 +14,7 @@
 #include <string>
 
 #include "dfl2.h"
+#include "cache.cuh"
 #include "dfl2_internal.cuh"
 
 namespace {
@@ -223,6 +224,42 @@ dfl2_status check_topk_device(const void* logits, const void* cand_idx, const vo
 // Records the calling thread's error message; returns st.
 dfl2_status report_error(dfl2_status st, const char* msg) { return fail(st, "%s", msg); }
 dfl2_status report_cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+dfl2_status report_errorf(dfl2_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return st;
+}
+dfl2_status check_args_host(const PtrArg* a, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (!a[i].p) {
+      if (a[i].optional) continue;
+      return fail(DFL2_ERR_INVALID_ARG, "%s is NULL", a[i].name);
+    }
+    if (reinterpret_cast<uintptr_t>(a[i].p) % static_cast<uintptr_t>(a[i].align))
+      return fail(DFL2_ERR_INVALID_ARG, "%s is not %d-byte aligned", a[i].name, a[i].align);
+  }
+  return DFL2_OK;
+}
+dfl2_status check_args_device(const PtrArg* a, int n) {
+  DFL2_TRY(ensure_device());
+  for (int i = 0; i < n; ++i) {
+    if (!a[i].p) continue;
+    cudaPointerAttributes at;
+    cudaError_t e = cudaPointerGetAttributes(&at, a[i].p);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return fail(DFL2_ERR_INVALID_ARG, "%s is not a CUDA pointer (%s)", a[i].name,
+                  cudaGetErrorName(e));
+    }
+    if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged)
+      return fail(DFL2_ERR_INVALID_ARG, "%s must be device memory", a[i].name);
+  }
+  return DFL2_OK;
+}
 }  // namespace dfl2
 
 extern "C" {

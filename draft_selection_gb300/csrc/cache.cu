@@ -1,0 +1,598 @@
+// The paged key/value cache: taking, sharing and giving back pages, and moving
+// rows of keys and values (include/dfl2.h, "The cache").
+//
+// Bookkeeping.  A page is free iff its count is 0, and the free pages are kept
+// as a bit map besides: finding the N lowest free pages is then one scan of
+// pages/8 bytes by one CTA, and giving a page back is one atomicOr, whose order
+// does not matter.  So a call's result is a function of the state before it.
+//
+// Moving rows.  All copies are pure traffic: a position's row in one layer is
+// kv_heads pieces of head_dim elements for K and as many for V, each at least
+// 16 bytes and 16-byte aligned.  One warp takes one position's row with eight
+// 16-byte loads a lane in flight (four of K, four of V) before the stores.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "cache.cuh"
+
+namespace dfl2 {
+namespace {
+
+constexpr int kBookThreads = 1024;
+constexpr int kListCap = 4096;  // pages handed out per round of the list below
+constexpr unsigned kAll = 0xffffffffu;
+
+// Sum over the threads before this one, and over all of them.
+__device__ __forceinline__ int block_scan(int v, int& total, int* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(kAll, x, off);
+    if (lane >= off) x += y;
+  }
+  __syncthreads();  // warp_sums may still be read from the scan before
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int w = warp_sums[lane];
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(kAll, w, off);
+      if (lane >= off) w += y;
+    }
+    warp_sums[lane] = w;
+  }
+  __syncthreads();
+  total = warp_sums[31];
+  return x - v + (warp ? warp_sums[warp - 1] : 0);
+}
+
+struct TakeArgs {
+  TableView t;  // reserve: seq = table_rows; fork: seq = dst
+  const int32_t* src;
+  int32_t* served;
+  int B;
+};
+
+// The table entries sequence b may need pages for: [c0, c1) of its row.
+struct Span {
+  int row, c0, c1;
+  bool ok;
+};
+template <bool kFork>
+__device__ __forceinline__ Span span_of(const TakeArgs& a, int b) {
+  Span s;
+  s.row = a.t.row_of(b);
+  const int len = a.t.length[b], ps = 1 << a.t.page_shift;
+  const int n = kFork ? 0 : a.t.count_of(b);
+  s.ok = s.row >= 0 && len >= 0 && len <= (1 << 30);
+  s.c0 = s.ok ? len >> a.t.page_shift : 0;
+  s.c1 = s.ok ? (len + n + ps - 1) >> a.t.page_shift : 0;
+  if (s.c1 > a.t.cols) s.ok = false;
+  return s;
+}
+
+// One CTA: which sequences get their pages, and the pages themselves.
+template <bool kFork>
+__global__ void __launch_bounds__(kBookThreads) take_kernel(const __grid_constant__ TakeArgs a) {
+  __shared__ int offs[kMaxSeqs];  // a sequence's need; then its first page's rank, -1 if unserved
+  __shared__ int list[kListCap];
+  __shared__ int warp_sums[32];
+  __shared__ int taken_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (tid == 0) taken_s = 0;
+
+  // the needs, a warp to a sequence
+  for (int b = warp; b < a.B; b += kBookThreads / 32) {
+    const Span s = span_of<kFork>(a, b);
+    int need = 0;
+    bool ok = s.ok;
+    if (ok) {
+      const int32_t* row = a.t.table + static_cast<int64_t>(s.row) * a.t.cols;
+      if (kFork) {
+        const int src = a.src[b];
+        bool good = static_cast<unsigned>(src) < static_cast<unsigned>(a.t.rows) && src != s.row;
+        if (good)
+          for (int c = lane; c < s.c1; c += 32)
+            good &= row[c] < 0 && a.t.page_at(src, c, true) >= 0;
+        ok = __all_sync(kAll, good);
+      }
+      for (int c = s.c0 + lane; c < s.c1; c += 32) need += row[c] < 0;
+      need = __reduce_add_sync(kAll, need);
+    }
+    if (lane == 0) offs[b] = ok ? need : -1;
+  }
+  // the free pages: each thread the words [w0, w1) of the bit map
+  const int words = (a.t.pages + 31) / 32;
+  const int wper = (words + kBookThreads - 1) / kBookThreads;
+  const int w0 = min(words, tid * wper), w1 = min(words, w0 + wper);
+  int mine = 0;
+  for (int w = w0; w < w1; ++w) mine += __popc(a.t.free_bits[w]);
+  int n_free, total;
+  int rank = block_scan(mine, n_free, warp_sums);  // rank of this thread's first free page
+  // served in order while the pages last
+  const int bper = (a.B + kBookThreads - 1) / kBookThreads;
+  const int b0 = min(a.B, tid * bper), b1 = min(a.B, b0 + bper);
+  int need = 0;
+  for (int b = b0; b < b1; ++b) need += max(0, offs[b]);
+  int cum = block_scan(need, total, warp_sums);
+  int reach = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = offs[b];
+    const bool ok = n >= 0 && (n == 0 || n <= n_free - cum);
+    a.served[b] = ok;
+    offs[b] = ok ? cum : -1;
+    cum += max(0, n);
+    if (ok && n > 0) reach = cum;
+  }
+  if (reach) atomicMax(&taken_s, reach);
+  __syncthreads();
+  const int taken = taken_s;
+
+  int w = w0;
+  uint32_t left = w < w1 ? a.t.free_bits[w] : 0u;
+  for (int r0 = 0; r0 < taken; r0 += kListCap) {
+    const int r1 = min(taken, r0 + kListCap);
+    // the pages of ranks [r0, r1), each from the thread that holds its word
+    while (w < w1 && rank < r1) {
+      uint32_t gone = 0;
+      while (left && rank < r1) {
+        const int bit = __ffs(left) - 1;
+        left &= left - 1;
+        gone |= 1u << bit;
+        const int page = w * 32 + bit;
+        list[rank - r0] = page;
+        a.t.refs[page] = 1;
+        ++rank;
+      }
+      if (gone) a.t.free_bits[w] &= ~gone;
+      if (!left) {
+        ++w;
+        left = w < w1 ? a.t.free_bits[w] : 0u;
+      }
+    }
+    __syncthreads();
+    for (int b = warp; b < a.B; b += kBookThreads / 32) {
+      if (offs[b] < 0 || offs[b] >= r1) continue;
+      const Span s = span_of<kFork>(a, b);
+      int32_t* row = a.t.table + static_cast<int64_t>(s.row) * a.t.cols;
+      // entries of lower rank were filled in the rounds before
+      int r = max(offs[b], r0);
+      for (int c = s.c0; c < s.c1 && r < r1; c += 32) {
+        const bool miss = c + lane < s.c1 && row[c + lane] < 0;
+        const unsigned m = __ballot_sync(kAll, miss);
+        const int at = r + __popc(m & ((1u << lane) - 1));
+        if (miss && at < r1) row[c + lane] = list[at - r0];
+        r += __popc(m);
+      }
+    }
+    __syncthreads();
+  }
+  if (kFork) {  // the whole pages, shared
+    for (int b = warp; b < a.B; b += kBookThreads / 32) {
+      if (offs[b] < 0) continue;
+      const Span s = span_of<kFork>(a, b);
+      const int32_t* from = a.t.table + static_cast<int64_t>(a.src[b]) * a.t.cols;
+      int32_t* row = a.t.table + static_cast<int64_t>(s.row) * a.t.cols;
+      for (int c = lane; c < s.c0; c += 32) {
+        const int p = from[c];
+        row[c] = p;
+        atomicAdd(&a.t.refs[p], 1);
+      }
+    }
+  }
+}
+
+// One holder of page p fewer.
+__device__ __forceinline__ void drop_page(const TableView& t, int p) {
+  if (static_cast<unsigned>(p) >= static_cast<unsigned>(t.pages)) {
+    record_error(t.err, kDevErrBadIndex);
+    return;
+  }
+  const int old = atomicSub(&t.refs[p], 1);
+  if (old == 1) {
+    atomicOr(&t.free_bits[p >> 5], 1u << (p & 31));
+  } else if (old < 1) {  // nobody held it: the state is not a cache's
+    atomicAdd(&t.refs[p], 1);
+    record_error(t.err, kDevErrBadIndex);
+  }
+}
+
+__global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ TableView t) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int row = t.row_of(blockIdx.x);
+  if (row < 0) return;
+  int32_t* r = t.table + static_cast<int64_t>(row) * t.cols;
+  for (int c = threadIdx.x; c < t.cols; c += blockDim.x) {
+    const int p = r[c] == -1 ? -1 : atomicExch(&r[c], -1);
+    if (p != -1) drop_page(t, p);
+  }
+}
+
+// ---- rows of keys and values ------------------------------------------------
+
+// x / d for 0 <= x < 2^16, 1 <= d < 2^16: with m = ceil(2^32 / d), x m / 2^32
+// exceeds x / d by less than x / 2^32 < 1 / d, so its floor is right.
+struct SmallDiv {
+  uint32_t m, d;
+  __device__ __forceinline__ uint32_t div(uint32_t x) const { return m ? __umulhi(x, m) : x; }
+};
+SmallDiv small_div(int d) {
+  return SmallDiv{d == 1 ? 0u : static_cast<uint32_t>(((1ull << 32) + d - 1) / d),
+                  static_cast<uint32_t>(d)};
+}
+
+// Strides in 16-byte units.
+struct RowView {
+  uint4* k;
+  uint4* v;
+  int64_t layer, page, head, slot;
+  int chunks;  // 16-byte pieces of a position's row: kv_heads * per_head
+  SmallDiv per_head;
+};
+RowView row_view(const dfl2_cache* c) {
+  const int per = 16 / elem_bytes(c->dtype);
+  return RowView{static_cast<uint4*>(c->k), static_cast<uint4*>(c->v), c->layer_stride / per,
+                 c->page_stride / per, c->head_stride / per, c->slot_stride / per,
+                 c->kv_heads * (c->head_dim / per), small_div(c->head_dim / per)};
+}
+
+// One warp copies a position's row of K and of V; fh, th: head strides.
+__device__ __forceinline__ void copy_row(const uint4* fk, const uint4* fv, int64_t fh, uint4* tk,
+                                         uint4* tv, int64_t th, int chunks, SmallDiv per_head,
+                                         int lane) {
+  for (int c0 = lane; c0 < chunks; c0 += 128) {
+    uint4 x[4], y[4];
+    int64_t to[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + 32 * i;
+      if (c >= chunks) break;
+      const uint32_t h = per_head.div(c), r = c - h * per_head.d;
+      x[i] = fk[h * fh + r];
+      y[i] = fv[h * fh + r];
+      to[i] = h * th + r;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c0 + 32 * i >= chunks) break;
+      tk[to[i]] = x[i];
+      tv[to[i]] = y[i];
+    }
+  }
+}
+
+struct WriteArgs {
+  TableView t;
+  RowView r;
+  const uint4* k_new;
+  const uint4* v_new;
+  int64_t nl, nb, nt, nh;  // strides of the new rows, 16-byte units
+  int layer, n_layers, B;
+};
+
+__global__ void __launch_bounds__(256) write_kernel(const __grid_constant__ WriteArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t items = static_cast<int64_t>(a.n_layers) * a.B * a.t.T;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
+       it += step) {
+    const int t = static_cast<int>(it % a.t.T);
+    const int64_t lb = it / a.t.T;
+    const int b = static_cast<int>(lb % a.B), l = static_cast<int>(lb / a.B);
+    if (t >= a.t.count_of(b)) continue;
+    const int row = a.t.row_of(b);
+    if (row < 0) continue;
+    const int pos = a.t.length[b] + t;
+    const int page = a.t.page_at(row, pos >> a.t.page_shift);
+    if (page < 0 || pos < 0) continue;
+    const int64_t from = l * a.nl + b * a.nb + t * a.nt;
+    const int64_t to = (a.layer + l) * a.r.layer + page * a.r.page +
+                       (pos & ((1 << a.t.page_shift) - 1)) * a.r.slot;
+    copy_row(a.k_new + from, a.v_new + from, a.nh, a.r.k + to, a.r.v + to, a.r.head, a.r.chunks,
+             a.r.per_head, lane);
+  }
+}
+
+struct ForkCopyArgs {
+  TableView t;
+  RowView r;
+  const int32_t* src;
+  const int32_t* served;
+  int layers, n;
+};
+
+// The positions of the partly filled last page, every layer.
+__global__ void __launch_bounds__(256) fork_copy_kernel(const __grid_constant__ ForkCopyArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, ps = 1 << a.t.page_shift;
+  const int64_t items = (static_cast<int64_t>(a.layers) * a.n) << a.t.page_shift;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
+       it += step) {
+    const int slot = static_cast<int>(it & (ps - 1));
+    const int64_t li = it >> a.t.page_shift;
+    const int i = static_cast<int>(li % a.n), l = static_cast<int>(li / a.n);
+    if (!a.served[i]) continue;
+    const int len = a.t.length[i];
+    if (slot >= (len & (ps - 1))) continue;
+    const int c = len >> a.t.page_shift;
+    const int64_t from_page = a.t.page_at(a.src[i], c), to_page = a.t.page_at(a.t.seq[i], c);
+    if (from_page < 0 || to_page < 0) continue;
+    const int64_t at = l * a.r.layer + slot * a.r.slot;
+    const int64_t from = at + from_page * a.r.page, to = at + to_page * a.r.page;
+    copy_row(a.r.k + from, a.r.v + from, a.r.head, a.r.k + to, a.r.v + to, a.r.head, a.r.chunks,
+             a.r.per_head, lane);
+  }
+}
+
+struct CompactArgs {
+  TableView t;
+  RowView r;
+  const int32_t* path;
+  const int32_t* n_path;
+  int32_t* new_length;
+  int layers, B;
+};
+
+// A thread owns one 16-byte column of K or V of one sequence and layer and
+// moves it down the path.  The path ascends strictly, so path[i] >= i and a row
+// that is written has been read before: reading ahead in batches is safe.
+__global__ void __launch_bounds__(128) compact_kernel(const __grid_constant__ CompactArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int kBatch = 8;
+  const int mask = (1 << a.t.page_shift) - 1;
+  const int64_t items = static_cast<int64_t>(a.layers) * a.B * 2 * a.r.chunks;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t it = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; it < items;
+       it += step) {
+    const uint32_t c = static_cast<uint32_t>(it % (2 * a.r.chunks));
+    const int64_t lb = it / (2 * a.r.chunks);
+    const int b = static_cast<int>(lb % a.B), l = static_cast<int>(lb / a.B);
+    const int count = a.t.count_of(b), n = min(a.n_path[b], count);
+    const int row = a.t.row_of(b);
+    if (row < 0 || n <= 0) continue;
+    const int len = a.t.length[b];
+    const bool is_v = c >= static_cast<uint32_t>(a.r.chunks);
+    const uint32_t col = is_v ? c - a.r.chunks : c;
+    const uint32_t h = a.r.per_head.div(col);
+    uint4* base = (is_v ? a.r.v : a.r.k) + l * a.r.layer + h * a.r.head +
+                  (col - h * a.r.per_head.d);
+    const int32_t* path = a.path + static_cast<int64_t>(b) * a.t.T;
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+      uint4 x[kBatch];
+      int64_t to[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = i0 + j;
+        to[j] = -1;
+        if (i >= n) continue;
+        const int from = path[i];
+        if (from == i) continue;
+        if (from < i || from >= count) {
+          record_error(a.t.err, kDevErrBadIndex);
+          continue;
+        }
+        const int64_t pf = a.t.page_at(row, (len + from) >> a.t.page_shift);
+        const int64_t pt = a.t.page_at(row, (len + i) >> a.t.page_shift);
+        if (pf < 0 || pt < 0) continue;
+        x[j] = base[pf * a.r.page + ((len + from) & mask) * a.r.slot];
+        to[j] = pt * a.r.page + ((len + i) & mask) * a.r.slot;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (to[j] >= 0) base[to[j]] = x[j];
+    }
+  }
+}
+
+// After the rows have moved: the new lengths, and the pages behind them given
+// back.  A warp to a sequence.
+__global__ void __launch_bounds__(128) trim_kernel(const __grid_constant__ CompactArgs a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int b = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (b >= a.B) return;
+  const int count = a.t.count_of(b), n = max(0, min(a.n_path[b], count)), len = a.t.length[b];
+  __syncwarp();  // new_length may be length
+  if (lane == 0) a.new_length[b] = len + n;
+  const int row = a.t.row_of(b);
+  if (row < 0 || len < 0) return;
+  const int ps = 1 << a.t.page_shift;
+  const int c1 = min(a.t.cols, (len + count + ps - 1) >> a.t.page_shift);
+  int32_t* r = a.t.table + static_cast<int64_t>(row) * a.t.cols;
+  for (int c = ((len + n + ps - 1) >> a.t.page_shift) + lane; c < c1; c += 32) {
+    const int p = atomicExch(&r[c], -1);
+    if (p != -1) drop_page(a.t, p);
+  }
+}
+
+dfl2_status check_batch(int B, int T, int max_t) {
+  if (B < 1) return report_errorf(DFL2_ERR_INVALID_ARG, "B=%d must be >= 1", B);
+  if (B > kMaxSeqs)
+    return report_errorf(DFL2_ERR_UNSUPPORTED, "B=%d: at most %d sequences a call", B, kMaxSeqs);
+  if (T < 0) return report_errorf(DFL2_ERR_INVALID_ARG, "T=%d must be >= 0", T);
+  if (T > max_t) return report_errorf(DFL2_ERR_UNSUPPORTED, "T=%d: at most %d", T, max_t);
+  return DFL2_OK;
+}
+
+int copy_blocks(int64_t items, int per_block) {
+  const int64_t want = (items + per_block - 1) / per_block;
+  return static_cast<int>(std::min<int64_t>(want, int64_t(1) << 20));
+}
+
+}  // namespace
+
+dfl2_status check_cache_host(const dfl2_cache* c) {
+  if (!c) return report_errorf(DFL2_ERR_INVALID_ARG, "cache is NULL");
+  const PtrArg ptrs[] = {{c->k, "cache k", 16},         {c->v, "cache v", 16},
+                         {c->table, "cache table", 4},  {c->refs, "cache refs", 4},
+                         {c->free_bits, "cache free_bits", 4}};
+  const dfl2_status st = check_args_host(ptrs, 5);
+  if (st != DFL2_OK) return st;
+  if (c->dtype != DFL2_F32 && c->dtype != DFL2_BF16 && c->dtype != DFL2_F16)
+    return report_errorf(DFL2_ERR_UNSUPPORTED, "cache dtype %d", c->dtype);
+  if (c->layers < 1 || c->pages < 1 || c->kv_heads < 1 || c->head_dim < 1 || c->rows < 1 ||
+      c->cols < 1)
+    return report_errorf(DFL2_ERR_INVALID_ARG, "every size of the cache must be >= 1");
+  if (c->page_size < 8 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+    return report_errorf(DFL2_ERR_UNSUPPORTED, "page_size %d: a power of two, 8 to 256",
+                         c->page_size);
+  const int per = 16 / elem_bytes(c->dtype);
+  if (c->head_dim % per)
+    return report_errorf(DFL2_ERR_UNSUPPORTED, "head_dim %d: a multiple of 16 bytes", c->head_dim);
+  if (static_cast<int64_t>(c->kv_heads) * c->head_dim >= 65536)
+    return report_errorf(DFL2_ERR_UNSUPPORTED, "kv_heads * head_dim must be below 65536");
+  for (int64_t s : {c->layer_stride, c->page_stride, c->head_stride, c->slot_stride})
+    if (s < 0 || s % per)
+      return report_errorf(DFL2_ERR_INVALID_ARG,
+                           "cache stride %lld: non-negative multiples of 16 bytes", (long long)s);
+  return DFL2_OK;
+}
+
+dfl2_status check_cache_device(const dfl2_cache* c) {
+  const PtrArg ptrs[] = {{c->k, "cache k", 16},         {c->v, "cache v", 16},
+                         {c->table, "cache table", 4},  {c->refs, "cache refs", 4},
+                         {c->free_bits, "cache free_bits", 4}};
+  return check_args_device(ptrs, 5);
+}
+
+}  // namespace dfl2
+
+#define DFL2_TRY(expr)              \
+  do {                              \
+    dfl2_status _st = (expr);       \
+    if (_st != DFL2_OK) return _st; \
+  } while (0)
+
+using dfl2::PtrArg;
+
+namespace {
+template <int N>
+dfl2_status check_all_host(const dfl2_cache* c, const PtrArg (&p)[N]) {
+  DFL2_TRY(dfl2::check_cache_host(c));
+  return dfl2::check_args_host(p, N);
+}
+template <int N>
+dfl2_status check_all_device(const dfl2_cache* c, const PtrArg (&p)[N]) {
+  DFL2_TRY(dfl2::check_cache_device(c));
+  return dfl2::check_args_device(p, N);
+}
+dfl2_status launched(cudaError_t e, const char* what) {
+  return e == cudaSuccess ? DFL2_OK : dfl2::report_cuda_error(e, what);
+}
+cudaStream_t cu(dfl2_stream s) { return reinterpret_cast<cudaStream_t>(s); }
+}  // namespace
+
+extern "C" {
+
+dfl2_status dfl2_cache_reserve(const dfl2_cache* cache, int B, int T, const int32_t* table_rows,
+                               const int32_t* length, const int32_t* count, int32_t* served,
+                               dfl2_stream stream) {
+  const PtrArg ptrs[] = {{table_rows, "table_rows", 4, true}, {length, "length", 4},
+                         {count, "count", 4, true}, {served, "served", 4}};
+  DFL2_TRY(dfl2::check_batch(B, T, 1 << 30));
+  DFL2_TRY(check_all_host(cache, ptrs));
+  DFL2_TRY(check_all_device(cache, ptrs));
+  const dfl2::TakeArgs a{dfl2::table_view(cache, table_rows, length, count, T), nullptr, served, B};
+  return launched(dfl2::launch_k(dfl2::take_kernel<false>, dim3(1), dim3(dfl2::kBookThreads), 0,
+                                 cu(stream), true, a),
+                  "cache reserve launch");
+}
+
+dfl2_status dfl2_cache_write(const dfl2_cache* cache, int layer, int n_layers, const void* k_new,
+                             const void* v_new, const int64_t* new_strides, int B, int T,
+                             const int32_t* table_rows, const int32_t* length,
+                             const int32_t* count, dfl2_stream stream) {
+  const PtrArg ptrs[] = {{k_new, "k_new", 16}, {v_new, "v_new", 16},
+                         {table_rows, "table_rows", 4, true}, {length, "length", 4},
+                         {count, "count", 4, true}};
+  DFL2_TRY(dfl2::check_batch(B, T, 1 << 30));
+  DFL2_TRY(check_all_host(cache, ptrs));
+  if (layer < 0 || n_layers < 1 || layer > cache->layers - n_layers)
+    return dfl2::report_errorf(DFL2_ERR_INVALID_ARG, "layers %d .. %d of %d", layer,
+                               layer + n_layers - 1, cache->layers);
+  if (!new_strides) return dfl2::report_errorf(DFL2_ERR_INVALID_ARG, "new_strides is NULL");
+  const int per = 16 / dfl2::elem_bytes(cache->dtype);
+  for (int i = 0; i < 4; ++i)
+    if (new_strides[i] < 0 || new_strides[i] % per)
+      return dfl2::report_errorf(DFL2_ERR_INVALID_ARG,
+                                 "new_strides[%d] = %lld: non-negative multiples of 16 bytes", i,
+                                 (long long)new_strides[i]);
+  DFL2_TRY(check_all_device(cache, ptrs));
+  if (T == 0) return DFL2_OK;
+  const dfl2::WriteArgs a{dfl2::table_view(cache, table_rows, length, count, T),
+                          dfl2::row_view(cache),
+                          static_cast<const uint4*>(k_new),
+                          static_cast<const uint4*>(v_new),
+                          new_strides[0] / per,
+                          new_strides[1] / per,
+                          new_strides[2] / per,
+                          new_strides[3] / per,
+                          layer,
+                          n_layers,
+                          B};
+  const int blocks = dfl2::copy_blocks(static_cast<int64_t>(n_layers) * B * T, 8);
+  return launched(dfl2::launch_k(dfl2::write_kernel, dim3(blocks), dim3(256), 0, cu(stream), true, a),
+                  "cache write launch");
+}
+
+dfl2_status dfl2_cache_compact(const dfl2_cache* cache, int B, int T, const int32_t* table_rows,
+                               const int32_t* length, const int32_t* count, const int32_t* path,
+                               const int32_t* n_path, int32_t* new_length, dfl2_stream stream) {
+  const PtrArg ptrs[] = {{table_rows, "table_rows", 4, true}, {length, "length", 4},
+                         {count, "count", 4, true}, {path, "path", 4}, {n_path, "n_path", 4},
+                         {new_length, "new_length", 4}};
+  DFL2_TRY(dfl2::check_batch(B, T, dfl2::kMaxTree));
+  DFL2_TRY(check_all_host(cache, ptrs));
+  DFL2_TRY(check_all_device(cache, ptrs));
+  const dfl2::CompactArgs a{dfl2::table_view(cache, table_rows, length, count, T),
+                            dfl2::row_view(cache), path, n_path, new_length, cache->layers, B};
+  const int64_t columns = static_cast<int64_t>(cache->layers) * B * 2 * a.r.chunks;
+  cudaError_t e = dfl2::launch_k(dfl2::compact_kernel, dim3(dfl2::copy_blocks(columns, 128)),
+                                 dim3(128), 0, cu(stream), true, a);
+  if (e == cudaSuccess)
+    e = dfl2::launch_k(dfl2::trim_kernel, dim3((B + 3) / 4), dim3(128), 0, cu(stream), true, a);
+  return launched(e, "cache compact launch");
+}
+
+dfl2_status dfl2_cache_fork(const dfl2_cache* cache, int n, const int32_t* src, const int32_t* dst,
+                            const int32_t* length, int32_t* served, dfl2_stream stream) {
+  const PtrArg ptrs[] = {{src, "src", 4}, {dst, "dst", 4}, {length, "length", 4},
+                         {served, "served", 4}};
+  DFL2_TRY(dfl2::check_batch(n, 0, 0));
+  DFL2_TRY(check_all_host(cache, ptrs));
+  DFL2_TRY(check_all_device(cache, ptrs));
+  const dfl2::TakeArgs a{dfl2::table_view(cache, dst, length, nullptr, 0), src, served, n};
+  cudaError_t e = dfl2::launch_k(dfl2::take_kernel<true>, dim3(1), dim3(dfl2::kBookThreads), 0,
+                                 cu(stream), true, a);
+  if (e == cudaSuccess) {
+    const dfl2::ForkCopyArgs f{a.t, dfl2::row_view(cache), src, served, cache->layers, n};
+    const int64_t items = static_cast<int64_t>(cache->layers) * n * cache->page_size;
+    e = dfl2::launch_k(dfl2::fork_copy_kernel, dim3(dfl2::copy_blocks(items, 8)), dim3(256), 0,
+                       cu(stream), true, f);
+  }
+  return launched(e, "cache fork launch");
+}
+
+dfl2_status dfl2_cache_free(const dfl2_cache* cache, int n, const int32_t* table_rows,
+                            dfl2_stream stream) {
+  const PtrArg ptrs[] = {{table_rows, "table_rows", 4}};
+  DFL2_TRY(dfl2::check_batch(n, 0, 0));
+  DFL2_TRY(check_all_host(cache, ptrs));
+  DFL2_TRY(check_all_device(cache, ptrs));
+  const dfl2::TableView t = dfl2::table_view(cache, table_rows, nullptr, nullptr, 0);
+  return launched(dfl2::launch_k(dfl2::free_kernel, dim3(n), dim3(256), 0, cu(stream), true, t),
+                  "cache free launch");
+}
+
+}  // extern "C"

@@ -74,7 +74,7 @@ typedef enum dfl2_status {
   DFL2_ERR_TIMEOUT = 5      /* a bounded in-kernel wait ran out (see dfl2_device_error) */
 } dfl2_status;
 
-typedef enum dfl2_dtype { DFL2_F32 = 0, DFL2_BF16 = 1 } dfl2_dtype;
+typedef enum dfl2_dtype { DFL2_F32 = 0, DFL2_BF16 = 1, DFL2_F16 = 2 } dfl2_dtype;
 
 /* Library version string, e.g. "dfl2 0.1 sm_103a". */
 const char* dfl2_version(void);
@@ -344,6 +344,158 @@ dfl2_status dfl2_verify(const float* p, const int32_t* tokens, const int32_t* sl
                         const float* q, const int32_t* cand_idx, int B, int L, int V, int greedy,
                         const uint64_t* seeds, uint64_t cycle_offset, int32_t* n_accepted,
                         int32_t* out_tokens, void* ws, size_t ws_bytes, dfl2_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * The target's side of a draft-verify turn: a paged key/value cache, the
+ * attention of a tree of drafted tokens over it, and the tree's acceptance.
+ * No counterpart on the pages, which leave the target model out; a chain of L
+ * drafted tokens (dfl2_tail) is the tree whose node i has parent i - 1.
+ *
+ * A turn of B sequences: node 0 of each tree is its last verified token, whose
+ * keys and values are not in the cache yet; nodes 1 .. are drafted.
+ *   dfl2_cache_reserve   pages for the nodes behind each sequence's length
+ *   dfl2_tree_mask       parents -> which nodes each node sees
+ *   per layer: dfl2_cache_write (the nodes' keys and values), dfl2_tree_attn
+ *   dfl2_tree_accept     the target's choice at each node -> the kept path
+ *   dfl2_cache_compact   the kept nodes' rows moved together, pages given back
+ * dfl2_cache_fork and dfl2_cache_free begin and end sequences.
+ *
+ * The cache.  Element c of position `slot` in page `page`, key head h, layer l
+ * of K is k[l*layer_stride + page*page_stride + h*head_stride +
+ * slot*slot_stride + c] (strides in elements, any order of the dimensions);
+ * V likewise from v.  The pages are shared by all layers and heads.
+ *   dtype       DFL2_BF16, DFL2_F16 or DFL2_F32 (the attention: the first two).
+ *   page_size   8, 16, 32, 64, 128 or 256 positions; head_dim * element size a
+ *               multiple of 16 bytes, and so every stride; k, v 16-byte aligned.
+ *   table       int32 [rows, cols]: entry i of a row is the page holding the
+ *               sequence's positions i*page_size .., -1 where there is none.
+ *   refs        int32 [pages]: how many table entries hold the page; 0 = free.
+ *   free_bits   uint32 [ceil(pages/32)]: bit p%32 of word p/32 is set iff page
+ *               p is free (bits past `pages` clear).
+ * All of it is the caller's memory.  A new cache has table -1, refs 0 and every
+ * page's bit set.  The calls below keep the three in step.  Pages are taken
+ * lowest number first, in the order of the call's sequences and then of
+ * positions, so the state after a call depends only on the state before it.
+ * Lengths (how many positions of a sequence hold committed tokens) are the
+ * caller's int32 arrays; no call needs them on the host.  Only the page that
+ * holds position `length` and those behind it are ever written for a sequence,
+ * and these are never shared: dfl2_cache_fork copies the partly filled one.
+ *
+ * Arguments that the calls share:
+ *   table_rows  int32 [B], the table row of each sequence, distinct within a
+ *               call; NULL: sequence b is row b.
+ *   length      int32 [B]: committed positions of each sequence.
+ *   count       int32 [B]: how many of the T nodes (or tokens) of the sequence
+ *               there are, 0 .. T (other values are taken to the nearer end);
+ *               NULL: T each.
+ *   integer arrays need 4-byte alignment, tensors of elements 16-byte.
+ * A table row or page number out of range is recorded in the device error word
+ * (dfl2_device_error); that sequence or position is then left out.
+ * ------------------------------------------------------------------------- */
+typedef struct dfl2_cache {
+  void* k;
+  void* v;
+  int32_t dtype; /* dfl2_dtype */
+  int32_t layers, pages, kv_heads, page_size, head_dim;
+  int64_t layer_stride, page_stride, head_stride, slot_stride;
+  int32_t* table;
+  int32_t rows, cols;
+  int32_t* refs;
+  uint32_t* free_bits;
+} dfl2_cache;
+
+/* Pages for positions length .. length+count-1 of each sequence: the missing
+ * entries of its table row in that range are filled.  served [B] int32: 1, or 0
+ * where the free pages did not reach (sequences are served in order while they
+ * do; one that needs no page is served in any case) or the row has too few
+ * entries; such a sequence is left as it was.  1 <= B <= 4096, T >= 0. */
+dfl2_status dfl2_cache_reserve(const dfl2_cache* cache, int B, int T, const int32_t* table_rows,
+                               const int32_t* length, const int32_t* count, int32_t* served,
+                               dfl2_stream stream);
+
+/* Rows of keys and values into layers layer .. layer+n_layers-1, positions
+ * length .. length+count-1.  k_new, v_new: element c of head h, token t,
+ * sequence b, layer layer+l at l*new_strides[0] + b*new_strides[1] +
+ * t*new_strides[2] + h*new_strides[3] + c (host array of four element strides,
+ * multiples of 16 bytes, for both).  Positions without a page are skipped and
+ * recorded as out of range. */
+dfl2_status dfl2_cache_write(const dfl2_cache* cache, int layer, int n_layers, const void* k_new,
+                             const void* v_new, const int64_t* new_strides, int B, int T,
+                             const int32_t* table_rows, const int32_t* length,
+                             const int32_t* count, dfl2_stream stream);
+
+/* After acceptance: in every layer, the rows of nodes path[b,0..n_path-1] (as
+ * dfl2_tree_accept gives them: strictly ascending) move to positions length,
+ * length+1, ..; pages of the range length .. length+count-1 that hold none of
+ * the kept rows are given back; new_length[b] = length[b] + n_path[b] (may be
+ * the same array as length).  path int32 [B,T], n_path int32 [B] (0 drops all
+ * drafted rows).  T <= 256. */
+dfl2_status dfl2_cache_compact(const dfl2_cache* cache, int B, int T, const int32_t* table_rows,
+                               const int32_t* length, const int32_t* count, const int32_t* path,
+                               const int32_t* n_path, int32_t* new_length, dfl2_stream stream);
+
+/* Sequence dst[i] (a table row whose entries are all -1) becomes a copy of the
+ * first length[i] positions of table row src[i], for n pairs in order; the same
+ * src may come several times, a dst once and as no src.  Whole pages are
+ * shared; the positions of a partly filled last page are copied in every layer
+ * into a page taken for it.  served [n] int32: 1, or 0 where the free pages did
+ * not reach (in order, as in dfl2_cache_reserve), dst held pages already or src
+ * lacks some; then dst is left as it was.  1 <= n <= 4096. */
+dfl2_status dfl2_cache_fork(const dfl2_cache* cache, int n, const int32_t* src,
+                            const int32_t* dst, const int32_t* length, int32_t* served,
+                            dfl2_stream stream);
+
+/* Gives back every page of n table rows and sets their entries to -1. */
+dfl2_status dfl2_cache_free(const dfl2_cache* cache, int n, const int32_t* table_rows,
+                            dfl2_stream stream);
+
+/* parents int32 [B,T]: parents[b,i] < i is the node that node i follows, -1
+ * none (node 0).  mask uint32 [B,T,ceil(T/32)]: bit j of row i is set iff j is i
+ * or an ancestor of i.  depth int32 [B,T] (nullable): the number of ancestors.
+ * Rows at and past count are 0.  A parent out of range is recorded and read as
+ * -1.  1 <= T <= 256. */
+dfl2_status dfl2_tree_mask(const int32_t* parents, int B, int T, const int32_t* count,
+                           uint32_t* mask, int32_t* depth, dfl2_stream stream);
+
+/* The path of the target's tokens through each tree.  tokens int32 [B,T] (that
+ * of node 0 is not read), target int32 [B,T]: the target's token after node i.
+ * From node 0 on: the lowest-numbered child whose token is the node's target
+ * token, while there is one.  path int32 [B,T]: the nodes, node 0 first, then
+ * -1; n_path int32 [B]; next_token int32 [B]: the last node's target token, the
+ * next turn's node 0.  With greedy targets this is the target's own greedy
+ * decoding; with target[b,i] drawn from the target's distribution at node i it
+ * keeps that distribution.  count 0 gives n_path 0 and next_token -1.
+ * 1 <= T <= 256. */
+dfl2_status dfl2_tree_accept(const int32_t* tokens, const int32_t* parents,
+                             const int32_t* target, int B, int T, const int32_t* count,
+                             int32_t* path, int32_t* n_path, int32_t* next_token,
+                             dfl2_stream stream);
+
+/* Attention of the nodes over the cache, in one layer:
+ *   s_j = scale <q[b,i,h], K[b,j,h*kv_heads/q_heads]>
+ *   out[b,i,h] = sum_j softmax(s)_j V[b,j]   over the positions j that node i
+ * sees: all of 0 .. length-1 and, of the nodes at length .. length+count-1,
+ * those whose bit is set in mask[b,i] (uint32 [B,T,ceil(T/32)]; NULL: node i
+ * sees nodes 0 .. i, a chain).  What a position that a node does not see holds
+ * has no influence on it, NaN included.  A node that sees nothing, or nothing
+ * but scores of -inf, and rows at and past count have out = 0, lse = -inf.
+ *   q, out      bf16 or fp16 as the cache; element c of head h, node i,
+ *               sequence b at b*strides[0] + i*strides[1] + h*strides[2] + c
+ *               (host arrays of three element strides, multiples of 8).  out
+ *               must not overlap q or the cache.
+ *   lse         float32 [B,T,q_heads] (nullable): log sum_j exp(s_j).
+ *   head_dim 64, 128 or 256; q_heads a multiple of kv_heads; 1 <= T <= 256;
+ *   1 <= B <= 65535; lengths below 2^30.
+ *   ws          dfl2_tree_attn_workspace_size bytes, scratch only.
+ * Scores, softmax and sums are float32; the weights are rounded to the cache's
+ * type for the product with V. */
+size_t dfl2_tree_attn_workspace_size(int B, int T, int q_heads, int kv_heads, int head_dim,
+                                     dfl2_dtype dtype);
+dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_cache* cache,
+                           int layer, int B, int T, int q_heads, const int32_t* table_rows,
+                           const int32_t* length, const int32_t* count, const uint32_t* mask,
+                           float scale, void* out, const int64_t* out_strides, float* lse,
+                           void* ws, size_t ws_bytes, dfl2_stream stream);
 
 #ifdef __cplusplus
 }
