@@ -21,6 +21,7 @@ enum DeviceError : uint32_t {
   kDevErrGemm = 3,       // projection GEMM pipeline wait ran out
   kDevErrConv = 4,       // conv GEMM pipeline wait ran out
   kDevErrBadIndex = 5,   // a candidate or verified token id outside [0, V)
+  kDevErrAttn = 6,       // tree attention pipeline wait ran out
 };
 
 // About two seconds at the GB300's maximum SM clock: far beyond any legitimate wait.

@@ -20,122 +20,13 @@
 // Softmax in one pass: with the running maximum m and sum l of a row, a tile
 // with row maximum m' multiplies l and o by 2^(m - m') before adding its own
 // terms (scores are kept times log2 e, so that exp is exp2).
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
-#include "cache.cuh"
+#include "tree_attn.cuh"
 
 namespace dfl2 {
 namespace {
-
-constexpr unsigned kAll = 0xffffffffu;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMaxLen = 1 << 30;
-
-struct AttnArgs {
-  TableView t;
-  const void* q;
-  int64_t qb, qt, qh;  // element strides
-  const void* k;       // the layer's keys and values
-  const void* v;
-  int64_t page_stride, head_stride, slot_stride;
-  const uint32_t* mask;  // [B][T][W], or NULL: a chain
-  int W;
-  int B, H, G;           // sequences, key heads, query heads per key head
-  float scale_log2;      // scale * log2 e
-  void* out;
-  int64_t ob, ot, oh;
-  float* lse;      // nullable
-  float* part_o;   // [grid][2][rows of a tile][D] unnormalised outputs
-  float2* part_ml; // [grid][2][rows of a tile] (maximum, sum)
-  int grid;        // CTAs of the main kernel
-  int row_tiles;   // ceil(T G / rows of a tile)
-};
-
-// What a row of length `len` and `n` nodes amounts to; n == 0: no units.
-struct Seq {
-  int row, len, n, tiles;
-};
-template <int kKeys>
-__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
-  Seq s;
-  s.row = a.t.row_of(b);
-  s.len = a.t.length[b];
-  s.n = a.t.count_of(b);
-  if (s.row < 0 || s.len < 0 || s.len > kMaxLen) s.n = 0;
-  s.tiles = s.n > 0 ? (s.len + s.n + kKeys - 1) / kKeys : 0;
-  return s;
-}
-
-// Units before sequence b (all of them for b = B), by a warp together.
-template <int kKeys>
-__device__ __forceinline__ int64_t units_before(const AttnArgs& a, int b) {
-  const int lane = threadIdx.x & 31;
-  int64_t x = 0;
-  for (int i = lane; i < b; i += 32) x += load_seq<kKeys>(a, i).tiles;
-#pragma unroll
-  for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(kAll, x, off);
-  return x * (a.H * a.row_tiles);
-}
-
-// The sequence that unit u falls in, and the units before it.
-template <int kKeys>
-__device__ __forceinline__ int find_seq(const AttnArgs& a, int64_t u, int64_t& before) {
-  const int lane = threadIdx.x & 31;
-  const int64_t per = a.H * a.row_tiles;
-  int64_t base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int64_t own = b0 + lane < a.B ? load_seq<kKeys>(a, b0 + lane).tiles * per : 0;
-    int64_t x = own;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(kAll, x, off);
-      if (lane >= off) x += y;
-    }
-    const unsigned hit = __ballot_sync(kAll, u < base + x);
-    if (hit) {
-      const int w = __ffs(hit) - 1;
-      before = base + __shfl_sync(kAll, x - own, w);
-      return b0 + w;
-    }
-    base += __shfl_sync(kAll, x, 31);
-  }
-  before = base;
-  return a.B;
-}
-
-// Where CTA c's range of `units` units on `n` CTAs begins, and whose range unit u is in.
-__device__ __forceinline__ int64_t range_start(int64_t units, int n, int c) {
-  return units * c / n;
-}
-__device__ __forceinline__ int range_of(int64_t units, int n, int64_t u) {
-  return static_cast<int>(((u + 1) * n - 1) / units);
-}
-
-// A place in the CTA's range of units.
-template <int kKeys>
-struct Cursor {
-  int64_t u;
-  int b, hr, tile;  // sequence, key head * row_tiles + row tile, tile
-  Seq s;
-  __device__ __forceinline__ void next(const AttnArgs& a) {
-    ++u;
-    if (++tile < s.tiles) return;
-    tile = 0;
-    if (++hr < a.H * a.row_tiles) return;
-    hr = 0;
-    do {
-      if (++b >= a.B) return;
-      s = load_seq<kKeys>(a, b);
-    } while (s.tiles == 0);
-  }
-};
 
 template <typename E>
 __device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], const uint32_t b0,
@@ -158,87 +49,18 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t r[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
 }
-// 2^x to two units in the last place; results below 2^-126 become 0.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-template <typename E>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {  // x in the low half
-  if constexpr (std::is_same_v<E, __half>) {
-    const __half2 h = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-template <typename E>
-__device__ __forceinline__ float to_f32(E x) {
-  if constexpr (std::is_same_v<E, __half>)
-    return __half2float(x);
-  else
-    return __bfloat162float(x);
-}
-template <typename E>
-constexpr uint32_t kExpMask = std::is_same_v<E, __half> ? 0x7C00u : 0x7F80u;
-
-// Two elements with those that are Inf or NaN set to 0; bad: whether there was one.
-template <typename E>
-__device__ __forceinline__ uint32_t finite2(uint32_t x, bool& bad) {
-  constexpr uint32_t lo = kExpMask<E>, hi = lo << 16;
-  if ((x & lo) == lo) {
-    x &= 0xFFFF0000u;
-    bad = true;
-  }
-  if ((x & hi) == hi) {
-    x &= 0x0000FFFFu;
-    bad = true;
-  }
-  return x;
-}
-
-// Whether node i of sequence b sees node j (0 <= j).
-__device__ __forceinline__ bool sees(const AttnArgs& a, int b, int n, int i, int j) {
-  if (j >= n) return false;
-  if (!a.mask) return j <= i;
-  return a.mask[(static_cast<int64_t>(b) * a.t.T + i) * a.W + (j >> 5)] >> (j & 31) & 1u;
-}
-
-// The Inf and NaN values, of the nodes of positions [p0, p1), that node i sees
-// in channel c: their sum, which decides that channel of the output.  Such
-// values are kept out of the matrix product, where a weight of 0 would spread
-// them to the nodes that do not see them.  Only ever called when there are any.
-template <typename E>
-__device__ __noinline__ float unseen_safe_sum(const AttnArgs& a, int b, const Seq& s, int h, int i,
-                                              int c, int p0, int p1) {
-  float x = 0.f;
-  for (int pos = max(p0, s.len); pos < min(p1, s.len + s.n); ++pos) {
-    if (!sees(a, b, s.n, i, pos - s.len)) continue;
-    const int64_t page = a.t.page_at(s.row, pos >> a.t.page_shift);
-    if (page < 0) continue;
-    const E* v = static_cast<const E*>(a.v) + page * a.page_stride + h * a.head_stride +
-                 (pos & ((1 << a.t.page_shift) - 1)) * a.slot_stride;
-    const float y = to_f32(v[c]);
-    if (!isfinite(y)) x += y;
-  }
-  return x;
-}
-
 // ---------------------------------------------------------------------------
 // Warp-level kernel.  Four warps, tiles of 64 keys, 16 keys to a warp: each warp
 // keeps its own maximum, sum and output for all rows and the four are added at
 // the end of a row tile, so no warp waits for another inside a tile but for its
 // keys' arrival.
 // ---------------------------------------------------------------------------
-constexpr int kWKeys = 64;
 constexpr int kWThreads = 128;
 
 template <int D, int kRows>
 struct WarpCfg {
   static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;
-  static constexpr int kTile = kWKeys * D * 2;  // bytes of K (or V) in a stage
+  static constexpr int kTile = kKeys * D * 2;  // bytes of K (or V) in a stage
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kJoin = kRows == 16 ? 64 : 32;  // channels added per round at the end
   static constexpr int kJoinBytes = kRows * kJoin * 4;
@@ -253,7 +75,7 @@ __global__ void __launch_bounds__(kWThreads, D == 256 ? 1 : 2)
   constexpr int kMT = kRows / 16;        // 16-row MMA tiles
   constexpr int kCPR = D / 8;            // 16-byte pieces of a key
   constexpr int kRowStep = kWThreads / kCPR;
-  constexpr int kPer = kWKeys / kRowStep;  // keys each thread copies a piece of, per tile
+  constexpr int kPer = kKeys / kRowStep;  // keys each thread copies a piece of, per tile
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem;
   uint8_t* qs = smem + C::kStages * 2 * C::kTile;
@@ -268,22 +90,22 @@ __global__ void __launch_bounds__(kWThreads, D == 256 ? 1 : 2)
   pdl_wait();
   pdl_launch_dependents();
 
-  const int64_t units = units_before<kWKeys>(a, a.B);
+  const int64_t units = units_before(a, a.B);
   const int n_cta = static_cast<int>(min(static_cast<int64_t>(a.grid), units));
   if (static_cast<int>(blockIdx.x) >= n_cta) return;
   const int64_t u0 = range_start(units, n_cta, blockIdx.x);
   const int64_t u1 = range_start(units, n_cta, blockIdx.x + 1);
 
-  Cursor<kWKeys> cur;
+  Cursor cur;
   {
     int64_t before;
     cur.u = u0;
-    cur.b = find_seq<kWKeys>(a, u0, before);
-    cur.s = load_seq<kWKeys>(a, cur.b);
+    cur.b = find_seq(a, u0, before);
+    cur.s = load_seq(a, cur.b);
     cur.hr = static_cast<int>((u0 - before) / cur.s.tiles);
     cur.tile = static_cast<int>((u0 - before) % cur.s.tiles);
   }
-  Cursor<kWKeys> ld = cur;
+  Cursor ld = cur;
 
   // ---- loads: thread -> piece cp of keys kr0, kr0 + kRowStep, .. ----
   const int cp = tid % kCPR, kr0 = tid / kCPR;
@@ -293,7 +115,7 @@ __global__ void __launch_bounds__(kWThreads, D == 256 ? 1 : 2)
     const int end = ld.s.len + ld.s.n;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int pos = ld.tile * kWKeys + kr0 + i * kRowStep;
+      const int pos = ld.tile * kKeys + kr0 + i * kRowStep;
       pages[i] = pos < end ? a.t.page_at(ld.s.row, pos >> a.t.page_shift) : -1;
     }
   };
@@ -304,7 +126,7 @@ __global__ void __launch_bounds__(kWThreads, D == 256 ? 1 : 2)
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int r = kr0 + i * kRowStep;
-        const int pos = ld.tile * kWKeys + r;
+        const int pos = ld.tile * kKeys + r;
         const bool ok = pages[i] >= 0;
         const int64_t at = static_cast<int64_t>(ok ? pages[i] : 0) * a.page_stride +
                            h * a.head_stride + (ok ? pos & ps1 : 0) * a.slot_stride + cp * 8;
@@ -362,7 +184,7 @@ __global__ void __launch_bounds__(kWThreads, D == 256 ? 1 : 2)
 
     uint8_t* kst = ring + stage * 2 * C::kTile + warp * 16 * (D * 2);
     uint8_t* vst = kst + C::kTile;
-    const int p0 = cur.tile * kWKeys + warp * 16;  // this warp's first position
+    const int p0 = cur.tile * kKeys + warp * 16;  // this warp's first position
     const bool edge = p0 + 16 > s.len;             // has nodes, or lies past the end
 
     // scores: rows x 16 keys
@@ -550,8 +372,8 @@ __global__ void __launch_bounds__(kWThreads, D == 256 ? 1 : 2)
           if (any_bad) {
             float* yy = reinterpret_cast<float*>(&y);
             for (int z = 0; z < 4; ++z)
-              yy[z] += unseen_safe_sum<E>(a, cur.b, s, h, node, c + z, tile_lo * kWKeys,
-                                          tile_hi * kWKeys);
+              yy[z] += unseen_safe_sum<E>(a, cur.b, s, h, node, c + z, tile_lo * kKeys,
+                                          tile_hi * kKeys);
           }
           if (whole) {
             if (node < s.n) {
@@ -579,7 +401,7 @@ __global__ void __launch_bounds__(kWThreads, D == 256 ? 1 : 2)
 
 // One warp to an output row: the parts that the CTAs left of it, in the order of
 // the keys; rows past a sequence's count are zeroed.
-template <typename E, int D, int kRows, int kKeys>
+template <typename E, int D>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnArgs a) {
   pdl_wait();
   pdl_launch_dependents();
@@ -590,7 +412,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
   if (x >= a.H * M) return;
   const int h = x / M, r = x % M;
   const int node = r / a.G, head = h * a.G + r % a.G;
-  const Seq s = load_seq<kKeys>(a, b);
+  const Seq s = load_seq(a, b);
   constexpr int kPer = D / 32;  // channels per lane
   E* out = static_cast<E*>(a.out) + b * a.ob + node * a.ot + head * a.oh + lane * kPer;
   float* lse = a.lse ? a.lse + (static_cast<int64_t>(b) * a.t.T + node) * (a.H * a.G) + head
@@ -600,15 +422,15 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
   for (int i = 0; i < kPer; ++i) y[i] = 0.f;
   float mm = -INFINITY, safe = 0.f, ll = 0.f;
   if (node < s.n) {
-    const int64_t units = units_before<kKeys>(a, a.B);
+    const int64_t units = units_before(a, a.B);
     const int n_cta = static_cast<int>(min(static_cast<int64_t>(a.grid), units));
-    const int64_t v0 = units_before<kKeys>(a, b) +
-                       static_cast<int64_t>(h * a.row_tiles + r / kRows) * s.tiles;
+    const int64_t v0 = units_before(a, b) +
+                       static_cast<int64_t>(h * a.row_tiles + r / a.rows) * s.tiles;
     const int c0 = range_of(units, n_cta, v0), c1 = range_of(units, n_cta, v0 + s.tiles - 1);
     if (c0 == c1) return;  // written by the CTA that had all of it
     const int slot0 = range_start(units, n_cta, c0) < v0 ? 1 : 0;
     auto part = [&](int c) {
-      return (static_cast<int64_t>(c) * 2 + (c == c0 ? slot0 : 0)) * kRows + r % kRows;
+      return (static_cast<int64_t>(c) * 2 + (c == c0 ? slot0 : 0)) * a.rows + r % a.rows;
     };
     for (int c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, a.part_ml[part(c)].x);
 #pragma unroll
@@ -637,19 +459,22 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
 
 // ---- plan ---------------------------------------------------------------------
 struct AttnPlan {
-  int rows;  // rows of a tile
+  bool tc;    // the tensor-core kernel
+  int rows;   // rows of a row tile
   int row_tiles, grid;
   size_t o_off, ml_off, ws_bytes;
 };
 
-// Rows of a tile: one 16-row MMA tile while all rows fit it (a decode step), two
-// otherwise, so that a key is loaded half as often; 256 channels leave
-// registers for one.
-AttnPlan attn_plan(int M, int D, int sms) {
+// The warp-level kernel for a few rows (one 16-row MMA tile while they fit it, two
+// up to 32 rows, so that a key is loaded half as often), the tensor cores' 128-row
+// tiles above; 256 channels, and strides that no tensor map takes, stay with the
+// warp-level kernel.
+AttnPlan attn_plan(int M, int D, bool tc_takes, int sms) {
   AttnPlan p;
-  p.rows = M <= 16 || D == 256 ? 16 : 32;
+  p.tc = tc_takes && M > 16;
+  p.rows = p.tc ? attn_tc_rows(M) : M <= 16 || D == 256 ? 16 : 32;
   p.row_tiles = (M + p.rows - 1) / p.rows;
-  p.grid = sms * (D == 256 ? 1 : 2);
+  p.grid = p.tc ? attn_tc_grid(p.rows, sms) : sms * (D == 256 ? 1 : 2);
   p.o_off = 0;
   p.ml_off = align_up(size_t(p.grid) * 2 * p.rows * D * sizeof(float), 256);
   p.ws_bytes = p.ml_off + align_up(size_t(p.grid) * 2 * p.rows * sizeof(float2), 256);
@@ -660,22 +485,33 @@ template <typename E, int D, int kRows>
 cudaError_t launch_warp(const AttnArgs& a, cudaStream_t s) {
   auto kernel = attn_warp_kernel<E, D, kRows>;
   constexpr size_t smem = WarpCfg<D, kRows>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  const cudaError_t e = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  e = launch_k(kernel, dim3(a.grid), dim3(kWThreads), smem, s, true, a);
+  return launch_k(kernel, dim3(a.grid), dim3(kWThreads), smem, s, true, a);
+}
+
+template <typename E, int D>
+cudaError_t launch_attn(const AttnArgs& a, const AttnPlan& p, const dfl2_cache* c,
+                        cudaStream_t s) {
+  cudaError_t e;
+  if (p.tc)
+    e = launch_attn_tc(a, c, s);
+  else if (D == 256 || p.rows == 16)
+    e = launch_warp<E, D, 16>(a, s);
+  else
+    e = launch_warp<E, D, D == 256 ? 16 : 32>(a, s);
   if (e != cudaSuccess) return e;
   const int warps = a.H * a.t.T * a.G;
-  return launch_k(combine_kernel<E, D, kRows, kWKeys>, dim3((warps + 7) / 8, a.B), dim3(256), 0, s,
-                  true, a);
+  return launch_k(combine_kernel<E, D>, dim3((warps + 7) / 8, a.B), dim3(256), 0, s, true, a);
 }
 
 template <typename E>
-cudaError_t launch_attn(const AttnArgs& a, const AttnPlan& p, int D, cudaStream_t s) {
-  if (D == 256) return launch_warp<E, 256, 16>(a, s);
-  if (D == 128)
-    return p.rows == 16 ? launch_warp<E, 128, 16>(a, s) : launch_warp<E, 128, 32>(a, s);
-  return p.rows == 16 ? launch_warp<E, 64, 16>(a, s) : launch_warp<E, 64, 32>(a, s);
+cudaError_t launch_attn_d(const AttnArgs& a, const AttnPlan& p, const dfl2_cache* c,
+                          cudaStream_t s) {
+  return c->head_dim == 64    ? launch_attn<E, 64>(a, p, c, s)
+         : c->head_dim == 128 ? launch_attn<E, 128>(a, p, c, s)
+                              : launch_attn<E, 256>(a, p, c, s);
 }
 
 dfl2_status check_shapes(int B, int T, int q_heads, int kv_heads, int head_dim, int dtype) {
@@ -710,7 +546,11 @@ size_t dfl2_tree_attn_workspace_size(int B, int T, int q_heads, int kv_heads, in
                                      dfl2_dtype dtype) {
   if (dfl2::check_shapes(B, T, q_heads, kv_heads, head_dim, dtype) != DFL2_OK) return 0;
   if (dfl2::check_args_device(nullptr, 0) != DFL2_OK) return 0;
-  return dfl2::attn_plan(T * (q_heads / kv_heads), head_dim, dfl2::device_info().sms).ws_bytes;
+  // (whichever kernel the cache's strides will allow)
+  const int M = T * (q_heads / kv_heads), sms = dfl2::device_info().sms;
+  const bool tc = head_dim != 256;
+  return std::max(dfl2::attn_plan(M, head_dim, false, sms).ws_bytes,
+                  dfl2::attn_plan(M, head_dim, tc, sms).ws_bytes);
 }
 
 dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_cache* cache,
@@ -737,7 +577,7 @@ dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_c
   DFL2_TRY(dfl2::check_args_device(ptrs, 7));
   DFL2_TRY(dfl2::check_cache_device(cache));
   const int G = q_heads / cache->kv_heads, D = cache->head_dim;
-  const dfl2::AttnPlan p = dfl2::attn_plan(T * G, D, dfl2::device_info().sms);
+  const dfl2::AttnPlan p = dfl2::attn_plan(T * G, D, dfl2::attn_tc_takes(cache), dfl2::device_info().sms);
   if (!ws || ws_bytes < p.ws_bytes)
     return dfl2::report_errorf(DFL2_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed",
                                ws ? ws_bytes : size_t(0), p.ws_bytes);
@@ -771,10 +611,12 @@ dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_c
   a.part_o = reinterpret_cast<float*>(w + p.o_off);
   a.part_ml = reinterpret_cast<float2*>(w + p.ml_off);
   a.grid = p.grid;
+  a.rows = p.rows;
   a.row_tiles = p.row_tiles;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->dtype == DFL2_F16 ? dfl2::launch_attn<__half>(a, p, D, s)
-                                                 : dfl2::launch_attn<__nv_bfloat16>(a, p, D, s);
+  const cudaError_t e = cache->dtype == DFL2_F16
+                            ? dfl2::launch_attn_d<__half>(a, p, cache, s)
+                            : dfl2::launch_attn_d<__nv_bfloat16>(a, p, cache, s);
   return e == cudaSuccess ? DFL2_OK : dfl2::report_cuda_error(e, "tree attention launch");
 }
 

@@ -1,0 +1,199 @@
+// What the two attention kernels share: their arguments, the division of the work
+// into units, what a node sees, and small conversions.  Not public.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "cache.cuh"
+
+namespace dfl2 {
+namespace {  // each translation unit its own copy
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxLen = 1 << 30;
+constexpr int kKeys = 64;  // keys of a tile, in both kernels
+
+}  // namespace
+
+struct AttnArgs {
+  TableView t;
+  const void* q;
+  int64_t qb, qt, qh;  // element strides
+  const void* k;       // the layer's keys and values
+  const void* v;
+  int64_t page_stride, head_stride, slot_stride;
+  const uint32_t* mask;  // [B][T][W], or NULL: a chain
+  int W;
+  int B, H, G;           // sequences, key heads, query heads per key head
+  float scale_log2;      // scale * log2 e
+  void* out;
+  int64_t ob, ot, oh;
+  float* lse;      // nullable
+  float* part_o;   // [grid][2][rows][D] unnormalised outputs
+  float2* part_ml; // [grid][2][rows] (maximum, sum)
+  int grid;        // CTAs of the main kernel
+  int rows;        // rows of a row tile
+  int row_tiles;   // ceil(T G / rows)
+};
+
+namespace {
+
+// What a row of length `len` and `n` nodes amounts to; n == 0: no units.
+struct Seq {
+  int row, len, n, tiles;
+};
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
+  Seq s;
+  s.row = a.t.row_of(b);
+  s.len = a.t.length[b];
+  s.n = a.t.count_of(b);
+  if (s.row < 0 || s.len < 0 || s.len > kMaxLen) s.n = 0;
+  s.tiles = s.n > 0 ? (s.len + s.n + kKeys - 1) / kKeys : 0;
+  return s;
+}
+
+// Units before sequence b (all of them for b = B), by a warp together.
+__device__ __forceinline__ int64_t units_before(const AttnArgs& a, int b) {
+  const int lane = threadIdx.x & 31;
+  int64_t x = 0;
+  for (int i = lane; i < b; i += 32) x += load_seq(a, i).tiles;
+#pragma unroll
+  for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(kAll, x, off);
+  return x * (a.H * a.row_tiles);
+}
+
+// The sequence that unit u falls in, and the units before it.
+__device__ __forceinline__ int find_seq(const AttnArgs& a, int64_t u, int64_t& before) {
+  const int lane = threadIdx.x & 31;
+  const int64_t per = a.H * a.row_tiles;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int64_t own = b0 + lane < a.B ? load_seq(a, b0 + lane).tiles * per : 0;
+    int64_t x = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(kAll, x, off);
+      if (lane >= off) x += y;
+    }
+    const unsigned hit = __ballot_sync(kAll, u < base + x);
+    if (hit) {
+      const int w = __ffs(hit) - 1;
+      before = base + __shfl_sync(kAll, x - own, w);
+      return b0 + w;
+    }
+    base += __shfl_sync(kAll, x, 31);
+  }
+  before = base;
+  return a.B;
+}
+
+// Where CTA c's range of `units` units on `n` CTAs begins, and whose range unit u is in.
+__device__ __forceinline__ int64_t range_start(int64_t units, int n, int c) {
+  return units * c / n;
+}
+__device__ __forceinline__ int range_of(int64_t units, int n, int64_t u) {
+  return static_cast<int>(((u + 1) * n - 1) / units);
+}
+
+// A place in the CTA's range of units.
+struct Cursor {
+  int64_t u;
+  int b, hr, tile;  // sequence, key head * row_tiles + row tile, tile
+  Seq s;
+  __device__ __forceinline__ void next(const AttnArgs& a) {
+    ++u;
+    if (++tile < s.tiles) return;
+    tile = 0;
+    if (++hr < a.H * a.row_tiles) return;
+    hr = 0;
+    do {
+      if (++b >= a.B) return;
+      s = load_seq(a, b);
+    } while (s.tiles == 0);
+  }
+};
+
+// 2^x to two units in the last place; results below 2^-126 become 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <typename E>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {  // x in the low half
+  if constexpr (std::is_same_v<E, __half>) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+template <typename E>
+__device__ __forceinline__ float to_f32(E x) {
+  if constexpr (std::is_same_v<E, __half>)
+    return __half2float(x);
+  else
+    return __bfloat162float(x);
+}
+template <typename E>
+constexpr uint32_t kExpMask = std::is_same_v<E, __half> ? 0x7C00u : 0x7F80u;
+
+// Two elements with those that are Inf or NaN set to 0; bad: whether there was one.
+template <typename E>
+__device__ __forceinline__ uint32_t finite2(uint32_t x, bool& bad) {
+  constexpr uint32_t lo = kExpMask<E>, hi = lo << 16;
+  if ((x & lo) == lo) {
+    x &= 0xFFFF0000u;
+    bad = true;
+  }
+  if ((x & hi) == hi) {
+    x &= 0x0000FFFFu;
+    bad = true;
+  }
+  return x;
+}
+
+// Whether node i of sequence b sees node j (0 <= j).
+__device__ __forceinline__ bool sees(const AttnArgs& a, int b, int n, int i, int j) {
+  if (j >= n) return false;
+  if (!a.mask) return j <= i;
+  return a.mask[(static_cast<int64_t>(b) * a.t.T + i) * a.W + (j >> 5)] >> (j & 31) & 1u;
+}
+
+// The Inf and NaN values, of the nodes of positions [p0, p1), that node i sees
+// in channel c: their sum, which decides that channel of the output.  Such
+// values are kept out of the matrix product, where a weight of 0 would spread
+// them to the nodes that do not see them.  Only ever called when there are any.
+template <typename E>
+__device__ __noinline__ float unseen_safe_sum(const AttnArgs& a, int b, const Seq& s, int h, int i,
+                                              int c, int p0, int p1) {
+  float x = 0.f;
+  for (int pos = max(p0, s.len); pos < min(p1, s.len + s.n); ++pos) {
+    if (!sees(a, b, s.n, i, pos - s.len)) continue;
+    const int64_t page = a.t.page_at(s.row, pos >> a.t.page_shift);
+    if (page < 0) continue;
+    const E* v = static_cast<const E*>(a.v) + page * a.page_stride + h * a.head_stride +
+                 (pos & ((1 << a.t.page_shift) - 1)) * a.slot_stride;
+    const float y = to_f32(v[c]);
+    if (!isfinite(y)) x += y;
+  }
+  return x;
+}
+
+}  // namespace
+
+// The tensor-core kernel (tree_attn_tc.cu): whether it takes this cache, its row
+// tile for M rows, its CTAs and its launch (without the combination of the parts).
+bool attn_tc_takes(const dfl2_cache* c);
+int attn_tc_rows(int M);
+int attn_tc_grid(int rows, int sms);
+cudaError_t launch_attn_tc(const AttnArgs& a, const dfl2_cache* c, cudaStream_t s);
+
+}  // namespace dfl2

@@ -1,0 +1,650 @@
+// Tree attention on the tensor cores (include/dfl2.h, dfl2_tree_attn; the split of
+// the work and the combination of parts are in tree_attn.cu).
+//
+// For a row tile of 128 rows (node, head) and tiles of 64 keys:
+//   S = Q K^T   tcgen05.mma, 128 x 64, Q and K in shared memory, S (float32) in TMEM
+//   P = 2^(scale log2 e S - m)   a thread to a row: its 64 scores come from TMEM,
+//               its weights go back over them, rounded to the cache's type
+//   O += P V    tcgen05.mma, 128 x D, P in TMEM, V in shared memory as it lies in
+//               the cache (keys x channels: the channel-major operand), O in TMEM
+// A row's statistics never leave its thread, so the softmax has no exchange at
+// all.  O is rescaled only when a row's maximum has risen by more than 2^8 since
+// the reference m was taken: weights up to 2^8 lose nothing in float32 sums or in
+// rounding to a floating type, and the rescaling (TMEM -> registers -> TMEM, after
+// the products in flight) then almost never happens past a row's first tiles.
+//
+// Roles: warp 0 loads K and V (TMA boxes of one page's rows x 64 channels,
+// 128-byte swizzle, into a ring of slots of one tile's K or V), warp 1 issues the
+// MMAs, four warps a stream do the softmax.  A stream is 128 rows.  The MMAs of
+// tile i+1's scores are issued before those of tile i's output, so that the
+// tensor core works while the softmax of tile i runs; S is double-buffered.
+// With M = T G rows up to 128: one stream, two CTAs on an SM.  Above: one CTA with
+// two streams (256 rows), which share each K and V tile, so that the shared-memory
+// fill per row, the next bound after HBM, is halved.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+
+#include "tree_attn.cuh"
+
+namespace dfl2 {
+namespace {
+
+constexpr int kLanes = 128;                // rows of a stream: the TMEM lanes
+constexpr float kRise = 8.f;               // log2 of the rise that O is rescaled at
+constexpr uint32_t kStreamCols = 256;      // TMEM columns of a stream: S, S, O
+
+template <int D, int NS>
+struct TcCfg {
+  static constexpr int kSlot = kKeys * D * 2;  // bytes of a tile's K (or V)
+  static constexpr int kSlots = (NS == 1 ? 81920 : 163840) / kSlot > 16
+                                    ? 16
+                                    : (NS == 1 ? 81920 : 163840) / kSlot;
+  static constexpr int kQ = kLanes * D * 2;    // bytes of a stream's Q
+  static constexpr int kThreads = 64 + NS * kLanes;
+  static constexpr int kBars = 2 * kSlots + NS * 6 + 1;
+  static constexpr size_t kSmem = size_t(NS) * kQ + size_t(kSlots) * kSlot + kBars * 8 + 64;
+};
+
+// Operand of 128-byte rows in the 128-byte swizzle whose contiguous dimension is
+// not the summed one: 64-element blocks along it `block` bytes apart, groups of
+// eight summed indices 1024 bytes apart.
+__device__ __forceinline__ uint64_t umma_desc_sw128_mn(const void* smem_tile, uint32_t block) {
+  uint64_t d = (static_cast<uint64_t>(smem_u32(smem_tile)) >> 4) & 0x3FFFull;
+  d |= static_cast<uint64_t>(block >> 4) << 16;  // leading byte offset
+  d |= uint64_t(1024 >> 4) << 32;                // stride byte offset
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(2) << 61;
+  return d;
+}
+// kind::f16, float32 accumulator; b_mn: B's contiguous dimension is N.
+template <typename E>
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
+  const uint32_t f = std::is_same_v<E, __half> ? 0u : 1u;
+  return (1u << 4) | (f << 7) | (f << 10) | ((b_mn ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// As umma_bf16 with A in TMEM.
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// Waits for this thread's tcgen05.ld; names r so that nothing reads it before.
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+      "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, "
+      "%27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z,
+                                            int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Which of the 64 positions from p0 on node i of sequence b sees (0 past the end).
+__device__ __forceinline__ uint64_t seen64(const AttnArgs& a, int b, const Seq& s, int i, int p0) {
+  if (i >= s.n) return 0;
+  const int ctx = max(0, min(64, s.len - p0));  // committed positions of the tile
+  uint64_t vis = ctx == 64 ? ~0ull : (1ull << ctx) - 1;
+  if (ctx == 64) return vis;
+  const int j0 = p0 + ctx - s.len;              // first node of the tile
+  if (j0 >= s.n) return vis;
+  uint64_t nodes;
+  if (a.mask) {
+    const uint32_t* w = a.mask + (static_cast<int64_t>(b) * a.t.T + i) * a.W;
+    const int w0 = j0 >> 5;
+    const uint64_t lo = w[w0], mid = w0 + 1 < a.W ? w[w0 + 1] : 0, hi = w0 + 2 < a.W ? w[w0 + 2] : 0;
+    const int sh = j0 & 31;
+    nodes = ((lo | mid << 32) >> sh) | (sh ? hi << (64 - sh) : 0);
+  } else {
+    nodes = i < j0 ? 0 : i - j0 >= 63 ? ~0ull : (2ull << (i - j0)) - 1;
+  }
+  const int left = s.n - j0;
+  if (left < 64) nodes &= (1ull << left) - 1;
+  return vis | nodes << ctx;
+}
+
+template <typename E, int D, int NS>
+__global__ void __launch_bounds__(64 + NS * kLanes, NS == 1 ? 2 : 1)
+    attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const int heads_first) {
+  using C = TcCfg<D, NS>;
+  constexpr int kBlk = D / 64;          // 64-channel blocks of a row
+  constexpr int kBlkBytes = kKeys * 128;  // one block of a K or V slot
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* qs = smem;                   // [NS][kBlk][128 rows][128 B]
+  uint8_t* ring = smem + NS * C::kQ;    // [slots][kBlk][64 keys][128 B]
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + C::kSlots * C::kSlot);
+  uint64_t* empty = full + C::kSlots;
+  uint64_t* q_full = empty + C::kSlots;  // [NS] a row tile's Q is in place
+  uint64_t* s_full = q_full + NS;        // [NS][2] scores are in TMEM
+  uint64_t* p_ready = s_full + 2 * NS;   // [NS][2] weights are in TMEM (the softmax may be a tile ahead)
+  uint64_t* pv_done = p_ready + 2 * NS;      // [NS] the output product is in O
+  uint64_t* all_done = pv_done + NS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + 1);
+  int* bad_seg = reinterpret_cast<int*>(tmem_slot + 1);  // [4] row tile that met Inf or NaN in V
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&q_full[s], 4);
+      mbar_init(&s_full[2 * s], 1);
+      mbar_init(&s_full[2 * s + 1], 1);
+      mbar_init(&p_ready[2 * s], 4);
+      mbar_init(&p_ready[2 * s + 1], 4);
+      mbar_init(&pv_done[s], 1);
+    }
+    mbar_init(all_done, 1);
+    for (int i = 0; i < 4; ++i) bad_seg[i] = -1;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, NS * kStreamCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // this CTA's range of units, and where it begins (each warp for itself)
+  const int64_t units = units_before(a, a.B);
+  const int n_cta = static_cast<int>(min(static_cast<int64_t>(a.grid), units));
+  int64_t u0 = 0, u1 = 0;
+  Cursor cur;
+  if (static_cast<int>(blockIdx.x) < n_cta) {
+    u0 = range_start(units, n_cta, blockIdx.x);
+    u1 = range_start(units, n_cta, blockIdx.x + 1);
+    int64_t before;
+    cur.u = u0;
+    cur.b = find_seq(a, u0, before);
+    cur.s = load_seq(a, cur.b);
+    cur.hr = static_cast<int>((u0 - before) / cur.s.tiles);
+    cur.tile = static_cast<int>((u0 - before) % cur.s.tiles);
+  }
+  int N = static_cast<int>(u1 - u0);
+  if (smem_u32(smem) & 1023u) {  // the swizzle counts on it
+    record_error(a.t.err, kDevErrAttn);
+    N = 0;
+  }
+  // The ring's order is K(0), K(1), V(0), K(2), V(1), ..: as the MMAs read them.
+  auto seq_k = [](int i) { return i == 0 ? 0 : 2 * i - 1; };
+  auto seq_v = [N](int i) { return i + 1 < N ? 2 * i + 2 : 2 * i + 1; };
+
+  if (warp == 0) {
+    // ---- loads ----
+    const int ps = 1 << a.t.page_shift;
+    const int box = min(ps, kKeys);           // positions of a TMA box
+    const int n_page = kKeys / box;           // pages of a tile
+    const int my_page = lane / kBlk, my_blk = lane % kBlk;
+    const bool mine = my_page < n_page;
+    auto page_of = [&](const Cursor& c) {     // this lane's page of the tile at c
+      const int pos = c.tile * kKeys + my_page * box;
+      // past the end: one page too far, which TMA reads as zeros
+      const int p = mine && pos < c.s.len + c.s.n ? a.t.page_at(c.s.row, pos >> a.t.page_shift) : -1;
+      return p < 0 ? a.t.pages : p;
+    };
+    int issued = 0;
+    bool ok = true;
+    auto load = [&](const CUtensorMap* tm, int h, int tile, int page) {
+      const int slot = issued % C::kSlots;
+      if (issued >= C::kSlots &&
+          !__all_sync(kAll, mbar_wait(&empty[slot], (issued / C::kSlots - 1) & 1, a.t.err))) {
+        record_error(a.t.err, kDevErrAttn);
+        ok = false;
+        return;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&full[slot], C::kSlot);
+      __syncwarp();
+      if (mine) {
+        uint8_t* dst = ring + slot * C::kSlot + my_blk * kBlkBytes + my_page * box * 128;
+        const int at = (tile * kKeys) & (ps - 1);
+        if (heads_first)
+          tma_load_4d(dst, tm, my_blk * 64, h, at, page, &full[slot]);
+        else
+          tma_load_4d(dst, tm, my_blk * 64, at, h, page, &full[slot]);
+      }
+      ++issued;
+    };
+    int page = 0, page_prev = 0, h_prev = 0, tile_prev = 0;
+    if (N > 0) page = page_of(cur);
+    for (int i = 0; i <= N && ok; ++i) {
+      int h = 0, tile = 0, page_next = 0;
+      if (i < N) {
+        h = cur.hr / a.row_tiles;
+        tile = cur.tile;
+        cur.next(a);
+        if (i + 1 < N) page_next = page_of(cur);
+        load(&tmK, h, tile, page);
+      }
+      if (i > 0 && ok) load(&tmV, h_prev, tile_prev, page_prev);
+      h_prev = h;
+      tile_prev = tile;
+      page_prev = page;
+      page = page_next;
+    }
+    // the copies still in flight land before the CTA ends
+    for (int j = max(0, issued - C::kSlots); j < issued; ++j)
+      mbar_wait(&full[j % C::kSlots], (j / C::kSlots) & 1, a.t.err);
+  } else if (warp == 1) {
+    // ---- MMAs ----
+    if (lane == 0) {
+      constexpr uint32_t id_qk = idesc_f16<E>(kLanes, kKeys, false);
+      constexpr uint32_t id_pv = idesc_f16<E>(kLanes, D, true);
+      bool ok = true, starts = true, starts_prev = false;
+      int seg = 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (ok && !mbar_wait(bar, parity, a.t.err)) {
+          record_error(a.t.err, kDevErrAttn);
+          ok = false;
+        }
+        return ok;
+      };
+      for (int i = 0; i <= N && ok; ++i) {
+        if (i < N) {  // scores of tile i
+          const int sq = seq_k(i), slot = sq % C::kSlots;
+          for (int s = 0; s < NS && ok; ++s) {
+            if (starts) wait(&q_full[s], seg & 1);
+            // S buffer i % 2 held the weights of tile i - 2
+            if (i >= 2) wait(&pv_done[s], (i - 2) & 1);
+          }
+          if (!wait(&full[slot], (sq / C::kSlots) & 1)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            const uint64_t ad = umma_desc_sw128(qs + s * C::kQ);
+            const uint64_t bd = umma_desc_sw128(ring + slot * C::kSlot);
+            const uint32_t acc = tmem + s * kStreamCols + (i & 1) * kKeys;
+#pragma unroll
+            for (int kb = 0; kb < kBlk; ++kb)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                umma_bf16(acc, ad + kb * (kLanes * 128 >> 4) + 2 * k,
+                          bd + kb * (kBlkBytes >> 4) + 2 * k, id_qk, kb > 0 || k > 0);
+            umma_commit(&s_full[2 * s + (i & 1)]);
+          }
+          umma_commit(&empty[slot]);
+        }
+        if (i > 0) {  // output of tile i - 1
+          const int sq = seq_v(i - 1), slot = sq % C::kSlots;
+          if (!wait(&full[slot], (sq / C::kSlots) & 1)) break;
+          for (int s = 0; s < NS; ++s) {
+            if (!wait(&p_ready[2 * s + ((i - 1) & 1)], ((i - 1) >> 1) & 1)) break;
+            tc_fence_after();
+            const uint64_t bd = umma_desc_sw128_mn(ring + slot * C::kSlot, kBlkBytes);
+            const uint32_t pa = tmem + s * kStreamCols + ((i - 1) & 1) * kKeys;
+            const uint32_t acc = tmem + s * kStreamCols + 2 * kKeys;
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 8 TMEM columns, 2 KB of V
+              umma_f16_ts(acc, pa + 8 * k, bd + k * (2048 >> 4), id_pv, !starts_prev || k > 0);
+            umma_commit(&pv_done[s]);
+          }
+          if (!ok) break;
+          umma_commit(&empty[slot]);
+        }
+        if (i < N) {
+          starts_prev = starts;
+          const int hr = cur.hr, b = cur.b;
+          cur.next(a);
+          starts = cur.hr != hr || cur.b != b;
+          seg += starts;
+        }
+      }
+      umma_commit(all_done);  // every MMA issued is complete before TMEM is freed
+      mbar_wait(all_done, 0, a.t.err);
+    }
+    __syncwarp();
+  } else if (N > 0) {
+    // ---- softmax: a thread to a row ----
+    const int stream = (warp - 2) >> 2;
+    const int quarter = warp & 3;  // the TMEM lanes a warp may read: 32 (warp % 4) ..
+    const int row_l = quarter * 32 + lane;
+    const uint32_t tbase = tmem + stream * kStreamCols + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t to = tbase + 2 * kKeys;  // O
+    const int M = a.t.T * a.G;
+    const float sl = fmaxf(fabsf(a.scale_log2), 1e-37f);
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok && !__all_sync(kAll, mbar_wait(bar, parity, a.t.err))) {
+        record_error(a.t.err, kDevErrAttn);
+        ok = false;
+      }
+      return ok;
+    };
+    // Q of the row tile at c, negated where the scale is negative
+    auto load_q = [&](const Cursor& c) {
+      const int h = c.hr / a.row_tiles;
+      const int r0 = (c.hr % a.row_tiles) * (NS * kLanes) + stream * kLanes;
+      const E* Q = static_cast<const E*>(a.q) + c.b * a.qb;
+      const int t = tid - 64 - stream * kLanes;
+      constexpr int kCPR = D / 8;
+#pragma unroll 4
+      for (int x = t; x < kLanes * kCPR; x += kLanes) {
+        const int r = x / kCPR, cc = x % kCPR;
+        uint4 val = make_uint4(0, 0, 0, 0);
+        if (r0 + r < M) {
+          val = *reinterpret_cast<const uint4*>(Q + (r0 + r) / a.G * a.qt +
+                                                (h * a.G + (r0 + r) % a.G) * a.qh + cc * 8);
+          val.x ^= flip;
+          val.y ^= flip;
+          val.z ^= flip;
+          val.w ^= flip;
+        }
+        uint8_t* dst = qs + stream * C::kQ + (cc >> 3) * (kLanes * 128) + r * 128 +
+                       (((cc & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(dst) = val;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[stream]);
+    };
+    load_q(cur);
+
+    float m = -INFINITY, l = 0.f;
+    int seg = 0, tile_lo = cur.tile;
+    for (int i = 0; i < N && ok; ++i) {
+      const Seq s = cur.s;
+      const int r0 = (cur.hr % a.row_tiles) * (NS * kLanes) + stream * kLanes;
+      const bool live = r0 + quarter * 32 < M;  // a warp without rows only keeps in step
+      const int p0 = cur.tile * kKeys;
+      const bool edge = p0 + kKeys > s.len;
+      const uint32_t ts = tbase + (i & 1) * kKeys;
+      if (!wait(&s_full[2 * stream + (i & 1)], (i >> 1) & 1)) break;
+      tc_fence_after();
+      if (live) {
+        uint32_t x[64];
+        tmem_ld32_issue(ts, x);
+        tmem_ld32_issue(ts + 32, x + 32);
+        tmem_ld32_wait(x);
+        tmem_ld32_wait(x + 32);
+        if (edge) {
+          const int r = r0 + row_l;
+          const uint64_t vis = r < M ? seen64(a, cur.b, s, r / a.G, p0) : 0;
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!(vis >> c & 1)) x[c] = 0xFF800000u;  // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(x[c]);
+#pragma unroll
+        for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+        if (cur.tile == tile_lo) {
+          m = top;
+          l = 0.f;
+        } else if (__any_sync(kAll, top > m + kRise)) {  // (m = -inf: anything above)
+          if (!wait(&pv_done[stream], (i - 1) & 1)) break;
+          tc_fence_after();
+          const float mn = top > m + kRise ? top : m;
+          const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+          l *= f;
+          m = mn;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32_issue(to + c, o);
+            tmem_ld32_wait(o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st32(to + c, o);
+          }
+        }
+        const float safe = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t p[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float y = ex2(fmaf(__uint_as_float(x[2 * c]), sl, -safe));
+          const float z = ex2(fmaf(__uint_as_float(x[2 * c + 1]), sl, -safe));
+          sum[(2 * c) & 3] += y;
+          sum[(2 * c + 1) & 3] += z;
+          p[c] = pack2<E>(y, z);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_st32(ts, p);
+        tmem_st_wait();
+      }
+      if (edge && stream == 0) {
+        // V's rows past the end are zeroed and Inf and NaN of nodes set aside
+        // (unseen_safe_sum): a weight of 0 would not keep them out of the product
+        const int sq = seq_v(i), slot = sq % C::kSlots;
+        if (!wait(&full[slot], (sq / C::kSlots) & 1)) break;
+        bool found = false;
+        const int end = s.len + s.n;
+        for (int x = tid - 64; x < C::kSlot / 16; x += kLanes) {
+          const int pos = p0 + (x & 511) / 8;  // 512 pieces to a 64-channel block
+          if (pos < s.len) continue;
+          uint4* at = reinterpret_cast<uint4*>(ring + slot * C::kSlot) + x;
+          uint4 y = make_uint4(0, 0, 0, 0);
+          if (pos < end) {
+            y = *at;
+            bool bad = false;
+            y.x = finite2<E>(y.x, bad);
+            y.y = finite2<E>(y.y, bad);
+            y.z = finite2<E>(y.z, bad);
+            y.w = finite2<E>(y.w, bad);
+            found |= bad;
+            if (!bad) continue;
+          }
+          *at = y;
+        }
+        if (found) bad_seg[seg & 3] = seg;
+        fence_proxy_async_smem();
+      }
+      const bool last = cur.tile + 1 == s.tiles, ends = last || i + 1 == N;
+      // The output is waited for below by the parity of its phase, which names it only
+      // between the completion of the product before it and that of the one behind it.
+      if (ends && i > 0 && !wait(&pv_done[stream], (i - 1) & 1)) break;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_ready[2 * stream + (i & 1)]);
+
+      if (ends) {
+        // ---- the end of this CTA's part of the row tile ----
+        const Cursor at = cur;
+        cur.next(a);
+        if (i + 1 < N) load_q(cur);  // every product with the old Q is complete (s_full)
+        if (!wait(&pv_done[stream], i & 1)) break;
+        tc_fence_after();
+        const bool whole = last && tile_lo == 0;
+        const int slot = tile_lo == 0 && !whole && at.u - at.tile > u0 ? 1 : 0;
+        if (live) {
+          const int r = r0 + row_l, node = r / a.G, h = at.hr / a.row_tiles;
+          const int head = h * a.G + r % a.G;
+          const bool bad = *reinterpret_cast<volatile int*>(&bad_seg[seg & 3]) == seg;
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * (NS * kLanes) +
+                               stream * kLanes + row_l;
+          E* out = static_cast<E*>(a.out) + at.b * a.ob + node * a.ot + head * a.oh;
+          const bool mine = r < M && node < s.n;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32_issue(to + c, o);
+            tmem_ld32_wait(o);
+            if (bad && mine)
+              for (int j = 0; j < 32; ++j) {
+                const float y = unseen_safe_sum<E>(a, at.b, s, h, node, c + j, tile_lo * kKeys,
+                                                   (at.tile + 1) * kKeys);
+                // (an index known at compile time keeps o in registers)
+#pragma unroll
+                for (int z = 0; z < 32; ++z)
+                  if (z == j) o[z] = __float_as_uint(__uint_as_float(o[z]) + y);
+              }
+            if (mine && whole) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint4 y;
+                uint32_t* yy = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                  yy[z] = pack2<E>(__uint_as_float(o[8 * j + 2 * z]) * inv,
+                                   __uint_as_float(o[8 * j + 2 * z + 1]) * inv);
+                *reinterpret_cast<uint4*>(out + c + 8 * j) = y;
+              }
+            } else if (mine) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(a.part_o + part * D + c + 4 * j) =
+                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+            __syncwarp();  // the next load is the whole warp's
+          }
+          if (mine && !whole) a.part_ml[part] = make_float2(m, l);
+          if (mine && whole && a.lse)
+            a.lse[(static_cast<int64_t>(at.b) * a.t.T + node) * (a.H * a.G) + head] =
+                (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
+        }
+        tc_fence_before();  // O is read before the next row tile's first product
+        tile_lo = cur.tile;
+        ++seg;
+      } else {
+        cur.next(a);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, NS * kStreamCols);
+}
+
+// ---- host -------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static std::mutex mu;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!fn) {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  return fn;
+}
+
+// Whether a position's row comes after the heads in memory ([.., page_size, heads, D]).
+bool heads_first(const dfl2_cache* c) { return c->slot_stride > c->head_stride && c->kv_heads > 1; }
+
+// One layer's K or V as [pages][heads][slots][D] (the middle two in the order of
+// their strides), boxes of one page's rows x 64 channels.
+bool page_map(const dfl2_cache* c, const void* base, bool f16, CUtensorMap* out) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = encoder();
+  if (!encode) return false;
+  const uint64_t D = c->head_dim, S = c->page_size, H = c->kv_heads;
+  // the stride of a dimension of one entry is never used, but has to be a stride
+  const uint64_t hs = (H > 1 ? c->head_stride : D) * 2, ss = c->slot_stride * 2;
+  const uint64_t pg = (c->pages > 1 ? c->page_stride : std::max(hs * H, ss * S) / 2) * 2;
+  const uint32_t rows = std::min<uint32_t>(c->page_size, kKeys);
+  const bool hf = heads_first(c);
+  const cuuint64_t dims[4] = {D, hf ? H : S, hf ? S : H, static_cast<cuuint64_t>(c->pages)};
+  const cuuint64_t strides[3] = {hf ? hs : ss, hf ? ss : hs, pg};
+  const cuuint32_t box[4] = {64, hf ? 1 : rows, hf ? rows : 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return encode(out, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename E, int D, int NS>
+cudaError_t launch_one(const AttnArgs& a, const CUtensorMap& k, const CUtensorMap& v, int hf,
+                       cudaStream_t s) {
+  auto kernel = attn_tc_kernel<E, D, NS>;
+  constexpr size_t smem = TcCfg<D, NS>::kSmem;
+  const cudaError_t e = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_k(kernel, dim3(a.grid), dim3(TcCfg<D, NS>::kThreads), smem, s, true, a, k, v, hf);
+}
+
+}  // namespace
+
+bool attn_tc_takes(const dfl2_cache* c) {
+  if (c->head_dim != 64 && c->head_dim != 128) return false;
+  // what a tensor map can hold: positive strides under 2^40 bytes, pages outermost
+  const int64_t inner = std::max(c->kv_heads > 1 ? c->head_stride : 0, c->slot_stride);
+  if (c->slot_stride < 8 || (c->kv_heads > 1 && c->head_stride < 8)) return false;
+  if (c->pages > 1 && c->page_stride < inner) return false;
+  return c->page_stride < (int64_t(1) << 38) && inner < (int64_t(1) << 38);
+}
+int attn_tc_rows(int M) { return M <= kLanes ? kLanes : 2 * kLanes; }
+int attn_tc_grid(int rows, int sms) { return rows == kLanes ? 2 * sms : sms; }
+
+cudaError_t launch_attn_tc(const AttnArgs& a, const dfl2_cache* c, cudaStream_t s) {
+  const bool f16 = c->dtype == DFL2_F16;
+  alignas(64) CUtensorMap tk, tv;
+  if (!page_map(c, a.k, f16, &tk) || !page_map(c, a.v, f16, &tv)) return cudaErrorInvalidValue;
+  const int hf = heads_first(c);
+  const bool two = a.rows > kLanes;
+  if (c->head_dim == 128) {
+    if (f16)
+      return two ? launch_one<__half, 128, 2>(a, tk, tv, hf, s)
+                 : launch_one<__half, 128, 1>(a, tk, tv, hf, s);
+    return two ? launch_one<__nv_bfloat16, 128, 2>(a, tk, tv, hf, s)
+               : launch_one<__nv_bfloat16, 128, 1>(a, tk, tv, hf, s);
+  }
+  if (f16)
+    return two ? launch_one<__half, 64, 2>(a, tk, tv, hf, s)
+               : launch_one<__half, 64, 1>(a, tk, tv, hf, s);
+  return two ? launch_one<__nv_bfloat16, 64, 2>(a, tk, tv, hf, s)
+             : launch_one<__nv_bfloat16, 64, 1>(a, tk, tv, hf, s);
+}
+
+}  // namespace dfl2
