@@ -14,9 +14,9 @@
 // the products in flight) then almost never happens past a row's first tiles.
 //
 // Roles: warp 0 loads K and V (TMA boxes of one page's rows x 64 channels,
-// 128-byte swizzle, into a ring of slots of one tile's K or V), warp 1 issues the
-// MMAs, four warps a stream do the softmax.  A stream is 128 rows.  The MMAs of
-// tile i+1's scores are issued before those of tile i's output, so that the
+// 128-byte swizzle, into a ring of slots of one tile's K or V); a stream, 128
+// rows, has one warp that issues its MMAs and four that do its softmax.  The MMAs
+// of tile i+1's scores are issued before those of tile i's output, so that the
 // tensor core works while the softmax of tile i runs; S is double-buffered.
 // With M = T G rows up to 128: one stream, two CTAs on an SM.  Above: one CTA with
 // two streams (256 rows), which share each K and V tile, so that the shared-memory
@@ -44,8 +44,8 @@ struct TcCfg {
                                     ? 16
                                     : (NS == 1 ? 81920 : 163840) / kSlot;
   static constexpr int kQ = kLanes * D * 2;    // bytes of a stream's Q
-  static constexpr int kThreads = 64 + NS * kLanes;
-  static constexpr int kBars = 2 * kSlots + NS * 6 + 1;
+  static constexpr int kThreads = 32 * (1 + NS) + NS * kLanes;
+  static constexpr int kBars = 2 * kSlots + NS * 7;
   static constexpr size_t kSmem = size_t(NS) * kQ + size_t(kSlots) * kSlot + kBars * 8 + 64;
 };
 
@@ -128,6 +128,36 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, 
       : "memory");
 }
 
+// Two float32 operations in one instruction, and a maximum of three.
+__device__ __forceinline__ uint64_t pack_f32x2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack_u32x2(uint32_t x, uint32_t y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t r, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Which of the 64 positions from p0 on node i of sequence b sees (0 past the end).
 __device__ __forceinline__ uint64_t seen64(const AttnArgs& a, int b, const Seq& s, int i, int p0) {
   if (i >= s.n) return 0;
@@ -152,7 +182,7 @@ __device__ __forceinline__ uint64_t seen64(const AttnArgs& a, int b, const Seq& 
 }
 
 template <typename E, int D, int NS>
-__global__ void __launch_bounds__(64 + NS * kLanes, NS == 1 ? 2 : 1)
+__global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
     attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const int heads_first) {
   using C = TcCfg<D, NS>;
@@ -167,15 +197,18 @@ __global__ void __launch_bounds__(64 + NS * kLanes, NS == 1 ? 2 : 1)
   uint64_t* s_full = q_full + NS;        // [NS][2] scores are in TMEM
   uint64_t* p_ready = s_full + 2 * NS;   // [NS][2] weights are in TMEM (the softmax may be a tile ahead)
   uint64_t* pv_done = p_ready + 2 * NS;      // [NS] the output product is in O
-  uint64_t* all_done = pv_done + NS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + 1);
+  uint64_t* all_done = pv_done + NS;     // [NS]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + NS);
   int* bad_seg = reinterpret_cast<int*>(tmem_slot + 1);  // [4] row tile that met Inf or NaN in V
+  // Warps that have cleaned an edge tile's V, counted up: stream 0 may be several tiles
+  // ahead of stream 1, more than a barrier's parity can tell apart.
+  uint32_t* v_clean = reinterpret_cast<uint32_t*>(bad_seg + 4);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], NS);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&q_full[s], 4);
@@ -184,8 +217,9 @@ __global__ void __launch_bounds__(64 + NS * kLanes, NS == 1 ? 2 : 1)
       mbar_init(&p_ready[2 * s], 4);
       mbar_init(&p_ready[2 * s + 1], 4);
       mbar_init(&pv_done[s], 1);
+      mbar_init(&all_done[s], 1);
     }
-    mbar_init(all_done, 1);
+    *v_clean = 0;
     for (int i = 0; i < 4; ++i) bad_seg[i] = -1;
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
@@ -278,13 +312,17 @@ __global__ void __launch_bounds__(64 + NS * kLanes, NS == 1 ? 2 : 1)
     // the copies still in flight land before the CTA ends
     for (int j = max(0, issued - C::kSlots); j < issued; ++j)
       mbar_wait(&full[j % C::kSlots], (j / C::kSlots) & 1, a.t.err);
-  } else if (warp == 1) {
-    // ---- MMAs ----
+  } else if (warp <= NS) {
+    // ---- a stream's MMAs ----
     if (lane == 0) {
       constexpr uint32_t id_qk = idesc_f16<E>(kLanes, kKeys, false);
       constexpr uint32_t id_pv = idesc_f16<E>(kLanes, D, true);
-      bool ok = true, starts = true, starts_prev = false;
+      const int st = warp - 1;
+      const uint32_t tb = tmem + st * kStreamCols;
+      const uint64_t ad = umma_desc_sw128(qs + st * C::kQ);
+      bool ok = true, starts = true, starts_prev = false, edge = false, edge_prev = false;
       int seg = 0;
+      uint32_t edges = 0;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (ok && !mbar_wait(bar, parity, a.t.err)) {
           record_error(a.t.err, kDevErrAttn);
@@ -295,60 +333,60 @@ __global__ void __launch_bounds__(64 + NS * kLanes, NS == 1 ? 2 : 1)
       for (int i = 0; i <= N && ok; ++i) {
         if (i < N) {  // scores of tile i
           const int sq = seq_k(i), slot = sq % C::kSlots;
-          for (int s = 0; s < NS && ok; ++s) {
-            if (starts) wait(&q_full[s], seg & 1);
-            // S buffer i % 2 held the weights of tile i - 2
-            if (i >= 2) wait(&pv_done[s], (i - 2) & 1);
-          }
+          edge = (cur.tile + 1) * kKeys > cur.s.len;
+          if (starts && !wait(&q_full[st], seg & 1)) break;
+          // S buffer i % 2 held the weights of tile i - 2
+          if (i >= 2 && !wait(&pv_done[st], (i - 2) & 1)) break;
           if (!wait(&full[slot], (sq / C::kSlots) & 1)) break;
           tc_fence_after();
+          const uint64_t bd = umma_desc_sw128(ring + slot * C::kSlot);
 #pragma unroll
-          for (int s = 0; s < NS; ++s) {
-            const uint64_t ad = umma_desc_sw128(qs + s * C::kQ);
-            const uint64_t bd = umma_desc_sw128(ring + slot * C::kSlot);
-            const uint32_t acc = tmem + s * kStreamCols + (i & 1) * kKeys;
+          for (int kb = 0; kb < kBlk; ++kb)
 #pragma unroll
-            for (int kb = 0; kb < kBlk; ++kb)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_bf16(acc, ad + kb * (kLanes * 128 >> 4) + 2 * k,
-                          bd + kb * (kBlkBytes >> 4) + 2 * k, id_qk, kb > 0 || k > 0);
-            umma_commit(&s_full[2 * s + (i & 1)]);
-          }
+            for (int k = 0; k < 4; ++k)
+              umma_bf16(tb + (i & 1) * kKeys, ad + kb * (kLanes * 128 >> 4) + 2 * k,
+                        bd + kb * (kBlkBytes >> 4) + 2 * k, id_qk, kb > 0 || k > 0);
+          umma_commit(&s_full[2 * st + (i & 1)]);
           umma_commit(&empty[slot]);
         }
         if (i > 0) {  // output of tile i - 1
           const int sq = seq_v(i - 1), slot = sq % C::kSlots;
           if (!wait(&full[slot], (sq / C::kSlots) & 1)) break;
-          for (int s = 0; s < NS; ++s) {
-            if (!wait(&p_ready[2 * s + ((i - 1) & 1)], ((i - 1) >> 1) & 1)) break;
-            tc_fence_after();
-            const uint64_t bd = umma_desc_sw128_mn(ring + slot * C::kSlot, kBlkBytes);
-            const uint32_t pa = tmem + s * kStreamCols + ((i - 1) & 1) * kKeys;
-            const uint32_t acc = tmem + s * kStreamCols + 2 * kKeys;
-#pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 8 TMEM columns, 2 KB of V
-              umma_f16_ts(acc, pa + 8 * k, bd + k * (2048 >> 4), id_pv, !starts_prev || k > 0);
-            umma_commit(&pv_done[s]);
+          if (!wait(&p_ready[2 * st + ((i - 1) & 1)], ((i - 1) >> 1) & 1)) break;
+          if (edge_prev) {  // stream 0's softmax cleans V; the others' products wait for it
+            edges += 4;
+            if (st > 0 && !wait_count_above(v_clean, edges - 1, a.t.err)) {
+              record_error(a.t.err, kDevErrAttn);
+              break;
+            }
           }
-          if (!ok) break;
+          tc_fence_after();
+          const uint64_t bd = umma_desc_sw128_mn(ring + slot * C::kSlot, kBlkBytes);
+          const uint32_t pa = tb + ((i - 1) & 1) * kKeys;
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 8 TMEM columns, 2 KB of V
+            umma_f16_ts(tb + 2 * kKeys, pa + 8 * k, bd + k * (2048 >> 4), id_pv,
+                        !starts_prev || k > 0);
+          umma_commit(&pv_done[st]);
           umma_commit(&empty[slot]);
         }
         if (i < N) {
           starts_prev = starts;
+          edge_prev = edge;
           const int hr = cur.hr, b = cur.b;
           cur.next(a);
           starts = cur.hr != hr || cur.b != b;
           seg += starts;
         }
       }
-      umma_commit(all_done);  // every MMA issued is complete before TMEM is freed
-      mbar_wait(all_done, 0, a.t.err);
+      umma_commit(&all_done[st]);  // every MMA issued is complete before TMEM is freed
+      mbar_wait(&all_done[st], 0, a.t.err);
     }
     __syncwarp();
   } else if (N > 0) {
     // ---- softmax: a thread to a row ----
-    const int stream = (warp - 2) >> 2;
+    constexpr int kFirst = 32 * (1 + NS);  // the first softmax thread
+    const int stream = (tid - kFirst) / kLanes;
     const int quarter = warp & 3;  // the TMEM lanes a warp may read: 32 (warp % 4) ..
     const int row_l = quarter * 32 + lane;
     const uint32_t tbase = tmem + stream * kStreamCols + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -356,20 +394,17 @@ __global__ void __launch_bounds__(64 + NS * kLanes, NS == 1 ? 2 : 1)
     const int M = a.t.T * a.G;
     const float sl = fmaxf(fabsf(a.scale_log2), 1e-37f);
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-    bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok && !__all_sync(kAll, mbar_wait(bar, parity, a.t.err))) {
-        record_error(a.t.err, kDevErrAttn);
-        ok = false;
-      }
-      return ok;
+      if (__all_sync(kAll, mbar_wait(bar, parity, a.t.err))) return true;
+      record_error(a.t.err, kDevErrAttn);
+      return false;
     };
     // Q of the row tile at c, negated where the scale is negative
     auto load_q = [&](const Cursor& c) {
       const int h = c.hr / a.row_tiles;
       const int r0 = (c.hr % a.row_tiles) * (NS * kLanes) + stream * kLanes;
       const E* Q = static_cast<const E*>(a.q) + c.b * a.qb;
-      const int t = tid - 64 - stream * kLanes;
+      const int t = tid - kFirst - stream * kLanes;
       constexpr int kCPR = D / 8;
 #pragma unroll 4
       for (int x = t; x < kLanes * kCPR; x += kLanes) {
@@ -393,168 +428,194 @@ __global__ void __launch_bounds__(64 + NS * kLanes, NS == 1 ? 2 : 1)
     };
     load_q(cur);
 
-    float m = -INFINITY, l = 0.f;
-    int seg = 0, tile_lo = cur.tile;
-    for (int i = 0; i < N && ok; ++i) {
-      const Seq s = cur.s;
-      const int r0 = (cur.hr % a.row_tiles) * (NS * kLanes) + stream * kLanes;
+    bool ok = true;
+    int i = 0;  // tile of this CTA's range
+    for (int seg = 0; i < N && ok; ++seg) {
+      // this CTA's part [tile_lo, tile_hi) of a row tile
+      const Cursor at = cur;
+      const Seq s = at.s;
+      const int tile_lo = at.tile, tile_hi = min(s.tiles, tile_lo + (N - i));
+      const int h = at.hr / a.row_tiles;
+      const int r0 = (at.hr - h * a.row_tiles) * (NS * kLanes) + stream * kLanes;
       const bool live = r0 + quarter * 32 < M;  // a warp without rows only keeps in step
-      const int p0 = cur.tile * kKeys;
-      const bool edge = p0 + kKeys > s.len;
-      const uint32_t ts = tbase + (i & 1) * kKeys;
-      if (!wait(&s_full[2 * stream + (i & 1)], (i >> 1) & 1)) break;
-      tc_fence_after();
-      if (live) {
-        uint32_t x[64];
-        tmem_ld32_issue(ts, x);
-        tmem_ld32_issue(ts + 32, x + 32);
-        tmem_ld32_wait(x);
-        tmem_ld32_wait(x + 32);
-        if (edge) {
-          const int r = r0 + row_l;
-          const uint64_t vis = r < M ? seen64(a, cur.b, s, r / a.G, p0) : 0;
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!(vis >> c & 1)) x[c] = 0xFF800000u;  // -inf
-        }
-        float mx[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(x[c]);
-#pragma unroll
-        for (int c = 4; c < 64; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(x[c]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
-        if (cur.tile == tile_lo) {
-          m = top;
-          l = 0.f;
-        } else if (__any_sync(kAll, top > m + kRise)) {  // (m = -inf: anything above)
-          if (!wait(&pv_done[stream], (i - 1) & 1)) break;
-          tc_fence_after();
-          const float mn = top > m + kRise ? top : m;
-          const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
-          l *= f;
-          m = mn;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32_issue(to + c, o);
-            tmem_ld32_wait(o);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st32(to + c, o);
-          }
-        }
-        const float safe = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t p[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float y = ex2(fmaf(__uint_as_float(x[2 * c]), sl, -safe));
-          const float z = ex2(fmaf(__uint_as_float(x[2 * c + 1]), sl, -safe));
-          sum[(2 * c) & 3] += y;
-          sum[(2 * c + 1) & 3] += z;
-          p[c] = pack2<E>(y, z);
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_st32(ts, p);
-        tmem_st_wait();
-      }
-      if (edge && stream == 0) {
-        // V's rows past the end are zeroed and Inf and NaN of nodes set aside
-        // (unseen_safe_sum): a weight of 0 would not keep them out of the product
-        const int sq = seq_v(i), slot = sq % C::kSlots;
-        if (!wait(&full[slot], (sq / C::kSlots) & 1)) break;
-        bool found = false;
-        const int end = s.len + s.n;
-        for (int x = tid - 64; x < C::kSlot / 16; x += kLanes) {
-          const int pos = p0 + (x & 511) / 8;  // 512 pieces to a 64-channel block
-          if (pos < s.len) continue;
-          uint4* at = reinterpret_cast<uint4*>(ring + slot * C::kSlot) + x;
-          uint4 y = make_uint4(0, 0, 0, 0);
-          if (pos < end) {
-            y = *at;
-            bool bad = false;
-            y.x = finite2<E>(y.x, bad);
-            y.y = finite2<E>(y.y, bad);
-            y.z = finite2<E>(y.z, bad);
-            y.w = finite2<E>(y.w, bad);
-            found |= bad;
-            if (!bad) continue;
-          }
-          *at = y;
-        }
-        if (found) bad_seg[seg & 3] = seg;
-        fence_proxy_async_smem();
-      }
-      const bool last = cur.tile + 1 == s.tiles, ends = last || i + 1 == N;
-      // The output is waited for below by the parity of its phase, which names it only
-      // between the completion of the product before it and that of the one behind it.
-      if (ends && i > 0 && !wait(&pv_done[stream], (i - 1) & 1)) break;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_ready[2 * stream + (i & 1)]);
+      const int r = r0 + row_l, node = r / a.G;
+      float m = -INFINITY, l = 0.f;
 
-      if (ends) {
-        // ---- the end of this CTA's part of the row tile ----
-        const Cursor at = cur;
-        cur.next(a);
-        if (i + 1 < N) load_q(cur);  // every product with the old Q is complete (s_full)
-        if (!wait(&pv_done[stream], i & 1)) break;
+      // One tile.  kEdge: it has nodes, or positions past the end.
+      auto tile_step = [&](auto edge_tag, int tile) {
+        constexpr bool kEdge = decltype(edge_tag)::value;
+        const int p0 = tile * kKeys;
+        const uint32_t ts = tbase + (i & 1) * kKeys;
+        if (!wait(&s_full[2 * stream + (i & 1)], (i >> 1) & 1)) return false;
         tc_fence_after();
-        const bool whole = last && tile_lo == 0;
-        const int slot = tile_lo == 0 && !whole && at.u - at.tile > u0 ? 1 : 0;
         if (live) {
-          const int r = r0 + row_l, node = r / a.G, h = at.hr / a.row_tiles;
-          const int head = h * a.G + r % a.G;
-          const bool bad = *reinterpret_cast<volatile int*>(&bad_seg[seg & 3]) == seg;
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * (NS * kLanes) +
-                               stream * kLanes + row_l;
-          E* out = static_cast<E*>(a.out) + at.b * a.ob + node * a.ot + head * a.oh;
-          const bool mine = r < M && node < s.n;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32_issue(to + c, o);
-            tmem_ld32_wait(o);
-            if (bad && mine)
-              for (int j = 0; j < 32; ++j) {
-                const float y = unseen_safe_sum<E>(a, at.b, s, h, node, c + j, tile_lo * kKeys,
-                                                   (at.tile + 1) * kKeys);
-                // (an index known at compile time keeps o in registers)
+          uint32_t x[64];
+          tmem_ld32_issue(ts, x);
+          tmem_ld32_issue(ts + 32, x + 32);
+          tmem_ld32_wait(x);
+          tmem_ld32_wait(x + 32);
+          if (kEdge) {
+            const uint64_t vis = r < M ? seen64(a, at.b, s, node, p0) : 0;
 #pragma unroll
-                for (int z = 0; z < 32; ++z)
-                  if (z == j) o[z] = __float_as_uint(__uint_as_float(o[z]) + y);
-              }
-            if (mine && whole) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint4 y;
-                uint32_t* yy = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                  yy[z] = pack2<E>(__uint_as_float(o[8 * j + 2 * z]) * inv,
-                                   __uint_as_float(o[8 * j + 2 * z + 1]) * inv);
-                *reinterpret_cast<uint4*>(out + c + 8 * j) = y;
-              }
-            } else if (mine) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(a.part_o + part * D + c + 4 * j) =
-                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-            }
-            __syncwarp();  // the next load is the whole warp's
+            for (int c = 0; c < 64; ++c)
+              if (!(vis >> c & 1)) x[c] = 0xFF800000u;  // -inf
           }
-          if (mine && !whole) a.part_ml[part] = make_float2(m, l);
-          if (mine && whole && a.lse)
-            a.lse[(static_cast<int64_t>(at.b) * a.t.T + node) * (a.H * a.G) + head] =
-                (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
+          float mx[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(x[c]);
+#pragma unroll
+          for (int c = 4; c < 60; c += 8)
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              mx[z] = max3(mx[z], __uint_as_float(x[c + z]), __uint_as_float(x[c + 4 + z]));
+          const float top =
+              max3(max3(mx[0], __uint_as_float(x[60]), __uint_as_float(x[61])),
+                   max3(mx[1], __uint_as_float(x[62]), __uint_as_float(x[63])),
+                   fmaxf(mx[2], mx[3])) * sl;
+          if (tile == tile_lo) {
+            m = top;
+          } else if (__any_sync(kAll, top > m + kRise)) {  // (m = -inf: anything above)
+            if (!wait(&pv_done[stream], (i - 1) & 1)) return false;
+            tc_fence_after();
+            const float mn = top > m + kRise ? top : m;
+            const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+            l *= f;
+            m = mn;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32_issue(to + c, o);
+              tmem_ld32_wait(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(to + c, o);
+            }
+          }
+          const float safe = m == -INFINITY ? 0.f : m;
+          const uint64_t sl2 = pack_f32x2(sl, sl), off2 = pack_f32x2(-safe, -safe);
+          uint64_t sum[2] = {0, 0};
+          uint32_t p[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const uint64_t y2 = fma_f32x2(pack_u32x2(x[2 * c], x[2 * c + 1]), sl2, off2);
+            float y, z;
+            unpack_f32x2(y2, y, z);
+            y = ex2(y);
+            z = ex2(z);
+            sum[c & 1] = add_f32x2(sum[c & 1], pack_f32x2(y, z));
+            p[c] = pack2<E>(y, z);
+          }
+          float s0, s1;
+          unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+          tmem_st32(ts, p);
+          tmem_st_wait();
         }
-        tc_fence_before();  // O is read before the next row tile's first product
-        tile_lo = cur.tile;
-        ++seg;
-      } else {
+        if (kEdge && stream == 0) {
+          // V's rows past the end are zeroed and Inf and NaN of nodes set aside
+          // (unseen_safe_sum): a weight of 0 would not keep them out of the product
+          const int sq = seq_v(i), slot = sq % C::kSlots;
+          if (!wait(&full[slot], (sq / C::kSlots) & 1)) return false;
+          bool found = false;
+          const int end = s.len + s.n;
+          for (int x = tid - kFirst; x < C::kSlot / 16; x += kLanes) {
+            const int pos = p0 + (x & 511) / 8;  // 512 pieces to a 64-channel block
+            if (pos < s.len) continue;
+            uint4* v = reinterpret_cast<uint4*>(ring + slot * C::kSlot) + x;
+            uint4 y = make_uint4(0, 0, 0, 0);
+            if (pos < end) {
+              y = *v;
+              bool bad = false;
+              y.x = finite2<E>(y.x, bad);
+              y.y = finite2<E>(y.y, bad);
+              y.z = finite2<E>(y.z, bad);
+              y.w = finite2<E>(y.w, bad);
+              found |= bad;
+              if (!bad) continue;
+            }
+            *v = y;
+          }
+          if (found) bad_seg[seg & 3] = seg;
+          fence_proxy_async_smem();
+        }
+        // The output is waited for below by the parity of its phase, which names it only
+        // between the completion of the product before it and that of the one behind it.
+        if (tile + 1 == tile_hi && i > 0 && !wait(&pv_done[stream], (i - 1) & 1)) return false;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&p_ready[2 * stream + (i & 1)]);
+          if (kEdge && stream == 0 && NS > 1) add_release_cta(v_clean, 1);
+        }
+        ++i;
+        return true;
+      };
+      const int plain_hi = max(tile_lo, min(tile_hi, s.len / kKeys));
+      int tile = tile_lo;
+      for (; tile < plain_hi && ok; ++tile) ok = tile_step(std::false_type{}, tile);
+      for (; tile < tile_hi && ok; ++tile) ok = tile_step(std::true_type{}, tile);
+      if (!ok) break;
+
+      // ---- the end of this CTA's part of the row tile ----
+      cur.u += tile_hi - tile_lo;
+      cur.tile = tile_hi;
+      if (cur.tile == s.tiles) {
+        --cur.u;
+        --cur.tile;
         cur.next(a);
       }
+      if (i < N) load_q(cur);  // every product with the old Q is complete (s_full)
+      if (!wait(&pv_done[stream], (i - 1) & 1)) break;
+      tc_fence_after();
+      const bool whole = tile_hi == s.tiles && tile_lo == 0;
+      const int slot = tile_lo == 0 && !whole && at.u > u0 ? 1 : 0;
+      if (live) {
+        const int head = h * a.G + r - node * a.G;
+        const bool bad = *reinterpret_cast<volatile int*>(&bad_seg[seg & 3]) == seg;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * (NS * kLanes) +
+                             stream * kLanes + row_l;
+        E* out = static_cast<E*>(a.out) + at.b * a.ob + node * a.ot + head * a.oh;
+        const bool mine = r < M && node < s.n;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32_issue(to + c, o);
+          tmem_ld32_wait(o);
+          if (bad && mine)
+            for (int j = 0; j < 32; ++j) {
+              const float y = unseen_safe_sum<E>(a, at.b, s, h, node, c + j, tile_lo * kKeys,
+                                                 tile_hi * kKeys);
+              // (an index known at compile time keeps o in registers)
+#pragma unroll
+              for (int z = 0; z < 32; ++z)
+                if (z == j) o[z] = __float_as_uint(__uint_as_float(o[z]) + y);
+            }
+          if (mine && whole) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint4 y;
+              uint32_t* yy = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                yy[z] = pack2<E>(__uint_as_float(o[8 * j + 2 * z]) * inv,
+                                 __uint_as_float(o[8 * j + 2 * z + 1]) * inv);
+              *reinterpret_cast<uint4*>(out + c + 8 * j) = y;
+            }
+          } else if (mine) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(a.part_o + part * D + c + 4 * j) =
+                  make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+          __syncwarp();  // the next load is the whole warp's
+        }
+        if (mine && !whole) a.part_ml[part] = make_float2(m, l);
+        if (mine && whole && a.lse)
+          a.lse[(static_cast<int64_t>(at.b) * a.t.T + node) * (a.H * a.G) + head] =
+              (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
+      }
+      tc_fence_before();  // O is read before the next row tile's first product
     }
   }
   tc_fence_before();
