@@ -49,6 +49,16 @@ struct TcCfg {
   static constexpr size_t kSmem = size_t(NS) * kQ + size_t(kSlots) * kSlot + kBars * 8 + 64;
 };
 
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 // Operand of 128-byte rows in the 128-byte swizzle whose contiguous dimension is
 // not the summed one: 64-element blocks along it `block` bytes apart, groups of
 // eight summed indices 1024 bytes apart.
@@ -253,8 +263,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
     record_error(a.t.err, kDevErrAttn);
     N = 0;
   }
-  // The ring's order is K(0), K(1), V(0), K(2), V(1), ..: as the MMAs read them.
-  auto seq_k = [](int i) { return i == 0 ? 0 : 2 * i - 1; };
+  // The ring's order is K(0), K(1), V(0), K(2), V(1), ..: as the MMAs read them.  V(i)'s place:
   auto seq_v = [N](int i) { return i + 1 < N ? 2 * i + 2 : 2 * i + 1; };
 
   if (warp == 0) {
@@ -314,54 +323,67 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
       mbar_wait(&full[j % C::kSlots], (j / C::kSlots) & 1, a.t.err);
   } else if (warp <= NS) {
     // ---- a stream's MMAs ----
-    if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_f16<E>(kLanes, kKeys, false);
-      constexpr uint32_t id_pv = idesc_f16<E>(kLanes, D, true);
-      const int st = warp - 1;
-      const uint32_t tb = tmem + st * kStreamCols;
-      const uint64_t ad = umma_desc_sw128(qs + st * C::kQ);
-      bool ok = true, starts = true, starts_prev = false, edge = false, edge_prev = false;
-      int seg = 0;
-      uint32_t edges = 0;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (ok && !mbar_wait(bar, parity, a.t.err)) {
-          record_error(a.t.err, kDevErrAttn);
-          ok = false;
-        }
-        return ok;
-      };
-      for (int i = 0; i <= N && ok; ++i) {
-        if (i < N) {  // scores of tile i
-          const int sq = seq_k(i), slot = sq % C::kSlots;
-          edge = (cur.tile + 1) * kKeys > cur.s.len;
-          if (starts && !wait(&q_full[st], seg & 1)) break;
-          // S buffer i % 2 held the weights of tile i - 2
-          if (i >= 2 && !wait(&pv_done[st], (i - 2) & 1)) break;
-          if (!wait(&full[slot], (sq / C::kSlots) & 1)) break;
-          tc_fence_after();
-          const uint64_t bd = umma_desc_sw128(ring + slot * C::kSlot);
+    // The whole warp walks the loop and one elected lane issues: the descriptors are
+    // then warp-uniform, which the MMA's operands have to be (from a single lane's
+    // loop each MMA cost about 100 cycles of moves to uniform registers).
+    constexpr uint32_t id_qk = idesc_f16<E>(kLanes, kKeys, false);
+    constexpr uint32_t id_pv = idesc_f16<E>(kLanes, D, true);
+    const int st = __shfl_sync(kAll, warp, 0) - 1;
+    const uint32_t tb = __shfl_sync(kAll, tmem, 0) + st * kStreamCols;
+    const uint64_t ad = umma_desc_sw128(qs + st * C::kQ);
+    const uint64_t bd_qk = umma_desc_sw128(ring);
+    const uint64_t bd_pv = umma_desc_sw128_mn(ring, kBlkBytes);
+    const int n = __shfl_sync(kAll, N, 0);
+    bool ok = true, starts_prev = false, edge = false, edge_prev = false;
+    bool starts = true;
+    int seg = 0, slot = 0, ph = 0;  // the ring's next slot in MMA order, and its phase
+    uint32_t edges = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!__all_sync(kAll, mbar_wait(bar, parity, a.t.err))) {
+        record_error(a.t.err, kDevErrAttn);
+        ok = false;
+      }
+      return ok;
+    };
+    for (int i = 0; i <= n; ++i) {
+      if (i < n) {  // scores of tile i
+        edge = __any_sync(kAll, (cur.tile + 1) * kKeys > cur.s.len);
+        if (starts && !wait(&q_full[st], seg & 1)) break;
+        // S buffer i % 2 held the weights of tile i - 2
+        if (i >= 2 && !wait(&pv_done[st], (i - 2) & 1)) break;
+        if (!wait(&full[slot], ph)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t bd = bd_qk + slot * (C::kSlot >> 4);
+          const uint32_t acc = tb + (i & 1) * kKeys;
 #pragma unroll
           for (int kb = 0; kb < kBlk; ++kb)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_bf16(tb + (i & 1) * kKeys, ad + kb * (kLanes * 128 >> 4) + 2 * k,
+              umma_bf16(acc, ad + kb * (kLanes * 128 >> 4) + 2 * k,
                         bd + kb * (kBlkBytes >> 4) + 2 * k, id_qk, kb > 0 || k > 0);
           umma_commit(&s_full[2 * st + (i & 1)]);
           umma_commit(&empty[slot]);
         }
-        if (i > 0) {  // output of tile i - 1
-          const int sq = seq_v(i - 1), slot = sq % C::kSlots;
-          if (!wait(&full[slot], (sq / C::kSlots) & 1)) break;
-          if (!wait(&p_ready[2 * st + ((i - 1) & 1)], ((i - 1) >> 1) & 1)) break;
-          if (edge_prev) {  // stream 0's softmax cleans V; the others' products wait for it
-            edges += 4;
-            if (st > 0 && !wait_count_above(v_clean, edges - 1, a.t.err)) {
-              record_error(a.t.err, kDevErrAttn);
-              break;
-            }
+        __syncwarp();
+        if (++slot == C::kSlots) {
+          slot = 0;
+          ph ^= 1;
+        }
+      }
+      if (i > 0) {  // output of tile i - 1
+        if (!wait(&full[slot], ph)) break;
+        if (!wait(&p_ready[2 * st + ((i - 1) & 1)], ((i - 1) >> 1) & 1)) break;
+        if (edge_prev) {  // stream 0's softmax cleans V; the others' products wait for it
+          edges += 4;
+          if (st > 0 && !__all_sync(kAll, wait_count_above(v_clean, edges - 1, a.t.err))) {
+            record_error(a.t.err, kDevErrAttn);
+            break;
           }
-          tc_fence_after();
-          const uint64_t bd = umma_desc_sw128_mn(ring + slot * C::kSlot, kBlkBytes);
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t bd = bd_pv + slot * (C::kSlot >> 4);
           const uint32_t pa = tb + ((i - 1) & 1) * kKeys;
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 8 TMEM columns, 2 KB of V
@@ -370,18 +392,24 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
           umma_commit(&pv_done[st]);
           umma_commit(&empty[slot]);
         }
-        if (i < N) {
-          starts_prev = starts;
-          edge_prev = edge;
-          const int hr = cur.hr, b = cur.b;
-          cur.next(a);
-          starts = cur.hr != hr || cur.b != b;
-          seg += starts;
+        __syncwarp();
+        if (++slot == C::kSlots) {
+          slot = 0;
+          ph ^= 1;
         }
       }
-      umma_commit(&all_done[st]);  // every MMA issued is complete before TMEM is freed
-      mbar_wait(&all_done[st], 0, a.t.err);
+      if (i < n) {
+        starts_prev = starts;
+        edge_prev = edge;
+        const int hr = cur.hr, b = cur.b;
+        cur.next(a);
+        starts = __any_sync(kAll, cur.hr != hr || cur.b != b);
+        seg += starts;
+      }
     }
+    // every MMA issued is complete before TMEM is freed
+    if (elect_one()) umma_commit(&all_done[st]);
+    mbar_wait(&all_done[st], 0, a.t.err);
     __syncwarp();
   } else if (N > 0) {
     // ---- softmax: a thread to a row ----
