@@ -4,7 +4,7 @@
 // For a row tile of 128 rows (node, head) and tiles of 64 keys:
 //   S = Q K^T   tcgen05.mma, 128 x 64, Q and K in shared memory, S (float32) in TMEM
 //   P = 2^(scale log2 e S - m)   a thread to a row: its 64 scores come from TMEM,
-//               its weights go back over them, rounded to the cache's type
+//               its weights go back there, rounded to the cache's type
 //   O += P V    tcgen05.mma, 128 x D, P in TMEM, V in shared memory as it lies in
 //               the cache (keys x channels: the channel-major operand), O in TMEM
 // A row's statistics never leave its thread, so the softmax has no exchange at
@@ -15,9 +15,12 @@
 //
 // Roles: warp 0 loads K and V (TMA boxes of one page's rows x 64 channels,
 // 128-byte swizzle, into a ring of slots of one tile's K or V); a stream, 128
-// rows, has one warp that issues its MMAs and four that do its softmax.  The MMAs
-// of tile i+1's scores are issued before those of tile i's output, so that the
-// tensor core works while the softmax of tile i runs; S is double-buffered.
+// rows, has one warp that issues its MMAs and four that do its softmax.  A row's
+// scores are in registers soon after they are in TMEM, so one S is enough: the
+// scores of tile i+1 are computed over those of tile i while its softmax runs.  P
+// has two buffers, so neither product ever waits for the other one (with two S
+// and P written over S, tile i+1's scores waited for tile i-1's output: 1830 cycles
+// a pair of tiles at 256 rows instead of REPLACE).
 // With M = T G rows up to 128: one stream, two CTAs on an SM.  Above: one CTA with
 // two streams (256 rows), which share each K and V tile, so that the shared-memory
 // fill per row, the next bound after HBM, is halved.
@@ -35,7 +38,8 @@ namespace {
 
 constexpr int kLanes = 128;                // rows of a stream: the TMEM lanes
 constexpr float kRise = 8.f;               // log2 of the rise that O is rescaled at
-constexpr uint32_t kStreamCols = 256;      // TMEM columns of a stream: S, S, O
+constexpr uint32_t kStreamCols = 256;      // TMEM columns of a stream: S, P, P, O
+constexpr uint32_t kColP = kKeys, kColO = 2 * kKeys;
 
 template <int D, int NS>
 struct TcCfg {
@@ -45,7 +49,7 @@ struct TcCfg {
                                     : (NS == 1 ? 81920 : 163840) / kSlot;
   static constexpr int kQ = kLanes * D * 2;    // bytes of a stream's Q
   static constexpr int kThreads = 32 * (1 + NS) + NS * kLanes;
-  static constexpr int kBars = 2 * kSlots + NS * 7;
+  static constexpr int kBars = 2 * kSlots + NS * 8;
   static constexpr size_t kSmem = size_t(NS) * kQ + size_t(kSlots) * kSlot + kBars * 8 + 64;
 };
 
@@ -204,10 +208,14 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + C::kSlots * C::kSlot);
   uint64_t* empty = full + C::kSlots;
   uint64_t* q_full = empty + C::kSlots;  // [NS] a row tile's Q is in place
-  uint64_t* s_full = q_full + NS;        // [NS][2] scores are in TMEM
-  uint64_t* p_ready = s_full + 2 * NS;   // [NS][2] weights are in TMEM (the softmax may be a tile ahead)
-  uint64_t* pv_done = p_ready + 2 * NS;      // [NS] the output product is in O
-  uint64_t* all_done = pv_done + NS;     // [NS]
+  uint64_t* s_full = q_full + NS;        // [NS] scores are in TMEM
+  uint64_t* s_read = s_full + NS;        // [NS] and in registers
+  // The weights of tile i, and the output product that took them, have a barrier for
+  // even and one for odd tiles, as P has: each side may be a tile ahead of the other,
+  // and a barrier's parity tells only two neighbouring phases apart.
+  uint64_t* p_ready = s_read + NS;       // [NS][2] weights are in TMEM
+  uint64_t* pv_done = p_ready + 2 * NS;  // [NS][2] the output product is in O
+  uint64_t* all_done = pv_done + 2 * NS; // [NS]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + NS);
   int* bad_seg = reinterpret_cast<int*>(tmem_slot + 1);  // [4] row tile that met Inf or NaN in V
   // Warps that have cleaned an edge tile's V, counted up: stream 0 may be several tiles
@@ -222,11 +230,12 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&q_full[s], 4);
-      mbar_init(&s_full[2 * s], 1);
-      mbar_init(&s_full[2 * s + 1], 1);
-      mbar_init(&p_ready[2 * s], 4);
-      mbar_init(&p_ready[2 * s + 1], 4);
-      mbar_init(&pv_done[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&s_read[s], 4);
+      for (int z = 0; z < 2; ++z) {
+        mbar_init(&p_ready[2 * s + z], 4);
+        mbar_init(&pv_done[2 * s + z], 1);
+      }
       mbar_init(&all_done[s], 1);
     }
     *v_clean = 0;
@@ -349,20 +358,18 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
       if (i < n) {  // scores of tile i
         edge = __any_sync(kAll, (cur.tile + 1) * kKeys > cur.s.len);
         if (starts && !wait(&q_full[st], seg & 1)) break;
-        // S buffer i % 2 held the weights of tile i - 2
-        if (i >= 2 && !wait(&pv_done[st], (i - 2) & 1)) break;
+        if (i > 0 && !wait(&s_read[st], (i - 1) & 1)) break;
         if (!wait(&full[slot], ph)) break;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t bd = bd_qk + slot * (C::kSlot >> 4);
-          const uint32_t acc = tb + (i & 1) * kKeys;
 #pragma unroll
           for (int kb = 0; kb < kBlk; ++kb)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_bf16(acc, ad + kb * (kLanes * 128 >> 4) + 2 * k,
+              umma_bf16(tb, ad + kb * (kLanes * 128 >> 4) + 2 * k,
                         bd + kb * (kBlkBytes >> 4) + 2 * k, id_qk, kb > 0 || k > 0);
-          umma_commit(&s_full[2 * st + (i & 1)]);
+          umma_commit(&s_full[st]);
           umma_commit(&empty[slot]);
         }
         __syncwarp();
@@ -384,12 +391,12 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
         tc_fence_after();
         if (elect_one()) {
           const uint64_t bd = bd_pv + slot * (C::kSlot >> 4);
-          const uint32_t pa = tb + ((i - 1) & 1) * kKeys;
+          const uint32_t pa = tb + kColP + ((i - 1) & 1) * (kKeys / 2);
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 8 TMEM columns, 2 KB of V
-            umma_f16_ts(tb + 2 * kKeys, pa + 8 * k, bd + k * (2048 >> 4), id_pv,
+            umma_f16_ts(tb + kColO, pa + 8 * k, bd + k * (2048 >> 4), id_pv,
                         !starts_prev || k > 0);
-          umma_commit(&pv_done[st]);
+          umma_commit(&pv_done[2 * st + ((i - 1) & 1)]);
           umma_commit(&empty[slot]);
         }
         __syncwarp();
@@ -418,7 +425,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
     const int quarter = warp & 3;  // the TMEM lanes a warp may read: 32 (warp % 4) ..
     const int row_l = quarter * 32 + lane;
     const uint32_t tbase = tmem + stream * kStreamCols + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t to = tbase + 2 * kKeys;  // O
+    const uint32_t to = tbase + kColO;
     const int M = a.t.T * a.G;
     const float sl = fmaxf(fabsf(a.scale_log2), 1e-37f);
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -473,15 +480,22 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
       auto tile_step = [&](auto edge_tag, int tile) {
         constexpr bool kEdge = decltype(edge_tag)::value;
         const int p0 = tile * kKeys;
-        const uint32_t ts = tbase + (i & 1) * kKeys;
-        if (!wait(&s_full[2 * stream + (i & 1)], (i >> 1) & 1)) return false;
+        const int odd = i & 1, turn = (i >> 1) & 1;
+        if (!wait(&s_full[stream], odd)) return false;
+        // tile i - 2's weights leave their buffer to tile i's (long since)
+        if (i >= 2 && !wait(&pv_done[2 * stream + odd], turn ^ 1)) return false;
         tc_fence_after();
-        if (live) {
+        if (!live) {
+          if (lane == 0) mbar_arrive(&s_read[stream]);
+        } else {
           uint32_t x[64];
-          tmem_ld32_issue(ts, x);
-          tmem_ld32_issue(ts + 32, x + 32);
+          tmem_ld32_issue(tbase, x);
+          tmem_ld32_issue(tbase + 32, x + 32);
           tmem_ld32_wait(x);
           tmem_ld32_wait(x + 32);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_read[stream]);
           if (kEdge) {
             const uint64_t vis = r < M ? seen64(a, at.b, s, node, p0) : 0;
 #pragma unroll
@@ -503,7 +517,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
           if (tile == tile_lo) {
             m = top;
           } else if (__any_sync(kAll, top > m + kRise)) {  // (m = -inf: anything above)
-            if (!wait(&pv_done[stream], (i - 1) & 1)) return false;
+            if (!wait(&pv_done[2 * stream + (odd ^ 1)], ((i - 1) >> 1) & 1)) return false;
             tc_fence_after();
             const float mn = top > m + kRise ? top : m;
             const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
@@ -536,7 +550,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
           float s0, s1;
           unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
-          tmem_st32(ts, p);
+          tmem_st32(tbase + kColP + odd * (kKeys / 2), p);
           tmem_st_wait();
         }
         if (kEdge && stream == 0) {
@@ -566,13 +580,10 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
           if (found) bad_seg[seg & 3] = seg;
           fence_proxy_async_smem();
         }
-        // The output is waited for below by the parity of its phase, which names it only
-        // between the completion of the product before it and that of the one behind it.
-        if (tile + 1 == tile_hi && i > 0 && !wait(&pv_done[stream], (i - 1) & 1)) return false;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&p_ready[2 * stream + (i & 1)]);
+          mbar_arrive(&p_ready[2 * stream + odd]);
           if (kEdge && stream == 0 && NS > 1) add_release_cta(v_clean, 1);
         }
         ++i;
@@ -593,7 +604,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
         cur.next(a);
       }
       if (i < N) load_q(cur);  // every product with the old Q is complete (s_full)
-      if (!wait(&pv_done[stream], (i - 1) & 1)) break;
+      if (!wait(&pv_done[2 * stream + ((i - 1) & 1)], ((i - 1) >> 1) & 1)) break;
       tc_fence_after();
       const bool whole = tile_hi == s.tiles && tile_lo == 0;
       const int slot = tile_lo == 0 && !whole && at.u > u0 ? 1 : 0;
