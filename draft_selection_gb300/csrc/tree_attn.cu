@@ -90,21 +90,11 @@ __global__ void __launch_bounds__(kWThreads, D == 256 ? 1 : 2)
   pdl_wait();
   pdl_launch_dependents();
 
-  const int64_t units = units_before(a, a.B);
-  const int n_cta = static_cast<int>(min(static_cast<int64_t>(a.grid), units));
-  if (static_cast<int>(blockIdx.x) >= n_cta) return;
-  const int64_t u0 = range_start(units, n_cta, blockIdx.x);
-  const int64_t u1 = range_start(units, n_cta, blockIdx.x + 1);
-
-  Cursor cur;
-  {
-    int64_t before;
-    cur.u = u0;
-    cur.b = find_seq(a, u0, before);
-    cur.s = load_seq(a, cur.b);
-    cur.hr = static_cast<int>((u0 - before) / cur.s.tiles);
-    cur.tile = static_cast<int>((u0 - before) % cur.s.tiles);
-  }
+  const Range g = find_range(a, blockIdx.x);
+  const int64_t u0 = g.u0, u1 = g.u1;
+  if (tid == 0) a.cuts[blockIdx.x].b = -1;
+  if (u0 == u1) return;
+  Cursor cur = g.first;
   Cursor ld = cur;
 
   // ---- loads: thread -> piece cp of keys kr0, kr0 + kRowStep, .. ----
@@ -310,6 +300,11 @@ __global__ void __launch_bounds__(kWThreads, D == 256 ? 1 : 2)
       const int slot = tile_lo == 0 && !whole && cur.u + 1 == u1 &&
                                cur.u - cur.tile > u0 ? 1 : 0;
       const int tile_hi = cur.tile + 1;
+      if (cur.u + 1 == u1 && tid == 0) {
+        Cursor at = cur;
+        at.u -= cur.tile;  // the row tile's first unit
+        a.cuts[blockIdx.x] = make_cut(g, at, tile_lo, tile_hi, slot);
+      }
 #pragma unroll
       for (int i = 0; i < kMT; ++i)
 #pragma unroll
@@ -399,44 +394,56 @@ __global__ void __launch_bounds__(kWThreads, D == 256 ? 1 : 2)
   }
 }
 
-// One warp to an output row: the parts that the CTAs left of it, in the order of
-// the keys; rows past a sequence's count are zeroed.
+// The parts that the CTAs left of a row tile, added in the order of the keys, a warp
+// to a row: block column c takes the row tile that CTA c began and did not end (its
+// Cut), block rows divide the tile's rows, and the last B block columns zero what
+// lies past a sequence's count.
+// (A warp to every output row, looking up whether it was cut, took 76 us after the
+// 1.28 ms of 32 sequences of 64 nodes: most rows are whole.)
+constexpr int kCombineWarps = 8;
 template <typename E, int D>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kCombineWarps * 32)
+    combine_kernel(const __grid_constant__ AttnArgs a) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int M = a.t.T * a.G;
-  const int b = blockIdx.y;
-  const int x = blockIdx.x * 8 + (threadIdx.x >> 5);  // key head * M + row
-  if (x >= a.H * M) return;
-  const int h = x / M, r = x % M;
-  const int node = r / a.G, head = h * a.G + r % a.G;
-  const Seq s = load_seq(a, b);
   constexpr int kPer = D / 32;  // channels per lane
-  E* out = static_cast<E*>(a.out) + b * a.ob + node * a.ot + head * a.oh + lane * kPer;
-  float* lse = a.lse ? a.lse + (static_cast<int64_t>(b) * a.t.T + node) * (a.H * a.G) + head
-                     : nullptr;
-  float y[kPer];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int step = gridDim.y * kCombineWarps;
+  const int Hq = a.H * a.G;
+  if (static_cast<int>(blockIdx.x) >= a.grid) {
+    const int b = blockIdx.x - a.grid;
+    for (int x = load_seq(a, b).n * Hq + blockIdx.y * kCombineWarps + warp; x < a.t.T * Hq;
+         x += step) {
+      const int node = x / Hq, head = x - node * Hq;
+      uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<E*>(a.out) + b * a.ob + node * a.ot +
+                                                  head * a.oh + lane * kPer);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) y[i] = 0.f;
-  float mm = -INFINITY, safe = 0.f, ll = 0.f;
-  if (node < s.n) {
-    const int64_t units = units_before(a, a.B);
-    const int n_cta = static_cast<int>(min(static_cast<int64_t>(a.grid), units));
-    const int64_t v0 = units_before(a, b) +
-                       static_cast<int64_t>(h * a.row_tiles + r / a.rows) * s.tiles;
-    const int c0 = range_of(units, n_cta, v0), c1 = range_of(units, n_cta, v0 + s.tiles - 1);
-    if (c0 == c1) return;  // written by the CTA that had all of it
-    const int slot0 = range_start(units, n_cta, c0) < v0 ? 1 : 0;
+      for (int i = 0; i < kPer / 2; ++i) out[i] = 0;
+      if (a.lse && lane == 0)
+        a.lse[(static_cast<int64_t>(b) * a.t.T + node) * Hq + head] = -INFINITY;
+    }
+    return;
+  }
+  const Cut cut = a.cuts[blockIdx.x];
+  if (cut.b < 0) return;
+  const int b = cut.b, c0 = blockIdx.x, c1 = cut.last_cta, slot0 = cut.slot;
+  const int h = cut.hr / a.row_tiles, r0 = (cut.hr - h * a.row_tiles) * a.rows;
+  const int n = load_seq(a, b).n;
+  const int rows = min(a.rows, n * a.G - r0);  // (rows past the count are zeroed above)
+  for (int r = blockIdx.y * kCombineWarps + warp; r < rows; r += step) {
     auto part = [&](int c) {
-      return (static_cast<int64_t>(c) * 2 + (c == c0 ? slot0 : 0)) * a.rows + r % a.rows;
+      return (static_cast<int64_t>(c) * 2 + (c == c0 ? slot0 : 0)) * a.rows + r;
     };
+    float mm = -INFINITY;
     for (int c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, a.part_ml[part(c)].x);
 #pragma unroll
     for (int off = 16; off; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kAll, mm, off));
-    safe = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 4
+    const float safe = mm == -INFINITY ? 0.f : mm;
+    float y[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) y[i] = 0.f;
+    float ll = 0.f;
+#pragma unroll 8
     for (int c = c0; c <= c1; ++c) {
       const float2 ml = a.part_ml[part(c)];
       const float w = ex2(ml.x - safe);
@@ -446,15 +453,14 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
       for (int i = 0; i < kPer; ++i) y[i] += p[i] * w;
     }
     const float inv = ll == 0.f ? 0.f : 1.f / ll;
+    const int node = (r0 + r) / a.G, head = h * a.G + (r0 + r) - node * a.G;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<E*>(a.out) + b * a.ob + node * a.ot +
+                                                head * a.oh + lane * kPer);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) y[i] *= inv;
+    for (int i = 0; i < kPer / 2; ++i) out[i] = pack2<E>(y[2 * i] * inv, y[2 * i + 1] * inv);
+    if (a.lse && lane == 0)  // log 0 = -inf: nothing seen
+      a.lse[(static_cast<int64_t>(b) * a.t.T + node) * Hq + head] = safe * kLn2 + logf(ll);
   }
-  uint32_t w[kPer / 2];
-#pragma unroll
-  for (int i = 0; i < kPer / 2; ++i) w[i] = pack2<E>(y[2 * i], y[2 * i + 1]);
-#pragma unroll
-  for (int i = 0; i < kPer / 2; ++i) reinterpret_cast<uint32_t*>(out)[i] = w[i];
-  if (lse && lane == 0) *lse = safe * kLn2 + logf(ll);  // log 0 = -inf: nothing seen
 }
 
 // ---- plan ---------------------------------------------------------------------
@@ -462,7 +468,7 @@ struct AttnPlan {
   bool tc;    // the tensor-core kernel
   int rows;   // rows of a row tile
   int row_tiles, grid;
-  size_t o_off, ml_off, ws_bytes;
+  size_t o_off, ml_off, cut_off, ws_bytes;
 };
 
 // The warp-level kernel for a few rows (one 16-row MMA tile while they fit it, two
@@ -477,7 +483,8 @@ AttnPlan attn_plan(int M, int D, bool tc_takes, int sms) {
   p.grid = p.tc ? attn_tc_grid(p.rows, sms) : sms * (D == 256 ? 1 : 2);
   p.o_off = 0;
   p.ml_off = align_up(size_t(p.grid) * 2 * p.rows * D * sizeof(float), 256);
-  p.ws_bytes = p.ml_off + align_up(size_t(p.grid) * 2 * p.rows * sizeof(float2), 256);
+  p.cut_off = p.ml_off + align_up(size_t(p.grid) * 2 * p.rows * sizeof(float2), 256);
+  p.ws_bytes = p.cut_off + align_up(size_t(p.grid) * sizeof(Cut), 256);
   return p;
 }
 
@@ -502,8 +509,9 @@ cudaError_t launch_attn(const AttnArgs& a, const AttnPlan& p, const dfl2_cache* 
   else
     e = launch_warp<E, D, D == 256 ? 16 : 32>(a, s);
   if (e != cudaSuccess) return e;
-  const int warps = a.H * a.t.T * a.G;
-  return launch_k(combine_kernel<E, D>, dim3((warps + 7) / 8, a.B), dim3(256), 0, s, true, a);
+  const int rows = std::min(a.rows, a.t.T * a.G);
+  return launch_k(combine_kernel<E, D>, dim3(a.grid + a.B, (rows + kCombineWarps - 1) / kCombineWarps),
+                  dim3(kCombineWarps * 32), 0, s, true, a);
 }
 
 template <typename E>
@@ -610,6 +618,7 @@ dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_c
   a.lse = lse;
   a.part_o = reinterpret_cast<float*>(w + p.o_off);
   a.part_ml = reinterpret_cast<float2*>(w + p.ml_off);
+  a.cuts = reinterpret_cast<dfl2::Cut*>(w + p.cut_off);
   a.grid = p.grid;
   a.rows = p.rows;
   a.row_tiles = p.row_tiles;

@@ -21,6 +21,13 @@ constexpr int kKeys = 64;  // keys of a tile, in both kernels
 
 }  // namespace
 
+// Left by each CTA for combine_kernel: the row tile that its range begins but does
+// not end, if there is one (b < 0: none).
+struct alignas(16) Cut {
+  int b, hr;
+  int last_cta;  // the parts are this CTA's and those of the CTAs up to last_cta
+  int slot;      // which of its two places this CTA's part is in
+};
 struct AttnArgs {
   TableView t;
   const void* q;
@@ -37,6 +44,7 @@ struct AttnArgs {
   float* lse;      // nullable
   float* part_o;   // [grid][2][rows][D] unnormalised outputs
   float2* part_ml; // [grid][2][rows] (maximum, sum)
+  Cut* cuts;       // [grid]
   int grid;        // CTAs of the main kernel
   int rows;        // rows of a row tile
   int row_tiles;   // ceil(T G / rows)
@@ -58,46 +66,18 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
   return s;
 }
 
-// Units before sequence b (all of them for b = B), by a warp together.
-__device__ __forceinline__ int64_t units_before(const AttnArgs& a, int b) {
-  const int lane = threadIdx.x & 31;
-  int64_t x = 0;
-  for (int i = lane; i < b; i += 32) x += load_seq(a, i).tiles;
-#pragma unroll
-  for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(kAll, x, off);
-  return x * (a.H * a.row_tiles);
-}
-
-// The sequence that unit u falls in, and the units before it.
-__device__ __forceinline__ int find_seq(const AttnArgs& a, int64_t u, int64_t& before) {
-  const int lane = threadIdx.x & 31;
-  const int64_t per = a.H * a.row_tiles;
-  int64_t base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int64_t own = b0 + lane < a.B ? load_seq(a, b0 + lane).tiles * per : 0;
-    int64_t x = own;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(kAll, x, off);
-      if (lane >= off) x += y;
-    }
-    const unsigned hit = __ballot_sync(kAll, u < base + x);
-    if (hit) {
-      const int w = __ffs(hit) - 1;
-      before = base + __shfl_sync(kAll, x - own, w);
-      return b0 + w;
-    }
-    base += __shfl_sync(kAll, x, 31);
-  }
-  before = base;
-  return a.B;
-}
-
-// Where CTA c's range of `units` units on `n` CTAs begins, and whose range unit u is in.
+// Where CTA c's range of `units` units on `n` CTAs begins, and whose range unit u
+// is in.  (32-bit divisions where they do: a 64-bit one is a chain of some 100
+// instructions.)
 __device__ __forceinline__ int64_t range_start(int64_t units, int n, int c) {
+  if (units < (1 << 20))  // n and c are at most a few thousand
+    return static_cast<uint32_t>(units) * static_cast<uint32_t>(c) / static_cast<uint32_t>(n);
   return units * c / n;
 }
 __device__ __forceinline__ int range_of(int64_t units, int n, int64_t u) {
+  if (units < (1 << 20))
+    return ((static_cast<uint32_t>(u) + 1) * static_cast<uint32_t>(n) - 1) /
+           static_cast<uint32_t>(units);
   return static_cast<int>(((u + 1) * n - 1) / units);
 }
 
@@ -125,6 +105,71 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// CTA `cta`'s range [u0, u1) of the units on n_cta CTAs, and the place where it
+// begins, by a warp together.  Up to 32 sequences need one load of their lengths.
+struct Range {
+  int64_t units, u0, u1;
+  int n_cta;
+  Cursor first;  // if u0 < u1
+};
+__device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
+  const int lane = threadIdx.x & 31;
+  const int per = a.H * a.row_tiles;
+  Range g;
+  Seq own{0, 0, 0, 0};
+  int64_t x = 0;
+  for (int b = lane; b < a.B; b += 32) {
+    own = load_seq(a, b);
+    x += own.tiles;
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(kAll, x, off);
+  g.units = x * per;
+  g.n_cta = static_cast<int>(min(static_cast<int64_t>(a.grid), g.units));
+  g.u0 = g.u1 = 0;
+  if (cta >= g.n_cta) return g;
+  g.u0 = range_start(g.units, g.n_cta, cta);
+  g.u1 = range_start(g.units, g.n_cta, cta + 1);
+  // the sequence that u0 falls in
+  int64_t base = 0;
+  for (int b0 = 0;; b0 += 32) {
+    if (a.B > 32) own = b0 + lane < a.B ? load_seq(a, b0 + lane) : Seq{0, 0, 0, 0};
+    int64_t sum = static_cast<int64_t>(own.tiles) * per;
+    const int64_t mine = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(kAll, sum, off);
+      if (lane >= off) sum += y;
+    }
+    const unsigned hit = __ballot_sync(kAll, g.u0 < base + sum);
+    if (hit) {
+      const int w = __ffs(hit) - 1;
+      const int64_t before = base + __shfl_sync(kAll, sum - mine, w);
+      g.first.u = g.u0;
+      g.first.b = b0 + w;
+      g.first.s = Seq{__shfl_sync(kAll, own.row, w), __shfl_sync(kAll, own.len, w),
+                      __shfl_sync(kAll, own.n, w), __shfl_sync(kAll, own.tiles, w)};
+      // within one sequence: at most 2^24 tiles of each of its row tiles
+      const int64_t in = g.u0 - before;
+      g.first.hr = in < (1ll << 32)
+                       ? static_cast<int>(static_cast<uint32_t>(in) /
+                                          static_cast<uint32_t>(g.first.s.tiles))
+                       : static_cast<int>(in / g.first.s.tiles);
+      g.first.tile = static_cast<int>(in - static_cast<int64_t>(g.first.hr) * g.first.s.tiles);
+      return g;
+    }
+    base += __shfl_sync(kAll, sum, 31);
+  }
+}
+
+__device__ __forceinline__ Cut make_cut(const Range& g, const Cursor& at, int tile_lo, int tile_hi,
+                                        int slot) {
+  Cut c{-1, 0, 0, 0};
+  if (tile_lo == 0 && tile_hi < at.s.tiles)
+    c = Cut{at.b, at.hr, range_of(g.units, g.n_cta, at.u + at.s.tiles - 1), slot};
+  return c;
+}
+
 template <typename E>
 __device__ __forceinline__ uint32_t pack2(float x, float y) {  // x in the low half
   if constexpr (std::is_same_v<E, __half>) {

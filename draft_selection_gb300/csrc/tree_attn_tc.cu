@@ -253,25 +253,16 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
   pdl_launch_dependents();
 
   // this CTA's range of units, and where it begins (each warp for itself)
-  const int64_t units = units_before(a, a.B);
-  const int n_cta = static_cast<int>(min(static_cast<int64_t>(a.grid), units));
-  int64_t u0 = 0, u1 = 0;
-  Cursor cur;
-  if (static_cast<int>(blockIdx.x) < n_cta) {
-    u0 = range_start(units, n_cta, blockIdx.x);
-    u1 = range_start(units, n_cta, blockIdx.x + 1);
-    int64_t before;
-    cur.u = u0;
-    cur.b = find_seq(a, u0, before);
-    cur.s = load_seq(a, cur.b);
-    cur.hr = static_cast<int>((u0 - before) / cur.s.tiles);
-    cur.tile = static_cast<int>((u0 - before) % cur.s.tiles);
-  }
-  int N = static_cast<int>(u1 - u0);
+  const Range g = find_range(a, blockIdx.x);
+  const int64_t u0 = g.u0;
+  Cursor cur = g.first;
+  int N = static_cast<int>(g.u1 - u0);
   if (smem_u32(smem) & 1023u) {  // the swizzle counts on it
     record_error(a.t.err, kDevErrAttn);
     N = 0;
   }
+  constexpr int kFirst = 32 * (1 + NS);  // the first softmax thread
+  if (tid == kFirst) a.cuts[blockIdx.x].b = -1;  // (it alone writes the cut, below)
   // The ring's order is K(0), K(1), V(0), K(2), V(1), ..: as the MMAs read them.  V(i)'s place:
   auto seq_v = [N](int i) { return i + 1 < N ? 2 * i + 2 : 2 * i + 1; };
 
@@ -420,7 +411,6 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
     __syncwarp();
   } else if (N > 0) {
     // ---- softmax: a thread to a row ----
-    constexpr int kFirst = 32 * (1 + NS);  // the first softmax thread
     const int stream = (tid - kFirst) / kLanes;
     const int quarter = warp & 3;  // the TMEM lanes a warp may read: 32 (warp % 4) ..
     const int row_l = quarter * 32 + lane;
@@ -608,6 +598,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, NS == 1 ? 2 : 1)
       tc_fence_after();
       const bool whole = tile_hi == s.tiles && tile_lo == 0;
       const int slot = tile_lo == 0 && !whole && at.u > u0 ? 1 : 0;
+      if (i == N && tid == kFirst) a.cuts[blockIdx.x] = make_cut(g, at, tile_lo, tile_hi, slot);
       if (live) {
         const int head = h * a.G + r - node * a.G;
         const bool bad = *reinterpret_cast<volatile int*>(&bad_seg[seg & 3]) == seg;
