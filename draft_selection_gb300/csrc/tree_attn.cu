@@ -20,400 +20,713 @@
 // Softmax in one pass: with the running maximum m and sum l of a row, a tile
 // with row maximum m' multiplies l and o by 2^(m - m') before adding its own
 // terms (scores are kept times log2 e, so that exp is exp2).
+//
+// For a row tile of 128 rows (node, head) and tiles of 64 keys:
+//   S = Q K^T   tcgen05.mma, 128 x 64, Q and K in shared memory, S (float32) in TMEM
+//   P = 2^(scale log2 e S - m)   a thread to a row: its 64 scores come from TMEM,
+//               its weights go back there, rounded to the cache's type
+//   O += P V    tcgen05.mma, 128 x D, P in TMEM, V in shared memory as it lies in
+//               the cache (keys x channels: the channel-major operand), O in TMEM
+// A row's statistics never leave its thread, so the softmax has no exchange at
+// all.  O is rescaled only when a row's maximum has risen by more than 2^8 since
+// the reference m was taken: weights up to 2^8 lose nothing in float32 sums or in
+// rounding to a floating type, and the rescaling (TMEM -> registers -> TMEM, after
+// the products in flight) then almost never happens past a row's first tiles.
+//
+// Roles: warp 0 loads K and V (TMA boxes of one page's rows x 64 channels,
+// 128-byte swizzle, into a ring of slots of one tile's K or V); a stream, 128
+// rows, has one warp that issues its MMAs and four that do its softmax.  A row's
+// scores are in registers soon after they are in TMEM, so one S is enough: the
+// scores of tile i+1 are computed over those of tile i while its softmax runs.  P
+// has two buffers, so neither product ever waits for the other one (with two S
+// and P written over S, tile i+1's scores waited for tile i-1's output: 1830 cycles
+// a pair of tiles at 256 rows instead of REPLACE).
+// With M = T G rows up to 128: one stream, two CTAs on an SM.  Above: one CTA with
+// two streams (256 rows), which share each K and V tile, so that the shared-memory
+// fill per row, the next bound after HBM, is halved.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "tree_attn.cuh"
 
 namespace dfl2 {
 namespace {
 
-template <typename E>
-__device__ __forceinline__ void mma16816(float d[4], const uint32_t a[4], const uint32_t b0,
-                                         const uint32_t b1) {
-  if constexpr (std::is_same_v<E, __half>)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t r[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
-}
-// ---------------------------------------------------------------------------
-// Warp-level kernel.  Four warps, tiles of 64 keys, 16 keys to a warp: each warp
-// keeps its own maximum, sum and output for all rows and the four are added at
-// the end of a row tile, so no warp waits for another inside a tile but for its
-// keys' arrival.
-// ---------------------------------------------------------------------------
-constexpr int kWThreads = 128;
+constexpr int kLanes = 128;                // rows of a stream: the TMEM lanes
+constexpr float kRise = 8.f;               // log2 of the rise that O is rescaled at
+constexpr uint32_t kColP = kKeys, kColO = 2 * kKeys;
 
-template <int D, int kRows>
-struct WarpCfg {
-  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 3 : 2;
-  static constexpr int kTile = kKeys * D * 2;  // bytes of K (or V) in a stage
-  static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kJoin = kRows == 16 ? 64 : 32;  // channels added per round at the end
-  static constexpr int kJoinBytes = kRows * kJoin * 4;
-  static constexpr size_t kSmem =
-      size_t(kStages) * 2 * kTile + kQBytes + kJoinBytes + 4 * kRows * 8 + 16;
+template <int D, int NS>
+struct TcCfg {
+  // 256 channels fill the SM with one stream: O alone is half of TMEM
+  static constexpr int kCtas = NS == 1 && D < 256 ? 2 : 1;     // on an SM
+  static constexpr uint32_t kStreamCols = D < 256 ? 256 : 512;  // TMEM columns: S, P, P, O
+  static constexpr int kSlot = kKeys * D * 2;                  // bytes of a tile's K (or V)
+  static constexpr int kRing = 163840 / kCtas / kSlot;
+  static constexpr int kSlots = kRing < 16 ? kRing : 16;
+  static constexpr int kQ = kLanes * D * 2;                    // bytes of a stream's Q
+  static constexpr int kThreads = 32 * (1 + NS) + NS * kLanes;
+  static constexpr int kBars = 2 * kSlots + NS * 8;
+  static constexpr size_t kSmem = size_t(NS) * kQ + size_t(kSlots) * kSlot + kBars * 8 + 64;
+  static_assert(NS * kStreamCols * kCtas <= 512, "TMEM");
+  static_assert((kSmem + 1024) * kCtas <= 233472, "shared memory");
 };
 
-template <typename E, int D, int kRows>
-__global__ void __launch_bounds__(kWThreads, D == 256 ? 1 : 2)
-    attn_warp_kernel(const __grid_constant__ AttnArgs a) {
-  using C = WarpCfg<D, kRows>;
-  constexpr int kMT = kRows / 16;        // 16-row MMA tiles
-  constexpr int kCPR = D / 8;            // 16-byte pieces of a key
-  constexpr int kRowStep = kWThreads / kCPR;
-  constexpr int kPer = kKeys / kRowStep;  // keys each thread copies a piece of, per tile
-  extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* ring = smem;
-  uint8_t* qs = smem + C::kStages * 2 * C::kTile;
-  float* join = reinterpret_cast<float*>(qs + C::kQBytes);
-  float2* ml_s = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(join) + C::kJoinBytes);
-  int* bad_s = reinterpret_cast<int*>(ml_s + 4 * kRows);
+// A wait whose first look nearly always succeeds; the rest is out of line, which
+// keeps the loops that wait short (mbar_wait in place, with a vote, took 85 cycles
+// when there was nothing to wait for, and more once its code had left the cache).
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, uint32_t* err) {
+  if (mbar_wait(bar, parity, err)) return true;
+  record_error(err, kDevErrAttn);
+  return false;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return wait_on(bar, parity, err);
+}
+
+// Places of a page map's outer dimensions, innermost 0.
+struct MapOrder {
+  int slot, head, page;
+};
+
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// Operand of 128-byte rows in the 128-byte swizzle whose contiguous dimension is
+// not the summed one: 64-element blocks along it `block` bytes apart, groups of
+// eight summed indices 1024 bytes apart.
+__device__ __forceinline__ uint64_t umma_desc_sw128_mn(const void* smem_tile, uint32_t block) {
+  uint64_t d = (static_cast<uint64_t>(smem_u32(smem_tile)) >> 4) & 0x3FFFull;
+  d |= static_cast<uint64_t>(block >> 4) << 16;  // leading byte offset
+  d |= uint64_t(1024 >> 4) << 32;                // stride byte offset
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(2) << 61;
+  return d;
+}
+// kind::f16, float32 accumulator; b_mn: B's contiguous dimension is N.
+template <typename E>
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
+  const uint32_t f = std::is_same_v<E, __half> ? 0u : 1u;
+  return (1u << 4) | (f << 7) | (f << 10) | ((b_mn ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// As umma_bf16 with A in TMEM.
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// Waits for this thread's tcgen05.ld; names r so that nothing reads it before.
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+      "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, "
+      "%27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z,
+                                            int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Two float32 operations in one instruction, and a maximum of three.
+__device__ __forceinline__ uint64_t pack_f32x2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack_u32x2(uint32_t x, uint32_t y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t r, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Which of the 64 positions from p0 on node i of sequence b sees (0 past the end).
+__device__ __forceinline__ uint64_t seen64(const AttnArgs& a, int b, const Seq& s, int i, int p0) {
+  if (i >= s.n) return 0;
+  const int ctx = max(0, min(64, s.len - p0));  // committed positions of the tile
+  uint64_t vis = ctx == 64 ? ~0ull : (1ull << ctx) - 1;
+  if (ctx == 64) return vis;
+  const int j0 = p0 + ctx - s.len;              // first node of the tile
+  if (j0 >= s.n) return vis;
+  uint64_t nodes;
+  if (a.mask) {
+    const uint32_t* w = a.mask + (static_cast<int64_t>(b) * a.t.T + i) * a.W;
+    const int w0 = j0 >> 5;
+    const uint64_t lo = w[w0], mid = w0 + 1 < a.W ? w[w0 + 1] : 0, hi = w0 + 2 < a.W ? w[w0 + 2] : 0;
+    const int sh = j0 & 31;
+    nodes = ((lo | mid << 32) >> sh) | (sh ? hi << (64 - sh) : 0);
+  } else {
+    nodes = i < j0 ? 0 : i - j0 >= 63 ? ~0ull : (2ull << (i - j0)) - 1;
+  }
+  const int left = s.n - j0;
+  if (left < 64) nodes &= (1ull << left) - 1;
+  return vis | nodes << ctx;
+}
+
+template <typename E, int D, int NS>
+__global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
+    attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ MapOrder order) {
+  using C = TcCfg<D, NS>;
+  constexpr int kBlk = D / 64;          // 64-channel blocks of a row
+  constexpr int kBlkBytes = kKeys * 128;  // one block of a K or V slot
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* qs = smem;                   // [NS][kBlk][128 rows][128 B]
+  uint8_t* ring = smem + NS * C::kQ;    // [slots][kBlk][64 keys][128 B]
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + C::kSlots * C::kSlot);
+  uint64_t* empty = full + C::kSlots;
+  uint64_t* q_full = empty + C::kSlots;  // [NS] a row tile's Q is in place
+  uint64_t* s_full = q_full + NS;        // [NS] scores are in TMEM
+  uint64_t* s_read = s_full + NS;        // [NS] and in registers
+  // The weights of tile i, and the output product that took them, have a barrier for
+  // even and one for odd tiles, as P has: each side may be a tile ahead of the other,
+  // and a barrier's parity tells only two neighbouring phases apart.
+  uint64_t* p_ready = s_read + NS;       // [NS][2] weights are in TMEM
+  uint64_t* pv_done = p_ready + 2 * NS;  // [NS][2] the output product is in O
+  uint64_t* all_done = pv_done + 2 * NS; // [NS]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + NS);
+  int* bad_seg = reinterpret_cast<int*>(tmem_slot + 1);  // [4] row tile that met Inf or NaN in V
+  // Warps that have cleaned an edge tile's V, counted up: stream 0 may be several tiles
+  // ahead of stream 1, more than a barrier's parity can tell apart.
+  uint32_t* v_clean = reinterpret_cast<uint32_t*>(bad_seg + 4);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const E* K = static_cast<const E*>(a.k);
-  const E* V = static_cast<const E*>(a.v);
-  const int ps1 = (1 << a.t.page_shift) - 1;
+  if (tid == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], NS);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&q_full[s], 4);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&s_read[s], 4);
+      for (int z = 0; z < 2; ++z) {
+        mbar_init(&p_ready[2 * s + z], 4);
+        mbar_init(&pv_done[2 * s + z], 1);
+      }
+      mbar_init(&all_done[s], 1);
+    }
+    *v_clean = 0;
+    for (int i = 0; i < 4; ++i) bad_seg[i] = -1;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, NS * C::kStreamCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_launch_dependents();
 
+  // this CTA's range of units, and where it begins (each warp for itself)
   const Range g = find_range(a, blockIdx.x);
-  const int64_t u0 = g.u0, u1 = g.u1;
-  if (tid == 0) a.cuts[blockIdx.x].b = -1;
-  if (u0 == u1) return;
+  const int64_t u0 = g.u0;
   Cursor cur = g.first;
-  Cursor ld = cur;
-
-  // ---- loads: thread -> piece cp of keys kr0, kr0 + kRowStep, .. ----
-  const int cp = tid % kCPR, kr0 = tid / kCPR;
-  int pages[kPer];
-  auto look_up = [&]() {  // the pages of the tile at ld
-    if (ld.u >= u1) return;
-    const int end = ld.s.len + ld.s.n;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int pos = ld.tile * kKeys + kr0 + i * kRowStep;
-      pages[i] = pos < end ? a.t.page_at(ld.s.row, pos >> a.t.page_shift) : -1;
-    }
-  };
-  auto issue = [&](int stage) {  // the copies of the tile at ld
-    if (ld.u < u1) {
-      uint8_t* st = ring + stage * 2 * C::kTile;
-      const int h = ld.hr / a.row_tiles;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int r = kr0 + i * kRowStep;
-        const int pos = ld.tile * kKeys + r;
-        const bool ok = pages[i] >= 0;
-        const int64_t at = static_cast<int64_t>(ok ? pages[i] : 0) * a.page_stride +
-                           h * a.head_stride + (ok ? pos & ps1 : 0) * a.slot_stride + cp * 8;
-        uint8_t* dst = st + r * (D * 2) + ((cp ^ (r & 7)) << 4);
-        cp_async16(dst, K + at, ok);
-        cp_async16(dst + C::kTile, V + at, ok);
-      }
-      ld.next(a);
-    }
-    cp_async_commit();
-  };
-  look_up();
-#pragma unroll
-  for (int s = 0; s < C::kStages - 1; ++s) {
-    issue(s);
-    look_up();
+  int N = static_cast<int>(g.u1 - u0);
+  if (smem_u32(smem) & 1023u) {  // the swizzle counts on it
+    record_error(a.t.err, kDevErrAttn);
+    N = 0;
   }
+  constexpr int kFirst = 32 * (1 + NS);  // the first softmax thread
+  if (tid == kFirst) {  // (it alone writes the cuts, below)
+    a.cuts[2 * blockIdx.x].b = -1;
+    a.cuts[2 * blockIdx.x + 1].b = -1;
+  }
+  // The ring's order is K(0), K(1), V(0), K(2), V(1), ..: as the MMAs read them.  V(i)'s place:
+  auto seq_v = [N](int i) { return i + 1 < N ? 2 * i + 2 : 2 * i + 1; };
 
-  float o[kMT][D / 8][4];
-  float m[kMT][2], l[kMT][2];
-  int stage = 0;
-  bool fresh = true;
-  int tile_lo = 0;  // first tile of this CTA's part of the row tile
-  int bad = 0;
-
-  for (; cur.u < u1;) {
-    const Seq s = cur.s;
-    const int h = cur.hr / a.row_tiles, r0 = (cur.hr % a.row_tiles) * kRows;
-    const int rows = min(kRows, a.t.T * a.G - r0);
-    if (fresh) {
-      fresh = false;
-      tile_lo = cur.tile;
-      bad = 0;
-      const E* Q = static_cast<const E*>(a.q) + cur.b * a.qb;
-      for (int x = tid; x < kRows * kCPR; x += kWThreads) {
-        const int r = x / kCPR, c = x % kCPR;
-        uint4 val = make_uint4(0, 0, 0, 0);
-        if (r < rows)
-          val = *reinterpret_cast<const uint4*>(Q + (r0 + r) / a.G * a.qt +
-                                                (h * a.G + (r0 + r) % a.G) * a.qh + c * 8);
-        *reinterpret_cast<uint4*>(qs + r * (D * 2) + ((c ^ (r & 7)) << 4)) = val;
+  if (warp == 0) {
+    // ---- loads ----
+    const int ps = 1 << a.t.page_shift;
+    const int box = min(ps, kKeys);           // positions of a TMA box
+    const int n_page = kKeys / box;           // pages of a tile
+    const int my_page = lane / kBlk, my_blk = lane % kBlk;
+    const bool mine = my_page < n_page;
+    auto page_of = [&](const Cursor& c) {     // this lane's page of the tile at c
+      const int pos = c.tile * kKeys + my_page * box;
+      // past the end: one page too far, which TMA reads as zeros
+      const int p = mine && pos < c.s.len + c.s.n ? a.t.page_at(c.s.row, pos >> a.t.page_shift) : -1;
+      return p < 0 ? a.t.pages : p;
+    };
+    int issued = 0;
+    bool ok = true;
+    int slot = 0, ph = 0;  // the next slot, and the phase of its last use
+    auto load = [&](const CUtensorMap* tm, int h, int tile, int page) {
+      if (issued >= C::kSlots && !wait(&empty[slot], ph ^ 1, a.t.err)) {
+        ok = false;
+        return;
       }
-#pragma unroll
-      for (int i = 0; i < kMT; ++i) {
-        m[i][0] = m[i][1] = -INFINITY;
-        l[i][0] = l[i][1] = 0.f;
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
-      }
-    }
-    cp_async_wait<C::kStages - 2>();
-    __syncthreads();  // the tile (and a new q) is here; everyone is done with the stage before
-    issue((stage + C::kStages - 1) % C::kStages);
-    look_up();
-
-    uint8_t* kst = ring + stage * 2 * C::kTile + warp * 16 * (D * 2);
-    uint8_t* vst = kst + C::kTile;
-    const int p0 = cur.tile * kKeys + warp * 16;  // this warp's first position
-    const bool edge = p0 + 16 > s.len;             // has nodes, or lies past the end
-
-    // scores: rows x 16 keys
-    float sc[kMT][2][4];
-#pragma unroll
-    for (int i = 0; i < kMT; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) sc[i][j][0] = sc[i][j][1] = sc[i][j][2] = sc[i][j][3] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      uint32_t kb[4];  // keys 0..7 and 8..15, channels 16 kk .. + 7 and + 8 ..
-      {
-        const int r = (lane & 7) + ((lane >> 4) << 3), c = 2 * kk + ((lane >> 3) & 1);
-        ldsm_x4(smem_u32(kst + r * (D * 2) + ((c ^ (r & 7)) << 4)), kb);
-      }
-#pragma unroll
-      for (int i = 0; i < kMT; ++i) {
-        uint32_t qa[4];
-        const int r = i * 16 + (lane & 15), c = 2 * kk + (lane >> 4);
-        ldsm_x4(smem_u32(qs + r * (D * 2) + ((c ^ (r & 7)) << 4)), qa);
-        mma16816<E>(sc[i][0], qa, kb[0], kb[1]);
-        mma16816<E>(sc[i][1], qa, kb[2], kb[3]);
-      }
-    }
-    // what a row does not see
-#pragma unroll
-    for (int i = 0; i < kMT; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = sc[i][j][e] * a.scale_log2;
-          if (edge) {
-            const int node = p0 + j * 8 + (lane & 3) * 2 + (e & 1) - s.len;
-            const int r = r0 + i * 16 + (lane >> 2) + (e >> 1) * 8;
-            if (node >= 0 && (r - r0 >= rows || !sees(a, cur.b, s.n, r / a.G, node)))
-              x = -INFINITY;
-          }
-          sc[i][j][e] = x;
-        }
-    // running maximum, weights, sum
-    bool moved = false;
-    float al[kMT][2];
-#pragma unroll
-    for (int i = 0; i < kMT; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(fmaxf(sc[i][0][2 * e], sc[i][0][2 * e + 1]),
-                        fmaxf(sc[i][1][2 * e], sc[i][1][2 * e + 1]));
-        x = fmaxf(x, __shfl_xor_sync(kAll, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(kAll, x, 2));
-        const float mn = fmaxf(m[i][e], x);
-        const float safe = mn == -INFINITY ? 0.f : mn;
-        al[i][e] = ex2(m[i][e] - safe);
-        moved |= mn != m[i][e];
-        m[i][e] = mn;
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const float p = ex2(sc[i][j][2 * e + z] - safe);
-            sc[i][j][2 * e + z] = p;
-            sum += p;
-          }
-        l[i][e] = l[i][e] * al[i][e] + sum;
-      }
-    if (__any_sync(kAll, moved)) {
-#pragma unroll
-      for (int i = 0; i < kMT; ++i)
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          o[i][j][0] *= al[i][0];
-          o[i][j][1] *= al[i][0];
-          o[i][j][2] *= al[i][1];
-          o[i][j][3] *= al[i][1];
-        }
-    }
-    if (edge) {  // Inf and NaN of nodes stay out of the product (unseen_safe_sum)
-      bool found = false;
-      for (int x = lane; x < 16 * kCPR; x += 32) {
-        if (p0 + x / kCPR < s.len) continue;
-        uint4* at = reinterpret_cast<uint4*>(vst) + x;
-        uint4 y = *at;
-        bool b4 = false;
-        y.x = finite2<E>(y.x, b4);
-        y.y = finite2<E>(y.y, b4);
-        y.z = finite2<E>(y.z, b4);
-        y.w = finite2<E>(y.w, b4);
-        if (b4) *at = y;
-        found |= b4;
-      }
-      bad |= __any_sync(kAll, found);
+      if (lane == 0) mbar_arrive_expect_tx(&full[slot], C::kSlot);
       __syncwarp();
-    }
-    // the weights (rounded to E: they multiply values of E, and their own rounding
-    // errors average out over the keys) times V
-    uint32_t pa[kMT][4];
-#pragma unroll
-    for (int i = 0; i < kMT; ++i) {
-      pa[i][0] = pack2<E>(sc[i][0][0], sc[i][0][1]);
-      pa[i][1] = pack2<E>(sc[i][0][2], sc[i][0][3]);
-      pa[i][2] = pack2<E>(sc[i][1][0], sc[i][1][1]);
-      pa[i][3] = pack2<E>(sc[i][1][2], sc[i][1][3]);
-    }
-#pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-      uint32_t vb[4];  // keys 0..7 / 8..15 of channels 16 j .. + 7, then of + 8 ..
-      const int r = lane & 15, c = 2 * j + (lane >> 4);
-      ldsm_x4_t(smem_u32(vst + r * (D * 2) + ((c ^ (r & 7)) << 4)), vb);
-#pragma unroll
-      for (int i = 0; i < kMT; ++i) {
-        mma16816<E>(o[i][2 * j], pa[i], vb[0], vb[1]);
-        mma16816<E>(o[i][2 * j + 1], pa[i], vb[2], vb[3]);
+      if (mine) {
+        uint8_t* dst = ring + slot * C::kSlot + my_blk * kBlkBytes + my_page * box * 128;
+        const int at = (tile * kKeys) & (ps - 1);
+        const int y = order.slot == 0 ? at : order.head == 0 ? h : page;
+        const int z = order.slot == 1 ? at : order.head == 1 ? h : page;
+        const int w = order.slot == 2 ? at : order.head == 2 ? h : page;
+        tma_load_4d(dst, tm, my_blk * 64, y, z, w, &full[slot]);
       }
+      ++issued;
+      if (++slot == C::kSlots) {
+        slot = 0;
+        ph ^= 1;
+      }
+    };
+    int page = 0, page_prev = 0, h_prev = 0, tile_prev = 0;
+    if (N > 0) page = page_of(cur);
+    for (int i = 0; i <= N && ok; ++i) {
+      int h = 0, tile = 0, page_next = 0;
+      if (i < N) {
+        h = cur.hr / a.row_tiles;
+        tile = cur.tile;
+        cur.next(a);
+        if (i + 1 < N) page_next = page_of(cur);
+        load(&tmK, h, tile, page);
+      }
+      if (i > 0 && ok) load(&tmV, h_prev, tile_prev, page_prev);
+      h_prev = h;
+      tile_prev = tile;
+      page_prev = page;
+      page = page_next;
     }
-    if (++stage == C::kStages) stage = 0;
+    // the copies still in flight land before the CTA ends
+    for (int j = max(0, issued - C::kSlots); j < issued; ++j)
+      mbar_wait(&full[j % C::kSlots], (j / C::kSlots) & 1, a.t.err);
+  } else if (warp <= NS) {
+    // ---- a stream's MMAs ----
+    // The whole warp walks the loop and one elected lane issues: the descriptors are
+    // then warp-uniform, which the MMA's operands have to be (from a single lane's
+    // loop each MMA cost about 100 cycles of moves to uniform registers).
+    constexpr uint32_t id_qk = idesc_f16<E>(kLanes, kKeys, false);
+    constexpr uint32_t id_pv = idesc_f16<E>(kLanes, D, true);
+    const int st = __shfl_sync(kAll, warp, 0) - 1;
+    const uint32_t tb = __shfl_sync(kAll, tmem, 0) + st * C::kStreamCols;
+    const uint64_t ad = umma_desc_sw128(qs + st * C::kQ);
+    const uint64_t bd_qk = umma_desc_sw128(ring);
+    const uint64_t bd_pv = umma_desc_sw128_mn(ring, kBlkBytes);
+    const int n = __shfl_sync(kAll, N, 0);
+    int slot = 0, ph = 0;  // the ring's next slot in MMA order, and its phase
+    auto advance = [&]() {
+      if (++slot == C::kSlots) {
+        slot = 0;
+        ph ^= 1;
+      }
+    };
+    auto scores = [&](int i, int slot, int ph) {  // of tile i
+      if (i > 0 && !wait(&s_read[st], (i - 1) & 1, a.t.err)) return false;
+      if (!wait(&full[slot], ph, a.t.err)) return false;
+      __syncwarp();
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t bd = bd_qk + slot * (C::kSlot >> 4);
+#pragma unroll
+        for (int kb = 0; kb < kBlk; ++kb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_bf16(tb, ad + kb * (kLanes * 128 >> 4) + 2 * k, bd + kb * (kBlkBytes >> 4) + 2 * k,
+                      id_qk, kb > 0 || k > 0);
+        umma_commit(&s_full[st]);
+        umma_commit(&empty[slot]);
+      }
+      __syncwarp();
+      return true;
+    };
+    uint32_t edges = 0;
+    bool first_prev = false, edge_prev = false;  // of the tile whose output is next
+    auto output = [&](int i, int slot, int ph) {  // of tile i
+      const int odd = i & 1;
+      if (!wait(&full[slot], ph, a.t.err)) return false;
+      if (!wait(&p_ready[2 * st + odd], (i >> 1) & 1, a.t.err)) return false;
+      if (edge_prev) {  // stream 0's softmax cleans V; the others' products wait for it
+        edges += 4;
+        if (st > 0 && !wait_count_above(v_clean, edges - 1, a.t.err)) {
+          record_error(a.t.err, kDevErrAttn);
+          return false;
+        }
+      }
+      __syncwarp();
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t bd = bd_pv + slot * (C::kSlot >> 4);
+        const uint32_t pa = tb + kColP + odd * (kKeys / 2);
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)  // 16 keys: 8 TMEM columns, 2 KB of V
+          umma_f16_ts(tb + kColO, pa + 8 * k, bd + k * (2048 >> 4), id_pv, !first_prev || k > 0);
+        umma_commit(&pv_done[2 * st + odd]);
+        umma_commit(&empty[slot]);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = true;
+    int i = 0;
+    for (int seg = 0; i < n && ok; ++seg) {
+      const int tile_lo = cur.tile, tile_hi = min(cur.s.tiles, tile_lo + (n - i));
+      const int edge_from = cur.s.len / kKeys;
+      // A row tile's first scores need its Q, which comes once the last scores before
+      // it are done: the output of the tile before goes first.
+      const int k_slot = slot, k_ph = ph;
+      advance();
+      if (i > 0) {
+        ok = output(i - 1, slot, ph);
+        advance();
+      }
+      ok = ok && wait(&q_full[st], seg & 1, a.t.err) && scores(i, k_slot, k_ph);
+      ++i;
+      first_prev = true;
+      edge_prev = tile_lo >= edge_from;
+      for (int tile = tile_lo + 1; tile < tile_hi && ok; ++tile, ++i) {
+        ok = scores(i, slot, ph);
+        advance();
+        ok = ok && output(i - 1, slot, ph);
+        advance();
+        first_prev = false;
+        edge_prev = tile >= edge_from;
+      }
+      cur.to(a, tile_hi);
+    }
+    if (n > 0 && ok) output(n - 1, slot, ph);
+    // every MMA issued is complete before TMEM is freed
+    if (elect_one()) umma_commit(&all_done[st]);
+    mbar_wait(&all_done[st], 0, a.t.err);
+    __syncwarp();
+  } else if (N > 0) {
+    // ---- softmax: a thread to a row ----
+    const int stream = (tid - kFirst) / kLanes;
+    const int quarter = warp & 3;  // the TMEM lanes a warp may read: 32 (warp % 4) ..
+    const int row_l = quarter * 32 + lane;
+    const uint32_t tbase = tmem + stream * C::kStreamCols + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t to = tbase + kColO;
+    const int M = a.t.T * a.G;
+    const float sl = fmaxf(fabsf(a.scale_log2), 1e-37f);
+    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    // Q of the row tile at c, negated where the scale is negative
+    auto load_q = [&](const Cursor& c) {
+      const int h = c.hr / a.row_tiles;
+      const int r0 = (c.hr % a.row_tiles) * (NS * kLanes) + stream * kLanes;
+      const E* Q = static_cast<const E*>(a.q) + c.b * a.qb;
+      const int t = tid - kFirst - stream * kLanes;
+      constexpr int kCPR = D / 8;
+#pragma unroll 4
+      for (int x = t; x < kLanes * kCPR; x += kLanes) {
+        const int r = x / kCPR, cc = x % kCPR;
+        uint4 val = make_uint4(0, 0, 0, 0);
+        if (r0 + r < M) {
+          val = *reinterpret_cast<const uint4*>(Q + (r0 + r) / a.G * a.qt +
+                                                (h * a.G + (r0 + r) % a.G) * a.qh + cc * 8);
+          val.x ^= flip;
+          val.y ^= flip;
+          val.z ^= flip;
+          val.w ^= flip;
+        }
+        uint8_t* dst = qs + stream * C::kQ + (cc >> 3) * (kLanes * 128) + r * 128 +
+                       (((cc & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(dst) = val;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[stream]);
+    };
+    load_q(cur);
 
-    // ---- the end of this CTA's part of the row tile ----
-    const bool last = cur.tile + 1 == s.tiles;
-    if (last || cur.u + 1 == u1) {
-      const bool whole = last && tile_lo == 0;
-      const int slot = tile_lo == 0 && !whole && cur.u + 1 == u1 &&
-                               cur.u - cur.tile > u0 ? 1 : 0;
-      const int tile_hi = cur.tile + 1;
-      if (cur.u + 1 == u1 && tid == 0) {
-        Cursor at = cur;
-        at.u -= cur.tile;  // the row tile's first unit
-        a.cuts[blockIdx.x] = make_cut(g, at, tile_lo, tile_hi, slot);
-      }
+    bool ok = true;
+    int i = 0;  // tile of this CTA's range
+    for (int seg = 0; i < N && ok; ++seg) {
+      // this CTA's part [tile_lo, tile_hi) of a row tile
+      const Cursor at = cur;
+      const Seq s = at.s;
+      const int tile_lo = at.tile, tile_hi = min(s.tiles, tile_lo + (N - i));
+      const int h = at.hr / a.row_tiles;
+      const int r0 = (at.hr - h * a.row_tiles) * (NS * kLanes) + stream * kLanes;
+      const bool live = r0 + quarter * 32 < M;  // a warp without rows only keeps in step
+      const int r = r0 + row_l, node = r / a.G;
+      float m = -INFINITY, l = 0.f;
+
+      // One tile.  kEdge: it has nodes, or positions past the end.
+      auto tile_step = [&](auto edge_tag, int tile) {
+        constexpr bool kEdge = decltype(edge_tag)::value;
+        const int p0 = tile * kKeys;
+        const int odd = i & 1, turn = (i >> 1) & 1;
+        if (!wait(&s_full[stream], odd, a.t.err)) return false;
+        // tile i - 2's weights leave their buffer to tile i's (long since)
+        if (i >= 2 && !wait(&pv_done[2 * stream + odd], turn ^ 1, a.t.err)) return false;
+        __syncwarp();
+        tc_fence_after();
+        if (!live) {
+          if (lane == 0) mbar_arrive(&s_read[stream]);
+        } else {
+          uint32_t x[64];
+          tmem_ld32_issue(tbase, x);
+          tmem_ld32_issue(tbase + 32, x + 32);
+          tmem_ld32_wait(x);
+          tmem_ld32_wait(x + 32);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_read[stream]);
+          if (kEdge) {
+            const uint64_t vis = r < M ? seen64(a, at.b, s, node, p0) : 0;
 #pragma unroll
-      for (int i = 0; i < kMT; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          l[i][e] += __shfl_xor_sync(kAll, l[i][e], 1);
-          l[i][e] += __shfl_xor_sync(kAll, l[i][e], 2);
-          if ((lane & 3) == 0)
-            ml_s[warp * kRows + i * 16 + e * 8 + (lane >> 2)] = make_float2(m[i][e], l[i][e]);
-        }
-      if (lane == 0) bad_s[warp] = bad;
-      __syncthreads();
-      const bool any_bad = bad_s[0] | bad_s[1] | bad_s[2] | bad_s[3];
-      // this warp's factor to the common maximum
-      float f[kMT][2];
-#pragma unroll
-      for (int i = 0; i < kMT; ++i)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = i * 16 + e * 8 + (lane >> 2);
-          float mm = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml_s[w * kRows + r].x);
-          f[i][e] = ex2(m[i][e] - (mm == -INFINITY ? 0.f : mm));
-        }
-#pragma unroll
-      for (int c0 = 0; c0 < D; c0 += C::kJoin) {
-        for (int w = 0; w < 4; ++w) {  // the four warps' outputs, in their order
-          if (warp == w) {
-#pragma unroll
-            for (int i = 0; i < kMT; ++i)
-#pragma unroll
-              for (int j = 0; j < C::kJoin / 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float2* at = reinterpret_cast<float2*>(
-                      join + (i * 16 + e * 8 + (lane >> 2)) * C::kJoin + j * 8 + (lane & 3) * 2);
-                  float2 x = make_float2(o[i][c0 / 8 + j][2 * e] * f[i][e],
-                                         o[i][c0 / 8 + j][2 * e + 1] * f[i][e]);
-                  if (w) {
-                    const float2 y = *at;
-                    x.x += y.x;
-                    x.y += y.y;
-                  }
-                  *at = x;
-                }
+            for (int c = 0; c < 64; ++c)
+              if (!(vis >> c & 1)) x[c] = 0xFF800000u;  // -inf
           }
-          __syncthreads();
-        }
-        for (int x = tid; x < rows * (C::kJoin / 4); x += kWThreads) {
-          const int r = x / (C::kJoin / 4), c = c0 + x % (C::kJoin / 4) * 4;
-          float mm = -INFINITY, ll = 0.f;
+          float mx[4];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) mm = fmaxf(mm, ml_s[w * kRows + r].x);
-          const float safe = mm == -INFINITY ? 0.f : mm;
+          for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(x[c]);
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            ll += ml_s[w * kRows + r].y * ex2(ml_s[w * kRows + r].x - safe);
-          float4 y = *reinterpret_cast<const float4*>(join + r * C::kJoin + (c - c0));
-          const int node = (r0 + r) / a.G, head = h * a.G + (r0 + r) % a.G;
-          if (any_bad) {
-            float* yy = reinterpret_cast<float*>(&y);
+          for (int c = 4; c < 60; c += 8)
+#pragma unroll
             for (int z = 0; z < 4; ++z)
-              yy[z] += unseen_safe_sum<E>(a, cur.b, s, h, node, c + z, tile_lo * kKeys,
-                                          tile_hi * kKeys);
-          }
-          if (whole) {
-            if (node < s.n) {
-              const float inv = ll == 0.f ? 0.f : 1.f / ll;
-              E* out = static_cast<E*>(a.out) + cur.b * a.ob + node * a.ot + head * a.oh + c;
-              *reinterpret_cast<uint2*>(out) = make_uint2(pack2<E>(y.x * inv, y.y * inv),
-                                                          pack2<E>(y.z * inv, y.w * inv));
-              if (a.lse && c == 0)
-                a.lse[(static_cast<int64_t>(cur.b) * a.t.T + node) * (a.H * a.G) + head] =
-                    safe * kLn2 + logf(ll);
+              mx[z] = max3(mx[z], __uint_as_float(x[c + z]), __uint_as_float(x[c + 4 + z]));
+          const float top =
+              max3(max3(mx[0], __uint_as_float(x[60]), __uint_as_float(x[61])),
+                   max3(mx[1], __uint_as_float(x[62]), __uint_as_float(x[63])),
+                   fmaxf(mx[2], mx[3])) * sl;
+          if (tile == tile_lo) {
+            m = top;
+          } else if (__any_sync(kAll, top > m + kRise)) {  // (m = -inf: anything above)
+            if (!wait(&pv_done[2 * stream + (odd ^ 1)], ((i - 1) >> 1) & 1, a.t.err)) return false;
+            __syncwarp();
+            tc_fence_after();
+            const float mn = top > m + kRise ? top : m;
+            const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+            l *= f;
+            m = mn;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32_issue(to + c, o);
+              tmem_ld32_wait(o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(to + c, o);
             }
-          } else {
-            const int64_t p = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * kRows + r;
-            *reinterpret_cast<float4*>(a.part_o + p * D + c) = y;
-            if (c == 0) a.part_ml[p] = make_float2(mm, ll);
           }
+          const float safe = m == -INFINITY ? 0.f : m;
+          const uint64_t sl2 = pack_f32x2(sl, sl), off2 = pack_f32x2(-safe, -safe);
+          uint64_t sum[2] = {0, 0};
+          uint32_t p[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const uint64_t y2 = fma_f32x2(pack_u32x2(x[2 * c], x[2 * c + 1]), sl2, off2);
+            float y, z;
+            unpack_f32x2(y2, y, z);
+            y = ex2(y);
+            z = ex2(z);
+            sum[c & 1] = add_f32x2(sum[c & 1], pack_f32x2(y, z));
+            p[c] = pack2<E>(y, z);
+          }
+          float s0, s1;
+          unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+          tmem_st32(tbase + kColP + odd * (kKeys / 2), p);
+          tmem_st_wait();
         }
-        __syncthreads();
+        if (kEdge && stream == 0) {
+          // V's rows past the end are zeroed and Inf and NaN of nodes set aside
+          // (unseen_safe_sum): a weight of 0 would not keep them out of the product
+          const int sq = seq_v(i), slot = sq % C::kSlots;
+          if (!wait(&full[slot], (sq / C::kSlots) & 1, a.t.err)) return false;
+          bool found = false;
+          const int end = s.len + s.n;
+          for (int x = tid - kFirst; x < C::kSlot / 16; x += kLanes) {
+            const int pos = p0 + (x & 511) / 8;  // 512 pieces to a 64-channel block
+            if (pos < s.len) continue;
+            uint4* v = reinterpret_cast<uint4*>(ring + slot * C::kSlot) + x;
+            uint4 y = make_uint4(0, 0, 0, 0);
+            if (pos < end) {
+              y = *v;
+              bool bad = false;
+              y.x = finite2<E>(y.x, bad);
+              y.y = finite2<E>(y.y, bad);
+              y.z = finite2<E>(y.z, bad);
+              y.w = finite2<E>(y.w, bad);
+              found |= bad;
+              if (!bad) continue;
+            }
+            *v = y;
+          }
+          if (found) bad_seg[seg & 3] = seg;
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&p_ready[2 * stream + odd]);
+          if (kEdge && stream == 0 && NS > 1) add_release_cta(v_clean, 1);
+        }
+        ++i;
+        return true;
+      };
+      const int plain_hi = max(tile_lo, min(tile_hi, s.len / kKeys));
+      int tile = tile_lo;
+      for (; tile < plain_hi && ok; ++tile) ok = tile_step(std::false_type{}, tile);
+      for (; tile < tile_hi && ok; ++tile) ok = tile_step(std::true_type{}, tile);
+      if (!ok) break;
+
+      // ---- the end of this CTA's part of the row tile ----
+      cur.to(a, tile_hi);
+      if (i < N) load_q(cur);  // every product with the old Q is complete (s_full)
+      if (!wait(&pv_done[2 * stream + ((i - 1) & 1)], ((i - 1) >> 1) & 1, a.t.err)) break;
+      __syncwarp();
+      tc_fence_after();
+      const bool whole = tile_hi == s.tiles && tile_lo == 0;
+      const int slot = tile_lo == 0 && !whole && at.u > u0 ? 1 : 0;
+      if (!whole && tid == kFirst)
+        a.cuts[2 * blockIdx.x + (tile_lo == 0)] =
+            make_cut(g, at.u - tile_lo, at.b, at.hr, s.tiles);
+      if (live) {
+        const int head = h * a.G + r - node * a.G;
+        const bool bad = *reinterpret_cast<volatile int*>(&bad_seg[seg & 3]) == seg;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * (NS * kLanes) +
+                             stream * kLanes + row_l;
+        E* out = static_cast<E*>(a.out) + at.b * a.ob + node * a.ot + head * a.oh;
+        const bool mine = r < M && node < s.n;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32_issue(to + c, o);
+          tmem_ld32_wait(o);
+          if (bad && mine)
+            for (int j = 0; j < 32; ++j) {
+              const float y = unseen_safe_sum<E>(a, at.b, s, h, node, c + j, tile_lo * kKeys,
+                                                 tile_hi * kKeys);
+              // (an index known at compile time keeps o in registers)
+#pragma unroll
+              for (int z = 0; z < 32; ++z)
+                if (z == j) o[z] = __float_as_uint(__uint_as_float(o[z]) + y);
+            }
+          if (mine && whole) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint4 y;
+              uint32_t* yy = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                yy[z] = pack2<E>(__uint_as_float(o[8 * j + 2 * z]) * inv,
+                                 __uint_as_float(o[8 * j + 2 * z + 1]) * inv);
+              *reinterpret_cast<uint4*>(out + c + 8 * j) = y;
+            }
+          } else if (mine) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(a.part_o + part * D + c + 4 * j) =
+                  make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+          __syncwarp();  // the next load is the whole warp's
+        }
+        if (mine && !whole) a.part_ml[part] = make_float2(m, l);
+        if (mine && whole && a.lse)
+          a.lse[(static_cast<int64_t>(at.b) * a.t.T + node) * (a.H * a.G) + head] =
+              (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
       }
-      fresh = true;
+      tc_fence_before();  // O is read before the next row tile's first product
     }
-    cur.next(a);
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, NS * C::kStreamCols);
 }
 
-// The parts that the CTAs left of a row tile, added in the order of the keys, a warp
-// to a row: block column c takes the row tile that CTA c began and did not end (its
-// Cut), block rows divide the tile's rows, and the last B block columns zero what
-// lies past a sequence's count.
+// The parts that the CTAs left of a row tile, added in the order of the keys.  The
+// P CTAs that have parts of a row tile lend it P block columns of kCombineY blocks,
+// so the more parts there are to add, the more blocks add them: each takes some of
+// the rows, one to a warp while the parts are few, several warps to a row where they
+// are many.  The last B block columns zero what lies past a sequence's count.
 // (A warp to every output row, looking up whether it was cut, took 76 us after the
-// 1.28 ms of 32 sequences of 64 nodes: most rows are whole.)
-constexpr int kCombineWarps = 8;
+// 1.28 ms of 32 sequences of 64 nodes; most rows are whole.)
+constexpr int kCombineWarps = 8, kCombineY = 4;
 template <typename E, int D>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     combine_kernel(const __grid_constant__ AttnArgs a) {
+  constexpr int kPer = D / 32;  // channels per lane
+  __shared__ float y_s[kCombineWarps][D];
+  __shared__ float l_s[kCombineWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int Hq = a.H * a.G;
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kPer = D / 32;  // channels per lane
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int step = gridDim.y * kCombineWarps;
-  const int Hq = a.H * a.G;
-  if (static_cast<int>(blockIdx.x) >= a.grid) {
-    const int b = blockIdx.x - a.grid;
-    for (int x = load_seq(a, b).n * Hq + blockIdx.y * kCombineWarps + warp; x < a.t.T * Hq;
-         x += step) {
+  if (static_cast<int>(blockIdx.x) >= 2 * a.grid) {
+    const int b = blockIdx.x - 2 * a.grid;
+    const int done = load_seq(a, b).n * Hq;
+    for (int x = done + blockIdx.y * kCombineWarps + warp; x < a.t.T * Hq;
+         x += kCombineY * kCombineWarps) {
       const int node = x / Hq, head = x - node * Hq;
       uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<E*>(a.out) + b * a.ob + node * a.ot +
                                                   head * a.oh + lane * kPer);
@@ -426,100 +739,162 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   }
   const Cut cut = a.cuts[blockIdx.x];
   if (cut.b < 0) return;
-  const int b = cut.b, c0 = blockIdx.x, c1 = cut.last_cta, slot0 = cut.slot;
+  const int b = cut.b, c0 = cut.c0, c1 = cut.c1_slot >> 1, slot0 = cut.c1_slot & 1;
+  const int parts = c1 - c0 + 1;
   const int h = cut.hr / a.row_tiles, r0 = (cut.hr - h * a.row_tiles) * a.rows;
-  const int n = load_seq(a, b).n;
-  const int rows = min(a.rows, n * a.G - r0);  // (rows past the count are zeroed above)
-  for (int r = blockIdx.y * kCombineWarps + warp; r < rows; r += step) {
-    auto part = [&](int c) {
+  const int rows = min(a.rows, load_seq(a, b).n * a.G - r0);  // (past the count: zeroed above)
+  // warps to a row: about four parts each
+  const int wide = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;
+  const int per_block = kCombineWarps / wide, sub = warp / wide, part0 = warp % wide;
+  const int id = (static_cast<int>(blockIdx.x) / 2 - c0) * kCombineY + blockIdx.y;
+  for (int rb = id * per_block; rb < rows; rb += parts * kCombineY * per_block) {
+    const int r = rb + sub;
+    auto at = [&](int c) {
       return (static_cast<int64_t>(c) * 2 + (c == c0 ? slot0 : 0)) * a.rows + r;
     };
-    float mm = -INFINITY;
-    for (int c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, a.part_ml[part(c)].x);
-#pragma unroll
-    for (int off = 16; off; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kAll, mm, off));
-    const float safe = mm == -INFINITY ? 0.f : mm;
-    float y[kPer];
+    float safe = 0.f, ll = 0.f, y[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) y[i] = 0.f;
-    float ll = 0.f;
-#pragma unroll 8
-    for (int c = c0; c <= c1; ++c) {
-      const float2 ml = a.part_ml[part(c)];
-      const float w = ex2(ml.x - safe);
-      const float* p = a.part_o + part(c) * D + lane * kPer;
-      ll += ml.y * w;
+    if (r < rows) {
+      float mm = -INFINITY;
+      for (int c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, a.part_ml[at(c)].x);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) y[i] += p[i] * w;
+      for (int off = 16; off; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kAll, mm, off));
+      safe = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 4
+      for (int c = c0 + part0; c <= c1; c += wide) {
+        const float2 ml = a.part_ml[at(c)];
+        const float w = ex2(ml.x - safe);
+        const float* p = a.part_o + at(c) * D + lane * kPer;
+        ll += ml.y * w;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) y[i] += p[i] * w;
+      }
     }
-    const float inv = ll == 0.f ? 0.f : 1.f / ll;
-    const int node = (r0 + r) / a.G, head = h * a.G + (r0 + r) - node * a.G;
-    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<E*>(a.out) + b * a.ob + node * a.ot +
-                                                head * a.oh + lane * kPer);
+    if (wide > 1) {
 #pragma unroll
-    for (int i = 0; i < kPer / 2; ++i) out[i] = pack2<E>(y[2 * i] * inv, y[2 * i + 1] * inv);
-    if (a.lse && lane == 0)  // log 0 = -inf: nothing seen
-      a.lse[(static_cast<int64_t>(b) * a.t.T + node) * Hq + head] = safe * kLn2 + logf(ll);
+      for (int i = 0; i < kPer; ++i) y_s[warp][lane * kPer + i] = y[i];
+      if (lane == 0) l_s[warp] = ll;
+      __syncthreads();
+      if (part0 == 0)
+        for (int w = warp + 1; w < warp + wide; ++w) {
+          ll += l_s[w];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) y[i] += y_s[w][lane * kPer + i];
+        }
+      __syncthreads();
+    }
+    if (r < rows && part0 == 0) {
+      const float inv = ll == 0.f ? 0.f : 1.f / ll;
+      const int node = (r0 + r) / a.G, head = h * a.G + (r0 + r) - node * a.G;
+      uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<E*>(a.out) + b * a.ob + node * a.ot +
+                                                  head * a.oh + lane * kPer);
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i) out[i] = pack2<E>(y[2 * i] * inv, y[2 * i + 1] * inv);
+      if (a.lse && lane == 0)  // log 0 = -inf: nothing seen
+        a.lse[(static_cast<int64_t>(b) * a.t.T + node) * Hq + head] = safe * kLn2 + logf(ll);
+    }
   }
+}
+
+// ---- host -------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static std::mutex mu;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!fn) {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }
+  return fn;
+}
+
+// One layer's K or V as [pages, heads, slots, D], the three outer dimensions in the
+// order of their strides, boxes of one page's rows x 64 channels.
+bool page_map(const dfl2_cache* c, const void* base, bool f16, const MapOrder& o, CUtensorMap* out) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = encoder();
+  if (!encode) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->head_dim)}, strides[3];
+  cuuint32_t box[4] = {64}, one[4] = {1, 1, 1, 1};
+  const int at[3] = {o.slot, o.head, o.page};
+  const int64_t size[3] = {c->page_size, c->kv_heads, c->pages};
+  const int64_t stride[3] = {c->slot_stride, c->head_stride, c->page_stride};
+  for (int d = 0; d < 3; ++d) {
+    dims[1 + at[d]] = static_cast<cuuint64_t>(size[d]);
+    // (the stride of a dimension of one entry is never used, but has to be one)
+    strides[at[d]] = static_cast<cuuint64_t>(size[d] > 1 ? stride[d] : c->head_dim) * 2;
+    box[1 + at[d]] = d == 0 ? std::min(c->page_size, kKeys) : 1;
+  }
+  return encode(out, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+MapOrder map_order(const dfl2_cache* c) {
+  const int64_t s = c->slot_stride, h = c->kv_heads > 1 ? c->head_stride : 0,
+                p = c->pages > 1 ? c->page_stride : INT64_MAX;
+  return MapOrder{(h < s) + (p < s), (s <= h) + (p < h), (s <= p) + (h <= p)};
 }
 
 // ---- plan ---------------------------------------------------------------------
 struct AttnPlan {
-  bool tc;    // the tensor-core kernel
-  int rows;   // rows of a row tile
+  int rows;  // rows of a row tile
   int row_tiles, grid;
   size_t o_off, ml_off, cut_off, ws_bytes;
 };
 
-// The warp-level kernel for a few rows (one 16-row MMA tile while they fit it, two
-// up to 32 rows, so that a key is loaded half as often), the tensor cores' 128-row
-// tiles above; 256 channels, and strides that no tensor map takes, stay with the
-// warp-level kernel.
-AttnPlan attn_plan(int M, int D, bool tc_takes, int sms) {
+// One stream's 128 rows while they are enough (or 256 channels leave room for no
+// second stream), two streams' 256 above: see the top of this file.
+AttnPlan attn_plan(int M, int D, int sms) {
   AttnPlan p;
-  p.tc = tc_takes && M > 16;
-  p.rows = p.tc ? attn_tc_rows(M) : M <= 16 || D == 256 ? 16 : 32;
+  p.rows = M <= kLanes || D == 256 ? kLanes : 2 * kLanes;
   p.row_tiles = (M + p.rows - 1) / p.rows;
-  p.grid = p.tc ? attn_tc_grid(p.rows, sms) : sms * (D == 256 ? 1 : 2);
+  p.grid = p.rows == kLanes && D < 256 ? 2 * sms : sms;
   p.o_off = 0;
   p.ml_off = align_up(size_t(p.grid) * 2 * p.rows * D * sizeof(float), 256);
   p.cut_off = p.ml_off + align_up(size_t(p.grid) * 2 * p.rows * sizeof(float2), 256);
-  p.ws_bytes = p.cut_off + align_up(size_t(p.grid) * sizeof(Cut), 256);
+  p.ws_bytes = p.cut_off + align_up(size_t(p.grid) * 2 * sizeof(Cut), 256);
   return p;
 }
 
-template <typename E, int D, int kRows>
-cudaError_t launch_warp(const AttnArgs& a, cudaStream_t s) {
-  auto kernel = attn_warp_kernel<E, D, kRows>;
-  constexpr size_t smem = WarpCfg<D, kRows>::kSmem;
+template <typename E, int D, int NS>
+cudaError_t launch_main(const AttnArgs& a, const CUtensorMap& k, const CUtensorMap& v,
+                        const MapOrder& o, cudaStream_t s) {
+  auto kernel = attn_kernel<E, D, NS>;
+  constexpr size_t smem = TcCfg<D, NS>::kSmem;
   const cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_k(kernel, dim3(a.grid), dim3(kWThreads), smem, s, true, a);
+  return launch_k(kernel, dim3(a.grid), dim3(TcCfg<D, NS>::kThreads), smem, s, true, a, k, v, o);
 }
 
 template <typename E, int D>
-cudaError_t launch_attn(const AttnArgs& a, const AttnPlan& p, const dfl2_cache* c,
-                        cudaStream_t s) {
+cudaError_t launch_attn(const AttnArgs& a, const dfl2_cache* c, cudaStream_t s) {
+  const MapOrder o = map_order(c);
+  alignas(64) CUtensorMap tk, tv;
+  const bool f16 = std::is_same_v<E, __half>;
+  if (!page_map(c, a.k, f16, o, &tk) || !page_map(c, a.v, f16, o, &tv))
+    return cudaErrorInvalidValue;
   cudaError_t e;
-  if (p.tc)
-    e = launch_attn_tc(a, c, s);
-  else if (D == 256 || p.rows == 16)
-    e = launch_warp<E, D, 16>(a, s);
+  if constexpr (D == 256)
+    e = launch_main<E, D, 1>(a, tk, tv, o, s);
   else
-    e = launch_warp<E, D, D == 256 ? 16 : 32>(a, s);
+    e = a.rows == kLanes ? launch_main<E, D, 1>(a, tk, tv, o, s)
+                         : launch_main<E, D, 2>(a, tk, tv, o, s);
   if (e != cudaSuccess) return e;
-  const int rows = std::min(a.rows, a.t.T * a.G);
-  return launch_k(combine_kernel<E, D>, dim3(a.grid + a.B, (rows + kCombineWarps - 1) / kCombineWarps),
-                  dim3(kCombineWarps * 32), 0, s, true, a);
+  return launch_k(combine_kernel<E, D>, dim3(2 * a.grid + a.B, kCombineY), dim3(kCombineWarps * 32),
+                  0, s, true, a);
 }
 
 template <typename E>
-cudaError_t launch_attn_d(const AttnArgs& a, const AttnPlan& p, const dfl2_cache* c,
-                          cudaStream_t s) {
-  return c->head_dim == 64    ? launch_attn<E, 64>(a, p, c, s)
-         : c->head_dim == 128 ? launch_attn<E, 128>(a, p, c, s)
-                              : launch_attn<E, 256>(a, p, c, s);
+cudaError_t launch_attn_d(const AttnArgs& a, const dfl2_cache* c, cudaStream_t s) {
+  return c->head_dim == 64    ? launch_attn<E, 64>(a, c, s)
+         : c->head_dim == 128 ? launch_attn<E, 128>(a, c, s)
+                              : launch_attn<E, 256>(a, c, s);
 }
 
 dfl2_status check_shapes(int B, int T, int q_heads, int kv_heads, int head_dim, int dtype) {
@@ -554,11 +929,7 @@ size_t dfl2_tree_attn_workspace_size(int B, int T, int q_heads, int kv_heads, in
                                      dfl2_dtype dtype) {
   if (dfl2::check_shapes(B, T, q_heads, kv_heads, head_dim, dtype) != DFL2_OK) return 0;
   if (dfl2::check_args_device(nullptr, 0) != DFL2_OK) return 0;
-  // (whichever kernel the cache's strides will allow)
-  const int M = T * (q_heads / kv_heads), sms = dfl2::device_info().sms;
-  const bool tc = head_dim != 256;
-  return std::max(dfl2::attn_plan(M, head_dim, false, sms).ws_bytes,
-                  dfl2::attn_plan(M, head_dim, tc, sms).ws_bytes);
+  return dfl2::attn_plan(T * (q_heads / kv_heads), head_dim, dfl2::device_info().sms).ws_bytes;
 }
 
 dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_cache* cache,
@@ -576,16 +947,25 @@ dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_c
     return dfl2::report_errorf(DFL2_ERR_INVALID_ARG, "layer %d of %d", layer, cache->layers);
   if (!q_strides || !out_strides)
     return dfl2::report_errorf(DFL2_ERR_INVALID_ARG, "q_strides and out_strides are needed");
+  const int dims[3] = {B, T, q_heads};
   for (int i = 0; i < 3; ++i)
-    if (q_strides[i] < 0 || q_strides[i] % 8 || out_strides[i] < 0 || out_strides[i] % 8)
+    if (dims[i] > 1 &&
+        (q_strides[i] < 0 || q_strides[i] % 8 || out_strides[i] < 0 || out_strides[i] % 8))
       return dfl2::report_errorf(DFL2_ERR_INVALID_ARG,
                                  "strides of q and out: non-negative multiples of 8");
+  // a tensor map's strides are positive and under 2^40 bytes
+  const int64_t most = int64_t(1) << 38;
+  if (cache->slot_stride < 1 || cache->slot_stride > most ||
+      (cache->kv_heads > 1 && (cache->head_stride < 1 || cache->head_stride > most)) ||
+      (cache->pages > 1 && (cache->page_stride < 1 || cache->page_stride > most)))
+    return dfl2::report_errorf(DFL2_ERR_UNSUPPORTED,
+                               "the attention needs cache strides of 1 .. 2^38 elements");
   if (!std::isfinite(scale))
     return dfl2::report_errorf(DFL2_ERR_INVALID_ARG, "scale %g must be finite", double(scale));
   DFL2_TRY(dfl2::check_args_device(ptrs, 7));
   DFL2_TRY(dfl2::check_cache_device(cache));
   const int G = q_heads / cache->kv_heads, D = cache->head_dim;
-  const dfl2::AttnPlan p = dfl2::attn_plan(T * G, D, dfl2::attn_tc_takes(cache), dfl2::device_info().sms);
+  const dfl2::AttnPlan p = dfl2::attn_plan(T * G, D, dfl2::device_info().sms);
   if (!ws || ws_bytes < p.ws_bytes)
     return dfl2::report_errorf(DFL2_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed",
                                ws ? ws_bytes : size_t(0), p.ws_bytes);
@@ -624,8 +1004,8 @@ dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_c
   a.row_tiles = p.row_tiles;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = cache->dtype == DFL2_F16
-                            ? dfl2::launch_attn_d<__half>(a, p, cache, s)
-                            : dfl2::launch_attn_d<__nv_bfloat16>(a, p, cache, s);
+                            ? dfl2::launch_attn_d<__half>(a, cache, s)
+                            : dfl2::launch_attn_d<__nv_bfloat16>(a, cache, s);
   return e == cudaSuccess ? DFL2_OK : dfl2::report_cuda_error(e, "tree attention launch");
 }
 

@@ -1,5 +1,5 @@
-// What the two attention kernels share: their arguments, the division of the work
-// into units, what a node sees, and small conversions.  Not public.
+// The attention kernels' arguments, the division of their work into units, what a
+// node sees, and small conversions.  Not public.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -17,17 +17,18 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxLen = 1 << 30;
-constexpr int kKeys = 64;  // keys of a tile, in both kernels
+constexpr int kKeys = 64;  // keys of a tile
 
 }  // namespace
 
-// Left by each CTA for combine_kernel: the row tile that its range begins but does
-// not end, if there is one (b < 0: none).
+// A row tile that several CTAs have parts of, as each of them leaves it for
+// combine_kernel (b < 0: none): the CTAs c0 .. c1, in the order of the keys, and
+// which of its two places CTA c0's part is in (the others': the first).
 struct alignas(16) Cut {
-  int b, hr;
-  int last_cta;  // the parts are this CTA's and those of the CTAs up to last_cta
-  int slot;      // which of its two places this CTA's part is in
+  int b, hr, c0;
+  int c1_slot;  // c1 * 2 + slot
 };
+
 struct AttnArgs {
   TableView t;
   const void* q;
@@ -44,7 +45,7 @@ struct AttnArgs {
   float* lse;      // nullable
   float* part_o;   // [grid][2][rows][D] unnormalised outputs
   float2* part_ml; // [grid][2][rows] (maximum, sum)
-  Cut* cuts;       // [grid]
+  Cut* cuts;       // [grid][2]: of the row tiles a CTA's range goes on with, and begins
   int grid;        // CTAs of the main kernel
   int rows;        // rows of a row tile
   int row_tiles;   // ceil(T G / rows)
@@ -86,6 +87,12 @@ struct Cursor {
   int64_t u;
   int b, hr, tile;  // sequence, key head * row_tiles + row tile, tile
   Seq s;
+  // On to tile `hi` of this row tile, or, where that is its end, to the next one.
+  __device__ __forceinline__ void to(const AttnArgs& a, int hi) {
+    u += hi - 1 - tile;
+    tile = hi - 1;
+    next(a);
+  }
   __device__ __forceinline__ void next(const AttnArgs& a) {
     ++u;
     if (++tile < s.tiles) return;
@@ -162,12 +169,10 @@ __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
   }
 }
 
-__device__ __forceinline__ Cut make_cut(const Range& g, const Cursor& at, int tile_lo, int tile_hi,
-                                        int slot) {
-  Cut c{-1, 0, 0, 0};
-  if (tile_lo == 0 && tile_hi < at.s.tiles)
-    c = Cut{at.b, at.hr, range_of(g.units, g.n_cta, at.u + at.s.tiles - 1), slot};
-  return c;
+// Of the row tile whose first unit is v0.
+__device__ __forceinline__ Cut make_cut(const Range& g, int64_t v0, int b, int hr, int tiles) {
+  const int c0 = range_of(g.units, g.n_cta, v0), c1 = range_of(g.units, g.n_cta, v0 + tiles - 1);
+  return Cut{b, hr, c0, c1 * 2 + (range_start(g.units, g.n_cta, c0) < v0 ? 1 : 0)};
 }
 
 template <typename E>
@@ -233,12 +238,5 @@ __device__ __noinline__ float unseen_safe_sum(const AttnArgs& a, int b, const Se
 }
 
 }  // namespace
-
-// The tensor-core kernel (tree_attn_tc.cu): whether it takes this cache, its row
-// tile for M rows, its CTAs and its launch (without the combination of the parts).
-bool attn_tc_takes(const dfl2_cache* c);
-int attn_tc_rows(int M);
-int attn_tc_grid(int rows, int sms);
-cudaError_t launch_attn_tc(const AttnArgs& a, const dfl2_cache* c, cudaStream_t s);
 
 }  // namespace dfl2
