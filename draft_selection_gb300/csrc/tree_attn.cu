@@ -10,12 +10,16 @@
 // work is two matrix products around an exponential.
 //
 // Split.  Lengths live on the device and differ by sequence, so the host
-// cannot cut the work.  A unit is one tile of keys of one (sequence, key head,
-// row tile); every CTA takes an equal, contiguous range of the units, whatever
-// sequences it spans.  A CTA that covers all tiles of a row tile writes its
-// output; one that covers a part writes its running maximum, sum and
-// unnormalised output to the workspace (a range has at most two such ends), and
-// combine_kernel adds the parts in the order of the keys.
+// cannot cut the work.  A unit is one tile of keys of one sequence and key head;
+// the units are cut into equal, contiguous ranges, whatever sequences they span, as
+// many as the GPU holds CTAs, or where the M rows need several row tiles, as many
+// as it holds groups of one CTA for each row tile: the CTAs of a group walk the
+// same keys side by side, so that HBM is read once and L2 serves the rest (with
+// each row tile a range of its own, 32 sequences of 16 to 32 thousand positions and
+// 512 rows read their keys twice: 1.37 ms instead of REPLACE2).  A CTA that covers
+// all tiles of a head writes its output; one that covers a part writes its running
+// maximum, sum and unnormalised output to the workspace (a range has at most two
+// such ends), and combine_kernel adds the parts in the order of the keys.
 //
 // Softmax in one pass: with the running maximum m and sum l of a row, a tile
 // with row maximum m' multiplies l and o by 2^(m - m') before adding its own
@@ -294,7 +298,8 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
   pdl_launch_dependents();
 
   // this CTA's range of units, and where it begins (each warp for itself)
-  const Range g = find_range(a, blockIdx.x);
+  const int range = blockIdx.x / a.row_tiles, row_tile = blockIdx.x - range * a.row_tiles;
+  const Range g = find_range(a, range);
   const int64_t u0 = g.u0;
   Cursor cur = g.first;
   int N = static_cast<int>(g.u1 - u0);
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
     for (int i = 0; i <= N && ok; ++i) {
       int h = 0, tile = 0, page_next = 0;
       if (i < N) {
-        h = cur.hr / a.row_tiles;
+        h = cur.h;
         tile = cur.tile;
         cur.next(a);
         if (i + 1 < N) page_next = page_of(cur);
@@ -473,12 +478,14 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
     const uint32_t tbase = tmem + stream * C::kStreamCols + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t to = tbase + kColO;
     const int M = a.t.T * a.G;
+    const int r0 = row_tile * (NS * kLanes) + stream * kLanes;
+    const bool live = r0 + quarter * 32 < M;  // a warp without rows only keeps in step
+    const int r = r0 + row_l, node = r / a.G;
     const float sl = fmaxf(fabsf(a.scale_log2), 1e-37f);
     const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
     // Q of the row tile at c, negated where the scale is negative
     auto load_q = [&](const Cursor& c) {
-      const int h = c.hr / a.row_tiles;
-      const int r0 = (c.hr % a.row_tiles) * (NS * kLanes) + stream * kLanes;
+      const int h = c.h;
       const E* Q = static_cast<const E*>(a.q) + c.b * a.qb;
       const int t = tid - kFirst - stream * kLanes;
       constexpr int kCPR = D / 8;
@@ -511,10 +518,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
       const Cursor at = cur;
       const Seq s = at.s;
       const int tile_lo = at.tile, tile_hi = min(s.tiles, tile_lo + (N - i));
-      const int h = at.hr / a.row_tiles;
-      const int r0 = (at.hr - h * a.row_tiles) * (NS * kLanes) + stream * kLanes;
-      const bool live = r0 + quarter * 32 < M;  // a warp without rows only keeps in step
-      const int r = r0 + row_l, node = r / a.G;
+      const int h = at.h;
       float m = -INFINITY, l = 0.f;
 
       // One tile.  kEdge: it has nodes, or positions past the end.
@@ -648,7 +652,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
       const int slot = tile_lo == 0 && !whole && at.u > u0 ? 1 : 0;
       if (!whole && tid == kFirst)
         a.cuts[2 * blockIdx.x + (tile_lo == 0)] =
-            make_cut(g, at.u - tile_lo, at.b, at.hr, s.tiles);
+            make_cut(g, at.u - tile_lo, at.b, h, s.tiles);
       if (live) {
         const int head = h * a.G + r - node * a.G;
         const bool bad = *reinterpret_cast<volatile int*>(&bad_seg[seg & 3]) == seg;
@@ -705,7 +709,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
 }
 
 // The parts that the CTAs left of a row tile, added in the order of the keys.  The
-// P CTAs that have parts of a row tile lend it P block columns of kCombineY blocks,
+// P ranges that have parts of it lend it P block columns of kCombineY blocks,
 // so the more parts there are to add, the more blocks add them: each takes some of
 // the rows, one to a warp while the parts are few, several warps to a row where they
 // are many.  The last B block columns zero what lies past a sequence's count.
@@ -722,8 +726,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   const int Hq = a.H * a.G;
   pdl_wait();
   pdl_launch_dependents();
-  if (static_cast<int>(blockIdx.x) >= 2 * a.grid) {
-    const int b = blockIdx.x - 2 * a.grid;
+  const int ctas = a.grid * a.row_tiles;
+  if (static_cast<int>(blockIdx.x) >= 2 * ctas) {
+    const int b = blockIdx.x - 2 * ctas;
     const int done = load_seq(a, b).n * Hq;
     for (int x = done + blockIdx.y * kCombineWarps + warp; x < a.t.T * Hq;
          x += kCombineY * kCombineWarps) {
@@ -741,16 +746,18 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   if (cut.b < 0) return;
   const int b = cut.b, c0 = cut.c0, c1 = cut.c1_slot >> 1, slot0 = cut.c1_slot & 1;
   const int parts = c1 - c0 + 1;
-  const int h = cut.hr / a.row_tiles, r0 = (cut.hr - h * a.row_tiles) * a.rows;
+  const int range = blockIdx.x / 2 / a.row_tiles, row_tile = blockIdx.x / 2 - range * a.row_tiles;
+  const int h = cut.h, r0 = row_tile * a.rows;
   const int rows = min(a.rows, load_seq(a, b).n * a.G - r0);  // (past the count: zeroed above)
   // warps to a row: about four parts each
   const int wide = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;
   const int per_block = kCombineWarps / wide, sub = warp / wide, part0 = warp % wide;
-  const int id = (static_cast<int>(blockIdx.x) / 2 - c0) * kCombineY + blockIdx.y;
+  const int id = (range - c0) * kCombineY + blockIdx.y;
   for (int rb = id * per_block; rb < rows; rb += parts * kCombineY * per_block) {
     const int r = rb + sub;
     auto at = [&](int c) {
-      return (static_cast<int64_t>(c) * 2 + (c == c0 ? slot0 : 0)) * a.rows + r;
+      return ((static_cast<int64_t>(c) * a.row_tiles + row_tile) * 2 + (c == c0 ? slot0 : 0)) * a.rows +
+             r;
     };
     float safe = 0.f, ll = 0.f, y[kPer];
 #pragma unroll
@@ -853,11 +860,13 @@ AttnPlan attn_plan(int M, int D, int sms) {
   AttnPlan p;
   p.rows = M <= kLanes || D == 256 ? kLanes : 2 * kLanes;
   p.row_tiles = (M + p.rows - 1) / p.rows;
-  p.grid = p.rows == kLanes && D < 256 ? 2 * sms : sms;
+  p.grid = std::max(1, (p.rows == kLanes && D < 256 ? 2 * sms : sms) / p.row_tiles);
+  const size_t ctas = size_t(p.grid) * p.row_tiles;
+  const size_t parts = p.grid > 1 ? ctas * 2 : 0;  // one range cuts nothing
   p.o_off = 0;
-  p.ml_off = align_up(size_t(p.grid) * 2 * p.rows * D * sizeof(float), 256);
-  p.cut_off = p.ml_off + align_up(size_t(p.grid) * 2 * p.rows * sizeof(float2), 256);
-  p.ws_bytes = p.cut_off + align_up(size_t(p.grid) * 2 * sizeof(Cut), 256);
+  p.ml_off = align_up(parts * p.rows * D * sizeof(float), 256);
+  p.cut_off = p.ml_off + align_up(parts * p.rows * sizeof(float2), 256);
+  p.ws_bytes = p.cut_off + align_up(ctas * 2 * sizeof(Cut), 256);
   return p;
 }
 
@@ -869,7 +878,7 @@ cudaError_t launch_main(const AttnArgs& a, const CUtensorMap& k, const CUtensorM
   const cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_k(kernel, dim3(a.grid), dim3(TcCfg<D, NS>::kThreads), smem, s, true, a, k, v, o);
+  return launch_k(kernel, dim3(a.grid * a.row_tiles), dim3(TcCfg<D, NS>::kThreads), smem, s, true, a, k, v, o);
 }
 
 template <typename E, int D>
@@ -886,7 +895,7 @@ cudaError_t launch_attn(const AttnArgs& a, const dfl2_cache* c, cudaStream_t s) 
     e = a.rows == kLanes ? launch_main<E, D, 1>(a, tk, tv, o, s)
                          : launch_main<E, D, 2>(a, tk, tv, o, s);
   if (e != cudaSuccess) return e;
-  return launch_k(combine_kernel<E, D>, dim3(2 * a.grid + a.B, kCombineY), dim3(kCombineWarps * 32),
+  return launch_k(combine_kernel<E, D>, dim3(2 * a.grid * a.row_tiles + a.B, kCombineY), dim3(kCombineWarps * 32),
                   0, s, true, a);
 }
 

@@ -21,11 +21,11 @@ constexpr int kKeys = 64;  // keys of a tile
 
 }  // namespace
 
-// A row tile that several CTAs have parts of, as each of them leaves it for
-// combine_kernel (b < 0: none): the CTAs c0 .. c1, in the order of the keys, and
-// which of its two places CTA c0's part is in (the others': the first).
+// The keys of a sequence and head that several ranges have parts of, as each CTA
+// leaves it for combine_kernel (b < 0: none): the ranges c0 .. c1, in the order of
+// the keys, and which of its two places c0's part is in (the others': the first).
 struct alignas(16) Cut {
-  int b, hr, c0;
+  int b, h, c0;
   int c1_slot;  // c1 * 2 + slot
 };
 
@@ -43,10 +43,10 @@ struct AttnArgs {
   void* out;
   int64_t ob, ot, oh;
   float* lse;      // nullable
-  float* part_o;   // [grid][2][rows][D] unnormalised outputs
-  float2* part_ml; // [grid][2][rows] (maximum, sum)
-  Cut* cuts;       // [grid][2]: of the row tiles a CTA's range goes on with, and begins
-  int grid;        // CTAs of the main kernel
+  float* part_o;   // [CTAs][2][rows][D] unnormalised outputs
+  float2* part_ml; // [CTAs][2][rows] (maximum, sum)
+  Cut* cuts;       // [CTAs][2]: of the row tiles a CTA goes on with, and begins
+  int grid;        // ranges that the units are cut into; row_tiles CTAs share one
   int rows;        // rows of a row tile
   int row_tiles;   // ceil(T G / rows)
 };
@@ -67,8 +67,7 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
   return s;
 }
 
-// Where CTA c's range of `units` units on `n` CTAs begins, and whose range unit u
-// is in.  (32-bit divisions where they do: a 64-bit one is a chain of some 100
+// Where range c of `units` units in `n` ranges begins, and which range unit u is in.  (32-bit divisions where they do: a 64-bit one is a chain of some 100
 // instructions.)
 __device__ __forceinline__ int64_t range_start(int64_t units, int n, int c) {
   if (units < (1 << 20))  // n and c are at most a few thousand
@@ -82,12 +81,12 @@ __device__ __forceinline__ int range_of(int64_t units, int n, int64_t u) {
   return static_cast<int>(((u + 1) * n - 1) / units);
 }
 
-// A place in the CTA's range of units.
+// A place in a range of units.
 struct Cursor {
   int64_t u;
-  int b, hr, tile;  // sequence, key head * row_tiles + row tile, tile
+  int b, h, tile;  // sequence, key head, tile
   Seq s;
-  // On to tile `hi` of this row tile, or, where that is its end, to the next one.
+  // On to tile `hi` of this head, or, where that is its end, to the next one.
   __device__ __forceinline__ void to(const AttnArgs& a, int hi) {
     u += hi - 1 - tile;
     tile = hi - 1;
@@ -97,8 +96,8 @@ struct Cursor {
     ++u;
     if (++tile < s.tiles) return;
     tile = 0;
-    if (++hr < a.H * a.row_tiles) return;
-    hr = 0;
+    if (++h < a.H) return;
+    h = 0;
     do {
       if (++b >= a.B) return;
       s = load_seq(a, b);
@@ -112,8 +111,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// CTA `cta`'s range [u0, u1) of the units on n_cta CTAs, and the place where it
-// begins, by a warp together.  Up to 32 sequences need one load of their lengths.
+// Range `cta` [u0, u1) of the units in n_cta ranges, and the place where it begins, by a warp together.  Up to 32 sequences need one load of their lengths.
 struct Range {
   int64_t units, u0, u1;
   int n_cta;
@@ -121,7 +119,7 @@ struct Range {
 };
 __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
   const int lane = threadIdx.x & 31;
-  const int per = a.H * a.row_tiles;
+  const int per = a.H;
   Range g;
   Seq own{0, 0, 0, 0};
   int64_t x = 0;
@@ -156,23 +154,23 @@ __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
       g.first.b = b0 + w;
       g.first.s = Seq{__shfl_sync(kAll, own.row, w), __shfl_sync(kAll, own.len, w),
                       __shfl_sync(kAll, own.n, w), __shfl_sync(kAll, own.tiles, w)};
-      // within one sequence: at most 2^24 tiles of each of its row tiles
+      // within one sequence: at most 2^24 tiles of each of its heads
       const int64_t in = g.u0 - before;
-      g.first.hr = in < (1ll << 32)
+      g.first.h = in < (1ll << 32)
                        ? static_cast<int>(static_cast<uint32_t>(in) /
                                           static_cast<uint32_t>(g.first.s.tiles))
                        : static_cast<int>(in / g.first.s.tiles);
-      g.first.tile = static_cast<int>(in - static_cast<int64_t>(g.first.hr) * g.first.s.tiles);
+      g.first.tile = static_cast<int>(in - static_cast<int64_t>(g.first.h) * g.first.s.tiles);
       return g;
     }
     base += __shfl_sync(kAll, sum, 31);
   }
 }
 
-// Of the row tile whose first unit is v0.
-__device__ __forceinline__ Cut make_cut(const Range& g, int64_t v0, int b, int hr, int tiles) {
+// Of the head whose first unit is v0.
+__device__ __forceinline__ Cut make_cut(const Range& g, int64_t v0, int b, int h, int tiles) {
   const int c0 = range_of(g.units, g.n_cta, v0), c1 = range_of(g.units, g.n_cta, v0 + tiles - 1);
-  return Cut{b, hr, c0, c1 * 2 + (range_start(g.units, g.n_cta, c0) < v0 ? 1 : 0)};
+  return Cut{b, h, c0, c1 * 2 + (range_start(g.units, g.n_cta, c0) < v0 ? 1 : 0)};
 }
 
 template <typename E>
