@@ -93,11 +93,6 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* e
   return wait_on(bar, parity, err);
 }
 
-// Places of a page map's outer dimensions, innermost 0.
-struct MapOrder {
-  int slot, head, page;
-};
-
 // One lane of a converged warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -217,6 +212,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+__device__ __forceinline__ void tma_prefetch_4d(const void* tmap, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(tmap),
+               "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
 // Which of the 64 positions from p0 on node i of sequence b sees (0 past the end).
 __device__ __forceinline__ uint64_t seen64(const AttnArgs& a, int b, const Seq& s, int i, int p0) {
   if (i >= s.n) return 0;
@@ -242,8 +246,9 @@ __device__ __forceinline__ uint64_t seen64(const AttnArgs& a, int b, const Seq& 
 
 template <typename E, int D, int NS>
 __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
-    attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ MapOrder order) {
+    attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmQ,
+                const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV) {
   using C = TcCfg<D, NS>;
   constexpr int kBlk = D / 64;          // 64-channel blocks of a row
   constexpr int kBlkBytes = kKeys * 128;  // one block of a K or V slot
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
       mbar_init(&empty[i], NS);
     }
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&q_full[s], 4);
+      mbar_init(&q_full[s], 1);
       mbar_init(&s_full[s], 1);
       mbar_init(&s_read[s], 4);
       for (int z = 0; z < 2; ++z) {
@@ -286,6 +291,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
     *v_clean = 0;
     for (int i = 0; i < 4; ++i) bad_seg[i] = -1;
     fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
@@ -341,10 +347,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
       if (mine) {
         uint8_t* dst = ring + slot * C::kSlot + my_blk * kBlkBytes + my_page * box * 128;
         const int at = (tile * kKeys) & (ps - 1);
-        const int y = order.slot == 0 ? at : order.head == 0 ? h : page;
-        const int z = order.slot == 1 ? at : order.head == 1 ? h : page;
-        const int w = order.slot == 2 ? at : order.head == 2 ? h : page;
-        tma_load_4d(dst, tm, my_blk * 64, y, z, w, &full[slot]);
+        tma_load_4d(dst, tm, my_blk * 64, at, h, page, &full[slot]);
       }
       ++issued;
       if (++slot == C::kSlots) {
@@ -411,6 +414,20 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
       __syncwarp();
       return true;
     };
+    // This stream's rows of Q: G heads of the nodes from node0 on, row by row
+    const int node0 = (row_tile * NS + st) * a.stream_rows / a.G;
+    const uint32_t q_bytes = kBlk * 128 * a.stream_rows;
+    auto load_q = [&](const Cursor& c) {
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&q_full[st], q_bytes);
+#pragma unroll
+        for (int kb = 0; kb < kBlk; ++kb)
+          tma_load_4d(qs + st * C::kQ + kb * (kLanes * 128), &tmQ, kb * 64, c.h * a.G, node0, c.b,
+                      &q_full[st]);
+      }
+      __syncwarp();
+    };
+    if (n > 0) load_q(cur);
     uint32_t edges = 0;
     bool first_prev = false, edge_prev = false;  // of the tile whose output is next
     auto output = [&](int i, int slot, int ph) {  // of tile i
@@ -443,13 +460,25 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
     for (int seg = 0; i < n && ok; ++seg) {
       const int tile_lo = cur.tile, tile_hi = min(cur.s.tiles, tile_lo + (n - i));
       const int edge_from = cur.s.len / kKeys;
-      // A row tile's first scores need its Q, which comes once the last scores before
-      // it are done: the output of the tile before goes first.
+      // A new head's Q replaces the old one as soon as the last scores with that are
+      // done, and comes while the softmax and the output of that tile go on.
       const int k_slot = slot, k_ph = ph;
       advance();
       if (i > 0) {
-        ok = output(i - 1, slot, ph);
+        ok = wait(&s_read[st], (i - 1) & 1, a.t.err);
+        __syncwarp();
+        if (ok) load_q(cur);
+        ok = ok && output(i - 1, slot, ph);
         advance();
+      }
+      if (i + tile_hi - tile_lo < n) {  // the next head's Q on its way into L2
+        Cursor next = cur;
+        next.to(a, tile_hi);
+        if (elect_one())
+#pragma unroll
+          for (int kb = 0; kb < kBlk; ++kb)
+            tma_prefetch_4d(&tmQ, kb * 64, next.h * a.G, node0, next.b);
+        __syncwarp();
       }
       ok = ok && wait(&q_full[st], seg & 1, a.t.err) && scores(i, k_slot, k_ph);
       ++i;
@@ -478,39 +507,12 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
     const uint32_t tbase = tmem + stream * C::kStreamCols + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t to = tbase + kColO;
     const int M = a.t.T * a.G;
-    const int r0 = row_tile * (NS * kLanes) + stream * kLanes;
-    const bool live = r0 + quarter * 32 < M;  // a warp without rows only keeps in step
-    const int r = r0 + row_l, node = r / a.G;
+    const int r0 = (row_tile * NS + stream) * a.stream_rows;
+    // (a warp without rows only keeps in step)
+    const bool live = quarter * 32 < a.stream_rows && r0 + quarter * 32 < M;
+    const int r = row_l < a.stream_rows ? r0 + row_l : M, node = r / a.G;
     const float sl = fmaxf(fabsf(a.scale_log2), 1e-37f);
-    const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-    // Q of the row tile at c, negated where the scale is negative
-    auto load_q = [&](const Cursor& c) {
-      const int h = c.h;
-      const E* Q = static_cast<const E*>(a.q) + c.b * a.qb;
-      const int t = tid - kFirst - stream * kLanes;
-      constexpr int kCPR = D / 8;
-#pragma unroll 4
-      for (int x = t; x < kLanes * kCPR; x += kLanes) {
-        const int r = x / kCPR, cc = x % kCPR;
-        uint4 val = make_uint4(0, 0, 0, 0);
-        if (r0 + r < M) {
-          val = *reinterpret_cast<const uint4*>(Q + (r0 + r) / a.G * a.qt +
-                                                (h * a.G + (r0 + r) % a.G) * a.qh + cc * 8);
-          val.x ^= flip;
-          val.y ^= flip;
-          val.z ^= flip;
-          val.w ^= flip;
-        }
-        uint8_t* dst = qs + stream * C::kQ + (cc >> 3) * (kLanes * 128) + r * 128 +
-                       (((cc & 7) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(dst) = val;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[stream]);
-    };
-    load_q(cur);
-
+    const bool negative = a.scale_log2 < 0.f;
     bool ok = true;
     int i = 0;  // tile of this CTA's range
     for (int seg = 0; i < N && ok; ++seg) {
@@ -542,6 +544,9 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_read[stream]);
+          if (negative)
+#pragma unroll
+            for (int c = 0; c < 64; ++c) x[c] ^= 0x80000000u;
           if (kEdge) {
             const uint64_t vis = r < M ? seen64(a, at.b, s, node, p0) : 0;
 #pragma unroll
@@ -605,24 +610,27 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
           // (unseen_safe_sum): a weight of 0 would not keep them out of the product
           const int sq = seq_v(i), slot = sq % C::kSlots;
           if (!wait(&full[slot], (sq / C::kSlots) & 1, a.t.err)) return false;
+          constexpr int kPieces = C::kSlot / 16 / kLanes;
+          uint4* v = reinterpret_cast<uint4*>(ring + slot * C::kSlot) + (tid - kFirst);
+          uint4 y[kPieces];
+#pragma unroll
+          for (int z = 0; z < kPieces; ++z) y[z] = v[z * kLanes];
           bool found = false;
-          const int end = s.len + s.n;
-          for (int x = tid - kFirst; x < C::kSlot / 16; x += kLanes) {
-            const int pos = p0 + (x & 511) / 8;  // 512 pieces to a 64-channel block
-            if (pos < s.len) continue;
-            uint4* v = reinterpret_cast<uint4*>(ring + slot * C::kSlot) + x;
-            uint4 y = make_uint4(0, 0, 0, 0);
-            if (pos < end) {
-              y = *v;
-              bool bad = false;
-              y.x = finite2<E>(y.x, bad);
-              y.y = finite2<E>(y.y, bad);
-              y.z = finite2<E>(y.z, bad);
-              y.w = finite2<E>(y.w, bad);
-              found |= bad;
-              if (!bad) continue;
+#pragma unroll
+          for (int z = 0; z < kPieces; ++z) {
+            // 512 pieces to a 64-channel block, 8 to a key
+            const int pos = p0 + ((tid - kFirst + z * kLanes) & 511) / 8;
+            bool bad = false;
+            y[z].x = finite2<E>(y[z].x, bad);
+            y[z].y = finite2<E>(y[z].y, bad);
+            y[z].z = finite2<E>(y[z].z, bad);
+            y[z].w = finite2<E>(y[z].w, bad);
+            if (pos >= s.len + s.n) {
+              v[z * kLanes] = make_uint4(0, 0, 0, 0);
+            } else if (bad && pos >= s.len) {
+              v[z * kLanes] = y[z];
+              found = true;
             }
-            *v = y;
           }
           if (found) bad_seg[seg & 3] = seg;
           fence_proxy_async_smem();
@@ -636,6 +644,8 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
         ++i;
         return true;
       };
+      if (a.mask && r < M && tile_hi * kKeys > s.len)  // read at the head's last tiles
+        prefetch_l1(a.mask + (static_cast<int64_t>(at.b) * a.t.T + node) * a.W);
       const int plain_hi = max(tile_lo, min(tile_hi, s.len / kKeys));
       int tile = tile_lo;
       for (; tile < plain_hi && ok; ++tile) ok = tile_step(std::false_type{}, tile);
@@ -644,7 +654,6 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
 
       // ---- the end of this CTA's part of the row tile ----
       cur.to(a, tile_hi);
-      if (i < N) load_q(cur);  // every product with the old Q is complete (s_full)
       if (!wait(&pv_done[2 * stream + ((i - 1) & 1)], ((i - 1) >> 1) & 1, a.t.err)) break;
       __syncwarp();
       tc_fence_after();
@@ -657,8 +666,8 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
         const int head = h * a.G + r - node * a.G;
         const bool bad = *reinterpret_cast<volatile int*>(&bad_seg[seg & 3]) == seg;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * (NS * kLanes) +
-                             stream * kLanes + row_l;
+        const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * a.rows +
+                             stream * a.stream_rows + row_l;
         E* out = static_cast<E*>(a.out) + at.b * a.ob + node * a.ot + head * a.oh;
         const bool mine = r < M && node < s.n;
 #pragma unroll 1
@@ -820,47 +829,44 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// One layer's K or V as [pages, heads, slots, D], the three outer dimensions in the
-// order of their strides, boxes of one page's rows x 64 channels.
-bool page_map(const dfl2_cache* c, const void* base, bool f16, const MapOrder& o, CUtensorMap* out) {
+// A tensor map of 16-bit elements [n3, n2, n1, D] with element strides, boxes of
+// 64 channels x b1 x b2, 128-byte swizzle.
+bool map_4d(const void* base, bool f16, int D, const int64_t (&n)[3], const int64_t (&stride)[3],
+            int b1, int b2, CUtensorMap* out) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = encoder();
   if (!encode) return false;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->head_dim)}, strides[3];
-  cuuint32_t box[4] = {64}, one[4] = {1, 1, 1, 1};
-  const int at[3] = {o.slot, o.head, o.page};
-  const int64_t size[3] = {c->page_size, c->kv_heads, c->pages};
-  const int64_t stride[3] = {c->slot_stride, c->head_stride, c->page_stride};
-  for (int d = 0; d < 3; ++d) {
-    dims[1 + at[d]] = static_cast<cuuint64_t>(size[d]);
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D)}, strides[3];
+  for (int i = 0; i < 3; ++i) {
+    dims[1 + i] = static_cast<cuuint64_t>(n[i]);
     // (the stride of a dimension of one entry is never used, but has to be one)
-    strides[at[d]] = static_cast<cuuint64_t>(size[d] > 1 ? stride[d] : c->head_dim) * 2;
-    box[1 + at[d]] = d == 0 ? std::min(c->page_size, kKeys) : 1;
+    strides[i] = static_cast<cuuint64_t>(n[i] > 1 ? stride[i] : D) * 2;
   }
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2), 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
   return encode(out, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                 const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-MapOrder map_order(const dfl2_cache* c) {
-  const int64_t s = c->slot_stride, h = c->kv_heads > 1 ? c->head_stride : 0,
-                p = c->pages > 1 ? c->page_stride : INT64_MAX;
-  return MapOrder{(h < s) + (p < s), (s <= h) + (p < h), (s <= p) + (h <= p)};
-}
 
 // ---- plan ---------------------------------------------------------------------
 struct AttnPlan {
-  int rows;  // rows of a row tile
+  int stream_rows, rows;  // rows of a stream and of a row tile
   int row_tiles, grid;
   size_t o_off, ml_off, cut_off, ws_bytes;
 };
 
-// One stream's 128 rows while they are enough (or 256 channels leave room for no
-// second stream), two streams' 256 above: see the top of this file.
-AttnPlan attn_plan(int M, int D, int sms) {
+// A stream has as many whole nodes as 128 rows hold.  One stream while it is enough
+// (or 256 channels leave room for no second one), two above: see the top of this
+// file.
+AttnPlan attn_plan(int T, int G, int D, int sms) {
   AttnPlan p;
-  p.rows = M <= kLanes || D == 256 ? kLanes : 2 * kLanes;
+  const int M = T * G;
+  p.stream_rows = kLanes / G * G;
+  const int streams = M <= p.stream_rows || D == 256 ? 1 : 2;
+  p.rows = streams * p.stream_rows;
   p.row_tiles = (M + p.rows - 1) / p.rows;
-  p.grid = std::max(1, (p.rows == kLanes && D < 256 ? 2 * sms : sms) / p.row_tiles);
+  p.grid = std::max(1, (streams == 1 && D < 256 ? 2 * sms : sms) / p.row_tiles);
   const size_t ctas = size_t(p.grid) * p.row_tiles;
   const size_t parts = p.grid > 1 ? ctas * 2 : 0;  // one range cuts nothing
   p.o_off = 0;
@@ -871,29 +877,34 @@ AttnPlan attn_plan(int M, int D, int sms) {
 }
 
 template <typename E, int D, int NS>
-cudaError_t launch_main(const AttnArgs& a, const CUtensorMap& k, const CUtensorMap& v,
-                        const MapOrder& o, cudaStream_t s) {
+cudaError_t launch_main(const AttnArgs& a, const CUtensorMap& q, const CUtensorMap& k,
+                        const CUtensorMap& v, cudaStream_t s) {
   auto kernel = attn_kernel<E, D, NS>;
   constexpr size_t smem = TcCfg<D, NS>::kSmem;
   const cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  return launch_k(kernel, dim3(a.grid * a.row_tiles), dim3(TcCfg<D, NS>::kThreads), smem, s, true, a, k, v, o);
+  return launch_k(kernel, dim3(a.grid * a.row_tiles), dim3(TcCfg<D, NS>::kThreads), smem, s, true,
+                  a, q, k, v);
 }
 
 template <typename E, int D>
 cudaError_t launch_attn(const AttnArgs& a, const dfl2_cache* c, cudaStream_t s) {
-  const MapOrder o = map_order(c);
-  alignas(64) CUtensorMap tk, tv;
+  alignas(64) CUtensorMap tq, tk, tv;
   const bool f16 = std::is_same_v<E, __half>;
-  if (!page_map(c, a.k, f16, o, &tk) || !page_map(c, a.v, f16, o, &tv))
+  const int64_t qn[3] = {a.H * a.G, a.t.T, a.B}, qs[3] = {a.qh, a.qt, a.qb};
+  const int64_t n[3] = {c->page_size, c->kv_heads, c->pages};
+  const int64_t st[3] = {c->slot_stride, c->head_stride, c->page_stride};
+  const int box = std::min(c->page_size, kKeys);
+  if (!map_4d(a.q, f16, D, qn, qs, a.G, a.stream_rows / a.G, &tq) ||
+      !map_4d(a.k, f16, D, n, st, box, 1, &tk) || !map_4d(a.v, f16, D, n, st, box, 1, &tv))
     return cudaErrorInvalidValue;
   cudaError_t e;
   if constexpr (D == 256)
-    e = launch_main<E, D, 1>(a, tk, tv, o, s);
+    e = launch_main<E, D, 1>(a, tq, tk, tv, s);
   else
-    e = a.rows == kLanes ? launch_main<E, D, 1>(a, tk, tv, o, s)
-                         : launch_main<E, D, 2>(a, tk, tv, o, s);
+    e = a.rows == a.stream_rows ? launch_main<E, D, 1>(a, tq, tk, tv, s)
+                                : launch_main<E, D, 2>(a, tq, tk, tv, s);
   if (e != cudaSuccess) return e;
   return launch_k(combine_kernel<E, D>, dim3(2 * a.grid * a.row_tiles + a.B, kCombineY), dim3(kCombineWarps * 32),
                   0, s, true, a);
@@ -913,9 +924,10 @@ dfl2_status check_shapes(int B, int T, int q_heads, int kv_heads, int head_dim, 
   if (q_heads % kv_heads)
     return report_errorf(DFL2_ERR_INVALID_ARG, "q_heads=%d is no multiple of kv_heads=%d", q_heads,
                          kv_heads);
-  if (B > 65535 || T > kMaxTree || q_heads > 65535)
-    return report_errorf(DFL2_ERR_UNSUPPORTED, "B=%d, T=%d, q_heads=%d: at most 65535, %d, 65535",
-                         B, T, q_heads, kMaxTree);
+  if (B > 65535 || T > kMaxTree || q_heads / kv_heads > kLanes)
+    return report_errorf(DFL2_ERR_UNSUPPORTED,
+                         "B=%d, T=%d, q_heads/kv_heads=%d: at most 65535, %d, %d", B, T,
+                         q_heads / kv_heads, kMaxTree, kLanes);
   if (head_dim != 64 && head_dim != 128 && head_dim != 256)
     return report_errorf(DFL2_ERR_UNSUPPORTED, "head_dim=%d: 64, 128 or 256", head_dim);
   if (dtype != DFL2_BF16 && dtype != DFL2_F16)
@@ -938,7 +950,7 @@ size_t dfl2_tree_attn_workspace_size(int B, int T, int q_heads, int kv_heads, in
                                      dfl2_dtype dtype) {
   if (dfl2::check_shapes(B, T, q_heads, kv_heads, head_dim, dtype) != DFL2_OK) return 0;
   if (dfl2::check_args_device(nullptr, 0) != DFL2_OK) return 0;
-  return dfl2::attn_plan(T * (q_heads / kv_heads), head_dim, dfl2::device_info().sms).ws_bytes;
+  return dfl2::attn_plan(T, q_heads / kv_heads, head_dim, dfl2::device_info().sms).ws_bytes;
 }
 
 dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_cache* cache,
@@ -956,25 +968,26 @@ dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_c
     return dfl2::report_errorf(DFL2_ERR_INVALID_ARG, "layer %d of %d", layer, cache->layers);
   if (!q_strides || !out_strides)
     return dfl2::report_errorf(DFL2_ERR_INVALID_ARG, "q_strides and out_strides are needed");
+  // a tensor map's strides are positive, under 2^40 bytes and multiples of 16
+  const int64_t most = int64_t(1) << 38;
   const int dims[3] = {B, T, q_heads};
   for (int i = 0; i < 3; ++i)
-    if (dims[i] > 1 &&
-        (q_strides[i] < 0 || q_strides[i] % 8 || out_strides[i] < 0 || out_strides[i] % 8))
-      return dfl2::report_errorf(DFL2_ERR_INVALID_ARG,
-                                 "strides of q and out: non-negative multiples of 8");
-  // a tensor map's strides are positive and under 2^40 bytes
-  const int64_t most = int64_t(1) << 38;
-  if (cache->slot_stride < 1 || cache->slot_stride > most ||
-      (cache->kv_heads > 1 && (cache->head_stride < 1 || cache->head_stride > most)) ||
-      (cache->pages > 1 && (cache->page_stride < 1 || cache->page_stride > most)))
-    return dfl2::report_errorf(DFL2_ERR_UNSUPPORTED,
-                               "the attention needs cache strides of 1 .. 2^38 elements");
+    for (const int64_t st : {q_strides[i], out_strides[i]})
+      if (dims[i] > 1 && (st < 1 || st > most || st % 8))
+        return dfl2::report_errorf(DFL2_ERR_INVALID_ARG,
+                                   "strides of q and out: multiples of 8 from 8 to 2^38");
+  const int cdims[3] = {cache->page_size, cache->kv_heads, cache->pages};
+  const int64_t cst[3] = {cache->slot_stride, cache->head_stride, cache->page_stride};
+  for (int i = 0; i < 3; ++i)
+    if (cdims[i] > 1 && (cst[i] < 1 || cst[i] > most))
+      return dfl2::report_errorf(DFL2_ERR_UNSUPPORTED,
+                                 "the attention needs cache strides of 8 .. 2^38 elements");
   if (!std::isfinite(scale))
     return dfl2::report_errorf(DFL2_ERR_INVALID_ARG, "scale %g must be finite", double(scale));
   DFL2_TRY(dfl2::check_args_device(ptrs, 7));
   DFL2_TRY(dfl2::check_cache_device(cache));
   const int G = q_heads / cache->kv_heads, D = cache->head_dim;
-  const dfl2::AttnPlan p = dfl2::attn_plan(T * G, D, dfl2::device_info().sms);
+  const dfl2::AttnPlan p = dfl2::attn_plan(T, G, D, dfl2::device_info().sms);
   if (!ws || ws_bytes < p.ws_bytes)
     return dfl2::report_errorf(DFL2_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed",
                                ws ? ws_bytes : size_t(0), p.ws_bytes);
@@ -1010,6 +1023,7 @@ dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_c
   a.cuts = reinterpret_cast<dfl2::Cut*>(w + p.cut_off);
   a.grid = p.grid;
   a.rows = p.rows;
+  a.stream_rows = p.stream_rows;
   a.row_tiles = p.row_tiles;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = cache->dtype == DFL2_F16

@@ -47,6 +47,7 @@ struct AttnArgs {
   float2* part_ml; // [CTAs][2][rows] (maximum, sum)
   Cut* cuts;       // [CTAs][2]: of the row tiles a CTA goes on with, and begins
   int grid;        // ranges that the units are cut into; row_tiles CTAs share one
+  int stream_rows; // rows of a stream: whole nodes, at most 128
   int rows;        // rows of a row tile
   int row_tiles;   // ceil(T G / rows)
 };

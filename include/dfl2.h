@@ -481,11 +481,13 @@ dfl2_status dfl2_tree_accept(const int32_t* tokens, const int32_t* parents,
  * but scores of -inf, and rows at and past count have out = 0, lse = -inf.
  *   q, out      bf16 or fp16 as the cache; element c of head h, node i,
  *               sequence b at b*strides[0] + i*strides[1] + h*strides[2] + c
- *               (host arrays of three element strides, multiples of 8).  out
- *               must not overlap q or the cache.
+ *               (host arrays of three element strides, positive multiples of 8;
+ *               that of a dimension of one entry is not read).  out must not
+ *               overlap q or the cache.
  *   lse         float32 [B,T,q_heads] (nullable): log sum_j exp(s_j).
- *   head_dim 64, 128 or 256; q_heads a multiple of kv_heads; 1 <= T <= 256;
- *   1 <= B <= 65535; lengths below 2^30.
+ *   head_dim 64, 128 or 256; q_heads a multiple of kv_heads, at most 128 times it;
+ *   1 <= T <= 256; 1 <= B <= 65535; lengths up to 2^30; every cache stride of a
+ *   dimension of more than one entry positive.
  *   ws          dfl2_tree_attn_workspace_size bytes, scratch only.
  * Scores, softmax and sums are float32; the weights are rounded to the cache's
  * type for the product with V. */

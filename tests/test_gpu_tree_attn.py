@@ -172,6 +172,11 @@ def test_layouts(T):
     c.check(out, lse)
     a, _ = c.run(lse=False)
     assert torch.equal(a, out)
+    b, _ = c.run(q=c.q.cuda().transpose(1, 2).contiguous().transpose(1, 2))  # heads outside nodes
+    assert torch.equal(b, out)
+    one = Case([100], T, 8, 1, 64, 32, nhd=True, seed=6, spare=0)  # dimensions of one entry
+    out, lse = one.run()
+    one.check(out, lse)
 
 
 @pytest.mark.parametrize("T", [5, 48])
