@@ -137,10 +137,18 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None  # torch's current stream as an address, without a Stream object (3 us a call)
+
+
 def _stream(stream):
+    global _raw_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            import torch
+            torch.cuda.init()
+            get, dev = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _raw_stream = lambda: get(dev())  # noqa: E731
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -368,19 +376,32 @@ def dfl2_tail_tables(logits, verified_tok, hidden, W_H, P_A, P_B, temperature: f
 
 
 # ---- the paged cache and trees of drafted tokens ---------------------------------
-def _i32(t, name, shape=None):
-    """An int32 device array's address; None stays None.  The C side cannot see
-    types, so a wrong one is an error here."""
-    if t is None or isinstance(t, int):
-        return t
-    import torch
-    if t.dtype != torch.int32:
+# These calls are short (a few microseconds on the GPU), so their marshalling is kept
+# short too: types and shapes, which the C side cannot see, are checked in one pass.
+_S3, _S4 = ctypes.c_int64 * 3, ctypes.c_int64 * 4
+
+
+def _i32(t, name, shape):
+    """An int32 device array's address, of the given shape; None stays None."""
+    if t is None:
+        return None
+    if t.dtype != _torch().int32:
         raise TypeError(f"{name} must be int32, not {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {shape}, not {tuple(t.shape)} with strides "
+                         f"{t.stride()}")
     return t.data_ptr()
+
+
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _strides(t):
@@ -397,7 +418,7 @@ class Cache:
     table int32 [rows, cols], refs int32 [pages], free_bits int32 [ceil(pages/32)]."""
 
     def __init__(self, k, v, table, refs, free_bits):
-        import torch
+        torch = _torch()
         codes = {torch.float32: DFL2_F32, torch.bfloat16: DFL2_BF16, torch.float16: DFL2_F16}
         if k.dtype not in codes or v.dtype != k.dtype:
             raise TypeError(f"k and v must both be float32, bf16 or fp16, not {k.dtype}, {v.dtype}")
@@ -408,11 +429,11 @@ class Cache:
         layers, pages, heads, page_size, dim = k.shape
         if table.dim() != 2:
             raise ValueError("table must be [rows, cols]")
-        _i32(table, "table")
+        _i32(table, "table", table.shape)
         _i32(refs, "refs", (pages,))
         _i32(free_bits, "free_bits", ((pages + 31) // 32,))
         self.k, self.v, self.table, self.refs, self.free_bits = k, v, table, refs, free_bits
-        self.dtype = k.dtype
+        self.dtype, self.kv_heads, self.head_dim = k.dtype, heads, dim
         self._s = _CacheStruct(
             k.data_ptr(), v.data_ptr(), codes[k.dtype], layers, pages, heads, page_size, dim,
             st[0], st[1], st[2], st[3], table.data_ptr(), table.shape[0],
@@ -423,7 +444,7 @@ class Cache:
 def cache(layers: int, pages: int, kv_heads: int, page_size: int, head_dim: int, rows: int,
           cols: int, dtype=None, device="cuda") -> Cache:
     """A new, empty Cache (torch allocation; plumbing only)."""
-    import torch
+    torch = _torch()
     shape = (layers, pages, kv_heads, page_size, head_dim)
     dtype = dtype or torch.bfloat16
     bits = torch.full(((pages + 31) // 32,), -1, dtype=torch.int32, device=device)
@@ -435,41 +456,39 @@ def cache(layers: int, pages: int, kv_heads: int, page_size: int, head_dim: int,
                  torch.zeros(pages, dtype=torch.int32, device=device), bits)
 
 
-def _count(count, T, B):
-    """(T, address of the counts): a plain number is every sequence's count."""
-    if isinstance(count, int):
-        return count, None
-    return T, _i32(count, "count", (B,))
-
-
 def dfl2_cache_reserve(cache, length, count, served, rows=None, stream=None) -> None:
     """Pages for positions length .. length+count-1; served int32 [B] out.  count: int or [B]."""
-    B = length.shape[0]
-    T, n = _count(count, 1 << 30, B)
-    _check(load().dfl2_cache_reserve(cache._ref, B, T, _i32(rows, "rows", (B,)),
-                                     _i32(length, "length", (B,)), n,
-                                     _i32(served, "served", (B,)), _stream(stream)))
+    shape = length.shape
+    if isinstance(count, int):
+        T, n = count, None
+    else:
+        T, n = 1 << 30, _i32(count, "count", shape)
+    _check(load().dfl2_cache_reserve(cache._ref, shape[0], T, _i32(rows, "rows", shape),
+                                     _i32(length, "length", shape[:1]), n,
+                                     _i32(served, "served", shape), _stream(stream)))
 
 
 def dfl2_cache_write(cache, k_new, v_new, length, count=None, rows=None, layer: int = 0,
                      stream=None) -> None:
     """k_new, v_new [n_layers, B, T, kv_heads, head_dim] (one layer: without the first
     dimension) into layers layer .. of the cache, positions length .. length+count-1."""
-    s = cache._s
     if k_new.dim() == 4:
         k_new, v_new = k_new[None], v_new[None]
-    N, B, T = k_new.shape[:3]
+    N, B, T, H, D = k_new.shape
     if (k_new.dtype != cache.dtype or v_new.dtype != cache.dtype or v_new.shape != k_new.shape
-            or tuple(k_new.shape[3:]) != (s.kv_heads, s.head_dim)):
+            or H != cache.kv_heads or D != cache.head_dim):
         raise ValueError("k_new and v_new must be [n_layers, B, T, kv_heads, head_dim] of the "
                          "cache's type")
-    st = _strides(k_new)
-    if _strides(v_new) != st or k_new.stride(4) != 1:
+    st = k_new.stride()
+    if v_new.stride() != st and _strides(v_new) != _strides(k_new) or st[4] != 1:
         raise ValueError("k_new and v_new must have the same strides, the last of them 1")
-    T, n = _count(count, T, B) if not isinstance(count, int) else (min(T, count), None)
+    if isinstance(count, int):
+        T, count = min(T, count), None
+    shape = (B,)
     _check(load().dfl2_cache_write(cache._ref, layer, N, k_new.data_ptr(), v_new.data_ptr(),
-                                   (ctypes.c_int64 * 4)(*st[:4]), B, T, _i32(rows, "rows", (B,)),
-                                   _i32(length, "length", (B,)), n, _stream(stream)))
+                                   _S4(*st[:4]), B, T, _i32(rows, "rows", shape),
+                                   _i32(length, "length", shape), _i32(count, "count", shape),
+                                   _stream(stream)))
 
 
 def dfl2_cache_compact(cache, length, count, path, n_path, new_length, rows=None,
@@ -477,32 +496,37 @@ def dfl2_cache_compact(cache, length, count, path, n_path, new_length, rows=None
     """The rows of nodes path[b,:n_path] to positions length .., the pages behind them
     given back, new_length = length + n_path (may be length).  count: int or [B]."""
     B, T = path.shape
-    if isinstance(count, int) and count != T:
-        raise ValueError(f"path has room for {T} nodes, not {count}")
-    _, n = _count(count, T, B)
-    _check(load().dfl2_cache_compact(cache._ref, B, T, _i32(rows, "rows", (B,)),
-                                     _i32(length, "length", (B,)), n, _i32(path, "path"),
-                                     _i32(n_path, "n_path", (B,)),
-                                     _i32(new_length, "new_length", (B,)), _stream(stream)))
+    shape = (B,)
+    if isinstance(count, int):
+        if count != T:
+            raise ValueError(f"path has room for {T} nodes, not {count}")
+        count = None
+    _check(load().dfl2_cache_compact(cache._ref, B, T, _i32(rows, "rows", shape),
+                                     _i32(length, "length", shape), _i32(count, "count", shape),
+                                     _i32(path, "path", (B, T)), _i32(n_path, "n_path", shape),
+                                     _i32(new_length, "new_length", shape), _stream(stream)))
 
 
 def dfl2_cache_fork(cache, src, dst, length, served, stream=None) -> None:
     """Table rows dst become copies of the first length positions of rows src."""
-    n = src.shape[0]
-    _check(load().dfl2_cache_fork(cache._ref, n, _i32(src, "src", (n,)), _i32(dst, "dst", (n,)),
-                                  _i32(length, "length", (n,)), _i32(served, "served", (n,)),
-                                  _stream(stream)))
+    shape = src.shape
+    _check(load().dfl2_cache_fork(cache._ref, shape[0], _i32(src, "src", shape[:1]),
+                                  _i32(dst, "dst", shape), _i32(length, "length", shape),
+                                  _i32(served, "served", shape), _stream(stream)))
 
 
 def dfl2_cache_free(cache, rows, stream=None) -> None:
     """Every page of the table rows given back."""
-    _check(load().dfl2_cache_free(cache._ref, rows.shape[0], _i32(rows, "rows"), _stream(stream)))
+    shape = rows.shape
+    _check(load().dfl2_cache_free(cache._ref, shape[0], _i32(rows, "rows", shape[:1]),
+                                  _stream(stream)))
 
 
 def dfl2_tree_mask(parents, mask, depth=None, count=None, stream=None) -> None:
     """parents [B,T] -> mask int32 [B,T,ceil(T/32)] (bit j: node i sees node j), depth [B,T]."""
     B, T = parents.shape
-    _check(load().dfl2_tree_mask(_i32(parents, "parents"), B, T, _i32(count, "count", (B,)),
+    _check(load().dfl2_tree_mask(_i32(parents, "parents", (B, T)), B, T,
+                                 _i32(count, "count", (B,)),
                                  _i32(mask, "mask", (B, T, (T + 31) // 32)),
                                  _i32(depth, "depth", (B, T)), _stream(stream)))
 
@@ -510,45 +534,41 @@ def dfl2_tree_mask(parents, mask, depth=None, count=None, stream=None) -> None:
 def dfl2_tree_accept(tokens, parents, target, path, n_path, next_token, count=None,
                      stream=None) -> None:
     """The path of the target's tokens through each tree: path [B,T], n_path [B], next_token [B]."""
-    B, T = tokens.shape
-    _check(load().dfl2_tree_accept(_i32(tokens, "tokens"), _i32(parents, "parents", (B, T)),
-                                   _i32(target, "target", (B, T)), B, T,
-                                   _i32(count, "count", (B,)), _i32(path, "path", (B, T)),
-                                   _i32(n_path, "n_path", (B,)),
-                                   _i32(next_token, "next_token", (B,)), _stream(stream)))
-
-
-def _attn_dtype(dtype) -> int:
-    import torch
-    return {torch.float32: DFL2_F32, torch.bfloat16: DFL2_BF16, torch.float16: DFL2_F16}.get(
-        dtype, dtype)
+    B, T = shape = tokens.shape
+    one = (B,)
+    _check(load().dfl2_tree_accept(_i32(tokens, "tokens", shape), _i32(parents, "parents", shape),
+                                   _i32(target, "target", shape), B, T, _i32(count, "count", one),
+                                   _i32(path, "path", shape), _i32(n_path, "n_path", one),
+                                   _i32(next_token, "next_token", one), _stream(stream)))
 
 
 def dfl2_tree_attn_workspace_size(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int,
                                   dtype) -> int:
     """dtype: a torch dtype or DFL2_BF16 / DFL2_F16."""
+    torch = _torch()
+    code = {torch.float32: DFL2_F32, torch.bfloat16: DFL2_BF16, torch.float16: DFL2_F16}
     return int(load().dfl2_tree_attn_workspace_size(B, T, q_heads, kv_heads, head_dim,
-                                                    _attn_dtype(dtype)))
+                                                    code.get(dtype, dtype)))
 
 
 def dfl2_tree_attn(q, cache, layer: int, length, mask, out, ws, rows=None, count=None, lse=None,
                    scale=None, stream=None) -> None:
     """q [B,T,q_heads,head_dim] over layer `layer` of the cache -> out (as q), lse float32
     [B,T,q_heads].  mask int32 [B,T,ceil(T/32)], None for a chain; scale: head_dim ** -0.5."""
-    B, T, H, D = q.shape
-    s = cache._s
-    if q.dtype != cache.dtype or out.dtype != cache.dtype or out.shape != q.shape:
+    B, T, H, D = shape = q.shape
+    if q.dtype != cache.dtype or out.dtype != cache.dtype or out.shape != shape:
         raise ValueError("q and out must be [B, T, q_heads, head_dim] of the cache's type")
-    qs, os_ = _strides(q), _strides(out)
-    if D != s.head_dim or q.stride(3) != 1 or out.stride(3) != 1:
-        raise ValueError(f"head_dim {D} against the cache's {s.head_dim}, strides {qs}, {os_}")
+    qs, os_ = q.stride(), out.stride()
+    if D != cache.head_dim or qs[3] != 1 or os_[3] != 1:
+        raise ValueError(f"head_dim {D} against the cache's {cache.head_dim}, strides {qs}, {os_}")
+    lse_p = None
     if lse is not None:
-        import torch
-        if lse.dtype != torch.float32 or lse.shape != (B, T, H) or not lse.is_contiguous():
+        if (lse.dtype != _torch().float32 or lse.shape != shape[:3] or not lse.is_contiguous()):
             raise ValueError("lse must be contiguous float32 [B, T, q_heads]")
+        lse_p = lse.data_ptr()
+    one = (B,)
     _check(load().dfl2_tree_attn(
-        q.data_ptr(), (ctypes.c_int64 * 3)(*qs[:3]), cache._ref, layer, B, T, H,
-        _i32(rows, "rows", (B,)), _i32(length, "length", (B,)), _i32(count, "count", (B,)),
-        _i32(mask, "mask", (B, T, (T + 31) // 32)), D ** -0.5 if scale is None else float(scale),
-        out.data_ptr(), (ctypes.c_int64 * 3)(*os_[:3]), _ptr(lse), _ptr(ws), _nbytes(ws),
-        _stream(stream)))
+        q.data_ptr(), _S3(*qs[:3]), cache._ref, layer, B, T, H, _i32(rows, "rows", one),
+        _i32(length, "length", one), _i32(count, "count", one),
+        _i32(mask, "mask", (B, T, (T + 31) // 32)), D ** -0.5 if scale is None else scale,
+        out.data_ptr(), _S3(*os_[:3]), lse_p, ws.data_ptr(), _nbytes(ws), _stream(stream)))

@@ -523,8 +523,9 @@ dfl2_status dfl2_cache_write(const dfl2_cache* cache, int layer, int n_layers, c
                                layer + n_layers - 1, cache->layers);
   if (!new_strides) return dfl2::report_errorf(DFL2_ERR_INVALID_ARG, "new_strides is NULL");
   const int per = 16 / dfl2::elem_bytes(cache->dtype);
+  const int dims[4] = {n_layers, B, T, cache->kv_heads};
   for (int i = 0; i < 4; ++i)
-    if (new_strides[i] < 0 || new_strides[i] % per)
+    if (dims[i] > 1 && (new_strides[i] < 0 || new_strides[i] % per))
       return dfl2::report_errorf(DFL2_ERR_INVALID_ARG,
                                  "new_strides[%d] = %lld: non-negative multiples of 16 bytes", i,
                                  (long long)new_strides[i]);

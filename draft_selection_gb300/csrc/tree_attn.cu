@@ -52,6 +52,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <mutex>
 
@@ -718,13 +719,13 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
 }
 
 // The parts that the CTAs left of a row tile, added in the order of the keys.  The
-// P ranges that have parts of it lend it P block columns of kCombineY blocks,
+// P ranges that have parts of it lend it P block columns of gridDim.y blocks,
 // so the more parts there are to add, the more blocks add them: each takes some of
 // the rows, one to a warp while the parts are few, several warps to a row where they
 // are many.  The last B block columns zero what lies past a sequence's count.
 // (A warp to every output row, looking up whether it was cut, took 76 us after the
 // 1.28 ms of 32 sequences of 64 nodes; most rows are whole.)
-constexpr int kCombineWarps = 8, kCombineY = 4;
+constexpr int kCombineWarps = 8;
 template <typename E, int D>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     combine_kernel(const __grid_constant__ AttnArgs a) {
@@ -740,7 +741,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
     const int b = blockIdx.x - 2 * ctas;
     const int done = load_seq(a, b).n * Hq;
     for (int x = done + blockIdx.y * kCombineWarps + warp; x < a.t.T * Hq;
-         x += kCombineY * kCombineWarps) {
+         x += gridDim.y * kCombineWarps) {
       const int node = x / Hq, head = x - node * Hq;
       uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<E*>(a.out) + b * a.ob + node * a.ot +
                                                   head * a.oh + lane * kPer);
@@ -761,8 +762,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   // warps to a row: about four parts each
   const int wide = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;
   const int per_block = kCombineWarps / wide, sub = warp / wide, part0 = warp % wide;
-  const int id = (range - c0) * kCombineY + blockIdx.y;
-  for (int rb = id * per_block; rb < rows; rb += parts * kCombineY * per_block) {
+  const int id = (range - c0) * gridDim.y + blockIdx.y;
+  for (int rb = id * per_block; rb < rows; rb += parts * gridDim.y * per_block) {
     const int r = rb + sub;
     auto at = [&](int c) {
       return ((static_cast<int64_t>(c) * a.row_tiles + row_tile) * 2 + (c == c0 ? slot0 : 0)) * a.rows +
@@ -881,9 +882,16 @@ cudaError_t launch_main(const AttnArgs& a, const CUtensorMap& q, const CUtensorM
                         const CUtensorMap& v, cudaStream_t s) {
   auto kernel = attn_kernel<E, D, NS>;
   constexpr size_t smem = TcCfg<D, NS>::kSmem;
-  const cudaError_t e = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static std::atomic<uint64_t> ready{0};  // devices on which the kernel may use that much
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (!(ready.load() >> dev & 1)) {  // (ordinals are below 64: ensured with the device's state)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(uint64_t(1) << dev);
+  }
   return launch_k(kernel, dim3(a.grid * a.row_tiles), dim3(TcCfg<D, NS>::kThreads), smem, s, true,
                   a, q, k, v);
 }
@@ -906,7 +914,9 @@ cudaError_t launch_attn(const AttnArgs& a, const dfl2_cache* c, cudaStream_t s) 
     e = a.rows == a.stream_rows ? launch_main<E, D, 1>(a, tq, tk, tv, s)
                                 : launch_main<E, D, 2>(a, tq, tk, tv, s);
   if (e != cudaSuccess) return e;
-  return launch_k(combine_kernel<E, D>, dim3(2 * a.grid * a.row_tiles + a.B, kCombineY), dim3(kCombineWarps * 32),
+  // two parts, the fewest, bring as many warps as the row tile has rows
+  const int blocks = std::max(1, std::min(a.rows, a.t.T * a.G) / (2 * kCombineWarps));
+  return launch_k(combine_kernel<E, D>, dim3(2 * a.grid * a.row_tiles + a.B, blocks), dim3(kCombineWarps * 32),
                   0, s, true, a);
 }
 
