@@ -171,6 +171,26 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+      "%10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -213,6 +233,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// 32 bytes: a whole sector a thread, where rows lie apart (a store of 16 costs as many
+// passes for half the bytes)
+__device__ __forceinline__ void st_v8(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void prefetch_l1(const void* p) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
 }
@@ -528,10 +555,11 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
       auto tile_step = [&](auto edge_tag, int tile) {
         constexpr bool kEdge = decltype(edge_tag)::value;
         const int p0 = tile * kKeys;
-        const int odd = i & 1, turn = (i >> 1) & 1;
+        const int odd = i & 1;
+        const uint64_t vis = kEdge && r < M ? seen64(a, at.b, s, node, p0) : 0;
+        // (the MMA warp issued tile i - 2's output before these scores, so it is complete
+        // too, and its weights' buffer free for tile i's)
         if (!wait(&s_full[stream], odd, a.t.err)) return false;
-        // tile i - 2's weights leave their buffer to tile i's (long since)
-        if (i >= 2 && !wait(&pv_done[2 * stream + odd], turn ^ 1, a.t.err)) return false;
         __syncwarp();
         tc_fence_after();
         if (!live) {
@@ -549,26 +577,47 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
 #pragma unroll
             for (int c = 0; c < 64; ++c) x[c] ^= 0x80000000u;
           if (kEdge) {
-            const uint64_t vis = r < M ? seen64(a, at.b, s, node, p0) : 0;
 #pragma unroll
             for (int c = 0; c < 64; ++c)
               if (!(vis >> c & 1)) x[c] = 0xFF800000u;  // -inf
           }
-          float mx[4];
+          auto maximum = [&]() {
+            float mx[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(x[c]);
+            for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(x[c]);
 #pragma unroll
-          for (int c = 4; c < 60; c += 8)
+            for (int c = 4; c < 60; c += 8)
 #pragma unroll
-            for (int z = 0; z < 4; ++z)
-              mx[z] = max3(mx[z], __uint_as_float(x[c + z]), __uint_as_float(x[c + 4 + z]));
-          const float top =
-              max3(max3(mx[0], __uint_as_float(x[60]), __uint_as_float(x[61])),
-                   max3(mx[1], __uint_as_float(x[62]), __uint_as_float(x[63])),
-                   fmaxf(mx[2], mx[3])) * sl;
-          if (tile == tile_lo) {
-            m = top;
-          } else if (__any_sync(kAll, top > m + kRise)) {  // (m = -inf: anything above)
+              for (int z = 0; z < 4; ++z)
+                mx[z] = max3(mx[z], __uint_as_float(x[c + z]), __uint_as_float(x[c + 4 + z]));
+            return max3(max3(mx[0], __uint_as_float(x[60]), __uint_as_float(x[61])),
+                        max3(mx[1], __uint_as_float(x[62]), __uint_as_float(x[63])),
+                        fmaxf(mx[2], mx[3])) * sl;
+          };
+          bool known = tile == tile_lo;  // that m is near enough
+          if (known) m = maximum();
+          // The weights are taken with the reference as it is, beside the maximum that
+          // tells whether it will do, and again in the rare case that it does not.
+          uint64_t sum[2];
+          uint32_t p[32];
+          while (true) {
+            const float safe = m == -INFINITY ? 0.f : m;
+            const uint64_t sl2 = pack_f32x2(sl, sl), off2 = pack_f32x2(-safe, -safe);
+            sum[0] = sum[1] = 0;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const uint64_t y2 = fma_f32x2(pack_u32x2(x[2 * c], x[2 * c + 1]), sl2, off2);
+              float y, z;
+              unpack_f32x2(y2, y, z);
+              y = ex2(y);
+              z = ex2(z);
+              sum[c & 1] = add_f32x2(sum[c & 1], pack_f32x2(y, z));
+              p[c] = pack2<E>(y, z);
+            }
+            if (known) break;
+            const float top = maximum();
+            if (!__any_sync(kAll, top > m + kRise)) break;  // (m = -inf: anything above)
+            known = true;
             if (!wait(&pv_done[2 * stream + (odd ^ 1)], ((i - 1) >> 1) & 1, a.t.err)) return false;
             __syncwarp();
             tc_fence_after();
@@ -577,28 +626,13 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
             l *= f;
             m = mn;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32_issue(to + c, o);
-              tmem_ld32_wait(o);
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + c, o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st32(to + c, o);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st16(to + c, o);
             }
-          }
-          const float safe = m == -INFINITY ? 0.f : m;
-          const uint64_t sl2 = pack_f32x2(sl, sl), off2 = pack_f32x2(-safe, -safe);
-          uint64_t sum[2] = {0, 0};
-          uint32_t p[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const uint64_t y2 = fma_f32x2(pack_u32x2(x[2 * c], x[2 * c + 1]), sl2, off2);
-            float y, z;
-            unpack_f32x2(y2, y, z);
-            y = ex2(y);
-            z = ex2(z);
-            sum[c & 1] = add_f32x2(sum[c & 1], pack_f32x2(y, z));
-            p[c] = pack2<E>(y, z);
           }
           float s0, s1;
           unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
@@ -621,15 +655,11 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
           for (int z = 0; z < kPieces; ++z) {
             // 512 pieces to a 64-channel block, 8 to a key
             const int pos = p0 + ((tid - kFirst + z * kLanes) & 511) / 8;
-            bool bad = false;
-            y[z].x = finite2<E>(y[z].x, bad);
-            y[z].y = finite2<E>(y[z].y, bad);
-            y[z].z = finite2<E>(y[z].z, bad);
-            y[z].w = finite2<E>(y[z].w, bad);
             if (pos >= s.len + s.n) {
               v[z * kLanes] = make_uint4(0, 0, 0, 0);
-            } else if (bad && pos >= s.len) {
-              v[z * kLanes] = y[z];
+            } else if (pos >= s.len && not_finite<E>(y[z])) {
+              v[z * kLanes] = make_uint4(finite2<E>(y[z].x), finite2<E>(y[z].y),
+                                         finite2<E>(y[z].z), finite2<E>(y[z].w));
               found = true;
             }
           }
@@ -698,9 +728,8 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
             }
           } else if (mine) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(a.part_o + part * D + c + 4 * j) =
-                  make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int j = 0; j < 4; ++j)
+              st_v8(a.part_o + part * D + c + 8 * j, o + 8 * j);
           }
           __syncwarp();  // the next load is the whole warp's
         }
@@ -873,7 +902,7 @@ AttnPlan attn_plan(int T, int G, int D, int sms) {
   p.o_off = 0;
   p.ml_off = align_up(parts * p.rows * D * sizeof(float), 256);
   p.cut_off = p.ml_off + align_up(parts * p.rows * sizeof(float2), 256);
-  p.ws_bytes = p.cut_off + align_up(ctas * 2 * sizeof(Cut), 256);
+  p.ws_bytes = p.cut_off + align_up(ctas * 2 * sizeof(Cut), 256) + 256;  // (to align the base)
   return p;
 }
 
@@ -914,8 +943,9 @@ cudaError_t launch_attn(const AttnArgs& a, const dfl2_cache* c, cudaStream_t s) 
     e = a.rows == a.stream_rows ? launch_main<E, D, 1>(a, tq, tk, tv, s)
                                 : launch_main<E, D, 2>(a, tq, tk, tv, s);
   if (e != cudaSuccess) return e;
-  // two parts, the fewest, bring as many warps as the row tile has rows
-  const int blocks = std::max(1, std::min(a.rows, a.t.T * a.G) / (2 * kCombineWarps));
+  // (measured: four block rows to 256 rows; sixteen cost a decode step, whose blocks
+  // have next to nothing to do, 7 us of 10, one costs 427 rows in 61 nodes 14 of 46)
+  const int blocks = std::max(1, std::min(a.rows, a.t.T * a.G) / 64);
   return launch_k(combine_kernel<E, D>, dim3(2 * a.grid * a.row_tiles + a.B, blocks), dim3(kCombineWarps * 32),
                   0, s, true, a);
 }
@@ -1004,7 +1034,8 @@ dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_c
   const dfl2::PtrArg wsp[] = {{ws, "workspace", 16}};
   DFL2_TRY(dfl2::check_args_host(wsp, 1));
   DFL2_TRY(dfl2::check_args_device(wsp, 1));
-  uint8_t* w = static_cast<uint8_t*>(ws);
+  uint8_t* w = reinterpret_cast<uint8_t*>(
+      dfl2::align_up(reinterpret_cast<uintptr_t>(ws), 256));  // parts are stored 32 bytes at a time
   const int64_t at = layer * cache->layer_stride * 2;
   dfl2::AttnArgs a{};
   a.t = dfl2::table_view(cache, table_rows, length, count, T);

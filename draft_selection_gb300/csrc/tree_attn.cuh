@@ -194,19 +194,21 @@ __device__ __forceinline__ float to_f32(E x) {
 template <typename E>
 constexpr uint32_t kExpMask = std::is_same_v<E, __half> ? 0x7C00u : 0x7F80u;
 
-// Two elements with those that are Inf or NaN set to 0; bad: whether there was one.
+// Two elements with those that are Inf or NaN set to 0.
 template <typename E>
-__device__ __forceinline__ uint32_t finite2(uint32_t x, bool& bad) {
+__device__ __forceinline__ uint32_t finite2(uint32_t x) {
   constexpr uint32_t lo = kExpMask<E>, hi = lo << 16;
-  if ((x & lo) == lo) {
-    x &= 0xFFFF0000u;
-    bad = true;
-  }
-  if ((x & hi) == hi) {
-    x &= 0x0000FFFFu;
-    bad = true;
-  }
+  if ((x & lo) == lo) x &= 0xFFFF0000u;
+  if ((x & hi) == hi) x &= 0x0000FFFFu;
   return x;
+}
+// Whether one of eight elements is Inf or NaN: an exponent of all ones and one more
+// in its last place carries into the place of the sign, and no further.
+template <typename E>
+__device__ __forceinline__ bool not_finite(uint4 x) {
+  constexpr uint32_t m = kExpMask<E> * 0x10001u, one = (kExpMask<E> & -kExpMask<E>) * 0x10001u;
+  return (((x.x & m) + one) | ((x.y & m) + one) | ((x.z & m) + one) | ((x.w & m) + one)) &
+         0x80008000u;
 }
 
 // Whether node i of sequence b sees node j (0 <= j).
