@@ -747,20 +747,29 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
   if (warp == 1) tmem_dealloc(tmem, NS * C::kStreamCols);
 }
 
+__device__ __forceinline__ float4 scaled(float4 x, float f) {
+  return make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+}
+__device__ __forceinline__ void add_scaled(float4& y, float4 x, float f) {
+  y.x = fmaf(x.x, f, y.x);
+  y.y = fmaf(x.y, f, y.y);
+  y.z = fmaf(x.z, f, y.z);
+  y.w = fmaf(x.w, f, y.w);
+}
+
 // The parts that the CTAs left of a row tile, added in the order of the keys.  The
-// P ranges that have parts of it lend it P block columns of gridDim.y blocks,
-// so the more parts there are to add, the more blocks add them: each takes some of
-// the rows, one to a warp while the parts are few, several warps to a row where they
-// are many.  The last B block columns zero what lies past a sequence's count.
-// (A warp to every output row, looking up whether it was cut, took 76 us after the
-// 1.28 ms of 32 sequences of 64 nodes; most rows are whole.)
-constexpr int kCombineWarps = 8;
+// P ranges that have parts of it lend it P block columns of gridDim.y blocks, so the
+// more parts there are to add, the more blocks add them.  A warp takes 512 / D rows
+// at once, 16 channels a lane, and four parts at once, whose loads are all in flight
+// together; with more than four parts, 2, 4 or 8 warps share the rows.  The last B
+// block columns zero what lies past a sequence's count.
+constexpr int kCombineWarps = 8, kCombineParts = 4;
 template <typename E, int D>
 __global__ void __launch_bounds__(kCombineWarps * 32)
     combine_kernel(const __grid_constant__ AttnArgs a) {
-  constexpr int kPer = D / 32;  // channels per lane
-  __shared__ float y_s[kCombineWarps][D];
-  __shared__ float l_s[kCombineWarps];
+  constexpr int kLanesRow = D / 16, kRows = 32 / kLanesRow;  // lanes of a row, rows of a warp
+  __shared__ float4 y_s[kCombineWarps][4][32];
+  __shared__ float2 ml_s[kCombineWarps][kRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int Hq = a.H * a.G;
   pdl_wait();
@@ -773,9 +782,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
          x += gridDim.y * kCombineWarps) {
       const int node = x / Hq, head = x - node * Hq;
       uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<E*>(a.out) + b * a.ob + node * a.ot +
-                                                  head * a.oh + lane * kPer);
+                                                  head * a.oh);
 #pragma unroll
-      for (int i = 0; i < kPer / 2; ++i) out[i] = 0;
+      for (int i = 0; i < D / 64; ++i) out[lane + 32 * i] = 0;
       if (a.lse && lane == 0)
         a.lse[(static_cast<int64_t>(b) * a.t.T + node) * Hq + head] = -INFINITY;
     }
@@ -788,57 +797,91 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   const int range = blockIdx.x / 2 / a.row_tiles, row_tile = blockIdx.x / 2 - range * a.row_tiles;
   const int h = cut.h, r0 = row_tile * a.rows;
   const int rows = min(a.rows, load_seq(a, b).n * a.G - r0);  // (past the count: zeroed above)
-  // warps to a row: about four parts each
-  const int wide = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;
-  const int per_block = kCombineWarps / wide, sub = warp / wide, part0 = warp % wide;
+  const int wide = parts <= kCombineParts       ? 1
+                   : parts <= 2 * kCombineParts ? 2
+                   : parts <= 4 * kCombineParts ? 4
+                                                : 8;  // warps that share rows
+  const int per_block = kCombineWarps / wide * kRows, part0 = warp % wide;
   const int id = (range - c0) * gridDim.y + blockIdx.y;
   for (int rb = id * per_block; rb < rows; rb += parts * gridDim.y * per_block) {
-    const int r = rb + sub;
-    auto at = [&](int c) {
-      return ((static_cast<int64_t>(c) * a.row_tiles + row_tile) * 2 + (c == c0 ? slot0 : 0)) * a.rows +
-             r;
-    };
-    float safe = 0.f, ll = 0.f, y[kPer];
+    const int r = rb + warp / wide * kRows + lane / kLanesRow, j = lane % kLanesRow;
+    float m = -INFINITY, l = 0.f;
+    float4 y[4];  // channels 4 (j + kLanesRow q) .. + 3
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) y[i] = 0.f;
-    if (r < rows) {
-      float mm = -INFINITY;
-      for (int c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, a.part_ml[at(c)].x);
+    for (int q = 0; q < 4; ++q) y[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < rows)
+      for (int c = c0 + part0; c <= c1; c += kCombineParts * wide) {
+        float2 ml[kCombineParts];
+        float4 o[kCombineParts][4];
 #pragma unroll
-      for (int off = 16; off; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kAll, mm, off));
-      safe = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 4
-      for (int c = c0 + part0; c <= c1; c += wide) {
-        const float2 ml = a.part_ml[at(c)];
-        const float w = ex2(ml.x - safe);
-        const float* p = a.part_o + at(c) * D + lane * kPer;
-        ll += ml.y * w;
+        for (int z = 0; z < kCombineParts; ++z) {
+          const int cz = c + z * wide;
+          ml[z] = make_float2(-INFINITY, 0.f);
+          if (cz <= c1) {
+            const int64_t at = ((static_cast<int64_t>(cz) * a.row_tiles + row_tile) * 2 +
+                                (cz == c0 ? slot0 : 0)) * a.rows + r;
+            ml[z] = a.part_ml[at];
+            const float4* p = reinterpret_cast<const float4*>(a.part_o + at * D) + j;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) y[i] += p[i] * w;
+            for (int q = 0; q < 4; ++q) o[z][q] = p[q * kLanesRow];
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[z][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+        float mn = m;
+#pragma unroll
+        for (int z = 0; z < kCombineParts; ++z) mn = fmaxf(mn, ml[z].x);
+        const float safe = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2(m - safe);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[q] = scaled(y[q], f);
+#pragma unroll
+        for (int z = 0; z < kCombineParts; ++z) {
+          const float w = ex2(ml[z].x - safe);
+          l += ml[z].y * w;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) add_scaled(y[q], o[z][q], w);
+        }
       }
-    }
     if (wide > 1) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) y_s[warp][lane * kPer + i] = y[i];
-      if (lane == 0) l_s[warp] = ll;
+      for (int q = 0; q < 4; ++q) y_s[warp][q][lane] = y[q];
+      if (j == 0) ml_s[warp][lane / kLanesRow] = make_float2(m, l);
       __syncthreads();
-      if (part0 == 0)
-        for (int w = warp + 1; w < warp + wide; ++w) {
-          ll += l_s[w];
+      if (part0 == 0) {
+        float mn = m;
+        for (int w = warp + 1; w < warp + wide; ++w) mn = fmaxf(mn, ml_s[w][lane / kLanesRow].x);
+        const float safe = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2(m - safe);
+        l *= f;
 #pragma unroll
-          for (int i = 0; i < kPer; ++i) y[i] += y_s[w][lane * kPer + i];
+        for (int q = 0; q < 4; ++q) y[q] = scaled(y[q], f);
+        for (int w = warp + 1; w < warp + wide; ++w) {
+          const float2 ml = ml_s[w][lane / kLanesRow];
+          const float g = ex2(ml.x - safe);
+          l += ml.y * g;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) add_scaled(y[q], y_s[w][q][lane], g);
         }
+        m = mn;
+      }
       __syncthreads();
     }
     if (r < rows && part0 == 0) {
-      const float inv = ll == 0.f ? 0.f : 1.f / ll;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
       const int node = (r0 + r) / a.G, head = h * a.G + (r0 + r) - node * a.G;
-      uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<E*>(a.out) + b * a.ob + node * a.ot +
-                                                  head * a.oh + lane * kPer);
+      uint2* out = reinterpret_cast<uint2*>(static_cast<E*>(a.out) + b * a.ob + node * a.ot +
+                                            head * a.oh) + j;
 #pragma unroll
-      for (int i = 0; i < kPer / 2; ++i) out[i] = pack2<E>(y[2 * i] * inv, y[2 * i + 1] * inv);
-      if (a.lse && lane == 0)  // log 0 = -inf: nothing seen
-        a.lse[(static_cast<int64_t>(b) * a.t.T + node) * Hq + head] = safe * kLn2 + logf(ll);
+      for (int q = 0; q < 4; ++q)
+        out[q * kLanesRow] = make_uint2(pack2<E>(y[q].x * inv, y[q].y * inv),
+                                        pack2<E>(y[q].z * inv, y[q].w * inv));
+      if (a.lse && j == 0)  // log 0 = -inf: nothing seen
+        a.lse[(static_cast<int64_t>(b) * a.t.T + node) * Hq + head] =
+            (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
     }
   }
 }
