@@ -171,26 +171,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-      "%10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -594,30 +574,21 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
                         max3(mx[1], __uint_as_float(x[62]), __uint_as_float(x[63])),
                         fmaxf(mx[2], mx[3])) * sl;
           };
-          bool known = tile == tile_lo;  // that m is near enough
-          if (known) m = maximum();
-          // The weights are taken with the reference as it is, beside the maximum that
-          // tells whether it will do, and again in the rare case that it does not.
-          uint64_t sum[2];
-          uint32_t p[32];
-          while (true) {
-            const float safe = m == -INFINITY ? 0.f : m;
-            const uint64_t sl2 = pack_f32x2(sl, sl), off2 = pack_f32x2(-safe, -safe);
-            sum[0] = sum[1] = 0;
+          float mx[4];
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const uint64_t y2 = fma_f32x2(pack_u32x2(x[2 * c], x[2 * c + 1]), sl2, off2);
-              float y, z;
-              unpack_f32x2(y2, y, z);
-              y = ex2(y);
-              z = ex2(z);
-              sum[c & 1] = add_f32x2(sum[c & 1], pack_f32x2(y, z));
-              p[c] = pack2<E>(y, z);
-            }
-            if (known) break;
-            const float top = maximum();
-            if (!__any_sync(kAll, top > m + kRise)) break;  // (m = -inf: anything above)
-            known = true;
+          for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(x[c]);
+#pragma unroll
+          for (int c = 4; c < 60; c += 8)
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              mx[z] = max3(mx[z], __uint_as_float(x[c + z]), __uint_as_float(x[c + 4 + z]));
+          const float top =
+              max3(max3(mx[0], __uint_as_float(x[60]), __uint_as_float(x[61])),
+                   max3(mx[1], __uint_as_float(x[62]), __uint_as_float(x[63])),
+                   fmaxf(mx[2], mx[3])) * sl;
+          if (tile == tile_lo) {
+            m = top;
+          } else if (__any_sync(kAll, top > m + kRise)) {  // (m = -inf: anything above)
             if (!wait(&pv_done[2 * stream + (odd ^ 1)], ((i - 1) >> 1) & 1, a.t.err)) return false;
             __syncwarp();
             tc_fence_after();
@@ -626,13 +597,28 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
             l *= f;
             m = mn;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(to + c, o);
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32_issue(to + c, o);
+              tmem_ld32_wait(o);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st16(to + c, o);
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(to + c, o);
             }
+          }
+          const float safe = m == -INFINITY ? 0.f : m;
+          const uint64_t sl2 = pack_f32x2(sl, sl), off2 = pack_f32x2(-safe, -safe);
+          uint64_t sum[2] = {0, 0};
+          uint32_t p[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const uint64_t y2 = fma_f32x2(pack_u32x2(x[2 * c], x[2 * c + 1]), sl2, off2);
+            float y, z;
+            unpack_f32x2(y2, y, z);
+            y = ex2(y);
+            z = ex2(z);
+            sum[c & 1] = add_f32x2(sum[c & 1], pack_f32x2(y, z));
+            p[c] = pack2<E>(y, z);
           }
           float s0, s1;
           unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
