@@ -6,8 +6,8 @@
 // The G = q_heads / kv_heads query heads that share a key head read the same
 // keys, so the T nodes and G heads make one matrix of M = T G rows against the
 // keys of (sequence, key head): row r is node r / G, head h G + r % G.  Each key
-// and value is then read once per kRows rows and used 2 kRows times, and the
-// work is two matrix products around an exponential.
+// and value is then read once per row tile of up to 256 rows, and the work is two
+// matrix products around an exponential.
 //
 // Split.  Lengths live on the device and differ by sequence, so the host
 // cannot cut the work.  A unit is one tile of keys of one sequence and key head;
@@ -16,7 +16,7 @@
 // as it holds groups of one CTA for each row tile: the CTAs of a group walk the
 // same keys side by side, so that HBM is read once and L2 serves the rest (with
 // each row tile a range of its own, 32 sequences of 16 to 32 thousand positions and
-// 512 rows read their keys twice: 1.37 ms instead of REPLACE2).  A CTA that covers
+// 512 rows read their keys twice: 1.37 ms instead of 1.20).  A CTA that covers
 // all tiles of a head writes its output; one that covers a part writes its running
 // maximum, sum and unnormalised output to the workspace (a range has at most two
 // such ends), and combine_kernel adds the parts in the order of the keys.
@@ -44,10 +44,17 @@
 // scores of tile i+1 are computed over those of tile i while its softmax runs.  P
 // has two buffers, so neither product ever waits for the other one (with two S
 // and P written over S, tile i+1's scores waited for tile i-1's output: 1830 cycles
-// a pair of tiles at 256 rows instead of REPLACE).
+// a tile of two streams instead of 1450).
 // With M = T G rows up to 128: one stream, two CTAs on an SM.  Above: one CTA with
-// two streams (256 rows), which share each K and V tile, so that the shared-memory
-// fill per row, the next bound after HBM, is halved.
+// two streams (256 rows), which share each K and V tile, so that a tile crosses L2
+// and fills shared memory once for 256 rows.
+//
+// Bounds.  A tile of 64 keys of 128 channels is 32 KB: 1400 cycles of one SM's share
+// of HBM.  Its MMAs take a stream 384 + 256 cycles (measured: 48 for 128 x 64 x 16
+// with both operands in shared memory, which reads 6 KB at 128 bytes a cycle, 64 for
+// 128 x 128 x 16 with A in TMEM), and its softmax about 700 of a warp that shares
+// its scheduler with the other stream's.  So HBM bounds up to 128 rows, all three
+// meet at 256 (about 1450 cycles a tile), and the tensor cores bound what has more.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
