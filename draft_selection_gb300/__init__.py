@@ -12,6 +12,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 from . import build as _build
 
 STATUS = {0: "DFL2_OK", 1: "DFL2_ERR_INVALID_ARG", 2: "DFL2_ERR_UNSUPPORTED",
@@ -137,25 +139,24 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_raw_stream = None  # torch's current stream as an address, without a Stream object (3 us a call)
+_cuda_ready = False
 
 
 def _stream(stream):
-    global _raw_stream
+    """The stream's address; None: torch's current stream (looked up without making a
+    Stream object, which takes 3 us)."""
+    global _cuda_ready
     if stream is None:
-        if _raw_stream is None:
-            import torch
+        if not _cuda_ready:
             torch.cuda.init()
-            get, dev = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-            _raw_stream = lambda: get(dev())  # noqa: E731
-        return _raw_stream()
+            _cuda_ready = True
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 def _dtype_code(t) -> int:
-    import torch
     if t.dtype == torch.float32:
         return DFL2_F32
     if t.dtype == torch.bfloat16:
@@ -211,7 +212,6 @@ def dfl2_tail_workspace_size(B: int, L: int, V: int, d: int) -> int:
 
 def workspace(nbytes: int, device="cuda"):
     """A zero-filled device workspace of nbytes (torch allocation; plumbing only)."""
-    import torch
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
@@ -379,29 +379,20 @@ def dfl2_tail_tables(logits, verified_tok, hidden, W_H, P_A, P_B, temperature: f
 # These calls are short (a few microseconds on the GPU), so their marshalling is kept
 # short too: types and shapes, which the C side cannot see, are checked in one pass.
 _S3, _S4 = ctypes.c_int64 * 3, ctypes.c_int64 * 4
+_I32 = torch.int32
+_CODES = {torch.float32: DFL2_F32, torch.bfloat16: DFL2_BF16, torch.float16: DFL2_F16}
 
 
 def _i32(t, name, shape):
     """An int32 device array's address, of the given shape; None stays None."""
     if t is None:
         return None
-    if t.dtype != _torch().int32:
+    if t.dtype is not _I32:
         raise TypeError(f"{name} must be int32, not {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {shape}, not {tuple(t.shape)} with strides "
                          f"{t.stride()}")
     return t.data_ptr()
-
-
-_torch_module = None
-
-
-def _torch():
-    global _torch_module
-    if _torch_module is None:
-        import torch
-        _torch_module = torch
-    return _torch_module
 
 
 def _strides(t):
@@ -418,9 +409,7 @@ class Cache:
     table int32 [rows, cols], refs int32 [pages], free_bits int32 [ceil(pages/32)]."""
 
     def __init__(self, k, v, table, refs, free_bits):
-        torch = _torch()
-        codes = {torch.float32: DFL2_F32, torch.bfloat16: DFL2_BF16, torch.float16: DFL2_F16}
-        if k.dtype not in codes or v.dtype != k.dtype:
+        if k.dtype not in _CODES or v.dtype != k.dtype:
             raise TypeError(f"k and v must both be float32, bf16 or fp16, not {k.dtype}, {v.dtype}")
         st = _strides(k)
         if k.dim() != 5 or v.shape != k.shape or _strides(v) != st or k.stride(4) != 1:
@@ -435,7 +424,7 @@ class Cache:
         self.k, self.v, self.table, self.refs, self.free_bits = k, v, table, refs, free_bits
         self.dtype, self.kv_heads, self.head_dim = k.dtype, heads, dim
         self._s = _CacheStruct(
-            k.data_ptr(), v.data_ptr(), codes[k.dtype], layers, pages, heads, page_size, dim,
+            k.data_ptr(), v.data_ptr(), _CODES[k.dtype], layers, pages, heads, page_size, dim,
             st[0], st[1], st[2], st[3], table.data_ptr(), table.shape[0],
             table.shape[1], refs.data_ptr(), free_bits.data_ptr())
         self._ref = ctypes.byref(self._s)
@@ -444,7 +433,6 @@ class Cache:
 def cache(layers: int, pages: int, kv_heads: int, page_size: int, head_dim: int, rows: int,
           cols: int, dtype=None, device="cuda") -> Cache:
     """A new, empty Cache (torch allocation; plumbing only)."""
-    torch = _torch()
     shape = (layers, pages, kv_heads, page_size, head_dim)
     dtype = dtype or torch.bfloat16
     bits = torch.full(((pages + 31) // 32,), -1, dtype=torch.int32, device=device)
@@ -545,10 +533,8 @@ def dfl2_tree_accept(tokens, parents, target, path, n_path, next_token, count=No
 def dfl2_tree_attn_workspace_size(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int,
                                   dtype) -> int:
     """dtype: a torch dtype or DFL2_BF16 / DFL2_F16."""
-    torch = _torch()
-    code = {torch.float32: DFL2_F32, torch.bfloat16: DFL2_BF16, torch.float16: DFL2_F16}
     return int(load().dfl2_tree_attn_workspace_size(B, T, q_heads, kv_heads, head_dim,
-                                                    code.get(dtype, dtype)))
+                                                    _CODES.get(dtype, dtype)))
 
 
 def dfl2_tree_attn(q, cache, layer: int, length, mask, out, ws, rows=None, count=None, lse=None,
@@ -563,7 +549,7 @@ def dfl2_tree_attn(q, cache, layer: int, length, mask, out, ws, rows=None, count
         raise ValueError(f"head_dim {D} against the cache's {cache.head_dim}, strides {qs}, {os_}")
     lse_p = None
     if lse is not None:
-        if (lse.dtype != _torch().float32 or lse.shape != shape[:3] or not lse.is_contiguous()):
+        if (lse.dtype is not torch.float32 or lse.shape != shape[:3] or not lse.is_contiguous()):
             raise ValueError("lse must be contiguous float32 [B, T, q_heads]")
         lse_p = lse.data_ptr()
     one = (B,)

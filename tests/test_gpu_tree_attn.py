@@ -155,6 +155,30 @@ def test_ragged_batch(T, G):
     go(lens, T, 2 * G, 2, 128, 16, counts=counts, seed=T, rows=True)
 
 
+@pytest.mark.parametrize("T,G", [(100, 5), (61, 7), (256, 3), (3, 128), (2, 100), (129, 1), (9, 48)])
+def test_row_tiles(T, G):
+    """Rows in several tiles and streams, whole nodes in each; some of them past the count."""
+    go([200, 0, 70], T, G, 1, 64, 16, counts=[T, T, max(1, T // 3)], seed=T)
+    go([333], T, 2 * G, 2, 128, 32, seed=G, mask="random")
+
+
+def test_many_sequences():
+    """More sequences than a warp looks up at once, most of them without work."""
+    lens = [0] * 40 + [5, 300, 64] + [0] * 30 + [17] + [0] * 26
+    counts = [0] * 40 + [3, 2, 1] + [0] * 30 + [3] + [0] * 26
+    go(lens, 3, 4, 2, 128, 16, counts=counts, rows=True)
+    rng = np.random.default_rng(8)
+    go([int(x) for x in rng.integers(0, 90, 133)], 2, 4, 2, 64, 8, seed=8)
+
+
+def test_counts_past_their_ends():
+    c = Case([40, 9], 4, 4, 2, 128, 16, counts=[4, 0], seed=2)
+    want, wl = c.run()
+    c.count.copy_(torch.tensor([9, -3], dtype=torch.int32))
+    out, lse = c.run()
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
 def test_one_long_sequence():
     go([20011], 17, 4, 1, 128, 16, seed=1)
     go([20011], 1, 4, 2, 64, 64, seed=2, dtype=torch.float16)
