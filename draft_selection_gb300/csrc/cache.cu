@@ -74,7 +74,10 @@ __device__ __forceinline__ Span span_of(const TakeArgs& a, int b) {
   return s;
 }
 
-// One CTA: which sequences get their pages, and the pages themselves.
+// One CTA: which sequences get their pages, and the pages themselves.  Bound by its
+// dependent steps (lengths, table entries, two scans, the table again), not by the
+// pages/8 bytes of the map: 5.5 us cold for one sequence, 7 for 64 with 33 nodes each,
+// 17 for 128 forks (ncu, caches flushed), less in a turn, where PDL hides its start.
 template <bool kFork>
 __global__ void __launch_bounds__(kBookThreads) take_kernel(const __grid_constant__ TakeArgs a) {
   __shared__ int offs[kMaxSeqs];  // a sequence's need; then its first page's rank, -1 if unserved
@@ -276,6 +279,8 @@ struct WriteArgs {
   int layer, n_layers, B;
 };
 
+// Bound by HBM: 8 prompts of 300 to 2000 tokens into 24 layers, 8 heads x 128 channels,
+// 0.97 GB read and as much written, in 271 us: 7.2 TB/s (the copy peak is 6.8).
 __global__ void __launch_bounds__(256) write_kernel(const __grid_constant__ WriteArgs a) {
   pdl_wait();
   pdl_launch_dependents();
@@ -309,7 +314,9 @@ struct ForkCopyArgs {
   int layers, n;
 };
 
-// The positions of the partly filled last page, every layer.
+// The positions of the partly filled last page, every layer.  Bound by HBM: 128 forks
+// of 32 sequences, pages of 64, 32 layers, 617 MB written and a quarter of it read (a
+// parent's four children share it in L2), in 127 us: 6.1 TB/s.
 __global__ void __launch_bounds__(256) fork_copy_kernel(const __grid_constant__ ForkCopyArgs a) {
   pdl_wait();
   pdl_launch_dependents();
@@ -343,54 +350,72 @@ struct CompactArgs {
   int layers, B;
 };
 
-// A thread owns one 16-byte column of K or V of one sequence and layer and
-// moves it down the path.  The path ascends strictly, so path[i] >= i and a row
-// that is written has been read before: reading ahead in batches is safe.
-__global__ void __launch_bounds__(128) compact_kernel(const __grid_constant__ CompactArgs a) {
+// A block works out where a sequence's moving rows come from and go to once, a
+// thread to a node; then a thread owns one 16-byte column of K or V in one layer and
+// moves it down that list, eight rows in flight.  The path ascends strictly, so
+// path[i] >= i and a row that is written has been read before: reading ahead is safe.
+// Bound by the chain of dependent reads (path, table, rows).  The whole turn of 64
+// sequences, 16 layers: 62.2 us, 64.0 where every thread looked its rows up for itself.
+constexpr int kMoveThreads = kMaxTree;
+__global__ void __launch_bounds__(kMoveThreads)
+    compact_kernel(const __grid_constant__ CompactArgs a) {
+  __shared__ int64_t from_s[kMaxTree], to_s[kMaxTree];
+  __shared__ int warp_sums[kMoveThreads / 32];
+  constexpr int kBatch = 8;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int kBatch = 8;
-  const int mask = (1 << a.t.page_shift) - 1;
-  const int64_t items = static_cast<int64_t>(a.layers) * a.B * 2 * a.r.chunks;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; it < items;
-       it += step) {
-    const uint32_t c = static_cast<uint32_t>(it % (2 * a.r.chunks));
-    const int64_t lb = it / (2 * a.r.chunks);
-    const int b = static_cast<int>(lb % a.B), l = static_cast<int>(lb / a.B);
-    const int count = a.t.count_of(b), n = min(a.n_path[b], count);
-    const int row = a.t.row_of(b);
-    if (row < 0 || n <= 0) continue;
-    const int len = a.t.length[b];
-    const bool is_v = c >= static_cast<uint32_t>(a.r.chunks);
-    const uint32_t col = is_v ? c - a.r.chunks : c;
+  const int count = a.t.count_of(b), n = min(a.n_path[b], count), row = a.t.row_of(b);
+  if (row < 0 || n <= 0) return;
+  const int len = a.t.length[b], slots = (1 << a.t.page_shift) - 1;
+  bool moves = false;
+  int64_t src = 0, dst = 0;
+  if (tid < n) {
+    const int from = a.path[static_cast<int64_t>(b) * a.t.T + tid];
+    if (from != tid) {
+      const int64_t pf = from > tid && from < count
+                             ? a.t.page_at(row, (len + from) >> a.t.page_shift)
+                             : -1;
+      const int64_t pt = a.t.page_at(row, (len + tid) >> a.t.page_shift);
+      if (from < tid || from >= count) record_error(a.t.err, kDevErrBadIndex);
+      moves = pf >= 0 && pt >= 0;
+      src = pf * a.r.page + ((len + from) & slots) * a.r.slot;
+      dst = pt * a.r.page + ((len + tid) & slots) * a.r.slot;
+    }
+  }
+  const unsigned mine = __ballot_sync(kAll, moves);
+  if (lane == 0) warp_sums[warp] = __popc(mine);
+  __syncthreads();
+  int at = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kMoveThreads / 32; ++w) {
+    if (w < warp) at += warp_sums[w];
+    total += warp_sums[w];
+  }
+  if (moves) {
+    at += __popc(mine & ((1u << lane) - 1));
+    from_s[at] = src;
+    to_s[at] = dst;
+  }
+  __syncthreads();
+  if (total == 0) return;
+  const int columns = a.layers * 2 * a.r.chunks;
+  for (int c = blockIdx.x * kMoveThreads + tid; c < columns; c += gridDim.x * kMoveThreads) {
+    const int l = c / (2 * a.r.chunks);
+    uint32_t col = c - l * 2 * a.r.chunks;
+    const bool is_v = col >= static_cast<uint32_t>(a.r.chunks);
+    if (is_v) col -= a.r.chunks;
     const uint32_t h = a.r.per_head.div(col);
     uint4* base = (is_v ? a.r.v : a.r.k) + l * a.r.layer + h * a.r.head +
                   (col - h * a.r.per_head.d);
-    const int32_t* path = a.path + static_cast<int64_t>(b) * a.t.T;
-    for (int i0 = 0; i0 < n; i0 += kBatch) {
+    for (int i = 0; i < total; i += kBatch) {
       uint4 x[kBatch];
-      int64_t to[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = i0 + j;
-        to[j] = -1;
-        if (i >= n) continue;
-        const int from = path[i];
-        if (from == i) continue;
-        if (from < i || from >= count) {
-          record_error(a.t.err, kDevErrBadIndex);
-          continue;
-        }
-        const int64_t pf = a.t.page_at(row, (len + from) >> a.t.page_shift);
-        const int64_t pt = a.t.page_at(row, (len + i) >> a.t.page_shift);
-        if (pf < 0 || pt < 0) continue;
-        x[j] = base[pf * a.r.page + ((len + from) & mask) * a.r.slot];
-        to[j] = pt * a.r.page + ((len + i) & mask) * a.r.slot;
-      }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
-        if (to[j] >= 0) base[to[j]] = x[j];
+        if (i + j < total) x[j] = base[from_s[i + j]];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (i + j < total) base[to_s[i + j]] = x[j];
     }
   }
 }
@@ -444,6 +469,8 @@ dfl2_status check_cache_host(const dfl2_cache* c) {
   if (c->layers < 1 || c->pages < 1 || c->kv_heads < 1 || c->head_dim < 1 || c->rows < 1 ||
       c->cols < 1)
     return report_errorf(DFL2_ERR_INVALID_ARG, "every size of the cache must be >= 1");
+  if (c->layers > 4096)
+    return report_errorf(DFL2_ERR_UNSUPPORTED, "layers=%d: at most 4096", c->layers);
   if (c->page_size < 8 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
     return report_errorf(DFL2_ERR_UNSUPPORTED, "page_size %d: a power of two, 8 to 256",
                          c->page_size);
@@ -558,9 +585,12 @@ dfl2_status dfl2_cache_compact(const dfl2_cache* cache, int B, int T, const int3
   DFL2_TRY(check_all_device(cache, ptrs));
   const dfl2::CompactArgs a{dfl2::table_view(cache, table_rows, length, count, T),
                             dfl2::row_view(cache), path, n_path, new_length, cache->layers, B};
-  const int64_t columns = static_cast<int64_t>(cache->layers) * B * 2 * a.r.chunks;
-  cudaError_t e = dfl2::launch_k(dfl2::compact_kernel, dim3(dfl2::copy_blocks(columns, 128)),
-                                 dim3(128), 0, cu(stream), true, a);
+  // (at most 4096 layers of 2 x 16384 columns of a sequence: an int holds them)
+  const int64_t columns = static_cast<int64_t>(cache->layers) * 2 * a.r.chunks;
+  const int blocks = static_cast<int>(
+      std::min<int64_t>(1024, (columns + dfl2::kMoveThreads - 1) / dfl2::kMoveThreads));
+  cudaError_t e = dfl2::launch_k(dfl2::compact_kernel, dim3(blocks, B), dim3(dfl2::kMoveThreads), 0,
+                                 cu(stream), true, a);
   if (e == cudaSuccess)
     e = dfl2::launch_k(dfl2::trim_kernel, dim3((B + 3) / 4), dim3(128), 0, cu(stream), true, a);
   return launched(e, "cache compact launch");

@@ -1,6 +1,7 @@
 // Trees of drafted tokens: what each node sees, and the path of the target's
 // tokens through the tree (include/dfl2.h).  A few integers per node: both are
-// bound by the latency of their dependent steps, one warp to a sequence.
+// bound by the latency of their dependent steps (3.0 us each for a chain of 17, 4.2 and
+// 3.9 for 64 trees of 33 nodes; ncu, caches flushed), about 2 us of which is a launch.
 #include <cuda_runtime.h>
 
 #include "cache.cuh"
@@ -21,7 +22,7 @@ struct MaskArgs {
 };
 
 // One CTA a tree, a thread a node: up the chain of parents in shared memory, a
-// bit at a time (33 nodes are rarely deeper than 20: under a microsecond).
+// bit at a time, about 30 cycles a step (a tree of 33 nodes is rarely deeper than 20).
 __global__ void __launch_bounds__(kMaxTree) tree_mask_kernel(const __grid_constant__ MaskArgs a) {
   __shared__ int16_t par[kMaxTree];
   __shared__ uint32_t bits[kMaxTree][kMaxTree / 32 + 1];  // +1: rows on different banks
