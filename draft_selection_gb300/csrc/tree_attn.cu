@@ -709,15 +709,18 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
                 if (z == j) o[z] = __float_as_uint(__uint_as_float(o[z]) + y);
             }
           if (mine && whole) {
+            uint32_t y[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint4 y;
-              uint32_t* yy = reinterpret_cast<uint32_t*>(&y);
+            for (int j = 0; j < 16; ++j)
+              y[j] = pack2<E>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+            if (a.out32) {
+              st_v8(out + c, y);
+              st_v8(out + c + 16, y + 8);
+            } else {
 #pragma unroll
-              for (int z = 0; z < 4; ++z)
-                yy[z] = pack2<E>(__uint_as_float(o[8 * j + 2 * z]) * inv,
-                                 __uint_as_float(o[8 * j + 2 * z + 1]) * inv);
-              *reinterpret_cast<uint4*>(out + c + 8 * j) = y;
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(out + c + 8 * j) =
+                    make_uint4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
             }
           } else if (mine) {
 #pragma unroll
@@ -1095,6 +1098,9 @@ dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_c
   a.ot = out_strides[1];
   a.oh = out_strides[2];
   a.lse = lse;
+  a.out32 = reinterpret_cast<uintptr_t>(out) % 32 == 0;
+  for (int i = 0; i < 3; ++i)
+    if (dims[i] > 1 && out_strides[i] % 16) a.out32 = false;
   a.part_o = reinterpret_cast<float*>(w + p.o_off);
   a.part_ml = reinterpret_cast<float2*>(w + p.ml_off);
   a.cuts = reinterpret_cast<dfl2::Cut*>(w + p.cut_off);

@@ -42,6 +42,8 @@ struct AttnArgs {
   float scale_log2;      // scale * log2 e
   void* out;
   int64_t ob, ot, oh;
+  bool out32;      // every row of out begins on 32 bytes: stored so (143 us, 16 at a time 146:
+                   // 64 trees of 33 nodes)
   float* lse;      // nullable
   float* part_o;   // [CTAs][2][rows][D] unnormalised outputs
   float2* part_ml; // [CTAs][2][rows] (maximum, sum)

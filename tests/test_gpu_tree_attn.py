@@ -196,6 +196,9 @@ def test_layouts(T):
     c.check(out, lse)
     a, _ = c.run(lse=False)
     assert torch.equal(a, out)
+    part = torch.full((2, T, 8, 136), float("nan"), dtype=torch.bfloat16, device="cuda")
+    c.run(out=part[..., 8:])  # rows that begin on 16 bytes and not on 32
+    assert torch.equal(part[..., 8:], out) and torch.isnan(part[..., :8]).all()
     b, _ = c.run(q=c.q.cuda().transpose(1, 2).contiguous().transpose(1, 2))  # heads outside nodes
     assert torch.equal(b, out)
     one = Case([100], T, 8, 1, 64, 32, nhd=True, seed=6, spare=0)  # dimensions of one entry
