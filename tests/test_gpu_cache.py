@@ -209,6 +209,19 @@ def test_counts_as_a_number_and_no_rows():
     assert length.tolist() == [0, 0]
 
 
+def test_counts_no_row_can_hold():
+    p = Pair(3, 8, 40, 16)
+    big = (1 << 31) - 1
+    assert p.reserve([0, 1, 2], [5, 0, 100], [big, 1 << 30, 29]) == [0, 0, 0]
+    p.same()
+    assert p.reserve([0, 2], [0, 100], [128, 28]) == [1, 1]  # the last entries, to the brim
+    p.same()
+    served = i32([7])
+    dfl2.dfl2_cache_reserve(p.c, i32([-3]), 4, served)
+    assert served.tolist() == [0]
+    p.same()
+
+
 def test_odd_rows():
     """Rows whose 16-byte pieces are no power of two, in a part of a wider tensor."""
     k = torch.zeros(2, 7, 3, 8, 96, dtype=torch.float16, device="cuda")
