@@ -568,19 +568,6 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
             for (int c = 0; c < 64; ++c)
               if (!(vis >> c & 1)) x[c] = 0xFF800000u;  // -inf
           }
-          auto maximum = [&]() {
-            float mx[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(x[c]);
-#pragma unroll
-            for (int c = 4; c < 60; c += 8)
-#pragma unroll
-              for (int z = 0; z < 4; ++z)
-                mx[z] = max3(mx[z], __uint_as_float(x[c + z]), __uint_as_float(x[c + 4 + z]));
-            return max3(max3(mx[0], __uint_as_float(x[60]), __uint_as_float(x[61])),
-                        max3(mx[1], __uint_as_float(x[62]), __uint_as_float(x[63])),
-                        fmaxf(mx[2], mx[3])) * sl;
-          };
           float mx[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(x[c]);
