@@ -83,7 +83,10 @@ struct TcCfg {
   static constexpr int kQ = kLanes * D * 2;                    // bytes of a stream's Q
   static constexpr int kThreads = 32 * (1 + NS) + NS * kLanes;
   static constexpr int kBars = 2 * kSlots + NS * 8;
-  static constexpr size_t kSmem = size_t(NS) * kQ + size_t(kSlots) * kSlot + kBars * 8 + 64;
+  static constexpr int kBadSegs = 16;
+  static constexpr size_t kSmem = size_t(NS) * kQ + size_t(kSlots) * kSlot + kBars * 8 +
+                                  (2 + kBadSegs) * 4;
+  static_assert(kBadSegs > kSlots / 2 + 1, "a head's mark outlives its last reader");
   static_assert(NS * kStreamCols * kCtas <= 512, "TMEM");
   static_assert((kSmem + 1024) * kCtas <= 233472, "shared memory");
 };
@@ -282,10 +285,12 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
   uint64_t* pv_done = p_ready + 2 * NS;  // [NS][2] the output product is in O
   uint64_t* all_done = pv_done + 2 * NS; // [NS]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + NS);
-  int* bad_seg = reinterpret_cast<int*>(tmem_slot + 1);  // [4] row tile that met Inf or NaN in V
+  // Heads of this CTA's range, counted up, that met Inf or NaN in V.  Stream 0, which looks,
+  // may be as many tiles, so heads, ahead of stream 1 as half the ring has slots.
+  int* bad_seg = reinterpret_cast<int*>(tmem_slot + 1);  // [kBadSegs]
   // Warps that have cleaned an edge tile's V, counted up: stream 0 may be several tiles
   // ahead of stream 1, more than a barrier's parity can tell apart.
-  uint32_t* v_clean = reinterpret_cast<uint32_t*>(bad_seg + 4);
+  uint32_t* v_clean = reinterpret_cast<uint32_t*>(bad_seg + C::kBadSegs);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -304,7 +309,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
       mbar_init(&all_done[s], 1);
     }
     *v_clean = 0;
-    for (int i = 0; i < 4; ++i) bad_seg[i] = -1;
+    for (int i = 0; i < C::kBadSegs; ++i) bad_seg[i] = -1;
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
@@ -643,7 +648,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
               found = true;
             }
           }
-          if (found) bad_seg[seg & 3] = seg;
+          if (found) bad_seg[seg % C::kBadSegs] = seg;
           fence_proxy_async_smem();
         }
         tc_fence_before();
@@ -675,7 +680,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
             make_cut(g, at.u - tile_lo, at.b, h, s.tiles);
       if (live) {
         const int head = h * a.G + r - node * a.G;
-        const bool bad = *reinterpret_cast<volatile int*>(&bad_seg[seg & 3]) == seg;
+        const bool bad = *reinterpret_cast<volatile int*>(&bad_seg[seg % C::kBadSegs]) == seg;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * a.rows +
                              stream * a.stream_rows + row_l;

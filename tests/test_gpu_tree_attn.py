@@ -242,6 +242,24 @@ def test_unseen_nodes_hold_anything(T, G, dtype):
             assert torch.isnan(out[b, i]).all() and torch.isnan(lse[b, i]).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_inf_in_many_short_sequences(D):
+    """Every sequence is one tile with an Inf of its own: two streams of rows, one of which
+    may be several sequences ahead of the other."""
+    B, T = 3000, 20
+    c = Case([b % 44 for b in range(B)], T, 8, 1, D, 64, seed=D)
+    table = c.cache.table.cpu()
+    for b in range(B):
+        page = int(table[b, 0])
+        c.cache.v[0, page, 0, c.lens[b] + b % T, b % D] = float("inf")
+    out = c.run()[0].cpu()
+    for b in range(B):
+        want = torch.zeros(T, 8, D, dtype=torch.bool)
+        want[torch.from_numpy(np.nonzero(c.seen[b][:, b % T])[0]), :, b % D] = True
+        assert torch.equal(out[b] == float("inf"), want), b
+        assert torch.isfinite(out[b][~want]).all(), b
+
+
 def test_large_scores_and_scale():
     c = Case([300, 5], 7, 4, 2, 128, 16, amp=6.0, seed=9)
     out, lse = c.run()
