@@ -70,8 +70,8 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
   return s;
 }
 
-// Where range c of `units` units in `n` ranges begins, and which range unit u is in.  (32-bit divisions where they do: a 64-bit one is a chain of some 100
-// instructions.)
+// Where range c of `units` units in `n` ranges begins, and which range unit u is in.
+// (32-bit divisions where they do: a 64-bit one is a chain of some 100 instructions.)
 __device__ __forceinline__ int64_t range_start(int64_t units, int n, int c) {
   if (units < (1 << 20))  // n and c are at most a few thousand
     return static_cast<uint32_t>(units) * static_cast<uint32_t>(c) / static_cast<uint32_t>(n);
@@ -114,7 +114,8 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Range `cta` [u0, u1) of the units in n_cta ranges, and the place where it begins, by a warp together.  Up to 32 sequences need one load of their lengths.
+// Range `cta` [u0, u1) of the units in n_cta ranges, and the place where it begins, by a
+// warp together.  Up to 32 sequences need one load of their lengths.
 struct Range {
   int64_t units, u0, u1;
   int n_cta;
@@ -140,7 +141,7 @@ __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
   g.u1 = range_start(g.units, g.n_cta, cta + 1);
   // the sequence that u0 falls in
   int64_t base = 0;
-  for (int b0 = 0;; b0 += 32) {
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
     if (a.B > 32) own = b0 + lane < a.B ? load_seq(a, b0 + lane) : Seq{0, 0, 0, 0};
     int64_t sum = static_cast<int64_t>(own.tiles) * per;
     const int64_t mine = sum;
@@ -168,6 +169,8 @@ __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
     }
     base += __shfl_sync(kAll, sum, 31);
   }
+  g.u1 = g.u0;  // the lengths changed in between: no work, and no endless search
+  return g;
 }
 
 // Of the head whose first unit is v0.
