@@ -108,12 +108,17 @@ __global__ void __launch_bounds__(kBookThreads) take_kernel(const __grid_constan
     }
     if (lane == 0) offs[b] = ok ? need : -1;
   }
-  // the free pages: each thread the words [w0, w1) of the bit map
-  const int words = (a.t.pages + 31) / 32;
+  // the free pages: each thread the words [w0, w1) of the bit map (bits past the pages
+  // are none)
+  const int words = (a.t.pages - 1) / 32 + 1;
+  auto free_word = [&](int w) {
+    const uint32_t x = a.t.free_bits[w];
+    return w < words - 1 ? x : x & (0xffffffffu >> (31 - ((a.t.pages - 1) & 31)));
+  };
   const int wper = (words + kBookThreads - 1) / kBookThreads;
   const int w0 = min(words, tid * wper), w1 = min(words, w0 + wper);
   int mine = 0;
-  for (int w = w0; w < w1; ++w) mine += __popc(a.t.free_bits[w]);
+  for (int w = w0; w < w1; ++w) mine += __popc(free_word(w));
   int n_free, total;
   int rank = block_scan(mine, n_free, warp_sums);  // rank of this thread's first free page
   // served in order while the pages last
@@ -136,7 +141,7 @@ __global__ void __launch_bounds__(kBookThreads) take_kernel(const __grid_constan
   const int taken = taken_s;
 
   int w = w0;
-  uint32_t left = w < w1 ? a.t.free_bits[w] : 0u;
+  uint32_t left = w < w1 ? free_word(w) : 0u;
   for (int r0 = 0; r0 < taken; r0 += kListCap) {
     const int r1 = min(taken, r0 + kListCap);
     // the pages of ranks [r0, r1), each from the thread that holds its word
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kBookThreads) take_kernel(const __grid_constan
       if (gone) a.t.free_bits[w] &= ~gone;
       if (!left) {
         ++w;
-        left = w < w1 ? a.t.free_bits[w] : 0u;
+        left = w < w1 ? free_word(w) : 0u;
       }
     }
     __syncthreads();
@@ -528,6 +533,10 @@ dfl2_status dfl2_cache_reserve(const dfl2_cache* cache, int B, int T, const int3
                          {count, "count", 4, true}, {served, "served", 4}};
   DFL2_TRY(dfl2::check_batch(B, T, 1 << 30));
   DFL2_TRY(check_all_host(cache, ptrs));
+  // (the pages that all sequences lack are counted in 32 bits)
+  if (int64_t(B) * std::min<int64_t>(cache->cols, T / cache->page_size + 2) > INT32_MAX)
+    return dfl2::report_errorf(DFL2_ERR_UNSUPPORTED, "B=%d rows of %d entries: at most 2^31 - 1", B,
+                               cache->cols);
   DFL2_TRY(check_all_device(cache, ptrs));
   const dfl2::TakeArgs a{dfl2::table_view(cache, table_rows, length, count, T), nullptr, served, B};
   return launched(dfl2::launch_k(dfl2::take_kernel<false>, dim3(1), dim3(dfl2::kBookThreads), 0,
@@ -539,7 +548,7 @@ dfl2_status dfl2_cache_write(const dfl2_cache* cache, int layer, int n_layers, c
                              const void* v_new, const int64_t* new_strides, int B, int T,
                              const int32_t* table_rows, const int32_t* length,
                              const int32_t* count, dfl2_stream stream) {
-  const PtrArg ptrs[] = {{k_new, "k_new", 16}, {v_new, "v_new", 16},
+  const PtrArg ptrs[] = {{k_new, "k_new", 16, T == 0}, {v_new, "v_new", 16, T == 0},
                          {table_rows, "table_rows", 4, true}, {length, "length", 4},
                          {count, "count", 4, true}};
   DFL2_TRY(dfl2::check_batch(B, T, 1 << 30));

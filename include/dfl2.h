@@ -408,7 +408,8 @@ typedef struct dfl2_cache {
  * entries of its table row in that range are filled.  served [B] int32: 1, or 0
  * where the free pages did not reach (sequences are served in order while they
  * do; one that needs no page is served in any case) or the row has too few
- * entries; such a sequence is left as it was.  1 <= B <= 4096, T >= 0. */
+ * entries; such a sequence is left as it was.  1 <= B <= 4096, T >= 0, and B
+ * times the entries that T positions may lie in (at most cols) below 2^31. */
 dfl2_status dfl2_cache_reserve(const dfl2_cache* cache, int B, int T, const int32_t* table_rows,
                                const int32_t* length, const int32_t* count, int32_t* served,
                                dfl2_stream stream);
@@ -418,7 +419,7 @@ dfl2_status dfl2_cache_reserve(const dfl2_cache* cache, int B, int T, const int3
  * sequence b, layer layer+l at l*new_strides[0] + b*new_strides[1] +
  * t*new_strides[2] + h*new_strides[3] + c (host array of four element strides,
  * multiples of 16 bytes, for both).  Positions without a page are skipped and
- * recorded as out of range. */
+ * recorded as out of range.  T >= 0 (0: k_new and v_new may be NULL). */
 dfl2_status dfl2_cache_write(const dfl2_cache* cache, int layer, int n_layers, const void* k_new,
                              const void* v_new, const int64_t* new_strides, int B, int T,
                              const int32_t* table_rows, const int32_t* length,

@@ -112,6 +112,24 @@ def test_bookkeeping_refuses(lib):
     assert lib.dfl2_cache_free(c, 1, None, None) == INVALID
 
 
+def test_needs_that_32_bits_do_not_count_are_refused(lib):
+    c = cache(cols=1 << 20)
+    r = lib.dfl2_cache_reserve
+    assert r(c, 2048, 1 << 30, None, A, A, A, None) == UNSUPPORTED      # 2^31 entries
+    assert r(c, 2048, 16 << 20, None, A, None, A, None) == UNSUPPORTED
+    # (what is in range fails later, for want of a device or of its memory)
+    assert r(c, 2047, 1 << 30, None, A, A, A, None) not in (0, UNSUPPORTED)
+    assert r(c, 4096, 1 << 20, None, A, None, A, None) not in (0, UNSUPPORTED)
+
+
+def test_no_rows_to_write_need_no_address(lib):
+    w = lib.dfl2_cache_write
+    st = S4(0, 0, 0, 0)
+    args = 0, 1, None, None, st, 1, 0, None, A, None, None
+    assert w(cache(), *args) not in (0, INVALID, UNSUPPORTED)           # A is no device memory
+    assert w(cache(), 0, 1, None, A, st, 1, 1, None, A, None, None) == INVALID
+
+
 def test_trees_refuse(lib):
     m, t = lib.dfl2_tree_mask, lib.dfl2_tree_accept
     assert m(None, 1, 4, None, A, None, None) == INVALID

@@ -222,6 +222,29 @@ def test_counts_no_row_can_hold():
     p.same()
 
 
+def test_no_rows():
+    p = Pair(2, 4, 6, 8)
+    none = torch.zeros(2, 2, 0, p.c.kv_heads, p.c.head_dim, dtype=p.c.dtype, device="cuda")
+    length, served = i32([0, 0]), i32([7, 7])
+    dfl2.dfl2_cache_reserve(p.c, length, 0, served)
+    dfl2.dfl2_cache_write(p.c, none, none, length)
+    p.same()
+    assert served.tolist() == [1, 1]
+
+
+@pytest.mark.parametrize("pages", [1, 31, 33, 40])
+def test_map_bits_past_the_pages_are_no_pages(pages):
+    c = dfl2.cache(1, pages, 1, 8, 64, 2, 64)
+    c.free_bits.fill_(-1)
+    served = i32([7, 7])
+    dfl2.dfl2_cache_reserve(c, i32([0, 0]), i32([8 * pages - 8, 16]), served)
+    assert served.tolist() == [1, 0]
+    dfl2.dfl2_cache_reserve(c, i32([0, 0]), i32([8 * pages, 8]), served)
+    assert served.tolist() == [1, 0]
+    assert c.table[0, :pages].tolist() == list(range(pages)) and (c.table[1] == -1).all()
+    assert (c.refs == 1).all()
+
+
 def test_odd_rows():
     """Rows whose 16-byte pieces are no power of two, in a part of a wider tensor."""
     k = torch.zeros(2, 7, 3, 8, 96, dtype=torch.float16, device="cuda")
