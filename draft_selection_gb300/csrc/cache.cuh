@@ -57,14 +57,22 @@ struct TableView {
   __device__ __forceinline__ int count_of(int b) const {
     return count ? max(0, min(T, count[b])) : T;
   }
-  // A page number, or -1 (recorded, unless it is the plain "none" that may_lack allows).
-  __device__ __forceinline__ int page_at(int row, int i, bool may_lack = false) const {
-    const int p = static_cast<unsigned>(i) < static_cast<unsigned>(cols)
-                      ? table[static_cast<int64_t>(row) * cols + i]
-                      : -1;
+  // Entry i of a row as it stands, -1 past its end.
+  __device__ __forceinline__ int entry(int row, int i) const {
+    return static_cast<unsigned>(i) < static_cast<unsigned>(cols)
+               ? table[static_cast<int64_t>(row) * cols + i]
+               : -1;
+  }
+  // An entry that is a page number, or -1 (recorded, unless it is the plain "none" that
+  // may_lack allows).
+  __device__ __forceinline__ int checked(int p, bool may_lack = false) const {
     if (static_cast<unsigned>(p) < static_cast<unsigned>(pages)) return p;
     if (!may_lack || p != -1) record_error(err, kDevErrBadIndex);
     return -1;
+  }
+  // Both.
+  __device__ __forceinline__ int page_at(int row, int i, bool may_lack = false) const {
+    return checked(entry(row, i), may_lack);
   }
 };
 
