@@ -75,38 +75,58 @@ __device__ __forceinline__ Span span_of(const TakeArgs& a, int b) {
 
 // One CTA: which sequences get their pages, and the pages themselves.  Bound by its
 // dependent steps (lengths, table entries, two scans, the table again), not by the
-// pages/8 bytes of the map: 5.5 us cold for one sequence, 7 for 64 with 33 nodes each,
-// 17 for 128 forks (ncu, caches flushed), less in a turn, where PDL hides its start.
-template <bool kFork>
+// pages/8 bytes of the map: 5.5 us cold for one sequence (ncu, caches flushed), less in
+// a turn, where PDL hides its start.
+//
+// kWidth lanes of a warp look after a sequence: all 32 while the 32 warps hold every
+// sequence at once, else 8, so that up to 128 still go at once.  With a warp to each in
+// any case, 128 forks take 143.6 us instead of 135.7 and a turn of 64 sequences 62.6
+// instead of 60.9; with 8 lanes in any case, a long prompt's entries take four times the
+// steps.
+template <bool kFork, int kWidth>
 __global__ void __launch_bounds__(kBookThreads) take_kernel(const __grid_constant__ TakeArgs a) {
   __shared__ int offs[kMaxSeqs];  // a sequence's need; then its first page's rank, -1 if unserved
   __shared__ int list[kListCap];
   __shared__ int warp_sums[32];
   __shared__ int taken_s;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   pdl_wait();
   pdl_launch_dependents();
   if (tid == 0) taken_s = 0;
 
-  // the needs, a warp to a sequence
-  for (int b = warp; b < a.B; b += kBookThreads / 32) {
-    const Span s = span_of<kFork>(a, b);
+  constexpr int kGroups = kBookThreads / kWidth;
+  constexpr unsigned kGroupBits = kAll >> (32 - kWidth);
+  const int group = tid / kWidth, gl = lane % kWidth, g0 = lane - gl;  // g0: the group's lane 0
+  const int first = (tid - lane) / kWidth;  // the warp's first group
+  // the needs (the collectives are the warp's, so its groups take the same steps)
+  for (int b0 = 0; b0 + first < a.B; b0 += kGroups) {
+    const int b = b0 + group;
+    const bool there = b < a.B;
+    Span s{-1, 0, 0, false};
+    if (there) s = span_of<kFork>(a, b);
     int need = 0;
-    bool ok = s.ok;
-    if (ok) {
+    bool good = s.ok;
+    if (good) {
       const int32_t* row = a.t.table + static_cast<int64_t>(s.row) * a.t.cols;
       if (kFork) {
         const int src = a.src[b];
-        bool good = static_cast<unsigned>(src) < static_cast<unsigned>(a.t.rows) && src != s.row;
+        good = static_cast<unsigned>(src) < static_cast<unsigned>(a.t.rows) && src != s.row;
         if (good)
-          for (int c = lane; c < s.c1; c += 32)
+#pragma unroll 4
+          for (int c = gl; c < s.c1; c += kWidth)
             good &= row[c] < 0 && a.t.page_at(src, c, true) >= 0;
-        ok = __all_sync(kAll, good);
       }
-      for (int c = s.c0 + lane; c < s.c1; c += 32) need += row[c] < 0;
-      need = __reduce_add_sync(kAll, need);
+#pragma unroll 4
+      for (int c = s.c0 + gl; c < s.c1; c += kWidth) need += row[c] < 0;
     }
-    if (lane == 0) offs[b] = ok ? need : -1;
+    __syncwarp();
+    const bool ok = ((__ballot_sync(kAll, good) >> g0) & kGroupBits) == kGroupBits;
+    if (kWidth == 32)
+      need = __reduce_add_sync(kAll, need);
+    else
+#pragma unroll
+      for (int off = kWidth >> 1; off; off >>= 1) need += __shfl_xor_sync(kAll, need, off);
+    if (there && gl == 0) offs[b] = ok ? need : -1;
   }
   // the free pages: each thread the words [w0, w1) of the bit map (bits past the pages
   // are none)
@@ -163,29 +183,31 @@ __global__ void __launch_bounds__(kBookThreads) take_kernel(const __grid_constan
       }
     }
     __syncthreads();
-    for (int b = warp; b < a.B; b += kBookThreads / 32) {
-      if (offs[b] < 0 || offs[b] >= r1) continue;
-      const Span s = span_of<kFork>(a, b);
+    for (int b0 = 0; b0 + first < a.B; b0 += kGroups) {
+      const int b = b0 + group;
+      const bool takes = b < a.B && offs[b] >= 0 && offs[b] < r1;
+      Span s{-1, 0, 0, false};
+      if (takes) s = span_of<kFork>(a, b);
       int32_t* row = a.t.table + static_cast<int64_t>(s.row) * a.t.cols;
       // entries of lower rank were filled in the rounds before
-      int r = max(offs[b], r0);
-      for (int c = s.c0; c < s.c1 && r < r1; c += 32) {
-        const bool miss = c + lane < s.c1 && row[c + lane] < 0;
-        const unsigned m = __ballot_sync(kAll, miss);
-        const int at = r + __popc(m & ((1u << lane) - 1));
-        if (miss && at < r1) row[c + lane] = list[at - r0];
+      int r = takes ? max(offs[b], r0) : r1;
+      for (int c = s.c0; __any_sync(kAll, c < s.c1 && r < r1); c += kWidth) {
+        const bool miss = r < r1 && c + gl < s.c1 && row[c + gl] < 0;
+        const unsigned m = (__ballot_sync(kAll, miss) >> g0) & kGroupBits;
+        const int at = r + __popc(m & ((1u << gl) - 1));
+        if (miss && at < r1) row[c + gl] = list[at - r0];
         r += __popc(m);
       }
     }
     __syncthreads();
   }
   if (kFork) {  // the whole pages, shared
-    for (int b = warp; b < a.B; b += kBookThreads / 32) {
+    for (int b = group; b < a.B; b += kGroups) {
       if (offs[b] < 0) continue;
       const Span s = span_of<kFork>(a, b);
       const int32_t* from = a.t.table + static_cast<int64_t>(a.src[b]) * a.t.cols;
       int32_t* row = a.t.table + static_cast<int64_t>(s.row) * a.t.cols;
-      for (int c = lane; c < s.c0; c += 32) {
+      for (int c = gl; c < s.c0; c += kWidth) {
         const int p = from[c];
         row[c] = p;
         atomicAdd(&a.t.refs[p], 1);
@@ -454,6 +476,12 @@ dfl2_status check_batch(int B, int T, int max_t) {
   return DFL2_OK;
 }
 
+template <bool kFork>
+cudaError_t launch_take(const TakeArgs& a, cudaStream_t s) {
+  return launch_k(a.B <= kBookThreads / 32 ? take_kernel<kFork, 32> : take_kernel<kFork, 8>, dim3(1),
+                  dim3(kBookThreads), 0, s, true, a);
+}
+
 int copy_blocks(int64_t items, int per_block) {
   const int64_t want = (items + per_block - 1) / per_block;
   return static_cast<int>(std::min<int64_t>(want, int64_t(1) << 20));
@@ -539,9 +567,7 @@ dfl2_status dfl2_cache_reserve(const dfl2_cache* cache, int B, int T, const int3
                                cache->cols);
   DFL2_TRY(check_all_device(cache, ptrs));
   const dfl2::TakeArgs a{dfl2::table_view(cache, table_rows, length, count, T), nullptr, served, B};
-  return launched(dfl2::launch_k(dfl2::take_kernel<false>, dim3(1), dim3(dfl2::kBookThreads), 0,
-                                 cu(stream), true, a),
-                  "cache reserve launch");
+  return launched(dfl2::launch_take<false>(a, cu(stream)), "cache reserve launch");
 }
 
 dfl2_status dfl2_cache_write(const dfl2_cache* cache, int layer, int n_layers, const void* k_new,
@@ -612,8 +638,7 @@ dfl2_status dfl2_cache_fork(const dfl2_cache* cache, int n, const int32_t* src, 
   DFL2_TRY(check_all_host(cache, ptrs));
   DFL2_TRY(check_all_device(cache, ptrs));
   const dfl2::TakeArgs a{dfl2::table_view(cache, dst, length, nullptr, 0), src, served, n};
-  cudaError_t e = dfl2::launch_k(dfl2::take_kernel<true>, dim3(1), dim3(dfl2::kBookThreads), 0,
-                                 cu(stream), true, a);
+  cudaError_t e = dfl2::launch_take<true>(a, cu(stream));
   if (e == cudaSuccess) {
     const dfl2::ForkCopyArgs f{a.t, dfl2::row_view(cache), src, served, cache->layers, n};
     const int64_t items = static_cast<int64_t>(cache->layers) * n * cache->page_size;
