@@ -376,27 +376,30 @@ struct CompactArgs {
   int layers, B;
 };
 
-// A block works out where a sequence's moving rows come from and go to once, a
-// thread to a node; then a thread owns one 16-byte column of K or V in one layer and
-// moves it down that list, eight rows in flight.  The path ascends strictly, so
-// path[i] >= i and a row that is written has been read before: reading ahead is safe.
-// Bound by the chain of dependent reads (path, table, rows).  The whole turn of 64
-// sequences, 16 layers: 62.2 us, 64.0 where every thread looked its rows up for itself.
-constexpr int kMoveThreads = kMaxTree;
+// A cluster of blocks to a sequence.  Each block works out where the moving rows come
+// from and go to once, a thread to a node; then a thread owns one 16-byte column of K or
+// V in one layer and moves it down that list, eight rows in flight.  The path ascends
+// strictly, so path[i] >= i and a row that is written has been read before: reading ahead
+// is safe.  When every block of the cluster has read the table, the first one gives the
+// pages behind the kept rows back.
+// Bound by the chain of dependent reads (path, table, rows).  The turn of 64 sequences,
+// 16 layers: 61.1 us, with as many blocks as columns ask for and the pages given back by a
+// kernel of their own 61.3, which costs the host 1.9 us more a call; blocks of 1024
+// threads 61.7; every thread looking its rows up for itself 1.8 more.
+constexpr int kMoveThreads = 512, kMoveBlocks = 8;
 __global__ void __launch_bounds__(kMoveThreads)
     compact_kernel(const __grid_constant__ CompactArgs a) {
   __shared__ int64_t from_s[kMaxTree], to_s[kMaxTree];
-  __shared__ int warp_sums[kMoveThreads / 32];
+  __shared__ int warp_sums[kMaxTree / 32];
   constexpr int kBatch = 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
   pdl_wait();
   pdl_launch_dependents();
   const int count = a.t.count_of(b), n = min(a.n_path[b], count), row = a.t.row_of(b);
-  if (row < 0 || n <= 0) return;
   const int len = a.t.length[b], slots = (1 << a.t.page_shift) - 1;
   bool moves = false;
   int64_t src = 0, dst = 0;
-  if (tid < n) {
+  if (row >= 0 && tid < n) {
     const int from = a.path[static_cast<int64_t>(b) * a.t.T + tid];
     if (from != tid) {
       const int64_t pf = from > tid && from < count
@@ -410,11 +413,11 @@ __global__ void __launch_bounds__(kMoveThreads)
     }
   }
   const unsigned mine = __ballot_sync(kAll, moves);
-  if (lane == 0) warp_sums[warp] = __popc(mine);
+  if (lane == 0 && warp < kMaxTree / 32) warp_sums[warp] = __popc(mine);
   __syncthreads();
   int at = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < kMoveThreads / 32; ++w) {
+  for (int w = 0; w < kMaxTree / 32; ++w) {
     if (w < warp) at += warp_sums[w];
     total += warp_sums[w];
   }
@@ -424,8 +427,8 @@ __global__ void __launch_bounds__(kMoveThreads)
     to_s[at] = dst;
   }
   __syncthreads();
-  if (total == 0) return;
-  const int columns = a.layers * 2 * a.r.chunks;
+  cluster_arrive_release();  // this block has read the table and the length
+  const int columns = total > 0 ? a.layers * 2 * a.r.chunks : 0;
   for (int c = blockIdx.x * kMoveThreads + tid; c < columns; c += gridDim.x * kMoveThreads) {
     const int l = c / (2 * a.r.chunks);
     uint32_t col = c - l * 2 * a.r.chunks;
@@ -444,24 +447,15 @@ __global__ void __launch_bounds__(kMoveThreads)
         if (i + j < total) base[to_s[i + j]] = x[j];
     }
   }
-}
-
-// After the rows have moved: the new lengths, and the pages behind them given
-// back.  A warp to a sequence.
-__global__ void __launch_bounds__(128) trim_kernel(const __grid_constant__ CompactArgs a) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int b = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (b >= a.B) return;
-  const int count = a.t.count_of(b), n = max(0, min(a.n_path[b], count)), len = a.t.length[b];
-  __syncwarp();  // new_length may be length
-  if (lane == 0) a.new_length[b] = len + n;
-  const int row = a.t.row_of(b);
+  __syncwarp();
+  cluster_wait_acquire();
+  if (blockIdx.x > 0) return;
+  if (tid == 0) a.new_length[b] = len + max(0, n);
   if (row < 0 || len < 0) return;
   const int ps = 1 << a.t.page_shift;
   const int c1 = min(a.t.cols, (len + count + ps - 1) >> a.t.page_shift);
   int32_t* r = a.t.table + static_cast<int64_t>(row) * a.t.cols;
-  for (int c = ((len + n + ps - 1) >> a.t.page_shift) + lane; c < c1; c += 32) {
+  for (int c = ((len + max(0, n) + ps - 1) >> a.t.page_shift) + tid; c < c1; c += kMoveThreads) {
     const int p = atomicExch(&r[c], -1);
     if (p != -1) drop_page(a.t, p);
   }
@@ -619,14 +613,13 @@ dfl2_status dfl2_cache_compact(const dfl2_cache* cache, int B, int T, const int3
   DFL2_TRY(check_all_device(cache, ptrs));
   const dfl2::CompactArgs a{dfl2::table_view(cache, table_rows, length, count, T),
                             dfl2::row_view(cache), path, n_path, new_length, cache->layers, B};
-  // (at most 4096 layers of 2 x 16384 columns of a sequence: an int holds them)
+  // (at most 4096 layers of 2 x 16384 columns of a sequence: an int holds them; clusters
+  // of more than 8 blocks are not portable)
   const int64_t columns = static_cast<int64_t>(cache->layers) * 2 * a.r.chunks;
-  const int blocks = static_cast<int>(
-      std::min<int64_t>(1024, (columns + dfl2::kMoveThreads - 1) / dfl2::kMoveThreads));
-  cudaError_t e = dfl2::launch_k(dfl2::compact_kernel, dim3(blocks, B), dim3(dfl2::kMoveThreads), 0,
-                                 cu(stream), true, a);
-  if (e == cudaSuccess)
-    e = dfl2::launch_k(dfl2::trim_kernel, dim3((B + 3) / 4), dim3(128), 0, cu(stream), true, a);
+  int blocks = 1;
+  while (blocks < dfl2::kMoveBlocks && int64_t(blocks) * dfl2::kMoveThreads < columns) blocks *= 2;
+  const cudaError_t e = dfl2::launch_kc(dfl2::compact_kernel, dim3(blocks, B),
+                                        dim3(dfl2::kMoveThreads), 0, cu(stream), true, blocks, a);
   return launched(e, "cache compact launch");
 }
 
