@@ -239,6 +239,16 @@ __device__ __forceinline__ void tma_prefetch_4d(const void* tmap, int x, int y, 
                : "memory");
 }
 
+// Where 8 channels, from 8 c on, of a row of a stream's part are in part_o.  The 32 bytes
+// of four rows lie side by side, so a warp's store of 32 bytes a thread is of 8 whole
+// lines, not of 32 quarters (9 trees of 61 nodes, 7 heads of 64 channels a key head: 33.7
+// us, row by row 35.3; 64 trees of 33 nodes 143.3 and 144.1; 0.2 more for one token).
+constexpr int kPartStep = 4 * 8;  // floats from 8 channels to the next 8
+template <int D>
+__device__ __forceinline__ int part_at(int stream, int row, int c) {
+  return stream * (kLanes * D) + (row >> 2) * (4 * D) + c * kPartStep + (row & 3) * 8;
+}
+
 // Which of the 64 positions from p0 on node i of sequence b sees (0 past the end).
 __device__ __forceinline__ uint64_t seen64(const AttnArgs& a, int b, const Seq& s, int i, int p0) {
   if (i >= s.n) return 0;
@@ -703,8 +713,8 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
         const int head = h * a.G + r - node * a.G;
         const bool bad = *reinterpret_cast<volatile int*>(&bad_seg[seg % C::kBadSegs]) == seg;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * a.rows +
-                             stream * a.stream_rows + row_l;
+        const int64_t part = static_cast<int64_t>(blockIdx.x) * 2 + slot;
+        float* part_o = a.part_o + part * (NS * kLanes * D) + part_at<D>(stream, row_l, 0);
         E* out = static_cast<E*>(a.out) + at.b * a.ob + node * a.ot + head * a.oh;
         const bool mine = r < M && node < s.n;
 #pragma unroll 1
@@ -738,11 +748,12 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
           } else if (mine) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              st_v8(a.part_o + part * D + c + 8 * j, o + 8 * j);
+              st_v8(part_o + (c / 8 + j) * kPartStep, o + 8 * j);
           }
           __syncwarp();  // the next load is the whole warp's
         }
-        if (mine && !whole) a.part_ml[part] = make_float2(m, l);
+        if (mine && !whole)
+          a.part_ml[part * a.rows + stream * a.stream_rows + row_l] = make_float2(m, l);
         if (mine && whole && a.lse)
           a.lse[(static_cast<int64_t>(at.b) * a.t.T + node) * (a.H * a.G) + head] =
               (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
@@ -805,6 +816,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   const int parts = c1 - c0 + 1;
   const int range = blockIdx.x / 2 / a.row_tiles, row_tile = blockIdx.x / 2 - range * a.row_tiles;
   const int h = cut.h, r0 = row_tile * a.rows;
+  const int part_size = (a.rows > a.stream_rows ? 2 : 1) * (kLanes * D);
   const int rows = min(a.rows, load_seq(a, b).n * a.G - r0);  // (past the count: zeroed above)
   const int wide = parts <= kCombineParts       ? 1
                    : parts <= 2 * kCombineParts ? 2
@@ -814,6 +826,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   const int id = (range - c0) * gridDim.y + blockIdx.y;
   for (int rb = id * per_block; rb < rows; rb += parts * gridDim.y * per_block) {
     const int r = rb + warp / wide * kRows + lane / kLanesRow, j = lane % kLanesRow;
+    const int stream = r >= a.stream_rows;
+    const int at = part_at<D>(stream, r - stream * a.stream_rows, j / 2) / 4 + j % 2;
     float m = -INFINITY, l = 0.f;
     float4 y[4];  // channels 4 (j + kLanesRow q) .. + 3
 #pragma unroll
@@ -827,12 +841,11 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
           const int cz = c + z * wide;
           ml[z] = make_float2(-INFINITY, 0.f);
           if (cz <= c1) {
-            const int64_t at = ((static_cast<int64_t>(cz) * a.row_tiles + row_tile) * 2 +
-                                (cz == c0 ? slot0 : 0)) * a.rows + r;
-            ml[z] = a.part_ml[at];
-            const float4* p = reinterpret_cast<const float4*>(a.part_o + at * D) + j;
+            const int64_t part = (cz * a.row_tiles + row_tile) * 2 + (cz == c0 ? slot0 : 0);
+            ml[z] = a.part_ml[part * a.rows + r];
+            const float4* p = reinterpret_cast<const float4*>(a.part_o + part * part_size) + at;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) o[z][q] = p[q * kLanesRow];
+            for (int q = 0; q < 4; ++q) o[z][q] = p[q * (kLanesRow / 2 * kPartStep / 4)];
           } else {
 #pragma unroll
             for (int q = 0; q < 4; ++q) o[z][q] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -952,7 +965,7 @@ AttnPlan attn_plan(int T, int G, int D, int sms) {
   const size_t ctas = size_t(p.grid) * p.row_tiles;
   const size_t parts = p.grid > 1 ? ctas * 2 : 0;  // one range cuts nothing
   p.o_off = 0;
-  p.ml_off = align_up(parts * p.rows * D * sizeof(float), 256);
+  p.ml_off = align_up(parts * streams * kLanes * D * sizeof(float), 256);
   p.cut_off = p.ml_off + align_up(parts * p.rows * sizeof(float2), 256);
   p.ws_bytes = p.cut_off + align_up(ctas * 2 * sizeof(Cut), 256) + 256;  // (to align the base)
   return p;

@@ -45,7 +45,7 @@ struct AttnArgs {
   bool out32;      // every row of out begins on 32 bytes: stored so (143 us, 16 at a time 146:
                    // 64 trees of 33 nodes)
   float* lse;      // nullable
-  float* part_o;   // [CTAs][2][rows][D] unnormalised outputs
+  float* part_o;   // [CTAs][2][streams][128 rows x D] unnormalised outputs (part_at)
   float2* part_ml; // [CTAs][2][rows] (maximum, sum)
   Cut* cuts;       // [CTAs][2]: of the row tiles a CTA goes on with, and begins
   int grid;        // ranges that the units are cut into; row_tiles CTAs share one
