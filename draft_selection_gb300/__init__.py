@@ -47,15 +47,16 @@ def lib_path() -> str:
 
 
 def load():
-    """Loads libdfl2.so (built in-tree by draft_selection_gb300.build)."""
-    global _lib
+    """Loads libdfl2.so and its extension (built in-tree by draft_selection_gb300.build)."""
+    global _lib, _native
     if _lib is not None:
         return _lib
-    path = _build.LIB
-    if not os.path.exists(path):
-        raise RuntimeError(f"{path} is missing: build it with draft_selection_gb300.build.build() "
-                           "(nvcc, sm_103a); dfl2 has no other implementation")
-    L = ctypes.CDLL(path)
+    for path in (_build.LIB, _build.CALLS):
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "draft_selection_gb300.build.build() (nvcc, sm_103a); dfl2 has no "
+                               "other implementation")
+    L = ctypes.CDLL(_build.LIB)
     P, I, F, U64, SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_uint64,
                         ctypes.c_size_t)
     L.dfl2_version.restype = ctypes.c_char_p
@@ -115,7 +116,8 @@ def load():
                  "dfl2_walk", "dfl2_conv2", "dfl2_conv2_ws", "dfl2_tail", "dfl2_verify", "dfl2_tables_build",
                  "dfl2_select_tables", "dfl2_tail_tables"):
         getattr(L, name).restype = I
-    _lib = L
+    from . import _calls  # linked against the library
+    _lib, _native = L, _calls
     return _lib
 
 
@@ -376,23 +378,28 @@ def dfl2_tail_tables(logits, verified_tok, hidden, W_H, P_A, P_B, temperature: f
 
 
 # ---- the paged cache and trees of drafted tokens ---------------------------------
-# These calls are short (a few microseconds on the GPU), so their marshalling is kept
-# short too: types and shapes, which the C side cannot see, are checked in one pass.
-_S3, _S4 = ctypes.c_int64 * 3, ctypes.c_int64 * 4
-_I32 = torch.int32
+# These calls are short (a few microseconds on the GPU), so their marshalling is
+# csrc/calls.cpp's: types and shapes, which the C side cannot see, are checked there.
 _CODES = {torch.float32: DFL2_F32, torch.bfloat16: DFL2_BF16, torch.float16: DFL2_F16}
 
 
+class _Unloaded:
+    """Stands for the extension until the library is loaded."""
+
+    def __getattr__(self, name):
+        load()
+        return getattr(_native, name)
+
+
+_native = _Unloaded()
+
+
 def _i32(t, name, shape):
-    """An int32 device array's address, of the given shape; None stays None."""
-    if t is None:
-        return None
-    if t.dtype is not _I32:
+    if t.dtype != torch.int32:
         raise TypeError(f"{name} must be int32, not {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {shape}, not {tuple(t.shape)} with strides "
                          f"{t.stride()}")
-    return t.data_ptr()
 
 
 def _strides(t):
@@ -427,7 +434,7 @@ class Cache:
             k.data_ptr(), v.data_ptr(), _CODES[k.dtype], layers, pages, heads, page_size, dim,
             st[0], st[1], st[2], st[3], table.data_ptr(), table.shape[0],
             table.shape[1], refs.data_ptr(), free_bits.data_ptr())
-        self._ref = ctypes.byref(self._s)
+        self._address = ctypes.addressof(self._s)
 
 
 def cache(layers: int, pages: int, kv_heads: int, page_size: int, head_dim: int, rows: int,
@@ -446,88 +453,42 @@ def cache(layers: int, pages: int, kv_heads: int, page_size: int, head_dim: int,
 
 def dfl2_cache_reserve(cache, length, count, served, rows=None, stream=None) -> None:
     """Pages for positions length .. length+count-1; served int32 [B] out.  count: int or [B]."""
-    shape = length.shape
-    if isinstance(count, int):
-        T, n = count, None
-    else:
-        T, n = 1 << 30, _i32(count, "count", shape)
-    _check(load().dfl2_cache_reserve(cache._ref, shape[0], T, _i32(rows, "rows", shape),
-                                     _i32(length, "length", shape[:1]), n,
-                                     _i32(served, "served", shape), _stream(stream)))
+    _check(_native.cache_reserve(cache, length, count, served, rows, stream))
 
 
 def dfl2_cache_write(cache, k_new, v_new, length, count=None, rows=None, layer: int = 0,
                      stream=None) -> None:
     """k_new, v_new [n_layers, B, T, kv_heads, head_dim] (one layer: without the first
     dimension) into layers layer .. of the cache, positions length .. length+count-1."""
-    if k_new.dim() == 4:
-        k_new, v_new = k_new[None], v_new[None]
-    N, B, T, H, D = k_new.shape
-    if (k_new.dtype != cache.dtype or v_new.dtype != cache.dtype or v_new.shape != k_new.shape
-            or H != cache.kv_heads or D != cache.head_dim):
-        raise ValueError("k_new and v_new must be [n_layers, B, T, kv_heads, head_dim] of the "
-                         "cache's type")
-    st = k_new.stride()
-    if v_new.stride() != st and _strides(v_new) != _strides(k_new) or st[4] != 1:
-        raise ValueError("k_new and v_new must have the same strides, the last of them 1")
-    if isinstance(count, int):
-        T, count = min(T, count), None
-    shape = (B,)
-    _check(load().dfl2_cache_write(cache._ref, layer, N, k_new.data_ptr(), v_new.data_ptr(),
-                                   _S4(*st[:4]), B, T, _i32(rows, "rows", shape),
-                                   _i32(length, "length", shape), _i32(count, "count", shape),
-                                   _stream(stream)))
+    _check(_native.cache_write(cache, k_new, v_new, length, count, rows, layer, stream))
 
 
 def dfl2_cache_compact(cache, length, count, path, n_path, new_length, rows=None,
                        stream=None) -> None:
     """The rows of nodes path[b,:n_path] to positions length .., the pages behind them
     given back, new_length = length + n_path (may be length).  count: int or [B]."""
-    B, T = path.shape
-    shape = (B,)
-    if isinstance(count, int):
-        if count != T:
-            raise ValueError(f"path has room for {T} nodes, not {count}")
-        count = None
-    _check(load().dfl2_cache_compact(cache._ref, B, T, _i32(rows, "rows", shape),
-                                     _i32(length, "length", shape), _i32(count, "count", shape),
-                                     _i32(path, "path", (B, T)), _i32(n_path, "n_path", shape),
-                                     _i32(new_length, "new_length", shape), _stream(stream)))
+    _check(_native.cache_compact(cache, length, count, path, n_path, new_length, rows, stream))
 
 
 def dfl2_cache_fork(cache, src, dst, length, served, stream=None) -> None:
     """Table rows dst become copies of the first length positions of rows src."""
-    shape = src.shape
-    _check(load().dfl2_cache_fork(cache._ref, shape[0], _i32(src, "src", shape[:1]),
-                                  _i32(dst, "dst", shape), _i32(length, "length", shape),
-                                  _i32(served, "served", shape), _stream(stream)))
+    _check(_native.cache_fork(cache, src, dst, length, served, stream))
 
 
 def dfl2_cache_free(cache, rows, stream=None) -> None:
     """Every page of the table rows given back."""
-    shape = rows.shape
-    _check(load().dfl2_cache_free(cache._ref, shape[0], _i32(rows, "rows", shape[:1]),
-                                  _stream(stream)))
+    _check(_native.cache_free(cache, rows, stream))
 
 
 def dfl2_tree_mask(parents, mask, depth=None, count=None, stream=None) -> None:
     """parents [B,T] -> mask int32 [B,T,ceil(T/32)] (bit j: node i sees node j), depth [B,T]."""
-    B, T = parents.shape
-    _check(load().dfl2_tree_mask(_i32(parents, "parents", (B, T)), B, T,
-                                 _i32(count, "count", (B,)),
-                                 _i32(mask, "mask", (B, T, (T + 31) // 32)),
-                                 _i32(depth, "depth", (B, T)), _stream(stream)))
+    _check(_native.tree_mask(parents, mask, depth, count, stream))
 
 
 def dfl2_tree_accept(tokens, parents, target, path, n_path, next_token, count=None,
                      stream=None) -> None:
     """The path of the target's tokens through each tree: path [B,T], n_path [B], next_token [B]."""
-    B, T = shape = tokens.shape
-    one = (B,)
-    _check(load().dfl2_tree_accept(_i32(tokens, "tokens", shape), _i32(parents, "parents", shape),
-                                   _i32(target, "target", shape), B, T, _i32(count, "count", one),
-                                   _i32(path, "path", shape), _i32(n_path, "n_path", one),
-                                   _i32(next_token, "next_token", one), _stream(stream)))
+    _check(_native.tree_accept(tokens, parents, target, path, n_path, next_token, count, stream))
 
 
 def dfl2_tree_attn_workspace_size(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int,
@@ -541,20 +502,5 @@ def dfl2_tree_attn(q, cache, layer: int, length, mask, out, ws, rows=None, count
                    scale=None, stream=None) -> None:
     """q [B,T,q_heads,head_dim] over layer `layer` of the cache -> out (as q), lse float32
     [B,T,q_heads].  mask int32 [B,T,ceil(T/32)], None for a chain; scale: head_dim ** -0.5."""
-    B, T, H, D = shape = q.shape
-    if q.dtype != cache.dtype or out.dtype != cache.dtype or out.shape != shape:
-        raise ValueError("q and out must be [B, T, q_heads, head_dim] of the cache's type")
-    qs, os_ = q.stride(), out.stride()
-    if D != cache.head_dim or qs[3] != 1 or os_[3] != 1:
-        raise ValueError(f"head_dim {D} against the cache's {cache.head_dim}, strides {qs}, {os_}")
-    lse_p = None
-    if lse is not None:
-        if (lse.dtype is not torch.float32 or lse.shape != shape[:3] or not lse.is_contiguous()):
-            raise ValueError("lse must be contiguous float32 [B, T, q_heads]")
-        lse_p = lse.data_ptr()
-    one = (B,)
-    _check(load().dfl2_tree_attn(
-        q.data_ptr(), _S3(*qs[:3]), cache._ref, layer, B, T, H, _i32(rows, "rows", one),
-        _i32(length, "length", one), _i32(count, "count", one),
-        _i32(mask, "mask", (B, T, (T + 31) // 32)), D ** -0.5 if scale is None else scale,
-        out.data_ptr(), _S3(*os_[:3]), lse_p, ws.data_ptr(), _nbytes(ws), _stream(stream)))
+    _check(_native.tree_attn(q, cache, layer, length, mask, out, ws, rows, count, lse, scale,
+                             stream))

@@ -1,8 +1,10 @@
-"""Builds libdfl2.so in-tree from csrc/*.cu for sm_103a with nvcc.
+"""Builds libdfl2.so in-tree from csrc/*.cu for sm_103a with nvcc, and the Python
+extension _calls.so from csrc/calls.cpp with the host compiler.
 
 Each translation unit is compiled in parallel, then linked into one shared
-library that exports the C ABI of include/dfl2.h.  Rebuilds only when a source
-or header is newer than the library.
+library that exports the C ABI of include/dfl2.h; the extension is linked
+against it and torch.  Rebuilds only when a source or header is newer than the
+libraries.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdfl2.so")
+CALLS = os.path.join(PKG, "_calls.so")
+CALLS_SRC = os.path.join(CSRC, "calls.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 _lock = threading.Lock()
 
@@ -35,14 +40,14 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
+    return _sources() + [CALLS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
         os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
 def is_fresh() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -51,36 +56,65 @@ def cflags(extra=()):
                    "-I", INCLUDE, "-I", CSRC, "--expt-relaxed-constexpr", *extra]
 
 
+def calls_cmds(cc: str, obj: str, out: str):
+    """The commands that compile and link _calls.so."""
+    import torch
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("g++ not found: the Python extension of dfl2 cannot be built")
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")
+    dirs = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"), cuda,
+            sysconfig.get_paths()["include"]]
+    return ([cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             *(x for d in dirs for x in ("-isystem" if d != INCLUDE else "-I", d)),
+             "-c", CALLS_SRC, "-o", obj],
+            [cxx, "-shared", "-o", out, obj, "-L", PKG, "-ldfl2", "-Wl,-rpath,$ORIGIN",
+             "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"])
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile and link libdfl2.so; returns its path."""
+    """Compile and link libdfl2.so and _calls.so; returns the first one's path."""
     with _lock:
         if not force and is_fresh():
             return LIB
         os.makedirs(BUILD, exist_ok=True)
         cc = nvcc()
 
+        calls_obj = os.path.join(BUILD, "calls.o")
+        calls_tmp = CALLS + f".tmp{os.getpid()}"
+        calls_compile, calls_link = calls_cmds(cc, calls_obj, calls_tmp)
+
         def compile_one(src):
             obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
             cmd = [cc, *cflags(extra), "-c", src, "-o", obj]
+            if src == CALLS_SRC:
+                obj, cmd = calls_obj, calls_compile
             if verbose:
                 print(" ".join(cmd))
             r = subprocess.run(cmd, capture_output=True, text=True)
             if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stderr}")
+                raise RuntimeError(f"{os.path.basename(cmd[0])} failed on "
+                                   f"{os.path.basename(src)}:\n{r.stderr}")
             if verbose and r.stderr:
                 print(r.stderr)
             return obj
 
-        srcs = _sources()
+        def link(cmd, tmp, out):
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stderr}")
+            os.replace(tmp, out)
+
+        srcs = _sources() + [CALLS_SRC]
         with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
             objs = list(ex.map(compile_one, srcs))
         tmp = LIB + f".tmp{os.getpid()}"
-        cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-lrt", "-ldl",
-               "-lpthread"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stderr}")
-        os.replace(tmp, LIB)
+        link([cc, *ARCH, "-shared", "-o", tmp, *objs[:-1], "-lcudart_static", "-lrt", "-ldl",
+              "-lpthread"], tmp, LIB)
+        link(calls_link, calls_tmp, CALLS)
         return LIB
 
 

@@ -184,3 +184,48 @@ def test_binding_refuses_types_and_shapes():
                    c.free_bits)
     with pytest.raises(ValueError):
         dfl2.Cache(c.k, c.v, c.table, c.refs[:2], c.free_bits)
+
+
+def test_binding_refuses_what_is_no_tensor_or_number():
+    c = dfl2.cache(1, 4, 2, 16, 64, 2, 3, torch.float16, device="cpu")
+    i = torch.zeros(2, dtype=torch.int32)
+    ij = torch.zeros(2, 3, dtype=torch.int32)
+    with pytest.raises(TypeError):
+        dfl2.dfl2_cache_reserve(c, [0, 0], 4, i)
+    with pytest.raises(ValueError):
+        dfl2.dfl2_cache_reserve(c, ij, 4, i)
+    with pytest.raises(OverflowError):
+        dfl2.dfl2_cache_reserve(c, i, 1 << 31, i)
+    with pytest.raises(AttributeError):
+        dfl2.dfl2_cache_free(None, i)
+    with pytest.raises(TypeError):
+        dfl2.dfl2_cache_fork(c, i, i, i, i.numpy())
+    with pytest.raises(ValueError):
+        dfl2.dfl2_tree_mask(ij, ij)                      # mask [2, 3, 1]
+    with pytest.raises(ValueError):
+        dfl2.dfl2_tree_accept(ij, ij.t(), ij, ij, i, i)
+    new = torch.zeros(2, 5, 2, 64, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        dfl2.dfl2_cache_write(c, new[0], new[0], i)      # three dimensions
+    with pytest.raises(ValueError):
+        dfl2.dfl2_cache_write(c, new, new.transpose(0, 1).contiguous().transpose(0, 1), i)
+    with pytest.raises(TypeError):
+        dfl2.dfl2_cache_write(c, new, new, i, layer="0")
+    q = torch.zeros(2, 3, 4, 64, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        dfl2.dfl2_tree_attn(q[0], c, 0, i, None, q[0], i)
+    with pytest.raises(TypeError):
+        dfl2.dfl2_tree_attn(q, c, 0, i, None, q, i, scale="1")
+    with pytest.raises(ValueError):
+        dfl2.dfl2_tree_attn(q.transpose(2, 3), c, 0, i, None, q.transpose(2, 3), i)
+
+
+def test_binding_passes_the_c_sides_refusals_on():
+    c = dfl2.cache(1, 4, 2, 16, 64, 2, 3, torch.float16, device="cpu")
+    i = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: dfl2.dfl2_cache_free(c, i, stream=1),              # no device memory
+                 lambda: dfl2.dfl2_cache_reserve(c, i, 4, None, stream=1),  # no served
+                 lambda: dfl2.dfl2_cache_reserve(c, i, -1, i, stream=1)):
+        with pytest.raises(dfl2.Dfl2Error) as e:
+            call()
+        assert e.value.status != 0 and e.value.message
