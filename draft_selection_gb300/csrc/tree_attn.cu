@@ -52,9 +52,12 @@
 // Bounds.  A tile of 64 keys of 128 channels is 32 KB: 1400 cycles of one SM's share
 // of HBM.  Its MMAs take a stream 384 + 256 cycles (measured: 48 for 128 x 64 x 16
 // with both operands in shared memory, which reads 6 KB at 128 bytes a cycle, 64 for
-// 128 x 128 x 16 with A in TMEM), and its softmax about 700 of a warp that shares
-// its scheduler with the other stream's.  So HBM bounds up to 128 rows, all three
-// meet at 256 (about 1450 cycles a tile), and the tensor cores bound what has more.
+// 128 x 128 x 16 with A in TMEM).  Its softmax is a chain of 1350 to 1600 cycles a tile
+// for a warp that shares its scheduler with the other stream's: the scores from TMEM 125,
+// their maximum 190, the exponentials 540 alone and 640 to 770 beside the other warp's
+// (their unit: 256 each), barriers and the weights' store the rest.  So HBM bounds up to
+// 128 rows, all three meet at 256 (about 1400 cycles a tile), the tensor cores bound what
+// has more rows of 128 channels, and the softmax what has more of 64.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
