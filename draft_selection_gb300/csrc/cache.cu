@@ -64,8 +64,8 @@ struct Span {
 template <bool kFork>
 __device__ __forceinline__ Span span_of(const TakeArgs& a, int b) {
   Span s;
+  const int len = a.t.length[b], ps = 1 << a.t.page_shift;  // beside the row's
   s.row = a.t.row_of(b);
-  const int len = a.t.length[b], ps = 1 << a.t.page_shift;
   const int64_t end = static_cast<int64_t>(len) + (kFork ? 0 : a.t.count_of(b));
   s.ok = s.row >= 0 && len >= 0 && end <= static_cast<int64_t>(a.t.cols) << a.t.page_shift;
   s.c0 = s.ok ? len >> a.t.page_shift : 0;
@@ -75,8 +75,10 @@ __device__ __forceinline__ Span span_of(const TakeArgs& a, int b) {
 
 // One CTA: which sequences get their pages, and the pages themselves.  Bound by its
 // dependent steps (lengths, table entries, two scans, the table again), not by the
-// pages/8 bytes of the map: 5.5 us cold for one sequence (ncu, caches flushed), less in
-// a turn, where PDL hides its start.
+// pages/8 bytes of the map: 5.2 us for one sequence, 5.9 for 64 with 33 nodes each, 7.4
+// for 128 forks (ncu, caches flushed), less in a turn, where PDL hides its start.  Loads
+// that do not need each other are issued together (four forks with their copies: 9.9 us,
+// 10.9 one after the other).
 //
 // kWidth lanes of a warp look after a sequence: all 32 while the 32 warps hold every
 // sequence at once, else 8, so that up to 128 still go at once.  With a warp to each in
@@ -98,18 +100,28 @@ __global__ void __launch_bounds__(kBookThreads) take_kernel(const __grid_constan
   constexpr unsigned kGroupBits = kAll >> (32 - kWidth);
   const int group = tid / kWidth, gl = lane % kWidth, g0 = lane - gl;  // g0: the group's lane 0
   const int first = (tid - lane) / kWidth;  // the warp's first group
+  // the free pages: each thread the words [w0, w1) of the bit map (bits past the pages
+  // are none), the first of them on its way beside the tables
+  const int words = (a.t.pages - 1) / 32 + 1;
+  auto free_word = [&](int w) {
+    const uint32_t x = a.t.free_bits[w];
+    return w < words - 1 ? x : x & (0xffffffffu >> (31 - ((a.t.pages - 1) & 31)));
+  };
+  const int wper = (words + kBookThreads - 1) / kBookThreads;
+  const int w0 = min(words, tid * wper), w1 = min(words, w0 + wper);
+  uint32_t left = w0 < w1 ? free_word(w0) : 0u;
   // the needs (the collectives are the warp's, so its groups take the same steps)
   for (int b0 = 0; b0 + first < a.B; b0 += kGroups) {
     const int b = b0 + group;
     const bool there = b < a.B;
     Span s{-1, 0, 0, false};
+    const int src = kFork && there ? a.src[b] : -1;
     if (there) s = span_of<kFork>(a, b);
     int need = 0;
     bool good = s.ok;
     if (good) {
       const int32_t* row = a.t.table + static_cast<int64_t>(s.row) * a.t.cols;
       if (kFork) {
-        const int src = a.src[b];
         good = static_cast<unsigned>(src) < static_cast<unsigned>(a.t.rows) && src != s.row;
         if (good)
 #pragma unroll 4
@@ -128,17 +140,8 @@ __global__ void __launch_bounds__(kBookThreads) take_kernel(const __grid_constan
       for (int off = kWidth >> 1; off; off >>= 1) need += __shfl_xor_sync(kAll, need, off);
     if (there && gl == 0) offs[b] = ok ? need : -1;
   }
-  // the free pages: each thread the words [w0, w1) of the bit map (bits past the pages
-  // are none)
-  const int words = (a.t.pages - 1) / 32 + 1;
-  auto free_word = [&](int w) {
-    const uint32_t x = a.t.free_bits[w];
-    return w < words - 1 ? x : x & (0xffffffffu >> (31 - ((a.t.pages - 1) & 31)));
-  };
-  const int wper = (words + kBookThreads - 1) / kBookThreads;
-  const int w0 = min(words, tid * wper), w1 = min(words, w0 + wper);
-  int mine = 0;
-  for (int w = w0; w < w1; ++w) mine += __popc(free_word(w));
+  int mine = __popc(left);
+  for (int w = w0 + 1; w < w1; ++w) mine += __popc(free_word(w));
   int n_free, total;
   int rank = block_scan(mine, n_free, warp_sums);  // rank of this thread's first free page
   // served in order while the pages last
@@ -161,7 +164,6 @@ __global__ void __launch_bounds__(kBookThreads) take_kernel(const __grid_constan
   const int taken = taken_s;
 
   int w = w0;
-  uint32_t left = w < w1 ? free_word(w) : 0u;
   for (int r0 = 0; r0 < taken; r0 += kListCap) {
     const int r1 = min(taken, r0 + kListCap);
     // the pages of ranks [r0, r1), each from the thread that holds its word
@@ -318,10 +320,11 @@ __global__ void __launch_bounds__(256) write_kernel(const __grid_constant__ Writ
     const int t = static_cast<int>(it % a.t.T);
     const int64_t lb = it / a.t.T;
     const int b = static_cast<int>(lb % a.B), l = static_cast<int>(lb / a.B);
+    const int r = a.t.seq ? a.t.seq[b] : b, len = a.t.length[b];  // beside the count
     if (t >= a.t.count_of(b)) continue;
-    const int row = a.t.row_of(b);
+    const int row = a.t.checked_row(r);
     if (row < 0) continue;
-    const int pos = a.t.length[b] + t;
+    const int pos = len + t;
     const int page = a.t.page_at(row, pos >> a.t.page_shift);
     if (page < 0 || pos < 0) continue;
     const int64_t from = l * a.nl + b * a.nb + t * a.nt;
@@ -342,7 +345,7 @@ struct ForkCopyArgs {
 
 // The positions of the partly filled last page, every layer.  Bound by HBM: 128 forks
 // of 32 sequences, pages of 64, 32 layers, 617 MB written and a quarter of it read (a
-// parent's four children share it in L2), in 127 us: 6.1 TB/s.
+// parent's four children share it in L2), in 124 us: 6.2 TB/s.
 __global__ void __launch_bounds__(256) fork_copy_kernel(const __grid_constant__ ForkCopyArgs a) {
   pdl_wait();
   pdl_launch_dependents();
@@ -354,11 +357,11 @@ __global__ void __launch_bounds__(256) fork_copy_kernel(const __grid_constant__ 
     const int slot = static_cast<int>(it & (ps - 1));
     const int64_t li = it >> a.t.page_shift;
     const int i = static_cast<int>(li % a.n), l = static_cast<int>(li / a.n);
-    if (!a.served[i]) continue;
-    const int len = a.t.length[i];
+    const int served = a.served[i], len = a.t.length[i], src = a.src[i], dst = a.t.seq[i];
+    if (!served) continue;
     if (slot >= (len & (ps - 1))) continue;
     const int c = len >> a.t.page_shift;
-    const int64_t from_page = a.t.page_at(a.src[i], c), to_page = a.t.page_at(a.t.seq[i], c);
+    const int64_t from_page = a.t.page_at(src, c), to_page = a.t.page_at(dst, c);
     if (from_page < 0 || to_page < 0) continue;
     const int64_t at = l * a.r.layer + slot * a.r.slot;
     const int64_t from = at + from_page * a.r.page, to = at + to_page * a.r.page;
@@ -383,7 +386,7 @@ struct CompactArgs {
 // is safe.  When every block of the cluster has read the table, the first one gives the
 // pages behind the kept rows back.
 // Bound by the chain of dependent reads (path, table, rows).  The turn of 64 sequences,
-// 16 layers: 61.1 us, with as many blocks as columns ask for and the pages given back by a
+// 16 layers: 61.1 us (60.0 since the path is read beside the count), with as many blocks as columns ask for and the pages given back by a
 // kernel of their own 61.3, which costs the host 1.9 us more a call; blocks of 1024
 // threads 61.7; every thread looking its rows up for itself 1.8 more.
 constexpr int kMoveThreads = 512, kMoveBlocks = 8;
@@ -395,12 +398,12 @@ __global__ void __launch_bounds__(kMoveThreads)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
   pdl_wait();
   pdl_launch_dependents();
-  const int count = a.t.count_of(b), n = min(a.n_path[b], count), row = a.t.row_of(b);
-  const int len = a.t.length[b], slots = (1 << a.t.page_shift) - 1;
+  const int from = tid < a.t.T ? a.path[static_cast<int64_t>(b) * a.t.T + tid] : 0;
+  const int len = a.t.length[b], count = a.t.count_of(b), n = min(a.n_path[b], count);
+  const int row = a.t.row_of(b), slots = (1 << a.t.page_shift) - 1;
   bool moves = false;
   int64_t src = 0, dst = 0;
   if (row >= 0 && tid < n) {
-    const int from = a.path[static_cast<int64_t>(b) * a.t.T + tid];
     if (from != tid) {
       const int64_t pf = from > tid && from < count
                              ? a.t.page_at(row, (len + from) >> a.t.page_shift)

@@ -48,8 +48,8 @@ struct TableView {
   uint32_t* err;
 
   // The table row of sequence b; -1 (recorded) if out of range.
-  __device__ __forceinline__ int row_of(int b) const {
-    const int r = seq ? seq[b] : b;
+  __device__ __forceinline__ int row_of(int b) const { return checked_row(seq ? seq[b] : b); }
+  __device__ __forceinline__ int checked_row(int r) const {
     if (static_cast<unsigned>(r) < static_cast<unsigned>(rows)) return r;
     record_error(err, kDevErrBadIndex);
     return -1;

@@ -1,7 +1,7 @@
 // Trees of drafted tokens: what each node sees, and the path of the target's
 // tokens through the tree (include/dfl2.h).  A few integers per node: both are
-// bound by the latency of their dependent steps (3.0 us each for a chain of 17, 4.2 and
-// 3.9 for 64 trees of 33 nodes; ncu, caches flushed), about 2 us of which is a launch.
+// bound by the latency of their dependent steps (3.3 and 3.0 us for a chain of 17, 3.7 and
+// 3.6 for 64 trees of 33 nodes; ncu, caches flushed), about 2 us of which is a launch.
 #include <cuda_runtime.h>
 
 #include "cache.cuh"
@@ -29,9 +29,9 @@ __global__ void __launch_bounds__(kMaxTree) tree_mask_kernel(const __grid_consta
   pdl_wait();
   pdl_launch_dependents();
   const int b = blockIdx.x, i = threadIdx.x;
+  int p = i < a.T ? a.parents[static_cast<int64_t>(b) * a.T + i] : -1;  // beside the count
   const int n = a.count ? max(0, min(a.T, a.count[b])) : a.T;
   if (i < n) {
-    int p = a.parents[static_cast<int64_t>(b) * a.T + i];
     if (p < -1 || p >= i) {
       record_error(a.err, kDevErrBadIndex);
       p = -1;
@@ -67,7 +67,7 @@ struct AcceptArgs {
 };
 
 // One warp a tree, each lane up to eight nodes in registers: a step down is one
-// comparison per node and a warp-wide minimum.  A child's number is above its
+// comparison per node, a warp-wide minimum and a shuffle.  A child's number is above its
 // parent's, so there are at most T steps whatever the parents hold.
 __global__ void __launch_bounds__(128) tree_accept_kernel(const __grid_constant__ AcceptArgs a) {
   pdl_wait();
@@ -75,18 +75,26 @@ __global__ void __launch_bounds__(128) tree_accept_kernel(const __grid_constant_
   const int b = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (b >= a.B) return;
   const int64_t at = static_cast<int64_t>(b) * a.T;
-  const int n = a.count ? max(0, min(a.T, a.count[b])) : a.T;
-  int tok[kNodesPerLane], par[kNodesPerLane];
+  int tok[kNodesPerLane], par[kNodesPerLane], tgt[kNodesPerLane];
 #pragma unroll
-  for (int j = 0; j < kNodesPerLane; ++j) {
+  for (int j = 0; j < kNodesPerLane; ++j) {  // all loads at once, the count's beside them
     const int i = lane + 32 * j;
-    tok[j] = i < n ? a.tokens[at + i] : 0;
-    par[j] = i < n ? a.parents[at + i] : -2;
+    tok[j] = i < a.T ? a.tokens[at + i] : 0;
+    par[j] = i < a.T ? a.parents[at + i] : -2;
+    tgt[j] = i < a.T ? a.target[at + i] : -1;
   }
+  const int n = a.count ? max(0, min(a.T, a.count[b])) : a.T;
+#pragma unroll
+  for (int j = 0; j < kNodesPerLane; ++j)
+    if (lane + 32 * j >= n) par[j] = -2;
   int cur = 0, len = 0, want = -1;
   if (n > 0) {
     while (true) {
-      want = a.target[at + cur];
+      int x = tgt[0];
+#pragma unroll
+      for (int j = 1; j < kNodesPerLane; ++j)
+        if (j == cur >> 5) x = tgt[j];
+      want = __shfl_sync(kAll, x, cur & 31);
       if (lane == 0) a.path[at + len] = cur;
       ++len;
       unsigned child = 0x7fffffffu;
