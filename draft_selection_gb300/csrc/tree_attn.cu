@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
       const int slot = tile_lo == 0 && !whole && at.u > u0 ? 1 : 0;
       if (!whole && tid == kFirst)
         a.cuts[2 * blockIdx.x + (tile_lo == 0)] =
-            make_cut(g, at.u - tile_lo, at.b, h, s.tiles);
+            make_cut(g, at.u - tile_lo, at.b, h, s);
       if (live) {
         const int head = h * a.G + r - node * a.G;
         const bool bad = *reinterpret_cast<volatile int*>(&bad_seg[seg % C::kBadSegs]) == seg;
@@ -822,9 +822,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
   const int b = cut.b, c0 = cut.c0, c1 = cut.c1_slot >> 1, slot0 = cut.c1_slot & 1;
   const int parts = c1 - c0 + 1;
   const int range = blockIdx.x / 2 / a.row_tiles, row_tile = blockIdx.x / 2 - range * a.row_tiles;
-  const int h = cut.h, r0 = row_tile * a.rows;
+  const int h = cut.h_n >> 10, r0 = row_tile * a.rows;
   const int part_size = (a.rows > a.stream_rows ? 2 : 1) * (kLanes * D);
-  const int rows = min(a.rows, load_seq(a, b).n * a.G - r0);  // (past the count: zeroed above)
+  const int rows = min(a.rows, (cut.h_n & 1023) * a.G - r0);  // (past the count: zeroed above)
   const int wide = parts <= kCombineParts       ? 1
                    : parts <= 2 * kCombineParts ? 2
                    : parts <= 4 * kCombineParts ? 4

@@ -25,7 +25,9 @@ constexpr int kKeys = 64;  // keys of a tile
 // leaves it for combine_kernel (b < 0: none): the ranges c0 .. c1, in the order of
 // the keys, and which of its two places c0's part is in (the others': the first).
 struct alignas(16) Cut {
-  int b, h, c0;
+  int b;
+  int h_n;      // h * 1024 + the sequence's nodes (at most kMaxTree)
+  int c0;
   int c1_slot;  // c1 * 2 + slot
 };
 
@@ -174,9 +176,9 @@ __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
 }
 
 // Of the head whose first unit is v0.
-__device__ __forceinline__ Cut make_cut(const Range& g, int64_t v0, int b, int h, int tiles) {
-  const int c0 = range_of(g.units, g.n_cta, v0), c1 = range_of(g.units, g.n_cta, v0 + tiles - 1);
-  return Cut{b, h, c0, c1 * 2 + (range_start(g.units, g.n_cta, c0) < v0 ? 1 : 0)};
+__device__ __forceinline__ Cut make_cut(const Range& g, int64_t v0, int b, int h, const Seq& s) {
+  const int c0 = range_of(g.units, g.n_cta, v0), c1 = range_of(g.units, g.n_cta, v0 + s.tiles - 1);
+  return Cut{b, h * 1024 + s.n, c0, c1 * 2 + (range_start(g.units, g.n_cta, c0) < v0 ? 1 : 0)};
 }
 
 template <typename E>
