@@ -125,17 +125,27 @@ struct Range {
 };
 __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
   const int lane = threadIdx.x & 31;
-  const int per = a.H;
   Range g;
-  Seq own{0, 0, 0, 0};
-  int64_t x = 0;
-  for (int b = lane; b < a.B; b += 32) {
-    own = load_seq(a, b);
-    x += own.tiles;
-  }
+  Seq own;
+  int64_t mine, sum;  // units of this lane's sequence, and of all up to it
+  auto load = [&](int b0) {
+    own = b0 + lane < a.B ? load_seq(a, b0 + lane) : Seq{0, 0, 0, 0};
+    sum = mine = static_cast<int64_t>(own.tiles) * a.H;
 #pragma unroll
-  for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(kAll, x, off);
-  g.units = x * per;
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(kAll, sum, off);
+      if (lane >= off) sum += y;
+    }
+  };
+  load(0);
+  g.units = __shfl_sync(kAll, sum, 31);
+  if (a.B > 32) {
+    int64_t x = 0;
+    for (int b = lane + 32; b < a.B; b += 32) x += load_seq(a, b).tiles;
+#pragma unroll
+    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(kAll, x, off);
+    g.units += x * a.H;
+  }
   g.n_cta = static_cast<int>(min(static_cast<int64_t>(a.grid), g.units));
   g.u0 = g.u1 = 0;
   if (cta >= g.n_cta) return g;
@@ -144,14 +154,7 @@ __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
   // the sequence that u0 falls in
   int64_t base = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    if (a.B > 32) own = b0 + lane < a.B ? load_seq(a, b0 + lane) : Seq{0, 0, 0, 0};
-    int64_t sum = static_cast<int64_t>(own.tiles) * per;
-    const int64_t mine = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(kAll, sum, off);
-      if (lane >= off) sum += y;
-    }
+    if (b0 > 0) load(b0);
     const unsigned hit = __ballot_sync(kAll, g.u0 < base + sum);
     if (hit) {
       const int w = __ffs(hit) - 1;
