@@ -127,18 +127,18 @@ __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
   const int lane = threadIdx.x & 31;
   Range g;
   Seq own;
-  int64_t mine, sum;  // units of this lane's sequence, and of all up to it
+  int sum;  // tiles of the sequences up to this lane's: 32 times 2^24 at most
   auto load = [&](int b0) {
     own = b0 + lane < a.B ? load_seq(a, b0 + lane) : Seq{0, 0, 0, 0};
-    sum = mine = static_cast<int64_t>(own.tiles) * a.H;
+    sum = own.tiles;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(kAll, sum, off);
+      const int y = __shfl_up_sync(kAll, sum, off);
       if (lane >= off) sum += y;
     }
   };
   load(0);
-  g.units = __shfl_sync(kAll, sum, 31);
+  g.units = static_cast<int64_t>(__shfl_sync(kAll, sum, 31)) * a.H;
   if (a.B > 32) {
     int64_t x = 0;
     for (int b = lane + 32; b < a.B; b += 32) x += load_seq(a, b).tiles;
@@ -155,10 +155,10 @@ __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
   int64_t base = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     if (b0 > 0) load(b0);
-    const unsigned hit = __ballot_sync(kAll, g.u0 < base + sum);
+    const unsigned hit = __ballot_sync(kAll, g.u0 < base + static_cast<int64_t>(sum) * a.H);
     if (hit) {
       const int w = __ffs(hit) - 1;
-      const int64_t before = base + __shfl_sync(kAll, sum - mine, w);
+      const int64_t before = base + static_cast<int64_t>(__shfl_sync(kAll, sum - own.tiles, w)) * a.H;
       g.first.u = g.u0;
       g.first.b = b0 + w;
       g.first.s = Seq{__shfl_sync(kAll, own.row, w), __shfl_sync(kAll, own.len, w),
@@ -172,7 +172,7 @@ __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
       g.first.tile = static_cast<int>(in - static_cast<int64_t>(g.first.h) * g.first.s.tiles);
       return g;
     }
-    base += __shfl_sync(kAll, sum, 31);
+    base += static_cast<int64_t>(__shfl_sync(kAll, sum, 31)) * a.H;
   }
   g.u1 = g.u0;  // the lengths changed in between: no work, and no endless search
   return g;
