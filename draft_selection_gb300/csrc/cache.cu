@@ -386,9 +386,10 @@ struct CompactArgs {
 // is safe.  When every block of the cluster has read the table, the first one gives the
 // pages behind the kept rows back.
 // Bound by the chain of dependent reads (path, table, rows).  The turn of 64 sequences,
-// 16 layers: 61.1 us (60.0 since the path is read beside the count), with as many blocks as columns ask for and the pages given back by a
-// kernel of their own 61.3, which costs the host 1.9 us more a call; blocks of 1024
-// threads 61.7; every thread looking its rows up for itself 1.8 more.
+// 16 layers: 61.1 us (60.0 since the path is read beside the count); with as many blocks
+// as columns ask for and the pages given back by a kernel of their own 61.3, which costs
+// the host 1.9 us more a call; blocks of 1024 threads 61.7; every thread looking its rows
+// up for itself 1.8 more.
 constexpr int kMoveThreads = 512, kMoveBlocks = 8;
 __global__ void __launch_bounds__(kMoveThreads)
     compact_kernel(const __grid_constant__ CompactArgs a) {
@@ -475,8 +476,8 @@ dfl2_status check_batch(int B, int T, int max_t) {
 
 template <bool kFork>
 cudaError_t launch_take(const TakeArgs& a, cudaStream_t s) {
-  return launch_k(a.B <= kBookThreads / 32 ? take_kernel<kFork, 32> : take_kernel<kFork, 8>, dim3(1),
-                  dim3(kBookThreads), 0, s, true, a);
+  const auto kernel = a.B <= kBookThreads / 32 ? take_kernel<kFork, 32> : take_kernel<kFork, 8>;
+  return launch_k(kernel, dim3(1), dim3(kBookThreads), 0, s, true, a);
 }
 
 int copy_blocks(int64_t items, int per_block) {
@@ -601,8 +602,9 @@ dfl2_status dfl2_cache_write(const dfl2_cache* cache, int layer, int n_layers, c
                           n_layers,
                           B};
   const int blocks = dfl2::copy_blocks(static_cast<int64_t>(n_layers) * B * T, 8);
-  return launched(dfl2::launch_k(dfl2::write_kernel, dim3(blocks), dim3(256), 0, cu(stream), true, a),
-                  "cache write launch");
+  return launched(
+      dfl2::launch_k(dfl2::write_kernel, dim3(blocks), dim3(256), 0, cu(stream), true, a),
+      "cache write launch");
 }
 
 dfl2_status dfl2_cache_compact(const dfl2_cache* cache, int B, int T, const int32_t* table_rows,

@@ -36,7 +36,8 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
 const at::Tensor& tensor(PyObject* o, const char* name, int dims) {
   const at::Tensor& t = tensor(o, name);
   if (t.dim() != dims)
-    REFUSE(PyExc_ValueError, "%s must have %d dimensions, not %lld", name, dims, (long long)t.dim());
+    REFUSE(PyExc_ValueError, "%s must have %d dimensions, not %lld", name, dims,
+           (long long)t.dim());
   return t;
 }
 bool has_shape(const at::Tensor& t, Sizes shape) {
@@ -87,7 +88,8 @@ at::ScalarType type_of(const dfl2_cache* c) {
 }
 // None: torch's current stream; else an address or a torch stream.
 dfl2_stream stream_of(PyObject* o) {
-  if (o == Py_None) return reinterpret_cast<dfl2_stream>(c10::cuda::getCurrentCUDAStream().stream());
+  if (o == Py_None)
+    return reinterpret_cast<dfl2_stream>(c10::cuda::getCurrentCUDAStream().stream());
   PyObject* a = PyLong_Check(o) ? Py_NewRef(o) : PyObject_GetAttrString(o, "cuda_stream");
   if (!a) throw Raised();
   void* p = PyLong_AsVoidPtr(a);
@@ -217,7 +219,8 @@ PyObject* tree_accept(PyObject* const* a) {
 PyObject* tree_attn(PyObject* const* a) {
   // q, cache, layer, length, mask, out, ws, rows, count, lse, scale, stream
   const dfl2_cache* c = cache_of(a[1]);
-  const at::Tensor &q = tensor(a[0], "q", 4), &out = tensor(a[5], "out", 4), &ws = tensor(a[6], "ws");
+  const at::Tensor &q = tensor(a[0], "q", 4), &out = tensor(a[5], "out", 4),
+                   &ws = tensor(a[6], "ws");
   if (q.scalar_type() != type_of(c) || out.scalar_type() != type_of(c) || out.sizes() != q.sizes())
     REFUSE(PyExc_ValueError, "q and out must be [B, T, q_heads, head_dim] of the cache's type");
   if (q.size(3) != c->head_dim || q.stride(3) != 1 || out.stride(3) != 1)
@@ -239,7 +242,8 @@ PyObject* tree_attn(PyObject* const* a) {
     if (scale == -1. && PyErr_Occurred()) throw Raised();
   }
   const int layer = whole(a[2], "layer");
-  const int32_t *length = i32(a[3], "length", {B}), *mask = i32(a[4], "mask", {B, T, (T + 31ll) / 32}),
+  const int32_t *length = i32(a[3], "length", {B}),
+                *mask = i32(a[4], "mask", {B, T, (T + 31ll) / 32}),
                 *rows = i32(a[7], "rows", {B}), *n = i32(a[8], "count", {B});
   const void* qp = q.data_ptr();
   void *op = out.data_ptr(), *wp = ws.data_ptr();
@@ -247,8 +251,8 @@ PyObject* tree_attn(PyObject* const* a) {
   const dfl2_stream s = stream_of(a[11]);
   return run([&] {
     return dfl2_tree_attn(qp, qs, c, layer, B, T, H, rows, length, n,
-                          reinterpret_cast<const uint32_t*>(mask), static_cast<float>(scale), op, os,
-                          lse, wp, bytes, s);
+                          reinterpret_cast<const uint32_t*>(mask), static_cast<float>(scale), op,
+                          os, lse, wp, bytes, s);
   });
 }
 

@@ -237,7 +237,8 @@ __device__ __forceinline__ void prefetch_l1(const void* p) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
 }
 __device__ __forceinline__ void tma_prefetch_4d(const void* tmap, int x, int y, int z, int w) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(tmap),
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
+                   tmap),
                "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
 }
@@ -264,7 +265,8 @@ __device__ __forceinline__ uint64_t seen64(const AttnArgs& a, int b, const Seq& 
   if (a.mask) {
     const uint32_t* w = a.mask + (static_cast<int64_t>(b) * a.t.T + i) * a.W;
     const int w0 = j0 >> 5;
-    const uint64_t lo = w[w0], mid = w0 + 1 < a.W ? w[w0 + 1] : 0, hi = w0 + 2 < a.W ? w[w0 + 2] : 0;
+    const uint64_t lo = w[w0], mid = w0 + 1 < a.W ? w[w0 + 1] : 0,
+                   hi = w0 + 2 < a.W ? w[w0 + 2] : 0;
     const int sh = j0 & 31;
     nodes = ((lo | mid << 32) >> sh) | (sh ? hi << (64 - sh) : 0);
   } else {
@@ -279,7 +281,7 @@ template <typename E, int D, int NS>
 __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
     attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmQ,
                 const __grid_constant__ CUtensorMap tmK,
-                   const __grid_constant__ CUtensorMap tmV) {
+                const __grid_constant__ CUtensorMap tmV) {
   using C = TcCfg<D, NS>;
   constexpr int kBlk = D / 64;          // 64-channel blocks of a row
   constexpr int kBlkBytes = kKeys * 128;  // one block of a K or V slot
@@ -558,7 +560,8 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
     const int stream = (tid - kFirst) / kLanes;
     const int quarter = warp & 3;  // the TMEM lanes a warp may read: 32 (warp % 4) ..
     const int row_l = quarter * 32 + lane;
-    const uint32_t tbase = tmem + stream * C::kStreamCols + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t tbase =
+        tmem + stream * C::kStreamCols + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t to = tbase + kColO;
     const int M = a.t.T * a.G;
     const int r0 = (row_tile * NS + stream) * a.stream_rows;
@@ -1018,8 +1021,8 @@ cudaError_t launch_attn(const AttnArgs& a, const dfl2_cache* c, cudaStream_t s) 
   // (measured: four block rows to 256 rows; sixteen cost a decode step, whose blocks
   // have next to nothing to do, 7 us of 10, one costs 427 rows in 61 nodes 14 of 46)
   const int blocks = std::max(1, std::min(a.rows, a.t.T * a.G) / 64);
-  return launch_k(combine_kernel<E, D>, dim3(2 * a.grid * a.row_tiles + a.B, blocks), dim3(kCombineWarps * 32),
-                  0, s, true, a);
+  return launch_k(combine_kernel<E, D>, dim3(2 * a.grid * a.row_tiles + a.B, blocks),
+                  dim3(kCombineWarps * 32), 0, s, true, a);
 }
 
 template <typename E>
@@ -1043,7 +1046,8 @@ dfl2_status check_shapes(int B, int T, int q_heads, int kv_heads, int head_dim, 
   if (head_dim != 64 && head_dim != 128 && head_dim != 256)
     return report_errorf(DFL2_ERR_UNSUPPORTED, "head_dim=%d: 64, 128 or 256", head_dim);
   if (dtype != DFL2_BF16 && dtype != DFL2_F16)
-    return report_errorf(DFL2_ERR_UNSUPPORTED, "dtype %d: the attention takes bf16 and fp16", dtype);
+    return report_errorf(DFL2_ERR_UNSUPPORTED, "dtype %d: the attention takes bf16 and fp16",
+                         dtype);
   return DFL2_OK;
 }
 

@@ -158,7 +158,8 @@ __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
     const unsigned hit = __ballot_sync(kAll, g.u0 < base + static_cast<int64_t>(sum) * a.H);
     if (hit) {
       const int w = __ffs(hit) - 1;
-      const int64_t before = base + static_cast<int64_t>(__shfl_sync(kAll, sum - own.tiles, w)) * a.H;
+      const int64_t before =
+          base + static_cast<int64_t>(__shfl_sync(kAll, sum - own.tiles, w)) * a.H;
       g.first.u = g.u0;
       g.first.b = b0 + w;
       g.first.s = Seq{__shfl_sync(kAll, own.row, w), __shfl_sync(kAll, own.len, w),
