@@ -126,8 +126,10 @@ def test_no_rows_to_write_need_no_address(lib):
     w = lib.dfl2_cache_write
     st = S4(0, 0, 0, 0)
     args = 0, 1, None, None, st, 1, 0, None, A, None, None
-    assert w(cache(), *args) not in (0, INVALID, UNSUPPORTED)           # A is no device memory
+    assert w(cache(), *args) != 0                    # for want of a device, or A is not its memory
+    assert "k_new" not in dfl2.dfl2_last_error() and "v_new" not in dfl2.dfl2_last_error()
     assert w(cache(), 0, 1, None, A, st, 1, 1, None, A, None, None) == INVALID
+    assert "k_new" in dfl2.dfl2_last_error()
 
 
 def test_trees_refuse(lib):
