@@ -88,7 +88,7 @@ struct TcCfg {
   static constexpr int kBars = 2 * kSlots + NS * 8;
   static constexpr int kBadSegs = 16;
   static constexpr size_t kSmem = size_t(NS) * kQ + size_t(kSlots) * kSlot + kBars * 8 +
-                                  (2 + kBadSegs) * 4;
+                                  (1 + kBadSegs + 4) * 4;
   static_assert(kBadSegs > kSlots / 2 + 1, "a head's mark outlives its last reader");
   static_assert(NS * kStreamCols * kCtas <= 512, "TMEM");
   static_assert((kSmem + 1024) * kCtas <= 233472, "shared memory");
@@ -303,9 +303,11 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
   // Heads of this CTA's range, counted up, that met Inf or NaN in V.  Stream 0, which looks,
   // may be as many tiles, so heads, ahead of stream 1 as half the ring has slots.
   int* bad_seg = reinterpret_cast<int*>(tmem_slot + 1);  // [kBadSegs]
-  // Warps that have cleaned an edge tile's V, counted up: stream 0 may be several tiles
-  // ahead of stream 1, more than a barrier's parity can tell apart.
-  uint32_t* v_clean = reinterpret_cast<uint32_t*>(bad_seg + C::kBadSegs);
+  // Edge tiles whose V each of stream 0's warps has cleaned, counted up: stream 0 may be
+  // several tiles ahead of stream 1, more than a barrier's parity can tell apart, and one
+  // of its warps a tile ahead of another, so that a sum over them would not say which
+  // tile is clean.
+  uint32_t* v_clean = reinterpret_cast<uint32_t*>(bad_seg + C::kBadSegs);  // [4]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
       }
       mbar_init(&all_done[s], 1);
     }
-    *v_clean = 0;
+    for (int i = 0; i < 4; ++i) v_clean[i] = 0;
     for (int i = 0; i < C::kBadSegs; ++i) bad_seg[i] = -1;
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
@@ -491,8 +493,9 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
       if (!wait(&full[slot], ph, a.t.err)) return false;
       if (!wait(&p_ready[2 * st + odd], (i >> 1) & 1, a.t.err)) return false;
       if (edge_prev) {  // stream 0's softmax cleans V; the others' products wait for it
-        edges += 4;
-        if (st > 0 && !wait_count_above(v_clean, edges - 1, a.t.err)) {
+        ++edges;
+        if (st > 0 &&
+            !__all_sync(kAll, wait_count_above(v_clean + (lane & 3), edges - 1, a.t.err))) {
           record_error(a.t.err, kDevErrAttn);
           return false;
         }
@@ -696,7 +699,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&p_ready[2 * stream + odd]);
-          if (kEdge && stream == 0 && NS > 1) add_release_cta(v_clean, 1);
+          if (kEdge && stream == 0 && NS > 1) add_release_cta(v_clean + quarter, 1);
         }
         ++i;
         return true;
