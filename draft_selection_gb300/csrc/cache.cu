@@ -401,7 +401,9 @@ __global__ void __launch_bounds__(kMoveThreads)
   pdl_launch_dependents();
   const int from = tid < a.t.T ? a.path[static_cast<int64_t>(b) * a.t.T + tid] : 0;
   const int len = a.t.length[b], count = a.t.count_of(b), n = min(a.n_path[b], count);
-  const int row = a.t.row_of(b), slots = (1 << a.t.page_shift) - 1;
+  int row = a.t.row_of(b);
+  if (!a.t.checked_length(len)) row = -1;
+  const int slots = (1 << a.t.page_shift) - 1;
   bool moves = false;
   int64_t src = 0, dst = 0;
   if (row >= 0 && tid < n) {
@@ -454,8 +456,8 @@ __global__ void __launch_bounds__(kMoveThreads)
   __syncwarp();
   cluster_wait_acquire();
   if (blockIdx.x > 0) return;
-  if (tid == 0) a.new_length[b] = len + max(0, n);
-  if (row < 0 || len < 0) return;
+  if (tid == 0) a.new_length[b] = row < 0 ? len : len + max(0, n);
+  if (row < 0) return;
   const int ps = 1 << a.t.page_shift;
   const int c1 = min(a.t.cols, (len + count + ps - 1) >> a.t.page_shift);
   int32_t* r = a.t.table + static_cast<int64_t>(row) * a.t.cols;

@@ -27,6 +27,7 @@ dfl2_status check_cache_device(const dfl2_cache* c);
 
 constexpr int kMaxTree = 256;   // nodes of a tree
 constexpr int kMaxSeqs = 4096;  // sequences of one bookkeeping call
+constexpr int kMaxLen = 1 << 30;  // a sequence's length
 
 inline int elem_bytes(int dtype) { return dtype == DFL2_F32 ? 4 : 2; }
 inline int log2_of(int v) {
@@ -53,6 +54,13 @@ struct TableView {
     if (static_cast<unsigned>(r) < static_cast<unsigned>(rows)) return r;
     record_error(err, kDevErrBadIndex);
     return -1;
+  }
+  // Whether a sequence can be that long; if not, recorded.  (Positions behind a length near
+  // the largest integers would wrap round to entries before the table.)
+  __device__ __forceinline__ bool checked_length(int len) const {
+    if (static_cast<unsigned>(len) <= static_cast<unsigned>(kMaxLen)) return true;
+    record_error(err, kDevErrBadIndex);
+    return false;
   }
   __device__ __forceinline__ int count_of(int b) const {
     return count ? max(0, min(T, count[b])) : T;

@@ -16,7 +16,6 @@ namespace {  // each translation unit its own copy
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMaxLen = 1 << 30;
 constexpr int kKeys = 64;  // keys of a tile
 
 }  // namespace

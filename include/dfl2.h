@@ -384,13 +384,14 @@ dfl2_status dfl2_verify(const float* p, const int32_t* tokens, const int32_t* sl
  * Arguments that the calls share:
  *   table_rows  int32 [B], the table row of each sequence, distinct within a
  *               call; NULL: sequence b is row b.
- *   length      int32 [B]: committed positions of each sequence.
+ *   length      int32 [B]: committed positions of each sequence, 0 .. 2^30.
  *   count       int32 [B]: how many of the T nodes (or tokens) of the sequence
  *               there are, 0 .. T (other values are taken to the nearer end);
  *               NULL: T each.
  *   integer arrays need 4-byte alignment, tensors of elements 16-byte.
  * A table row or page number out of range is recorded in the device error word
- * (dfl2_device_error); that sequence or position is then left out.
+ * (dfl2_device_error); that sequence or position is then left out.  So is a
+ * sequence whose length is out of range, by dfl2_cache_compact.
  * ------------------------------------------------------------------------- */
 typedef struct dfl2_cache {
   void* k;
@@ -429,7 +430,7 @@ dfl2_status dfl2_cache_write(const dfl2_cache* cache, int layer, int n_layers, c
  * dfl2_tree_accept gives them: strictly ascending) move to positions length,
  * length+1, ..; pages of the range length .. length+count-1 that hold none of
  * the kept rows are given back; new_length[b] = length[b] + n_path[b] (may be
- * the same array as length).  path int32 [B,T], n_path int32 [B] (0 drops all
+ * the same array as length; a sequence left out keeps its length).  path int32 [B,T], n_path int32 [B] (0 drops all
  * drafted rows).  T <= 256. */
 dfl2_status dfl2_cache_compact(const dfl2_cache* cache, int B, int T, const int32_t* table_rows,
                                const int32_t* length, const int32_t* count, const int32_t* path,

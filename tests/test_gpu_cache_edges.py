@@ -1,0 +1,46 @@
+"""GPU tests of the cache's calls on lengths, rows and sizes out of the ordinary."""
+import numpy as np
+import pytest
+import torch
+
+import draft_selection_gb300 as dfl2
+from test_gpu_cache import Pair, _lib, i32  # noqa: F401  (the fixture builds and loads the library)
+
+pytestmark = pytest.mark.gpu
+
+BAD_LENGTHS = [(1 << 31) - 1, (1 << 31) - 20, (1 << 30) + 1, -1, -5, -(1 << 31)]
+
+
+def recorded():
+    torch.cuda.synchronize()
+    return dfl2.dfl2_device_error()
+
+
+def test_compaction_leaves_out_a_length_out_of_range():
+    """Neither entries far from the table nor rows that a length below 0 reaches with its last
+    nodes are touched; the other sequences are compacted, and the length stays."""
+    p = Pair(7, 6, 40, 8)
+    rows = list(range(7))
+    p.reserve(rows, [0] * 7, [40] * 7)
+    p.write(rows, [0] * 7, [40] * 7)
+    p.same()
+    path = np.tile([0, 2, 5, 6, 16, -1], (7, 1))
+    path = np.concatenate([path, np.full((7, 11), -1)], 1)
+    length = i32(BAD_LENGTHS + [20])
+    dfl2.dfl2_cache_compact(p.c, length, 17, i32(path), i32([5] * 7), length)
+    assert recorded() == 5
+    want = p.m.compact([6], [20], [17], path[6:], [5])
+    assert length.tolist() == BAD_LENGTHS + want
+    p.same()
+
+
+def test_compaction_of_a_row_out_of_range_keeps_the_length():
+    p = Pair(2, 4, 9, 8)
+    p.reserve([0, 1], [0, 0], [9, 30])
+    length = i32([3, 20])
+    dfl2.dfl2_cache_compact(p.c, length, 4, i32([[0, 1, 2, 3]] * 2), i32([4, 2]), length,
+                            rows=i32([2, 1]))
+    assert recorded() == 5
+    p.m.compact([1], [20], [4], [[0, 1]], [2])
+    assert length.tolist() == [3, 22]
+    p.same()
