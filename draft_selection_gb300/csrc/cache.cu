@@ -323,10 +323,10 @@ __global__ void __launch_bounds__(256) write_kernel(const __grid_constant__ Writ
     const int r = a.t.seq ? a.t.seq[b] : b, len = a.t.length[b];  // beside the count
     if (t >= a.t.count_of(b)) continue;
     const int row = a.t.checked_row(r);
-    if (row < 0) continue;
-    const int pos = len + t;
+    if (row < 0 || !a.t.checked_length(len)) continue;
+    const int pos = len + t;  // t is below 2^30
     const int page = a.t.page_at(row, pos >> a.t.page_shift);
-    if (page < 0 || pos < 0) continue;
+    if (page < 0) continue;
     const int64_t from = l * a.nl + b * a.nb + t * a.nt;
     const int64_t to = (a.layer + l) * a.r.layer + page * a.r.page +
                        (pos & ((1 << a.t.page_shift) - 1)) * a.r.slot;

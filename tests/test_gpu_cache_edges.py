@@ -44,3 +44,17 @@ def test_compaction_of_a_row_out_of_range_keeps_the_length():
     p.m.compact([1], [20], [4], [[0, 1]], [2])
     assert length.tolist() == [3, 22]
     p.same()
+
+
+def test_writes_leave_out_a_length_out_of_range():
+    """The last tokens behind a length just below 0 would lie at positions 0, 1, .."""
+    p = Pair(7, 6, 40, 8)
+    rows = list(range(7))
+    p.reserve(rows, [0] * 7, [40] * 7)
+    p.write(rows, [0] * 7, [40] * 7)
+    vals = p.fresh(7, 9)
+    new = p.spread(vals)
+    dfl2.dfl2_cache_write(p.c, new[:, :, :, 0], new[:, :, :, 1], i32(BAD_LENGTHS + [20]))
+    assert recorded() == 5
+    p.m.write([6], [20], [9], vals[6:])
+    p.same()
