@@ -67,7 +67,8 @@ __device__ __forceinline__ Span span_of(const TakeArgs& a, int b) {
   const int len = a.t.length[b], ps = 1 << a.t.page_shift;  // beside the row's
   s.row = a.t.row_of(b);
   const int64_t end = static_cast<int64_t>(len) + (kFork ? 0 : a.t.count_of(b));
-  s.ok = s.row >= 0 && len >= 0 && end <= static_cast<int64_t>(a.t.cols) << a.t.page_shift;
+  s.ok = s.row >= 0 && len >= 0 && len <= kMaxLen &&
+         end <= static_cast<int64_t>(a.t.cols) << a.t.page_shift;
   s.c0 = s.ok ? len >> a.t.page_shift : 0;
   s.c1 = s.ok ? static_cast<int>((end + ps - 1) >> a.t.page_shift) : 0;
   return s;

@@ -392,7 +392,7 @@ dfl2_status dfl2_verify(const float* p, const int32_t* tokens, const int32_t* sl
  * A table row or page number out of range is recorded in the device error word
  * (dfl2_device_error); that sequence or position is then left out.  So is a
  * sequence whose length is out of range, by dfl2_cache_compact and
- * dfl2_cache_write.
+ * dfl2_cache_write; dfl2_cache_reserve and dfl2_cache_fork report it unserved.
  * ------------------------------------------------------------------------- */
 typedef struct dfl2_cache {
   void* k;

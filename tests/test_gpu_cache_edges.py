@@ -58,3 +58,13 @@ def test_writes_leave_out_a_length_out_of_range():
     assert recorded() == 5
     p.m.write([6], [20], [9], vals[6:])
     p.same()
+
+
+def test_rows_with_room_past_the_longest_sequence():
+    """Entries for more than 2^30 positions do not make a length above that one."""
+    cols = (1 << 22) + 16
+    c = dfl2.cache(1, 4, 1, 256, 64, 2, cols)
+    served = i32([7, 7])
+    dfl2.dfl2_cache_reserve(c, i32([(1 << 30) + 1, 1 << 30]), 3, served)
+    assert recorded() == 0 and served.tolist() == [0, 1]
+    assert c.table[1, 1 << 22] == 0 and (c.table[0] == -1).all() and int(c.refs.sum()) == 1
