@@ -13,7 +13,8 @@ constexpr int kCand = 16;   // candidates kept per position
 constexpr int kRank = 256;  // width of A(.), B(.) and H(.)
 constexpr int kGroup = 16;  // channels sharing one conv correction
 
-// Codes a kernel records in the per-device error word when a bounded wait runs out.
+// Codes a kernel records in the per-device error word: a bounded wait that ran out, or an
+// index out of range.
 enum DeviceError : uint32_t {
   kDevErrNone = 0,
   kDevErrTopkFull = 1,   // top-16 consumer waited too long for a staged tile
@@ -27,13 +28,17 @@ enum DeviceError : uint32_t {
 // About two seconds at the GB300's maximum SM clock: far beyond any legitimate wait.
 constexpr long long kWaitCycles = 4000000000LL;
 // A wait that has lasted this long (about half a millisecond) also gives up as
-// soon as any kernel has recorded an error in the device's error word: once one
-// wait of a launch has run out, the launch's other waits end within about
-// kGiveUpCycles each instead of kWaitCycles.
+// soon as any kernel has recorded a wait that ran out in the device's error word: once
+// one wait of a launch has run out, the launch's other waits end within about
+// kGiveUpCycles each instead of kWaitCycles.  An index out of range stalls nothing, so
+// while that is all the word holds, waits go on.
 constexpr long long kGiveUpCycles = 1LL << 20;
 
+// The word keeps the first code, but a wait that ran out replaces an index out of range.
 __device__ __forceinline__ void record_error(uint32_t* err, uint32_t code) {
-  if (err) atomicCAS(err, 0u, code);
+  if (!err) return;
+  if (atomicCAS(err, 0u, code) == kDevErrBadIndex && code != kDevErrBadIndex)
+    atomicCAS(err, static_cast<uint32_t>(kDevErrBadIndex), code);
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -68,11 +73,13 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 // True when a wait that started at t0 must give up: kWaitCycles have passed,
-// or kGiveUpCycles have and the error word `err` (nullable) is set.
+// or kGiveUpCycles have and the error word `err` (nullable) names a wait that ran out.
 __device__ __forceinline__ bool wait_expired(long long t0, const uint32_t* err) {
   const long long dt = clock64() - t0;
   if (dt > kWaitCycles) return true;
-  return err && dt > kGiveUpCycles && *reinterpret_cast<const volatile uint32_t*>(err) != 0u;
+  if (!err || dt <= kGiveUpCycles) return false;
+  const uint32_t code = *reinterpret_cast<const volatile uint32_t*>(err);
+  return code != kDevErrNone && code != kDevErrBadIndex;
 }
 // Bounded wait on a phase: false when it expires (wait_expired) first.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,

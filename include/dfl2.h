@@ -46,9 +46,11 @@
  *     of SM clock) records a code in a per-device error word
  *     (dfl2_device_error) and the kernel carries on without the data it
  *     waited for, so that launch's outputs are undefined; it still ends and
- *     leaves the context usable.  Once the error word is set, every other wait
- *     that has lasted about 0.5 ms gives up too, so a launch whose pipeline
- *     stalls ends within a few seconds, not one full timeout per wait.
+ *     leaves the context usable.  Once the error word holds such a code, every
+ *     other wait that has lasted about 0.5 ms gives up too, so a launch whose
+ *     pipeline stalls ends within a few seconds, not one full timeout per wait.
+ *     (An index out of range, code 5, ends no wait, and a wait that runs out
+ *     replaces it in the word.)
  *   - Workspaces must be zero-filled once before their first use (for example
  *     with dfl2_workspace_init); the library keeps them valid afterwards.
  */
@@ -107,7 +109,7 @@ int dfl2_set_projection_engine(int engine);
 dfl2_status dfl2_workspace_init(void* ws, size_t ws_bytes, dfl2_stream stream);
 
 /* Reads, and if clear != 0 resets, the current device's error word.  0 means no
- * kernel recorded a failed wait.  SYNCHRONISES the current device. */
+ * kernel recorded a failed wait or an index out of range (5).  SYNCHRONISES the current device. */
 dfl2_status dfl2_device_error(uint32_t* code, int clear);
 
 /* ------------------------------------------------------------------ top-16

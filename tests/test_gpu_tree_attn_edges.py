@@ -33,3 +33,28 @@ def test_nan_in_nodes_of_two_last_tiles(T, G, D):
             assert torch.equal(out[b, blind], clean[b, blind]), b
             sees = torch.from_numpy(np.nonzero(c.seen[b][:, hit[b]])[0]).cuda()
             assert not torch.isfinite(out[b, sees][..., b % 7::9]).any(), b
+
+
+def slow_nodes():
+    """NaN in the values of one node of 256 in every sequence, several heads to a CTA."""
+    c = Case([100, 300, 37, 64] * 16, 256, 8, 8, 128, 16, seed=3, mask="chain")
+    table = c.cache.table.cpu()
+    for b, n in enumerate(c.lens):
+        c.cache.v[0, int(table[b, (n + 5) // 16]), :, (n + 5) % 16] = float("nan")
+    return c
+
+
+def test_a_recorded_index_ends_no_wait():
+    """An index out of range in the error word is an ordinary state: what is merely slow then
+    still ends whole."""
+    c = slow_nodes()
+    want, want_lse = c.run()
+    bad = torch.tensor([-1], dtype=torch.int32, device="cuda")
+    dfl2.dfl2_cache_free(c.cache, bad)
+    assert dfl2.dfl2_device_error(clear=False) == 5
+    q, out, lse = c.q.cuda(), torch.zeros_like(want), torch.zeros_like(want_lse)
+    ws = dfl2.workspace(dfl2.dfl2_tree_attn_workspace_size(*q.shape[:3], 8, 128, c.dtype))
+    dfl2.dfl2_tree_attn(q, c.cache, 0, c.length, c.mask, out, ws, lse=lse)
+    assert dfl2.dfl2_device_error() == 5
+    assert torch.equal(out.nan_to_num(7.0), want.nan_to_num(7.0)) and torch.equal(lse, want_lse)
+    assert torch.isnan(out[:, 5:]).all() and torch.isfinite(out[:, :5]).all()
