@@ -277,6 +277,59 @@ __device__ __forceinline__ uint64_t seen64(const AttnArgs& a, int b, const Seq& 
   return vis | nodes << ctx;
 }
 
+// The Inf and NaN values, of the nodes of positions [p0, p1), that node i (-1: none) sees,
+// added to this row's O at TMEM address `to`, by a warp together.  Such values are kept out
+// of the matrix product, where a weight of 0 would spread them to the nodes that do not see
+// them; their sum decides its channel of the output.  Only called when there are any; a
+// node's mask bit and page are looked up once for 32 channels (64 trees of 256 nodes, 8
+// heads, one NaN in each tree: 2.7 ms, channel by channel 50).
+template <typename E, int D>
+__device__ __noinline__ void add_unseen(const AttnArgs& a, uint32_t to, int b, const Seq& s, int h,
+                                        int i, int p0, int p1) {
+  const int j0 = max(0, p0 - s.len), j1 = i < 0 ? 0 : min(p1 - s.len, s.n);
+  const uint32_t* mask =
+      a.mask ? a.mask + (static_cast<int64_t>(b) * a.t.T + max(0, i)) * a.W : nullptr;
+  for (int c0 = 0; c0 < D; c0 += 32) {
+    float y[32];
+#pragma unroll
+    for (int c = 0; c < 32; ++c) y[c] = 0.f;
+    uint32_t word = 0;
+    for (int j = j0; j < j1; ++j) {
+      if (mask) {
+        if (j == j0 || (j & 31) == 0) word = mask[j >> 5];
+        if (!(word >> (j & 31) & 1u)) continue;
+      } else if (j > i) {
+        break;
+      }
+      const int pos = s.len + j;
+      const int64_t page = a.t.page_at(s.row, pos >> a.t.page_shift);
+      if (page < 0) continue;
+      const E* v = static_cast<const E*>(a.v) + page * a.page_stride + h * a.head_stride +
+                   (pos & ((1 << a.t.page_shift) - 1)) * a.slot_stride + c0;
+#pragma unroll
+      for (int c = 0; c < 32; c += 8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(v + c);
+        if (!not_finite<E>(x)) continue;
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+          const uint16_t bits = static_cast<uint16_t>(w[z / 2] >> (z % 2 * 16));
+          const float f = to_f32(*reinterpret_cast<const E*>(&bits));
+          if (!isfinite(f)) y[c + z] += f;
+        }
+      }
+    }
+    __syncwarp();
+    uint32_t o[32];
+    tmem_ld32_issue(to + c0, o);
+    tmem_ld32_wait(o);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) + y[c]);
+    tmem_st32(to + c0, o);
+  }
+  tmem_st_wait();
+}
+
 template <typename E, int D, int NS>
 __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
     attn_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap tmQ,
@@ -667,7 +720,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
         }
         if (kEdge && stream == 0) {
           // V's rows past the end are zeroed and Inf and NaN of nodes set aside
-          // (unseen_safe_sum): a weight of 0 would not keep them out of the product
+          // (add_unseen): a weight of 0 would not keep them out of the product
           const int sq = seq_v(i), slot = sq % C::kSlots;
           if (!wait(&full[slot], (sq / C::kSlots) & 1, a.t.err)) return false;
           constexpr int kPieces = C::kSlot / 16 / kLanes;
@@ -730,20 +783,13 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
         float* part_o = a.part_o + part * (NS * kLanes * D) + part_at<D>(stream, row_l, 0);
         E* out = static_cast<E*>(a.out) + at.b * a.ob + node * a.ot + head * a.oh;
         const bool mine = r < M && node < s.n;
+        if (__any_sync(kAll, bad))
+          add_unseen<E, D>(a, to, at.b, s, h, mine ? node : -1, tile_lo * kKeys, tile_hi * kKeys);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           tmem_ld32_issue(to + c, o);
           tmem_ld32_wait(o);
-          if (bad && mine)
-            for (int j = 0; j < 32; ++j) {
-              const float y = unseen_safe_sum<E>(a, at.b, s, h, node, c + j, tile_lo * kKeys,
-                                                 tile_hi * kKeys);
-              // (an index known at compile time keeps o in registers)
-#pragma unroll
-              for (int z = 0; z < 32; ++z)
-                if (z == j) o[z] = __float_as_uint(__uint_as_float(o[z]) + y);
-            }
           if (mine && whole) {
             uint32_t y[16];
 #pragma unroll

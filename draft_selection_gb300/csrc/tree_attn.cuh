@@ -221,33 +221,6 @@ __device__ __forceinline__ bool not_finite(uint4 x) {
          0x80008000u;
 }
 
-// Whether node i of sequence b sees node j (0 <= j).
-__device__ __forceinline__ bool sees(const AttnArgs& a, int b, int n, int i, int j) {
-  if (j >= n) return false;
-  if (!a.mask) return j <= i;
-  return a.mask[(static_cast<int64_t>(b) * a.t.T + i) * a.W + (j >> 5)] >> (j & 31) & 1u;
-}
-
-// The Inf and NaN values, of the nodes of positions [p0, p1), that node i sees
-// in channel c: their sum, which decides that channel of the output.  Such
-// values are kept out of the matrix product, where a weight of 0 would spread
-// them to the nodes that do not see them.  Only ever called when there are any.
-template <typename E>
-__device__ __noinline__ float unseen_safe_sum(const AttnArgs& a, int b, const Seq& s, int h, int i,
-                                              int c, int p0, int p1) {
-  float x = 0.f;
-  for (int pos = max(p0, s.len); pos < min(p1, s.len + s.n); ++pos) {
-    if (!sees(a, b, s.n, i, pos - s.len)) continue;
-    const int64_t page = a.t.page_at(s.row, pos >> a.t.page_shift);
-    if (page < 0) continue;
-    const E* v = static_cast<const E*>(a.v) + page * a.page_stride + h * a.head_stride +
-                 (pos & ((1 << a.t.page_shift) - 1)) * a.slot_stride;
-    const float y = to_f32(v[c]);
-    if (!isfinite(y)) x += y;
-  }
-  return x;
-}
-
 }  // namespace
 
 }  // namespace dfl2

@@ -58,3 +58,20 @@ def test_a_recorded_index_ends_no_wait():
     assert dfl2.dfl2_device_error() == 5
     assert torch.equal(out.nan_to_num(7.0), want.nan_to_num(7.0)) and torch.equal(lse, want_lse)
     assert torch.isnan(out[:, 5:]).all() and torch.isfinite(out[:, :5]).all()
+
+
+def test_nan_in_a_node_costs_no_more_than_its_nodes():
+    """Looking for the values that are no numbers takes time by the nodes that are seen, not by
+    nodes times channels: the limit is a tenth of what the latter took, 50 ms."""
+    c = slow_nodes()
+    q = c.q.cuda()
+    out = torch.empty_like(q)
+    ws = dfl2.workspace(dfl2.dfl2_tree_attn_workspace_size(*q.shape[:3], 8, 128, c.dtype))
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    for _ in range(3):
+        begin.record()
+        dfl2.dfl2_tree_attn(q, c.cache, 0, c.length, c.mask, out, ws)
+        end.record()
+    torch.cuda.synchronize()
+    assert begin.elapsed_time(end) < 5.0
+    assert dfl2.dfl2_device_error() == 0
