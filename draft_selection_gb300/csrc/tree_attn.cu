@@ -37,6 +37,12 @@
 // rounding to a floating type, and the rescaling (TMEM -> registers -> TMEM, after
 // the products in flight) then almost never happens past a row's first tiles.
 //
+// A page that a sequence lacks is read as NaN in K and as zeros in V.  A row's maximum is NaN
+// then, and only in that case does it look for such positions, which it leaves out.  (A word
+// of each tile's missing pages read with its scores, or the scores replaced in place, cost
+// every tile: 64 trees of 33 nodes 142.8 and 141.5 us instead of 141.0, 9 trees of 61 nodes
+// and 64 channels 34.0 and 33.5 instead of 32.8.)
+//
 // Roles: warp 0 loads K and V (TMA boxes of one page's rows x 64 channels,
 // 128-byte swizzle, into a ring of slots of one tile's K or V); a stream, 128
 // rows, has one warp that issues its MMAs and four that do its softmax.  A row's
@@ -87,9 +93,11 @@ struct TcCfg {
   static constexpr int kThreads = 32 * (1 + NS) + NS * kLanes;
   static constexpr int kBars = 2 * kSlots + NS * 8;
   static constexpr int kBadSegs = 16;
+  static constexpr int kHoles = 16;
   static constexpr size_t kSmem = size_t(NS) * kQ + size_t(kSlots) * kSlot + kBars * 8 +
-                                  (1 + kBadSegs + 4) * 4;
+                                  (1 + kBadSegs + 4 + 2 * kHoles) * 4;
   static_assert(kBadSegs > kSlots / 2 + 1, "a head's mark outlives its last reader");
+  static_assert(kHoles > kSlots / 2 + 3, "a tile's holes outlive their last reader");
   static_assert(NS * kStreamCols * kCtas <= 512, "TMEM");
   static_assert((kSmem + 1024) * kCtas <= 233472, "shared memory");
 };
@@ -220,10 +228,23 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
+__device__ __forceinline__ float max3(float a, float b, float c) {  // NaN if one is
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+__device__ __forceinline__ float max64(const uint32_t* x) {
+  float mx[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(x[c]);
+#pragma unroll
+  for (int c = 4; c < 60; c += 8)
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+      mx[z] = max3(mx[z], __uint_as_float(x[c + z]), __uint_as_float(x[c + 4 + z]));
+  return max3(max3(mx[0], __uint_as_float(x[60]), __uint_as_float(x[61])),
+              max3(mx[1], __uint_as_float(x[62]), __uint_as_float(x[63])),
+              max3(mx[2], mx[3], mx[3]));
 }
 
 // 32 bytes: a whole sector a thread, where rows lie apart (a store of 16 costs as many
@@ -275,6 +296,24 @@ __device__ __forceinline__ uint64_t seen64(const AttnArgs& a, int b, const Seq& 
   const int left = s.n - j0;
   if (left < 64) nodes &= (1ull << left) - 1;
   return vis | nodes << ctx;
+}
+
+// A row's 64 scores at TMEM address `at`: those of positions whose pages are among `hole`
+// (bit z * kBlk: the tile's z-th page) are NaN and become -inf.  The row's maximum.
+template <int kBlk>
+__device__ __noinline__ float leave_out(uint32_t at, uint32_t hole, int page_shift) {
+  uint32_t x[64];
+  tmem_ld32_issue(at, x);
+  tmem_ld32_issue(at + 32, x + 32);
+  tmem_ld32_wait(x);
+  tmem_ld32_wait(x + 32);
+#pragma unroll
+  for (int c = 0; c < 64; ++c)
+    if (hole >> (c >> page_shift) * kBlk & 1) x[c] = 0xFF800000u;
+  tmem_st32(at, x);
+  tmem_st32(at + 32, x + 32);
+  tmem_st_wait();
+  return max64(x);
 }
 
 // The Inf and NaN values, of the nodes of positions [p0, p1), that node i (-1: none) sees,
@@ -361,6 +400,11 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
   // of its warps a tile ahead of another, so that a sum over them would not say which
   // tile is clean.
   uint32_t* v_clean = reinterpret_cast<uint32_t*>(bad_seg + C::kBadSegs);  // [4]
+  // A tile that lacks pages: its number in this CTA's range, and a bit for each of the loads'
+  // lanes.  The loads may be as many tiles ahead of the softmax as half the ring has slots,
+  // and those of the products in flight.
+  int* hole_tile = reinterpret_cast<int*>(v_clean + 4);  // [kHoles]
+  uint32_t* holes = v_clean + 4 + C::kHoles;             // [kHoles]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
@@ -380,6 +424,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
     }
     for (int i = 0; i < 4; ++i) v_clean[i] = 0;
     for (int i = 0; i < C::kBadSegs; ++i) bad_seg[i] = -1;
+    for (int i = 0; i < C::kHoles; ++i) hole_tile[i] = -1;
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
@@ -431,9 +476,16 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
       const bool past = !mine || pos >= c.s.len + c.s.n;
       return Tile{c.h, c.tile, past ? -1 : a.t.entry(c.s.row, pos >> a.t.page_shift), past};
     };
-    auto page_of = [&](const Tile& t) {  // one page too far, which TMA reads as zeros, for none
-      const int p = t.past ? -1 : a.t.checked(t.entry);
-      return p < 0 ? a.t.pages : p;
+    // One page too far for none: V's rows are then zeros and K's NaN (map_4d).
+    auto page_of = [&](const Tile& t, int i) {
+      const bool in = static_cast<unsigned>(t.entry) < static_cast<unsigned>(a.t.pages);
+      const uint32_t hole = __ballot_sync(kAll, !in && !t.past);
+      if (hole && lane == 0) {  // before the arrival on K's barrier
+        record_error(a.t.err, kDevErrBadIndex);
+        hole_tile[i % C::kHoles] = i;
+        holes[i % C::kHoles] = hole;
+      }
+      return in ? t.entry : a.t.pages;
     };
     int issued = 0;
     bool ok = true;
@@ -475,7 +527,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
       }
       int page = 0;
       if (i < N) {
-        page = page_of(t);
+        page = page_of(t, i);
         load(&tmK, t.h, t.tile, page);
       }
       if (i > 0 && ok) load(&tmV, v_h, v_tile, v_page);
@@ -666,36 +718,48 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
             for (int c = 0; c < 64; ++c)
               if (!(vis >> c & 1)) x[c] = 0xFF800000u;  // -inf
           }
-          float mx[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(x[c]);
-#pragma unroll
-          for (int c = 4; c < 60; c += 8)
-#pragma unroll
-            for (int z = 0; z < 4; ++z)
-              mx[z] = max3(mx[z], __uint_as_float(x[c + z]), __uint_as_float(x[c + 4 + z]));
-          const float top =
-              max3(max3(mx[0], __uint_as_float(x[60]), __uint_as_float(x[61])),
-                   max3(mx[1], __uint_as_float(x[62]), __uint_as_float(x[63])),
-                   fmaxf(mx[2], mx[3])) * sl;
-          if (tile == tile_lo) {
-            m = top;
-          } else if (__any_sync(kAll, top > m + kRise)) {  // (m = -inf: anything above)
-            if (!wait(&pv_done[2 * stream + (odd ^ 1)], ((i - 1) >> 1) & 1, a.t.err)) return false;
-            __syncwarp();
-            tc_fence_after();
-            const float mn = top > m + kRise ? top : m;
-            const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
-            l *= f;
-            m = mn;
+          float top = r < M ? max64(x) * sl : -INFINITY;  // NaN if a score is
+          if (__any_sync(kAll, !(top <= m + kRise))) {  // (m = -inf: anything above)
+            if (__any_sync(kAll, top != top)) {
+              // the scores of positions without a page, which are NaN, become -inf
+              if (*reinterpret_cast<volatile int*>(&hole_tile[i % C::kHoles]) == i) {
+                // (out of line, by way of P's columns: in place it slows every tile)
+                const uint32_t hole = *reinterpret_cast<volatile uint32_t*>(&holes[i % C::kHoles]);
+                if (i > 0 && !wait(&pv_done[2 * stream + (odd ^ 1)], ((i - 1) >> 1) & 1, a.t.err))
+                  return false;
+                __syncwarp();
+                tc_fence_after();
+                tmem_st32(tbase + kColP, x);
+                tmem_st32(tbase + kColP + 32, x + 32);
+                tmem_st_wait();
+                top = leave_out<kBlk>(tbase + kColP, hole, a.t.page_shift) * sl;
+                if (r >= M) top = -INFINITY;
+                tmem_ld32_issue(tbase + kColP, x);
+                tmem_ld32_issue(tbase + kColP + 32, x + 32);
+                tmem_ld32_wait(x);
+                tmem_ld32_wait(x + 32);
+              }
+            }
+            if (tile == tile_lo) {
+              m = top == top ? top : 0.f;  // (NaN is in l, and need not rescale every tile)
+            } else {
+              if (!wait(&pv_done[2 * stream + (odd ^ 1)], ((i - 1) >> 1) & 1, a.t.err))
+                return false;
+              __syncwarp();
+              tc_fence_after();
+              const float mn = top > m + kRise ? top : m;
+              const float f = mn == -INFINITY ? 1.f : ex2(m - mn);
+              l *= f;
+              m = mn;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32_issue(to + c, o);
-              tmem_ld32_wait(o);
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32_issue(to + c, o);
+                tmem_ld32_wait(o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st32(to + c, o);
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_st32(to + c, o);
+              }
             }
           }
           const float safe = m == -INFINITY ? 0.f : m;
@@ -984,9 +1048,11 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 }
 
 // A tensor map of 16-bit elements [n3, n2, n1, D] with element strides, boxes of
-// 64 channels x b1 x b2, 128-byte swizzle.
+// 64 channels x b1 x b2, 128-byte swizzle.  What lies outside is read as zeros, or as NaN:
+// so K is, whose page may be none, and the softmax need not look for that in every tile, only
+// where a row's maximum is NaN.
 bool map_4d(const void* base, bool f16, int D, const int64_t (&n)[3], const int64_t (&stride)[3],
-            int b1, int b2, CUtensorMap* out) {
+            int b1, int b2, bool nan, CUtensorMap* out) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = encoder();
   if (!encode) return false;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(D)}, strides[3];
@@ -1000,7 +1066,8 @@ bool map_4d(const void* base, bool f16, int D, const int64_t (&n)[3], const int6
   return encode(out, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                 const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                nan ? CU_TENSOR_MAP_FLOAT_OOB_FILL_NAN_REQUEST_ZERO_FMA
+                    : CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // ---- plan ---------------------------------------------------------------------
@@ -1057,8 +1124,9 @@ cudaError_t launch_attn(const AttnArgs& a, const dfl2_cache* c, cudaStream_t s) 
   const int64_t n[3] = {c->page_size, c->kv_heads, c->pages};
   const int64_t st[3] = {c->slot_stride, c->head_stride, c->page_stride};
   const int box = std::min(c->page_size, kKeys);
-  if (!map_4d(a.q, f16, D, qn, qs, a.G, a.stream_rows / a.G, &tq) ||
-      !map_4d(a.k, f16, D, n, st, box, 1, &tk) || !map_4d(a.v, f16, D, n, st, box, 1, &tv))
+  if (!map_4d(a.q, f16, D, qn, qs, a.G, a.stream_rows / a.G, false, &tq) ||
+      !map_4d(a.k, f16, D, n, st, box, 1, true, &tk) ||
+      !map_4d(a.v, f16, D, n, st, box, 1, false, &tv))
     return cudaErrorInvalidValue;
   cudaError_t e;
   if constexpr (D == 256)

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import draft_selection_gb300 as dfl2
+from _tree_ref import attention, attention_bounds
 from test_gpu_tree_attn import Case, _lib  # noqa: F401  (the fixture builds and loads the library)
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +76,68 @@ def test_nan_in_a_node_costs_no_more_than_its_nodes():
     torch.cuda.synchronize()
     assert begin.elapsed_time(end) < 5.0
     assert dfl2.dfl2_device_error() == 0
+
+
+def check_without(c, out, lse, gone):
+    """As Case.check, without the positions gone[b] of sequence b."""
+    o, z = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, (n, cnt) in enumerate(zip(c.lens, c.counts)):
+        seen = np.ones((c.T, n + cnt), bool)
+        seen[:, n:] = c.seen[b][:, :cnt]
+        seen[cnt:] = False
+        seen[:, gone[b]] = False
+        kv = c.kv[b].double().numpy()
+        ref = attention(c.q[b].double().numpy(), kv[0], kv[1], seen, c.D ** -0.5)
+        ob, lb = attention_bounds(ref, c.dtype, c.D, n + cnt)
+        assert (np.abs(o[b] - ref[0]) <= ob).all(), (b, np.abs(o[b] - ref[0]).max())
+        dead = np.isneginf(ref[1])
+        assert np.array_equal(z[b][dead], ref[1][dead])
+        assert (np.abs(z[b][~dead] - ref[1][~dead]) <= lb[~dead]).all(), b
+
+
+@pytest.mark.parametrize("page", [8, 16, 32, 64, 256])
+@pytest.mark.parametrize("T,Hq,Hkv,D,dtype", [(1, 4, 2, 128, torch.bfloat16),
+                                              (20, 8, 1, 64, torch.float16),
+                                              (70, 4, 1, 128, torch.bfloat16),
+                                              (9, 8, 2, 256, torch.bfloat16)])
+def test_positions_without_a_page_are_left_out(T, Hq, Hkv, D, dtype, page):
+    """Entries that are -1 or name no page, among the committed positions, among the nodes and
+    everywhere: those positions count for nothing, and the index is recorded."""
+    lens = [700, 515, 300, 0, 1500, 64, 2000]
+    c = Case(lens, T, Hq, Hkv, D, page, dtype, seed=page + T)
+    rng = np.random.default_rng(page)
+    table = c.cache.table.cpu().numpy()
+    gone = []
+    for b, n in enumerate(lens):
+        used = -(-(n + T) // page)
+        if b == 4:
+            cols = np.arange(used)                    # a sequence that was given no pages
+        elif b == 5:
+            cols = np.arange(n // page, used)         # no pages for its nodes
+        elif b == 6:
+            cols = np.arange(max(1, used // 2))       # none for its first half
+        else:
+            cols = rng.permutation(used)[:1 + used // 7]
+        table[b, cols] = rng.choice([-1, 1 << 20, -7, c.cache.k.shape[1]], len(cols))
+        gone.append(np.concatenate([np.arange(x * page, min((x + 1) * page, n + T)) for x in cols]))
+    c.cache.table.copy_(torch.from_numpy(table))
+    q = c.q.cuda()
+    out = torch.full_like(q, float("nan"))
+    lse = torch.full(q.shape[:3], float("nan"), device="cuda")
+    ws = dfl2.workspace(dfl2.dfl2_tree_attn_workspace_size(*q.shape[:3], Hkv, D, dtype))
+    dfl2.dfl2_tree_attn(q, c.cache, 0, c.length, c.mask, out, ws, lse=lse)
+    assert dfl2.dfl2_device_error() == 5
+    check_without(c, out, lse, gone)
+
+
+@pytest.mark.parametrize("T", [3, 50])
+def test_nan_keys_of_committed_positions(T):
+    """A number that is none is no missing page: every node of that key head has it."""
+    c = Case([500, 300, 70], T, 8, 2, 128, 16, seed=T)
+    want, want_lse = c.run()
+    page = int(c.cache.table[1, 5])
+    c.cache.k[0, page, 1, 3] = float("nan")
+    out, lse = c.run()
+    assert torch.isnan(out[1, :, 4:]).all() and torch.isnan(lse[1, :, 4:]).all()
+    out[1, :, 4:], lse[1, :, 4:] = want[1, :, 4:], want_lse[1, :, 4:]
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
