@@ -855,6 +855,9 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
           tmem_ld32_issue(to + c, o);
           tmem_ld32_wait(o);
           if (mine && whole) {
+            if (l == 0.f)  // no score above -inf, whatever the values: 0 times Inf is NaN
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = 0;
             uint32_t y[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j)
@@ -1016,6 +1019,9 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
       __syncthreads();
     }
     if (r < rows && part0 == 0) {
+      if (l == 0.f)  // (as in attn_kernel)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) y[q] = make_float4(0.f, 0.f, 0.f, 0.f);
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int node = (r0 + r) / a.G, head = h * a.G + (r0 + r) - node * a.G;
       uint2* out = reinterpret_cast<uint2*>(static_cast<E*>(a.out) + b * a.ob + node * a.ot +

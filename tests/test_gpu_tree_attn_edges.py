@@ -141,3 +141,19 @@ def test_nan_keys_of_committed_positions(T):
     assert torch.isnan(out[1, :, 4:]).all() and torch.isnan(lse[1, :, 4:]).all()
     out[1, :, 4:], lse[1, :, 4:] = want[1, :, 4:], want_lse[1, :, 4:]
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("T,D,dtype", [(2, 64, torch.bfloat16), (40, 128, torch.float16),
+                                       (3, 256, torch.bfloat16)])
+def test_rows_with_scores_of_minus_infinity_only(T, D, dtype):
+    """Out is 0 and lse -inf whatever the values hold, in a sequence of one tile and in one that
+    is cut into parts."""
+    c = Case([20, 9000], T, 4, 2, D, 16, dtype, seed=D, mask="chain")
+    table = c.cache.table.cpu()
+    c.cache.k.fill_(float("-inf"))
+    q = torch.rand(2, T, 4, D, device="cuda").to(dtype) + 1
+    for b, n in enumerate(c.lens):
+        for j, x in ((3, float("inf")), (n - 1, float("nan")), (n + T - 1, float("-inf"))):
+            c.cache.v[0, int(table[b, j // 16]), :, j % 16, ::3] = x
+    out, lse = c.run(q=q)
+    assert (out == 0).all() and (lse == -np.inf).all()
