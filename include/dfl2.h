@@ -393,8 +393,8 @@ dfl2_status dfl2_verify(const float* p, const int32_t* tokens, const int32_t* sl
  *   integer arrays need 4-byte alignment, tensors of elements 16-byte.
  * A table row or page number out of range is recorded in the device error word
  * (dfl2_device_error); that sequence or position is then left out.  So is a
- * sequence whose length is out of range, by dfl2_cache_compact and
- * dfl2_cache_write; dfl2_cache_reserve and dfl2_cache_fork report it unserved.
+ * sequence whose length is out of range, except that dfl2_cache_reserve and
+ * dfl2_cache_fork only report it unserved.
  * ------------------------------------------------------------------------- */
 typedef struct dfl2_cache {
   void* k;
@@ -491,8 +491,8 @@ dfl2_status dfl2_tree_accept(const int32_t* tokens, const int32_t* parents,
  *               overlap q or the cache.
  *   lse         float32 [B,T,q_heads] (nullable): log sum_j exp(s_j).
  *   head_dim 64, 128 or 256; q_heads a multiple of kv_heads, at most 128 times it;
- *   1 <= T <= 256; 1 <= B <= 65535; lengths up to 2^30; every cache stride of a
- *   dimension of more than one entry positive.
+ *   1 <= T <= 256; 1 <= B <= 65535; every cache stride of a dimension of more than
+ *   one entry positive.
  *   ws          dfl2_tree_attn_workspace_size bytes, scratch only.
  * Scores, softmax and sums are float32; the weights are rounded to the cache's
  * type for the product with V. */

@@ -157,3 +157,16 @@ def test_rows_with_scores_of_minus_infinity_only(T, D, dtype):
             c.cache.v[0, int(table[b, j // 16]), :, j % 16, ::3] = x
     out, lse = c.run(q=q)
     assert (out == 0).all() and (lse == -np.inf).all()
+
+
+@pytest.mark.parametrize("length", [-1, -(1 << 31), (1 << 30) + 1, (1 << 31) - 1])
+def test_lengths_out_of_range_are_recorded(length):
+    c = Case([100, 30, 50], 3, 4, 2, 128, 16, seed=1)
+    want, want_lse = c.run()
+    c.length[1] = length
+    q, out, lse = c.q.cuda(), torch.empty_like(want), torch.empty_like(want_lse)
+    ws = dfl2.workspace(dfl2.dfl2_tree_attn_workspace_size(3, 3, 4, 2, 128, c.dtype))
+    dfl2.dfl2_tree_attn(q, c.cache, 0, c.length, c.mask, out, ws, lse=lse)
+    assert dfl2.dfl2_device_error() == 5
+    assert (out[1] == 0).all() and (lse[1] == -np.inf).all()
+    assert torch.equal(out[::2], want[::2]) and torch.equal(lse[::2], want_lse[::2])
