@@ -124,10 +124,13 @@ __global__ void __launch_bounds__(kBookThreads) take_kernel(const __grid_constan
       const int32_t* row = a.t.table + static_cast<int64_t>(s.row) * a.t.cols;
       if (kFork) {
         good = static_cast<unsigned>(src) < static_cast<unsigned>(a.t.rows) && src != s.row;
-        if (good)
+        if (good) {
 #pragma unroll 4
-          for (int c = gl; c < s.c1; c += kWidth)
-            good &= row[c] < 0 && a.t.page_at(src, c, true) >= 0;
+          for (int c = gl; c < s.c1; c += kWidth) good &= a.t.page_at(src, c, true) >= 0;
+          // (to the row's end: pages past the fork's last would be the next reserve's)
+#pragma unroll 8
+          for (int c = gl; c < a.t.cols; c += kWidth) good &= row[c] < 0;
+        }
       }
 #pragma unroll 4
       for (int c = s.c0 + gl; c < s.c1; c += kWidth) need += row[c] < 0;

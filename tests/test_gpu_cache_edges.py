@@ -68,3 +68,16 @@ def test_rows_with_room_past_the_longest_sequence():
     dfl2.dfl2_cache_reserve(c, i32([(1 << 30) + 1, 1 << 30]), 3, served)
     assert recorded() == 0 and served.tolist() == [0, 1]
     assert c.table[1, 1 << 22] == 0 and (c.table[0] == -1).all() and int(c.refs.sum()) == 1
+
+
+def test_fork_into_a_row_with_pages_is_refused_wherever_they_are():
+    """Also where the fork itself needs fewer entries, or none."""
+    p = Pair(6, 40, 60, 8)
+    p.reserve([0, 1, 2], [0, 0, 200], [100, 5, 9])      # row 2: pages behind position 200 only
+    before = p.c.table.clone()
+    served = i32([7] * 4)
+    dfl2.dfl2_cache_fork(p.c, i32([0, 0, 0, 0]), i32([1, 2, 3, 4]), i32([0, 20, 0, 20]), served)
+    assert served.tolist() == [0, 0, 1, 1]
+    assert torch.equal(p.c.table[:4], before[:4])
+    assert p.m.fork([0, 0], [3, 4], [0, 20]) == [1, 1]
+    p.same()
