@@ -120,10 +120,11 @@ __global__ void __launch_bounds__(kBookThreads) take_kernel(const __grid_constan
     if (there) s = span_of<kFork>(a, b);
     int need = 0;
     bool good = s.ok;
+    if (kFork && there) good &= a.t.checked_row(src) >= 0;
     if (good) {
       const int32_t* row = a.t.table + static_cast<int64_t>(s.row) * a.t.cols;
       if (kFork) {
-        good = static_cast<unsigned>(src) < static_cast<unsigned>(a.t.rows) && src != s.row;
+        good = src != s.row;
         if (good) {
 #pragma unroll 4
           for (int c = gl; c < s.c1; c += kWidth) good &= a.t.page_at(src, c, true) >= 0;

@@ -81,3 +81,14 @@ def test_fork_into_a_row_with_pages_is_refused_wherever_they_are():
     assert torch.equal(p.c.table[:4], before[:4])
     assert p.m.fork([0, 0], [3, 4], [0, 20]) == [1, 1]
     p.same()
+
+
+@pytest.mark.parametrize("src,dst", [(6, 3), (-1, 3), (1 << 30, 3), (0, 6), (0, -2)])
+def test_forks_of_rows_out_of_range_are_recorded(src, dst):
+    p = Pair(6, 4, 20, 8)
+    p.reserve([0], [0], [20])
+    served = i32([7, 7])
+    dfl2.dfl2_cache_fork(p.c, i32([src, 0]), i32([dst, 2]), i32([20, 20]), served)
+    assert recorded() == 5 and served.tolist() == [0, 1]
+    p.m.fork([0], [2], [20])
+    p.same()
