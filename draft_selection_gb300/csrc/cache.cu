@@ -472,10 +472,10 @@ __global__ void __launch_bounds__(kMoveThreads)
   }
 }
 
-dfl2_status check_batch(int B, int T, int max_t) {
+dfl2_status check_batch(int B, int T, int max_t, int max_b = kMaxBatch) {
   if (B < 1) return report_errorf(DFL2_ERR_INVALID_ARG, "B=%d must be >= 1", B);
-  if (B > kMaxSeqs)
-    return report_errorf(DFL2_ERR_UNSUPPORTED, "B=%d: at most %d sequences a call", B, kMaxSeqs);
+  if (B > max_b)
+    return report_errorf(DFL2_ERR_UNSUPPORTED, "B=%d: at most %d sequences a call", B, max_b);
   if (T < 0) return report_errorf(DFL2_ERR_INVALID_ARG, "T=%d must be >= 0", T);
   if (T > max_t) return report_errorf(DFL2_ERR_UNSUPPORTED, "T=%d: at most %d", T, max_t);
   return DFL2_OK;
@@ -564,7 +564,7 @@ dfl2_status dfl2_cache_reserve(const dfl2_cache* cache, int B, int T, const int3
                                dfl2_stream stream) {
   const PtrArg ptrs[] = {{table_rows, "table_rows", 4, true}, {length, "length", 4},
                          {count, "count", 4, true}, {served, "served", 4}};
-  DFL2_TRY(dfl2::check_batch(B, T, 1 << 30));
+  DFL2_TRY(dfl2::check_batch(B, T, 1 << 30, dfl2::kMaxSeqs));
   DFL2_TRY(check_all_host(cache, ptrs));
   // (the pages that all sequences lack are counted in 32 bits)
   if (int64_t(B) * std::min<int64_t>(cache->cols, T / cache->page_size + 2) > INT32_MAX)
@@ -639,7 +639,7 @@ dfl2_status dfl2_cache_fork(const dfl2_cache* cache, int n, const int32_t* src, 
                             const int32_t* length, int32_t* served, dfl2_stream stream) {
   const PtrArg ptrs[] = {{src, "src", 4}, {dst, "dst", 4}, {length, "length", 4},
                          {served, "served", 4}};
-  DFL2_TRY(dfl2::check_batch(n, 0, 0));
+  DFL2_TRY(dfl2::check_batch(n, 0, 0, dfl2::kMaxSeqs));
   DFL2_TRY(check_all_host(cache, ptrs));
   DFL2_TRY(check_all_device(cache, ptrs));
   const dfl2::TakeArgs a{dfl2::table_view(cache, dst, length, nullptr, 0), src, served, n};

@@ -26,7 +26,8 @@ dfl2_status check_cache_host(const dfl2_cache* c);
 dfl2_status check_cache_device(const dfl2_cache* c);
 
 constexpr int kMaxTree = 256;   // nodes of a tree
-constexpr int kMaxSeqs = 4096;  // sequences of one bookkeeping call
+constexpr int kMaxSeqs = 4096;  // sequences of one call that takes pages
+constexpr int kMaxBatch = 65535;  // and of any other: a grid's second dimension
 constexpr int kMaxLen = 1 << 30;  // a sequence's length
 
 inline int elem_bytes(int dtype) { return dtype == DFL2_F32 ? 4 : 2; }

@@ -118,9 +118,9 @@ __global__ void __launch_bounds__(128) tree_accept_kernel(const __grid_constant_
 dfl2_status check_tree(int B, int T) {
   if (B < 1 || T < 1)
     return report_errorf(DFL2_ERR_INVALID_ARG, "B=%d and T=%d must be >= 1", B, T);
-  if (B > 65535 || T > kMaxTree)
-    return report_errorf(DFL2_ERR_UNSUPPORTED, "B=%d, T=%d: at most 65535 trees of %d nodes", B, T,
-                         kMaxTree);
+  if (B > kMaxBatch || T > kMaxTree)
+    return report_errorf(DFL2_ERR_UNSUPPORTED, "B=%d, T=%d: at most %d trees of %d nodes", B, T,
+                         kMaxBatch, kMaxTree);
   return DFL2_OK;
 }
 

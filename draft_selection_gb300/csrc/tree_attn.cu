@@ -1162,10 +1162,10 @@ dfl2_status check_shapes(int B, int T, int q_heads, int kv_heads, int head_dim, 
   if (q_heads % kv_heads)
     return report_errorf(DFL2_ERR_INVALID_ARG, "q_heads=%d is no multiple of kv_heads=%d", q_heads,
                          kv_heads);
-  if (B > 65535 || T > kMaxTree || q_heads / kv_heads > kLanes)
+  if (B > kMaxBatch || T > kMaxTree || q_heads / kv_heads > kLanes)
     return report_errorf(DFL2_ERR_UNSUPPORTED,
-                         "B=%d, T=%d, q_heads/kv_heads=%d: at most 65535, %d, %d", B, T,
-                         q_heads / kv_heads, kMaxTree, kLanes);
+                         "B=%d, T=%d, q_heads/kv_heads=%d: at most %d, %d, %d", B, T,
+                         q_heads / kv_heads, kMaxBatch, kMaxTree, kLanes);
   if (head_dim != 64 && head_dim != 128 && head_dim != 256)
     return report_errorf(DFL2_ERR_UNSUPPORTED, "head_dim=%d: 64, 128 or 256", head_dim);
   if (dtype != DFL2_BF16 && dtype != DFL2_F16)

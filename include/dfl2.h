@@ -390,6 +390,8 @@ dfl2_status dfl2_verify(const float* p, const int32_t* tokens, const int32_t* sl
  *   count       int32 [B]: how many of the T nodes (or tokens) of the sequence
  *               there are, 0 .. T (other values are taken to the nearer end);
  *               NULL: T each.
+ *   B           1 .. 65535 sequences; dfl2_cache_reserve and dfl2_cache_fork, which
+ *               serve them in order, 1 .. 4096.
  *   integer arrays need 4-byte alignment, tensors of elements 16-byte.
  * A table row or page number out of range is recorded in the device error word
  * (dfl2_device_error); that sequence or position is then left out.  So is a

@@ -231,3 +231,17 @@ def test_binding_passes_the_c_sides_refusals_on():
         with pytest.raises(dfl2.Dfl2Error) as e:
             call()
         assert e.value.status != 0 and e.value.message
+
+
+def test_calls_that_take_no_pages_have_the_attentions_batch(lib):
+    """More than 4096 sequences are not refused (the call fails later, for want of a device or
+    of its memory), more than 65535 are."""
+    c = cache()
+    st = S4(0, 0, 512, 128)
+    calls = [lambda B: lib.dfl2_cache_write(c, 0, 1, A, A, st, B, 4, None, A, None, None),
+             lambda B: lib.dfl2_cache_compact(c, B, 4, None, A, None, A, A, A, None),
+             lambda B: lib.dfl2_cache_free(c, B, A, None)]
+    for call in calls:
+        assert call(4097) not in (0, UNSUPPORTED) and call(65535) not in (0, UNSUPPORTED)
+        assert call(65536) == UNSUPPORTED
+    assert lib.dfl2_cache_fork(c, 4097, A, A, A, A, None) == UNSUPPORTED

@@ -92,3 +92,18 @@ def test_forks_of_rows_out_of_range_are_recorded(src, dst):
     assert recorded() == 5 and served.tolist() == [0, 1]
     p.m.fork([0], [2], [20])
     p.same()
+
+
+def test_writes_compactions_and_ends_of_5000_sequences():
+    B = 5000
+    p = Pair(B, 2, 2 * B, 8, layers=1, H=1, D=64)
+    for a in range(0, B, 4000):
+        n = min(B - a, 4000)
+        p.reserve(list(range(a, a + n)), [0] * n, [11] * n)
+    rows = [int(x) for x in np.random.default_rng(0).permutation(B)]
+    p.write(rows, [0] * B, [11] * B)
+    path = [[0, 2, 5] if b % 3 else [0, 3, 4, 5, 6, 7, 8, 9, 10] for b in range(B)]
+    p.compact(rows, [0] * B, [11] * B, path, [len(x) for x in path])
+    p.same()
+    p.free(rows[:4500])
+    p.same()
