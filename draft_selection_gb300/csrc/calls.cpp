@@ -118,6 +118,7 @@ PyObject* cache_reserve(PyObject* const* a) {  // cache, length, count, served, 
   const dfl2_cache* c = cache_of(a[0]);
   const at::Tensor& len = tensor(a[1], "length", 1);
   const int B = size(len, 0, "length");
+  if (a[2] == Py_None) REFUSE(PyExc_TypeError, "count must be a number or int32 [B]");
   const bool same = PyLong_Check(a[2]);  // one count for all
   const int T = same ? whole(a[2], "count") : 1 << 30;
   const int32_t* n = same ? nullptr : i32(a[2], "count", {B});

@@ -245,3 +245,10 @@ def test_calls_that_take_no_pages_have_the_attentions_batch(lib):
         assert call(4097) not in (0, UNSUPPORTED) and call(65535) not in (0, UNSUPPORTED)
         assert call(65536) == UNSUPPORTED
     assert lib.dfl2_cache_fork(c, 4097, A, A, A, A, None) == UNSUPPORTED
+
+
+def test_binding_refuses_a_reserve_without_a_count():
+    c = dfl2.cache(1, 4, 2, 16, 64, 2, 3, torch.float16, device="cpu")
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(TypeError, match="count"):
+        dfl2.dfl2_cache_reserve(c, i, None, i, stream=1)
