@@ -5,14 +5,15 @@ entry point it calls, takes torch tensors (or raw integer addresses), passes
 their device pointers, sizes and the current CUDA stream to libdfl2.so, and
 raises Dfl2Error on a non-zero status.  Every step of the path runs in the
 library's CUDA kernels; there is no other implementation to fall back to, so a
-missing library is an error.
+missing library is an error.  torch is imported where a call needs it (its
+current stream, its types, an allocation): with addresses and an explicit stream
+the calls on addresses do without.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
-
-import torch
 
 from . import build as _build
 
@@ -46,16 +47,19 @@ def lib_path() -> str:
     return _build.LIB
 
 
+def _built(path):
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with "
+                           "draft_selection_gb300.build.build() (nvcc, sm_103a); dfl2 has no "
+                           "other implementation")
+
+
 def load():
-    """Loads libdfl2.so and its extension (built in-tree by draft_selection_gb300.build)."""
-    global _lib, _native
+    """Loads libdfl2.so (built in-tree by draft_selection_gb300.build)."""
+    global _lib
     if _lib is not None:
         return _lib
-    for path in (_build.LIB, _build.CALLS):
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with "
-                               "draft_selection_gb300.build.build() (nvcc, sm_103a); dfl2 has no "
-                               "other implementation")
+    _built(_build.LIB)
     L = ctypes.CDLL(_build.LIB)
     P, I, F, U64, SZ = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_uint64,
                         ctypes.c_size_t)
@@ -116,9 +120,20 @@ def load():
                  "dfl2_walk", "dfl2_conv2", "dfl2_conv2_ws", "dfl2_tail", "dfl2_verify", "dfl2_tables_build",
                  "dfl2_select_tables", "dfl2_tail_tables"):
         getattr(L, name).restype = I
-    from . import _calls  # linked against the library
-    _lib, _native = L, _calls
+    _lib = L
     return _lib
+
+
+def load_calls():
+    """Loads the extension behind the cache and tree calls, which is linked against the
+    library and torch; their first call does it."""
+    global _native
+    load()
+    _built(_build.CALLS)
+    import torch  # noqa: F401  (its libraries)
+    from . import _calls
+    _native = _calls
+    return _native
 
 
 def dfl2_last_error() -> str:
@@ -141,24 +156,27 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_cuda_ready = False
+_raw_stream = _device = None
 
 
 def _stream(stream):
     """The stream's address; None: torch's current stream (looked up without making a
     Stream object, which takes 3 us)."""
-    global _cuda_ready
+    global _raw_stream, _device
     if stream is None:
-        if not _cuda_ready:
+        if _raw_stream is None:
+            import torch
             torch.cuda.init()
-            _cuda_ready = True
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+            _raw_stream = torch._C._cuda_getCurrentRawStream
+            _device = torch._C._cuda_getDevice
+        return _raw_stream(_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 def _dtype_code(t) -> int:
+    import torch
     if t.dtype == torch.float32:
         return DFL2_F32
     if t.dtype == torch.bfloat16:
@@ -214,6 +232,7 @@ def dfl2_tail_workspace_size(B: int, L: int, V: int, d: int) -> int:
 
 def workspace(nbytes: int, device="cuda"):
     """A zero-filled device workspace of nbytes (torch allocation; plumbing only)."""
+    import torch
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
@@ -380,21 +399,24 @@ def dfl2_tail_tables(logits, verified_tok, hidden, W_H, P_A, P_B, temperature: f
 # ---- the paged cache and trees of drafted tokens ---------------------------------
 # These calls are short (a few microseconds on the GPU), so their marshalling is
 # csrc/calls.cpp's: types and shapes, which the C side cannot see, are checked there.
-_CODES = {torch.float32: DFL2_F32, torch.bfloat16: DFL2_BF16, torch.float16: DFL2_F16}
+@functools.cache
+def _codes():
+    import torch
+    return {torch.float32: DFL2_F32, torch.bfloat16: DFL2_BF16, torch.float16: DFL2_F16}
 
 
 class _Unloaded:
-    """Stands for the extension until the library is loaded."""
+    """Stands for the extension until a call needs it."""
 
     def __getattr__(self, name):
-        load()
-        return getattr(_native, name)
+        return getattr(load_calls(), name)
 
 
 _native = _Unloaded()
 
 
 def _i32(t, name, shape):
+    import torch
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be int32, not {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
@@ -416,7 +438,7 @@ class Cache:
     table int32 [rows, cols], refs int32 [pages], free_bits int32 [ceil(pages/32)]."""
 
     def __init__(self, k, v, table, refs, free_bits):
-        if k.dtype not in _CODES or v.dtype != k.dtype:
+        if k.dtype not in _codes() or v.dtype != k.dtype:
             raise TypeError(f"k and v must both be float32, bf16 or fp16, not {k.dtype}, {v.dtype}")
         st = _strides(k)
         if k.dim() != 5 or v.shape != k.shape or _strides(v) != st or k.stride(4) != 1:
@@ -431,7 +453,7 @@ class Cache:
         self.k, self.v, self.table, self.refs, self.free_bits = k, v, table, refs, free_bits
         self.dtype, self.kv_heads, self.head_dim = k.dtype, heads, dim
         self._s = _CacheStruct(
-            k.data_ptr(), v.data_ptr(), _CODES[k.dtype], layers, pages, heads, page_size, dim,
+            k.data_ptr(), v.data_ptr(), _codes()[k.dtype], layers, pages, heads, page_size, dim,
             st[0], st[1], st[2], st[3], table.data_ptr(), table.shape[0],
             table.shape[1], refs.data_ptr(), free_bits.data_ptr())
         self._address = ctypes.addressof(self._s)
@@ -440,6 +462,7 @@ class Cache:
 def cache(layers: int, pages: int, kv_heads: int, page_size: int, head_dim: int, rows: int,
           cols: int, dtype=None, device="cuda") -> Cache:
     """A new, empty Cache (torch allocation; plumbing only)."""
+    import torch
     shape = (layers, pages, kv_heads, page_size, head_dim)
     dtype = dtype or torch.bfloat16
     bits = torch.full(((pages + 31) // 32,), -1, dtype=torch.int32, device=device)
@@ -494,8 +517,8 @@ def dfl2_tree_accept(tokens, parents, target, path, n_path, next_token, count=No
 def dfl2_tree_attn_workspace_size(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int,
                                   dtype) -> int:
     """dtype: a torch dtype or DFL2_BF16 / DFL2_F16."""
-    return int(load().dfl2_tree_attn_workspace_size(B, T, q_heads, kv_heads, head_dim,
-                                                    _CODES.get(dtype, dtype)))
+    code = dtype if isinstance(dtype, int) else _codes().get(dtype, dtype)
+    return int(load().dfl2_tree_attn_workspace_size(B, T, q_heads, kv_heads, head_dim, code))
 
 
 def dfl2_tree_attn(q, cache, layer: int, length, mask, out, ws, rows=None, count=None, lse=None,
