@@ -3,13 +3,16 @@ extension _calls.so from csrc/calls.cpp with the host compiler.
 
 Each translation unit is compiled in parallel, then linked into one shared
 library that exports the C ABI of include/dfl2.h; the extension is linked
-against it and torch.  Rebuilds only when a source or header is newer than the
-libraries.
+against it and torch.  The library needs no torch: without it it is all that is
+built, and where the extension cannot be built the library is there all the same.
+Each is rebuilt only when a source or
+header of its own is newer.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -39,16 +42,29 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return _sources() + [CALLS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
-        os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+def _newer(out, deps) -> bool:
+    """Whether `out` is there and no older than what it is made from."""
+    if not os.path.exists(out):
+        return False
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(p) <= t
+               for p in [*deps, *glob.glob(os.path.join(INCLUDE, "*.h")), os.path.abspath(__file__)])
+
+
+def has_torch() -> bool:
+    return importlib.util.find_spec("torch") is not None
+
+
+def lib_fresh() -> bool:
+    return _newer(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")))
+
+
+def calls_fresh() -> bool:
+    return _newer(CALLS, [CALLS_SRC])
 
 
 def is_fresh() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return lib_fresh() and (calls_fresh() or not has_torch())
 
 
 def cflags(extra=()):
@@ -76,22 +92,16 @@ def calls_cmds(cc: str, obj: str, out: str):
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile and link libdfl2.so and _calls.so; returns the first one's path."""
+    """Compile and link libdfl2.so and, with torch, _calls.so; returns the first one's path."""
     with _lock:
-        if not force and is_fresh():
+        lib = force or not lib_fresh()
+        calls = has_torch() and (force or not calls_fresh())
+        if not (lib or calls):
             return LIB
         os.makedirs(BUILD, exist_ok=True)
         cc = nvcc()
 
-        calls_obj = os.path.join(BUILD, "calls.o")
-        calls_tmp = CALLS + f".tmp{os.getpid()}"
-        calls_compile, calls_link = calls_cmds(cc, calls_obj, calls_tmp)
-
-        def compile_one(src):
-            obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-            cmd = [cc, *cflags(extra), "-c", src, "-o", obj]
-            if src == CALLS_SRC:
-                obj, cmd = calls_obj, calls_compile
+        def compile_one(src, cmd):
             if verbose:
                 print(" ".join(cmd))
             r = subprocess.run(cmd, capture_output=True, text=True)
@@ -100,7 +110,18 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
                                    f"{os.path.basename(src)}:\n{r.stderr}")
             if verbose and r.stderr:
                 print(r.stderr)
+
+        def compile_cu(src):
+            obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
+            compile_one(src, [cc, *cflags(extra), "-c", src, "-o", obj])
             return obj
+
+        calls_tmp = CALLS + f".tmp{os.getpid()}"
+
+        def compile_calls():
+            compile_cmd, link_cmd = calls_cmds(cc, os.path.join(BUILD, "calls.o"), calls_tmp)
+            compile_one(CALLS_SRC, compile_cmd)
+            return link_cmd
 
         def link(cmd, tmp, out):
             r = subprocess.run(cmd, capture_output=True, text=True)
@@ -108,13 +129,15 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
                 raise RuntimeError(f"link failed:\n{r.stderr}")
             os.replace(tmp, out)
 
-        srcs = _sources() + [CALLS_SRC]
-        with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-            objs = list(ex.map(compile_one, srcs))
-        tmp = LIB + f".tmp{os.getpid()}"
-        link([cc, *ARCH, "-shared", "-o", tmp, *objs[:-1], "-lcudart_static", "-lrt", "-ldl",
-              "-lpthread"], tmp, LIB)
-        link(calls_link, calls_tmp, CALLS)
+        with cf.ThreadPoolExecutor(max_workers=8) as ex:
+            calls_link = ex.submit(compile_calls) if calls else None
+            if lib:
+                objs = list(ex.map(compile_cu, _sources()))
+                tmp = LIB + f".tmp{os.getpid()}"
+                link([cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-lrt", "-ldl",
+                      "-lpthread"], tmp, LIB)
+            if calls:
+                link(calls_link.result(), calls_tmp, CALLS)
         return LIB
 
 
