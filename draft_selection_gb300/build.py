@@ -5,13 +5,14 @@ Each translation unit is compiled in parallel, then linked into one shared
 library that exports the C ABI of include/dfl2.h; the extension is linked
 against it and torch.  The library needs no torch: without it it is all that is
 built, and where the extension cannot be built the library is there all the same.
-Each is rebuilt only when a source or
-header of its own is newer.
+Each is rebuilt only when a source or header of its own is newer, the extension
+for another Python or torch too.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -59,8 +60,25 @@ def lib_fresh() -> bool:
     return _newer(LIB, _sources() + glob.glob(os.path.join(CSRC, "*.cuh")))
 
 
+def calls_made_with() -> str:
+    """What the extension's binary interface depends on besides its sources."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # one that was not installed as a package
+        import torch
+        version = torch.__version__
+    return f"{sysconfig.get_config_var('SOABI')}, torch {version}\n"
+
+
+def _calls_note():
+    return os.path.join(BUILD, "calls.txt")
+
+
 def calls_fresh() -> bool:
-    return _newer(CALLS, [CALLS_SRC])
+    if not (_newer(CALLS, [CALLS_SRC]) and os.path.exists(_calls_note())):
+        return False
+    with open(_calls_note()) as f:
+        return f.read() == calls_made_with()
 
 
 def is_fresh() -> bool:
@@ -138,6 +156,8 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
                       "-lpthread"], tmp, LIB)
             if calls:
                 link(calls_link.result(), calls_tmp, CALLS)
+                with open(_calls_note(), "w") as f:
+                    f.write(calls_made_with())
         return LIB
 
 

@@ -70,3 +70,17 @@ def test_each_library_is_rebuilt_for_its_own_sources(elsewhere, monkeypatch):
     elsewhere.clear()
     dbuild.build()
     assert dbuild.is_fresh() and [("calls.cpp" in cmd) for cmd in elsewhere] == [True, False]
+
+
+def test_the_extension_is_rebuilt_for_another_torch_or_python(elsewhere, monkeypatch):
+    dbuild.build()
+    version = dbuild.importlib.metadata.version
+    assert dbuild.is_fresh()
+    monkeypatch.setattr(dbuild.importlib.metadata, "version", lambda name: version(name) + ".1")
+    assert dbuild.lib_fresh() and not dbuild.is_fresh()
+    elsewhere.clear()
+    dbuild.build()
+    assert dbuild.is_fresh() and [("calls.cpp" in cmd) for cmd in elsewhere] == [True, False]
+    var = dbuild.sysconfig.get_config_var
+    monkeypatch.setattr(dbuild.sysconfig, "get_config_var", lambda name: var(name) + "-other")
+    assert not dbuild.is_fresh()
