@@ -53,6 +53,8 @@
  *     replaces it in the word.)
  *   - Workspaces must be zero-filled once before their first use (for example
  *     with dfl2_workspace_init); the library keeps them valid afterwards.
+ *     dfl2_tree_attn's is the exception: scratch of that call, which overwrites
+ *     it, so it must not be a workspace that another entry point uses.
  */
 #ifndef DFL2_H
 #define DFL2_H
@@ -495,7 +497,9 @@ dfl2_status dfl2_tree_accept(const int32_t* tokens, const int32_t* parents,
  *   head_dim 64, 128 or 256; q_heads a multiple of kv_heads, at most 128 times it;
  *   1 <= T <= 256; 1 <= B <= 65535; every cache stride of a dimension of more than
  *   one entry positive.
- *   ws          dfl2_tree_attn_workspace_size bytes, scratch only.
+ *   ws          dfl2_tree_attn_workspace_size bytes, scratch only: need not be
+ *               zero-filled, and is overwritten, so not shared with the other entry
+ *               points, whose workspaces hold counters (zero-fill it again before).
  * Scores, softmax and sums are float32; the weights are rounded to the cache's
  * type for the product with V. */
 size_t dfl2_tree_attn_workspace_size(int B, int T, int q_heads, int kv_heads, int head_dim,
