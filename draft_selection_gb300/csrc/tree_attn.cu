@@ -580,7 +580,9 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
     // This stream's rows of Q: G heads of the nodes from node0 on, row by row
     const int node0 = (row_tile * NS + st) * a.stream_rows / a.G;
     const uint32_t q_bytes = kBlk * 128 * a.stream_rows;
+    int q_loads = 0;
     auto load_q = [&](const Cursor& c) {
+      ++q_loads;
       if (elect_one()) {
         mbar_arrive_expect_tx(&q_full[st], q_bytes);
 #pragma unroll
@@ -659,7 +661,9 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
       cur.to(a, tile_hi);
     }
     if (n > 0 && ok) output(n - 1, slot, ph);
-    // every MMA issued is complete before TMEM is freed
+    // Q's last copy has landed, also where a wait ran out before the look at it, and every
+    // MMA issued is complete before TMEM is freed
+    if (q_loads > 0) mbar_wait(&q_full[st], (q_loads - 1) & 1, a.t.err);
     if (elect_one()) umma_commit(&all_done[st]);
     mbar_wait(&all_done[st], 0, a.t.err);
     __syncwarp();
