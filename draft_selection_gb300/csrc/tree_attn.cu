@@ -105,10 +105,17 @@ struct TcCfg {
 // A wait whose first look nearly always succeeds; the rest is out of line, which
 // keeps the loops that wait short (mbar_wait in place, with a vote, took 85 cycles
 // when there was nothing to wait for, and more once its code had left the cache).
+// Lanes that wait together give up together: one that went on alone would wait at the
+// warp's next barrier for ever.
 __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, uint32_t* err) {
-  if (mbar_wait(bar, parity, err)) return true;
-  record_error(err, kDevErrAttn);
-  return false;
+  const unsigned lanes = __activemask();
+  const long long t0 = clock64();
+  while (!__any_sync(lanes, mbar_try_wait(bar, parity)))
+    if (__any_sync(lanes, wait_expired(t0, err))) {
+      record_error(err, kDevErrAttn);
+      return false;
+    }
+  return true;
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t* err) {
   if (mbar_try_wait(bar, parity)) return true;
