@@ -28,7 +28,8 @@
 // For a row tile of 128 rows (node, head) and tiles of 64 keys:
 //   S = Q K^T   tcgen05.mma, 128 x 64, Q and K in shared memory, S (float32) in TMEM
 //   P = 2^(scale log2 e S - m)   a thread to a row: its 64 scores come from TMEM,
-//               its weights go back there, rounded to the cache's type
+//               its weights go back there, rounded to the cache's type (float16: times
+//               2^7, and so is l: kLift)
 //   O += P V    tcgen05.mma, 128 x D, P in TMEM, V in shared memory as it lies in
 //               the cache (keys x channels: the channel-major operand), O in TMEM
 // A row's statistics never leave its thread, so the softmax has no exchange at
@@ -79,6 +80,13 @@ namespace {
 
 constexpr int kLanes = 128;                // rows of a stream: the TMEM lanes
 constexpr float kRise = 8.f;               // log2 of the rise that O is rescaled at
+// log2 of what the weights are taken times: with kRise they stay below float16's largest
+// number, 2^16, and a long tail of small ones that much above its smallest, 2^-24 (60,000
+// weights of 2^-19 beside one of 1 were 1.6% too large).  bfloat16 has float32's exponents.
+template <typename E>
+constexpr float kLift = std::is_same_v<E, __half> ? 7.f : 0.f;
+template <typename E>
+constexpr float kUnlift = std::is_same_v<E, __half> ? 1.f / 128.f : 1.f;
 constexpr uint32_t kColP = kKeys, kColO = 2 * kKeys;
 
 template <int D, int NS>
@@ -774,7 +782,8 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
             }
           }
           const float safe = m == -INFINITY ? 0.f : m;
-          const uint64_t sl2 = pack_f32x2(sl, sl), off2 = pack_f32x2(-safe, -safe);
+          const float off = kLift<E> - safe;
+          const uint64_t sl2 = pack_f32x2(sl, sl), off2 = pack_f32x2(off, off);
           uint64_t sum[2] = {0, 0};
           uint32_t p[32];
 #pragma unroll
@@ -893,7 +902,7 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
           a.part_ml[part * a.rows + stream * a.stream_rows + row_l] = make_float2(m, l);
         if (mine && whole && a.lse)
           a.lse[(static_cast<int64_t>(at.b) * a.t.T + node) * (a.H * a.G) + head] =
-              (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
+              (m == -INFINITY ? 0.f : m) * kLn2 + logf(l * kUnlift<E>);
       }
       tc_fence_before();  // O is read before the next row tile's first product
     }
@@ -1043,7 +1052,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32)
                                         pack2<E>(y[q].z * inv, y[q].w * inv));
       if (a.lse && j == 0)  // log 0 = -inf: nothing seen
         a.lse[(static_cast<int64_t>(b) * a.t.T + node) * Hq + head] =
-            (m == -INFINITY ? 0.f : m) * kLn2 + logf(l);
+            (m == -INFINITY ? 0.f : m) * kLn2 + logf(l * kUnlift<E>);
     }
   }
 }

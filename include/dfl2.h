@@ -501,7 +501,8 @@ dfl2_status dfl2_tree_accept(const int32_t* tokens, const int32_t* parents,
  *               zero-filled, and is overwritten, so not shared with the other entry
  *               points, whose workspaces hold counters (zero-fill it again before).
  * Scores, softmax and sums are float32; the weights are rounded to the cache's
- * type for the product with V. */
+ * type for the product with V (fp16: times 2^7, so that weights down to 2^-21 of
+ * a row's largest keep its 11 bits). */
 size_t dfl2_tree_attn_workspace_size(int B, int T, int q_heads, int kv_heads, int head_dim,
                                      dfl2_dtype dtype);
 dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_cache* cache,

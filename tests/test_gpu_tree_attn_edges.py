@@ -170,3 +170,29 @@ def test_lengths_out_of_range_are_recorded(length):
     assert dfl2.dfl2_device_error() == 5
     assert (out[1] == 0).all() and (lse[1] == -np.inf).all()
     assert torch.equal(out[::2], want[::2]) and torch.equal(lse[::2], want_lse[::2])
+
+
+@pytest.mark.parametrize("at", [0, 30000])
+def test_a_long_tail_of_small_weights(at):
+    """float16: one position has nearly all the weight of each, the others, of 2^-19 each, a tenth
+    of the weight together.  Sums as attention_bounds has them, and half a unit of each weight
+    and of the result, which small weights have too.  So many sequences (of the same pages) that
+    a block has most of one: a part of its own has a maximum of its own, and larger weights."""
+    n, X, B = 60000, 13.25, 400
+    c = Case([n], 1, 2, 1, 64, 64, torch.float16, seed=1)
+    c.cache.k.zero_()
+    c.cache.v.fill_(1.0)
+    page = int(c.cache.table[0, at // 64])
+    c.cache.k[0, page, 0, at % 64, 0] = X
+    c.cache.v[0, page, 0, at % 64] = 0.0
+    c.cache = dfl2.Cache(c.cache.k, c.cache.v, c.cache.table.repeat(B, 1), c.cache.refs,
+                         c.cache.free_bits)
+    c.length, c.mask = c.length.repeat(B), None
+    q = torch.zeros(B, 1, 2, 64, dtype=torch.float16, device="cuda")
+    q[..., 0] = 1.0
+    out, lse = c.run(q=q, scale=1.0)
+    tail = n * np.exp(-X)                     # n + 1 positions, one of them the large one
+    want = tail / (1 + tail)
+    far = (2 * 2.0**-11 + 2 * (n * 2.0**-24 + 8 * X * 2.0**-24)) * want
+    assert (out.double() - want).abs().max() <= far
+    assert (lse.double() - X - np.log1p(tail)).abs().max() <= n * 2.0**-24 + 2.0**-20
