@@ -107,3 +107,72 @@ def test_writes_compactions_and_ends_of_5000_sequences():
     p.same()
     p.free(rows[:4500])
     p.same()
+
+
+@pytest.mark.parametrize("layers,H,D,ps,dtype,nhd", [
+    (3, 8, 128, 16, torch.bfloat16, False),    # 768 columns of 16 bytes: two blocks a sequence
+    (7, 8, 128, 16, torch.float16, True),      # 1792: four, some threads without a column
+    (33, 5, 104, 8, torch.bfloat16, False),    # 4290: eight, some with two columns
+    (20, 8, 128, 32, torch.float32, False),    # 10240: eight, two or three columns each
+    (2, 33, 128, 8, torch.bfloat16, True)])    # more than 128 pieces of a row: 528
+def test_wide_rows_and_many_layers(layers, H, D, ps, dtype, nhd):
+    """Writes, compactions, forks and the pages that a compaction gives back, where a sequence's
+    rows are the work of several blocks and a warp takes a row in several turns."""
+    rng = np.random.default_rng(layers)
+    n = 7
+    p = Pair(2 * n, 14, 90, ps, layers=layers, H=H, D=D, dtype=dtype, nhd=nhd)
+    rows = [int(x) for x in rng.permutation(2 * n)]
+    rows, others = rows[:n], rows[n:]
+    length = [int(x) for x in rng.integers(0, 4 * ps, n)]
+    p.reserve(rows, [0] * n, length)
+    p.write(rows, [0] * n, length)
+    p.same()
+    for _ in range(3):
+        T = 3 * ps + 1
+        count = [int(x) for x in rng.integers(1, T + 1, n)]
+        count[0] = T
+        assert all(p.reserve(rows, length, count))
+        p.write(rows, length, count)
+        path = [sorted(int(x) for x in rng.permutation(c)[:rng.integers(0, min(c, ps) + 1)])
+                for c in count]
+        path[1] = list(range(len(path[1])))     # nothing moves
+        length = p.compact(rows, length, count, path, [len(x) for x in path])
+        p.same()
+        got = p.fork(rows, others, length)
+        p.same()
+        p.free([r for r, g in zip(others, got) if g])
+        p.same()
+
+
+@pytest.mark.parametrize("B", [33, 64, 127, 128, 129, 300])
+def test_more_sequences_than_a_pass_of_the_bookkeeping(B):
+    """More than 32 sequences share the block's warps: their tables' entries, several steps of
+    lanes each, and forks, which run short of pages."""
+    rng = np.random.default_rng(B)
+    p = Pair(3 * B, 70, 25 * B, 8, layers=1, H=1, D=64)
+    rows = [int(x) for x in rng.permutation(3 * B)]
+    a, b, c = rows[:B], rows[B:2 * B], rows[2 * B:]
+    length = [int(x) for x in rng.integers(0, 8 * 34, B)]
+    p.reserve(a, [0] * B, length)
+    p.same()
+    count = [int(x) for x in rng.integers(0, 8 * 34, B)]
+    got = p.reserve(a, length, count)           # on from pages that are there
+    p.same()
+    assert any(got)
+    p.write(a, [0] * B, length)
+    p.same()
+    at = [int(rng.integers(0, n + 1)) for n in length]
+    src = [int(x) for x in rng.integers(0, B, B)]
+    p.fork([a[i] for i in src], b, [at[i] for i in src])
+    p.same()
+    left = len(p.m.free_pages())
+    if left > B // 2:                            # all but a few pages away, then forks again
+        p.reserve([c[0]], [0], [min(70, left - B // 3) * 8])
+    big = p.fork([a[i] for i in src], c[1:] + [c[0]], [length[i] for i in src])
+    p.same()
+    assert any(big)
+    p.free(a)
+    p.same()
+    p.free(b + c)
+    p.same()
+    assert (p.m.refs == 0).all()
