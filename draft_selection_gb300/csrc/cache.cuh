@@ -63,6 +63,10 @@ struct TableView {
     record_error(err, kDevErrBadIndex);
     return false;
   }
+  __device__ __forceinline__ bool in_range(int row, int len) const {
+    return static_cast<unsigned>(row) < static_cast<unsigned>(rows) &&
+           static_cast<unsigned>(len) <= static_cast<unsigned>(kMaxLen);
+  }
   __device__ __forceinline__ int count_of(int b) const {
     return count ? max(0, min(T, count[b])) : T;
   }

@@ -65,8 +65,11 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
   Seq s;
   s.len = a.t.length[b];
   s.n = a.t.count_of(b);
-  s.row = a.t.row_of(b);  // (branches: the loads above are on their way)
-  if (s.row < 0 || !a.t.checked_length(s.len)) s.n = 0;
+  s.row = a.t.seq ? a.t.seq[b] : b;
+  if (!a.t.in_range(s.row, s.len)) {  // (one branch, behind all the loads)
+    record_error(a.t.err, kDevErrBadIndex);
+    s.n = 0;
+  }
   s.tiles = s.n > 0 ? (s.len + s.n + kKeys - 1) / kKeys : 0;
   return s;
 }
