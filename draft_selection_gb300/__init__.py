@@ -112,9 +112,10 @@ def load():
     L.dfl2_tree_attn_workspace_size.argtypes = [I, I, I, I, I, I]
     L.dfl2_tree_attn_workspace_size.restype = SZ
     L.dfl2_tree_attn.argtypes = [P, S, C, I, I, I, I, P, P, P, P, F, P, S, P, P, SZ, P]
+    L.dfl2_tree_verify.argtypes = [P, I, I, I, P, P, P, P, P, P, I, P, P, P, P]
     for name in ("dfl2_cache_reserve", "dfl2_cache_write", "dfl2_cache_compact",
                  "dfl2_cache_fork", "dfl2_cache_free", "dfl2_tree_mask", "dfl2_tree_accept",
-                 "dfl2_tree_attn"):
+                 "dfl2_tree_verify", "dfl2_tree_attn"):
         getattr(L, name).restype = I
     for name in ("dfl2_workspace_init", "dfl2_device_error", "dfl2_topk", "dfl2_select",
                  "dfl2_walk", "dfl2_conv2", "dfl2_conv2_ws", "dfl2_tail", "dfl2_verify", "dfl2_tables_build",
@@ -512,6 +513,16 @@ def dfl2_tree_accept(tokens, parents, target, path, n_path, next_token, count=No
                      stream=None) -> None:
     """The path of the target's tokens through each tree: path [B,T], n_path [B], next_token [B]."""
     _check(_native.tree_accept(tokens, parents, target, path, n_path, next_token, count, stream))
+
+
+def dfl2_tree_verify(p, tokens, parents, cand_idx, q, u, path, n_path, next_token, count=None,
+                     replace=False, stream=None) -> None:
+    """The path of sampled tokens through each tree, and the token after it: p float32 [B,T,V]
+    the target's probabilities, cand_idx and q [B,T,16] what the children of each node were
+    drawn from (replace: independently), u float32 [B,T] uniform numbers; outputs as
+    dfl2_tree_accept's."""
+    _check(_native.tree_verify(p, tokens, parents, cand_idx, q, u, path, n_path, next_token, count,
+                               replace, stream))
 
 
 def dfl2_tree_attn_workspace_size(B: int, T: int, q_heads: int, kv_heads: int, head_dim: int,

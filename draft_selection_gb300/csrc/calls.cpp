@@ -217,6 +217,34 @@ PyObject* tree_accept(PyObject* const* a) {
   });
 }
 
+// A float32 device array's address.
+float* f32(PyObject* o, const char* name, Sizes shape) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.scalar_type() != at::kFloat) REFUSE(PyExc_TypeError, "%s must be float32", name);
+  if (!has_shape(t, shape) || !t.is_contiguous())
+    REFUSE(PyExc_ValueError, "%s must be contiguous, of the shape that the others give it", name);
+  return static_cast<float*>(t.data_ptr());
+}
+
+PyObject* tree_verify(PyObject* const* a) {
+  // p, tokens, parents, cand_idx, q, u, path, n_path, next_token, count, replace, stream
+  const at::Tensor& p = tensor(a[0], "p", 3);
+  const int B = size(p, 0, "p"), T = size(p, 1, "p"), V = size(p, 2, "p");
+  const float* pp = f32(a[0], "p", {B, T, V});
+  const int32_t *tokens = i32(a[1], "tokens", {B, T}), *parents = i32(a[2], "parents", {B, T}),
+                *cand = i32(a[3], "cand_idx", {B, T, 16}), *n = i32(a[9], "count", {B});
+  const float *q = f32(a[4], "q", {B, T, 16}), *u = f32(a[5], "u", {B, T});
+  int32_t *path = i32(a[6], "path", {B, T}), *n_path = i32(a[7], "n_path", {B}),
+          *next = i32(a[8], "next_token", {B});
+  const int replace = PyObject_IsTrue(a[10]);
+  if (replace < 0) throw Raised();
+  const dfl2_stream s = stream_of(a[11]);
+  return run([&] {
+    return dfl2_tree_verify(pp, B, T, V, tokens, parents, n, cand, q, u, replace, path, n_path,
+                            next, s);
+  });
+}
+
 PyObject* tree_attn(PyObject* const* a) {
   // q, cache, layer, length, mask, out, ws, rows, count, lse, scale, stream
   const dfl2_cache* c = cache_of(a[1]);
@@ -283,6 +311,7 @@ PyMethodDef methods[] = {method<cache_reserve, 6>("cache_reserve"),
                          method<cache_free, 3>("cache_free"),
                          method<tree_mask, 5>("tree_mask"),
                          method<tree_accept, 8>("tree_accept"),
+                         method<tree_verify, 12>("tree_verify"),
                          method<tree_attn, 12>("tree_attn"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,

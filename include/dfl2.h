@@ -480,6 +480,41 @@ dfl2_status dfl2_tree_accept(const int32_t* tokens, const int32_t* parents,
                              int32_t* path, int32_t* n_path, int32_t* next_token,
                              dfl2_stream stream);
 
+/* The path of sampled tokens through each tree: speculative sampling with several
+ * drafted tokens at a position (the step of dfl2_verify, Leviathan et al., ICML 2023;
+ * Chen et al., 2023, applied to a node's children one after the other with what the
+ * ones before left of the target's distribution).  The tokens of the path and
+ * next_token follow the target's distribution, whatever q is, if the children of
+ * node i were drawn from it.
+ *   p           float32 [B,T,V]: the target's probabilities of the token after node i;
+ *               each row is taken to sum to 1.
+ *   tokens, parents  int32 [B,T] (node 0's token is not read; a parent that is not
+ *               below its node makes the node no child).
+ *   cand_idx, q int32 and float32 [B,T,16]: the children of node i were drawn from the
+ *               candidates cand_idx[b,i] with weights q[b,i] (dfl2_walk's; they need
+ *               not sum to 1), in the order of their numbers.  A candidate named twice
+ *               counts at its lowest slot; one outside [0, V) is recorded and, as a
+ *               weight that is not above 0, counts as 0.
+ *   replace     0: children drawn without replacement (distinct); else independently.
+ *   u           float32 [B,T], uniform in [0,1): u[b,c] decides about node c >= 1,
+ *               u[b,0] draws next_token.
+ * From node 0 on: r = p[b,i], d = q[b,i].  For each child c of the node, x = its token:
+ * passed over if d(x) = 0, else kept, and the next node, if u[b,c] d(x)/|d| < r(x)/|r|;
+ * else r becomes max(0, r/|r| - d/|d|) and, without replacement, d(x) becomes 0; if r is
+ * then 0 everywhere (p never exceeds q), it becomes p and the node's other children are
+ * passed over.  When no child is kept: next_token = the first index, in order, at which
+ * the running sum of r exceeds u[b,0] times its total (the last one with r > 0 if
+ * rounding leaves none; of p if r sums to 0, -1 if that does too).
+ * path, n_path, next_token: as dfl2_tree_accept's.  Decisions are taken in double
+ * precision; the running sums are those of exact addition to about 2^-48.  Rows with
+ * NaN, Inf or values below 0 are not supported.
+ * 1 <= T <= 256, 1 <= V <= 2^30; p, cand_idx 16-byte aligned (rows of p need not be). */
+dfl2_status dfl2_tree_verify(const float* p, int B, int T, int V, const int32_t* tokens,
+                             const int32_t* parents, const int32_t* count,
+                             const int32_t* cand_idx, const float* q, const float* u, int replace,
+                             int32_t* path, int32_t* n_path, int32_t* next_token,
+                             dfl2_stream stream);
+
 /* Attention of the nodes over the cache, in one layer:
  *   s_j = scale <q[b,i,h], K[b,j,h*kv_heads/q_heads]>
  *   out[b,i,h] = sum_j softmax(s)_j V[b,j]   over the positions j that node i
