@@ -13,9 +13,9 @@
 // path.  The row of the last draw is then cut into one range a warp.  The warps' sums are
 // exchanged through distributed shared memory, and the warp whose range the drawn number
 // falls in looks for the element.
-// Sums of the row are pairs of floats (the exact error of every addition is kept, Knuth's
-// two-sum): this GPU adds two doubles a cycle and SM, and the drawn index has to be that
-// of the exact sums.
+// Numbers are unevaluated sums of two floats (about 46 bits): decisions and the drawn index
+// have to be those of the exact sums, and this GPU's doubles are slow (two additions a cycle
+// and SM, 60 cycles each).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,7 +26,7 @@ namespace dfl2 {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kThreads = 512, kWarps = kThreads / 32, kMaxCluster = 8;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kCtas = 2, kMaxCluster = 8;
 
 struct TreeVerifyArgs {
   const float* p;
@@ -43,26 +43,63 @@ struct TreeVerifyArgs {
   uint32_t* err;
 };
 
-// hi + lo += x, the rounding error of every addition kept in lo.
-__device__ __forceinline__ void add_exact(float& hi, float& lo, float x) {
-  const float s = __fadd_rn(hi, x);
-  const float b = __fsub_rn(s, hi);
-  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
-  hi = s;
+// A number as the sum of two floats, the second at most half a unit of the first's last
+// place.  Additions and products by Knuth's two-sum and the fused remainder of a product.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair quick(float a, float b) {  // |a| >= |b|
+  const float s = __fadd_rn(a, b);
+  return {s, __fsub_rn(b, __fsub_rn(s, a))};
 }
-__device__ __forceinline__ double sum16(double x) {  // over the lanes of a half-warp
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), c = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, c)), __fsub_rn(b, c))};
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  const Pair s = two_sum(a.hi, b.hi);
+  return quick(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ Pair operator-(Pair a, Pair b) { return a + Pair{-b.hi, -b.lo}; }
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  const float p = __fmul_rn(a.hi, b.hi);
+  const float e = __fmaf_rn(a.hi, b.hi, -p);
+  return quick(p, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, e)));
+}
+__device__ __forceinline__ Pair operator*(Pair a, float b) { return a * Pair{b, 0.f}; }
+__device__ __forceinline__ Pair scaled(Pair a, float f) { return {a.hi * f, a.lo * f}; }  // f = 2^n
+__device__ __forceinline__ Pair operator/(Pair a, Pair b) {
+  const float q = __fdiv_rn(a.hi, b.hi);
+  const Pair r = a - b * q;
+  return quick(q, __fdiv_rn(r.hi, b.hi));
+}
+__device__ __forceinline__ bool operator<(Pair a, Pair b) {
+  return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo);
+}
+__device__ __forceinline__ Pair shfl(Pair x, int lane) {
+  return {__shfl_sync(kAll, x.hi, lane), __shfl_sync(kAll, x.lo, lane)};
+}
+__device__ __forceinline__ Pair shfl_xor(Pair x, int bit) {
+  return {__shfl_xor_sync(kAll, x.hi, bit), __shfl_xor_sync(kAll, x.lo, bit)};
+}
+__device__ __forceinline__ Pair sum16(Pair x) {  // over the lanes of a half-warp
 #pragma unroll
-  for (int off = 8; off; off >>= 1) x += __shfl_xor_sync(kAll, x, off);
+  for (int off = 8; off; off >>= 1) x = x + shfl_xor(x, off);
   return x;
 }
-__device__ __forceinline__ double scan32(double x) {
+__device__ __forceinline__ Pair scan32(Pair x) {  // over this lane and those before it
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const double y = __shfl_up_sync(kAll, x, off);
-    if (lane >= off) x += y;
+    const Pair y = {__shfl_up_sync(kAll, x.hi, off), __shfl_up_sync(kAll, x.lo, off)};
+    if (lane >= off) x = x + y;
   }
   return x;
+}
+// 2^-e for x in [2^e, 2^(e+1)), x normal and e within -125 .. 125; 1 otherwise.
+__device__ __forceinline__ float to_one(float x) {
+  const int e = static_cast<int>(__float_as_uint(x) >> 23);  // (x >= 0)
+  return e < 2 || e > 252 ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
 }
 
 // The row of the last draw.  Rows need not begin on 16 bytes: elements are numbered from
@@ -70,135 +107,165 @@ __device__ __forceinline__ double scan32(double x) {
 struct Row {
   const float4* base;
   int off, V, vecs;
-  // Elements 4 v - off .. + 3; 0 outside the row.
-  __device__ __forceinline__ float4 at(int v) const {
+  // Elements 4 v - off .. + 3 of a row, 0 where v is past `end` or not wholly inside.
+  __device__ __forceinline__ float4 inner(int v, int end) const {
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     const int e = 4 * v - off;
-    if (e >= 0 && e + 3 < V) return __ldg(base + v);
-    const float* f = reinterpret_cast<const float*>(base + v);
-    float4 x;
-    x.x = e >= 0 && e < V ? f[0] : 0.f;
-    x.y = e + 1 >= 0 && e + 1 < V ? f[1] : 0.f;
-    x.z = e + 2 >= 0 && e + 2 < V ? f[2] : 0.f;
-    x.w = e + 3 >= 0 && e + 3 < V ? f[3] : 0.f;
+    if (v < end && e >= 0 && e + 3 < V) x = __ldg(base + v);
+    return x;
+  }
+  // The row's first and last vectors where they are cut, else x.
+  __device__ __forceinline__ float4 ends(float4 x, int v) const {
+    const int e = 4 * v - off;
+    if (e < 0 || (e < V && e + 3 >= V)) {
+      const float* f = reinterpret_cast<const float*>(base + v);
+      x.x = e >= 0 ? f[0] : 0.f;
+      x.y = e + 1 >= 0 && e + 1 < V ? f[1] : 0.f;
+      x.z = e + 2 >= 0 && e + 2 < V ? f[2] : 0.f;
+      x.w = e + 3 < V ? f[3] : 0.f;
+    }
     return x;
   }
 };
 
-// What is drawn from: the row with the candidates' values replaced.  These are doubles
-// (their rounding to float would move the borders of all later elements by 2^-25 of them),
-// so they are added beside the row's, whose own values there count as 0.
+// Two floats in one register pair, for the two-sums of the row.
+__device__ __forceinline__ uint64_t pack(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack(uint64_t r, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {  // a - b, as b (-1) + a
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(b), "l"(0xBF800000BF800000ull), "l"(a));
+  return r;
+}
+// hi + lo += x, twice.
+__device__ __forceinline__ void add_exact2(uint64_t& hi, uint64_t& lo, uint64_t x) {
+  const uint64_t s = add2(hi, x), c = sub2(s, hi);
+  lo = add2(lo, add2(sub2(hi, sub2(s, c)), sub2(x, c)));
+  hi = s;
+}
+
+// What is drawn from: the row with the candidates' values replaced.  These are pairs (their
+// rounding to a float would move the borders of all later elements by 2^-25 of them), so
+// they are added beside the row's, whose own values there count as 0.
 struct Left {
   Row row;
-  int vec;    // of this lane's candidate (lanes 0 .. 15; -1: none)
-  int place;  // and which of the four
-  double val;
-  __device__ __forceinline__ bool within(int v0, int v1) const { return vec >= v0 && vec < v1; }
-};
-__device__ __forceinline__ void set4(float4& x, int e, float y) {
-  if (e == 0) x.x = y;
-  if (e == 1) x.y = y;
-  if (e == 2) x.z = y;
-  if (e == 3) x.w = y;
-}
-
-// The sum of vectors [v0, v1) by a warp, in every lane.
-__device__ __forceinline__ double range_sum(const Left& a, int v0, int v1, int lane) {
-  constexpr int kBatch = 8;
-  float hi[4] = {0.f, 0.f, 0.f, 0.f}, lo[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int v = v0; v < v1; v += 32 * kBatch) {
-    float4 x[kBatch];
+  const int* at;    // [16], the candidates' elements; -1: none
+  const Pair* val;
+  // The candidates in vectors [v0, v1), by a warp.
+  __device__ __forceinline__ unsigned among(int v0, int v1) const {
+    const int lane = threadIdx.x & 31, c = lane < kCand ? at[lane] : -1;
+    const int v = (c + row.off) >> 2;
+    return __ballot_sync(kAll, c >= 0 && v >= v0 && v < v1);
+  }
+  // The sum of vectors v, v + step, .. below v1; cand: the candidates that may be there.
+  __device__ __forceinline__ Pair sum(int v, int v1, int step, unsigned cand) const {
+    constexpr int kBatch = 8;
+    uint64_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll 1
+    for (; v < v1; v += step * kBatch) {
+      float4 x[kBatch];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int at = v + 32 * j + lane;
-      x[j] = at < v1 ? a.row.at(at) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    unsigned hit = __ballot_sync(kAll, a.within(v, min(v1, v + 32 * kBatch)));
-    while (hit) {
-      const int k = __ffs(hit) - 1;
-      hit &= hit - 1;
-      const int at = __shfl_sync(kAll, a.vec, k) - v, e = __shfl_sync(kAll, a.place, k);
-      if ((at & 31) == lane)
+      for (int j = 0; j < kBatch; ++j) x[j] = row.inner(v + step * j, v1);
+      if (cand || v < step || v + step * kBatch >= row.vecs)
 #pragma unroll
         for (int j = 0; j < kBatch; ++j)
-          if (j == at >> 5) set4(x[j], e, 0.f);
-    }
+          if (v + step * j < v1) x[j] = odd(x[j], v + step * j, cand);
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      add_exact(hi[0], lo[0], x[j].x);
-      add_exact(hi[1], lo[1], x[j].y);
-      add_exact(hi[2], lo[2], x[j].z);
-      add_exact(hi[3], lo[3], x[j].w);
-    }
-  }
-  float h = hi[0], l = lo[0];
-#pragma unroll
-  for (int j = 1; j < 4; ++j) {
-    add_exact(h, l, hi[j]);
-    l += lo[j];
-  }
-  double s = static_cast<double>(h) + static_cast<double>(l);
-  if (a.within(v0, v1)) s += a.val;
-#pragma unroll
-  for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(kAll, s, off);
-  return s;
-}
-
-// The first element of vectors [v0, v1) whose running sum exceeds t, by a warp; the last
-// one with mass if there is none, -1 if that is none either.
-__device__ __noinline__ int range_find(const Left& a, int v0, int v1, double t, int lane) {
-  double before = 0.;
-  int last = -1;
-  for (int v = v0; v < v1; v += 32) {
-    const float4 x =
-        v + lane < v1 ? a.row.at(v + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-    double y[4] = {x.x, x.y, x.z, x.w};
-    unsigned cand = __ballot_sync(kAll, a.within(v, min(v1, v + 32)));
-    while (cand) {
-      const int k = __ffs(cand) - 1;
-      cand &= cand - 1;
-      const int at = __shfl_sync(kAll, a.vec, k) - v, e = __shfl_sync(kAll, a.place, k);
-      const double val = __shfl_sync(kAll, a.val, k);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (at == lane && e == j) y[j] = val;
-    }
-    const double s = (y[0] + y[1]) + (y[2] + y[3]);
-    const double to = before + scan32(s);
-    const int e0 = 4 * (v + lane) - a.row.off;
-    int m = -1;  // the lane's last element with mass, and the first past t
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (y[j] > 0.) m = j;
-    const unsigned hit = __ballot_sync(kAll, to > t && m >= 0);
-    if (hit) {
-      double c = to - s;
-      int e = m;
-      bool found = false;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        c += y[j];
-        if (!found && y[j] > 0. && c > t) {
-          found = true;
-          e = j;
-        }
+      for (int j = 0; j < kBatch; ++j) {
+        if (v + step * j >= v1) break;
+        add_exact2(hi[0], lo[0], pack(x[j].x, x[j].y));
+        add_exact2(hi[1], lo[1], pack(x[j].z, x[j].w));
       }
-      return __shfl_sync(kAll, e0 + e, __ffs(hit) - 1);
     }
-    if (m >= 0) last = e0 + m;
-    before = __shfl_sync(kAll, to, 31);
+    float h[4], l[4];
+    unpack(hi[0], h[0], h[1]);
+    unpack(hi[1], h[2], h[3]);
+    unpack(lo[0], l[0], l[1]);
+    unpack(lo[1], l[2], l[3]);
+    return (quick(h[0], l[0]) + quick(h[1], l[1])) + (quick(h[2], l[2]) + quick(h[3], l[3]));
   }
-  return __reduce_max_sync(kAll, last);
+  // Vector v where the row is cut, and without the candidates among `which`.
+  __device__ __noinline__ float4 odd(float4 x, int v, unsigned which) const {
+    x = row.ends(x, v);
+    for (; which; which &= which - 1) {
+      const int c = at[__ffs(which) - 1] + row.off;
+      if (c >> 2 != v) continue;
+      if ((c & 3) == 0) x.x = 0.f;
+      if ((c & 3) == 1) x.y = 0.f;
+      if ((c & 3) == 2) x.z = 0.f;
+      if ((c & 3) == 3) x.w = 0.f;
+    }
+    return x;
+  }
+};
+
+// By a warp: which of the lanes' values, in order, the running sum first exceeds t at (the
+// last one above 0 if none, -1 if that is none either), and t less what comes before it.
+__device__ __forceinline__ int find32(Pair x, Pair& t, bool above) {
+  const Pair to = scan32(x);
+  unsigned hit = __ballot_sync(kAll, above && t < to);
+  if (!hit) {
+    hit = __ballot_sync(kAll, above);
+    if (!hit) return -1;
+    hit = 1u << (31 - __clz(hit));
+  }
+  const int w = __ffs(hit) - 1;
+  t = shfl(t - (to - x), w);
+  return w;
 }
 
-__global__ void __launch_bounds__(kThreads)
+// The element of vectors [v0, v1) at which the running sum first exceeds t, by a warp:
+// 32 parts a step, down to a vector a lane.
+__device__ __noinline__ int find(const Left& a, int v0, int v1, Pair t, int lane) {
+  while (true) {
+    const int each = (v1 - v0 + 31) / 32;
+    const int w0 = min(v1, v0 + lane * each), w1 = min(v1, w0 + each);
+    const unsigned cand = a.among(v0, v1);
+    Pair s = a.sum(w0, w1, 1, cand);
+    for (unsigned c = cand; c; c &= c - 1) {
+      const int k = __ffs(c) - 1, v = (a.at[k] + a.row.off) >> 2;
+      if (v >= w0 && v < w1) s = s + a.val[k];
+    }
+    const int w = find32(s, t, s.hi > 0.f);
+    if (w < 0) return -1;
+    if (each > 1) {
+      v1 = __shfl_sync(kAll, w1, w);
+      v0 = __shfl_sync(kAll, w0, w);
+      continue;
+    }
+    // an element a lane
+    const int e = 4 * (v0 + w) - a.row.off + lane;
+    Pair x = {0.f, 0.f};
+    if (lane < 4 && e >= 0 && e < a.row.V) {
+      x.hi = __ldg(reinterpret_cast<const float*>(a.row.base) + a.row.off + e);
+      for (unsigned c = cand; c; c &= c - 1)
+        if (a.at[__ffs(c) - 1] == e) x = a.val[__ffs(c) - 1];
+    }
+    const int z = find32(x, t, x.hi > 0.f);
+    return z < 0 ? -1 : __shfl_sync(kAll, e, z);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, kCtas)
     tree_verify_kernel(const __grid_constant__ TreeVerifyArgs a) {
   __shared__ float r_s[kMaxTree][kCand], d_s[kMaxTree][kCand];
   __shared__ int8_t slot_s[kMaxTree];  // of a node's token among its parent's candidates
-  __shared__ double val_s[kCand];      // the candidates' part of what is left
-  __shared__ int vec_s[kCand];
+  __shared__ int16_t up_s[kMaxTree];   // its parent; -1: no child
   __shared__ float u_s[kMaxTree];
+  __shared__ int at_s[kCand];          // the last node's candidates, and their part of what
+  __shared__ Pair val_s[kCand];        // is left
   __shared__ int node_s, got_s, owner_s;
-  __shared__ double sums_s[kMaxCluster * kWarps];  // every warp of the cluster's
+  __shared__ uint64_t sums_s[kMaxCluster * kWarps];  // every warp of the cluster's (a Pair)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.y, rank = blockIdx.x, ranks = gridDim.x;
   const int T = a.T, V = a.V;
@@ -209,93 +276,129 @@ __global__ void __launch_bounds__(kThreads)
   const int n = a.count ? max(0, min(T, a.count[b])) : T;
 
   // ---- every node's candidates: p and q, 0 for one out of range or named before ----
-  for (int x = tid; x - lane < n * kCand; x += kThreads) {
-    const bool in = x < n * kCand;
-    const int c = in ? a.cand[at * kCand + x] : -1;
-    float q = in ? a.q[at * kCand + x] : 0.f;
-    const bool ok = static_cast<unsigned>(c) < static_cast<unsigned>(V);
-    if (in && !ok) record_error(a.err, kDevErrBadIndex);
-    float p = ok ? a.p[(at + x / kCand) * V + c] : 0.f;
-    bool again = false;
-#pragma unroll
-    for (int k = 1; k < kCand; ++k) {
-      const int y = __shfl_up_sync(kAll, c, k, kCand);
-      again |= (lane & 15) >= k && y == c;
-    }
-    if (!ok || again) p = q = 0.f;
-    if (in) {
-      r_s[x / kCand][x % kCand] = p;
-      d_s[x / kCand][x % kCand] = q > 0.f ? q : 0.f;
-    }
-  }
-  int8_t slot = -1;
+  // (loads that do not need each other first: a node's number, token and parent beside them)
+  int up = -1, token = -1;
+  float u = 0.f;
   if (tid < n) {
-    const int up = a.parents[at + tid], x = a.tokens[at + tid];
-    if (up >= 0 && up < tid) {
-      const int4* c = reinterpret_cast<const int4*>(a.cand + (at + up) * kCand);
+    up = a.parents[at + tid];
+    token = a.tokens[at + tid];
+    u = a.u[at + tid];
+  }
+  constexpr int kBatch = 2;
+  for (int x0 = tid; x0 - lane < n * kCand; x0 += kBatch * kThreads) {
+    int c[kBatch];
+    float p[kBatch], q[kBatch];
 #pragma unroll
-      for (int j = 3; j >= 0; --j) {
-        const int4 y = __ldg(c + j);
-        if (y.w == x) slot = 4 * j + 3;
-        if (y.z == x) slot = 4 * j + 2;
-        if (y.y == x) slot = 4 * j + 1;
-        if (y.x == x) slot = 4 * j;
+    for (int z = 0; z < kBatch; ++z) {
+      const int x = x0 + z * kThreads;
+      c[z] = x < n * kCand ? a.cand[at * kCand + x] : -1;
+      q[z] = x < n * kCand ? a.q[at * kCand + x] : 0.f;
+    }
+#pragma unroll
+    for (int z = 0; z < kBatch; ++z) {
+      const int x = x0 + z * kThreads;
+      const bool ok = static_cast<unsigned>(c[z]) < static_cast<unsigned>(V);
+      if (x < n * kCand && !ok) record_error(a.err, kDevErrBadIndex);
+      p[z] = ok ? a.p[(at + x / kCand) * V + c[z]] : 0.f;
+      if (!ok || !(q[z] > 0.f)) q[z] = 0.f;
+    }
+#pragma unroll
+    for (int z = 0; z < kBatch; ++z) {
+      const int x = x0 + z * kThreads;
+      bool again = false;
+#pragma unroll
+      for (int k = 1; k < kCand; ++k) {
+        const int y = __shfl_up_sync(kAll, c[z], k, kCand);
+        again |= (lane & 15) >= k && y == c[z];
+      }
+      if (x < n * kCand) {
+        r_s[x / kCand][x % kCand] = again ? 0.f : p[z];
+        d_s[x / kCand][x % kCand] = again ? 0.f : q[z];
       }
     }
   }
   if (tid < kMaxTree) {
-    slot_s[tid] = slot;
-    if (tid < n) u_s[tid] = a.u[at + tid];
+    int slot = -1;
+    if (tid < n && up >= 0 && up < tid) {
+      const int4* c = reinterpret_cast<const int4*>(a.cand + (at + up) * kCand);
+#pragma unroll
+      for (int j = 3; j >= 0; --j) {
+        const int4 y = __ldg(c + j);
+        if (y.w == token) slot = 4 * j + 3;
+        if (y.z == token) slot = 4 * j + 2;
+        if (y.y == token) slot = 4 * j + 1;
+        if (y.x == token) slot = 4 * j;
+      }
+    }
+    slot_s[tid] = static_cast<int8_t>(slot);
+    up_s[tid] = static_cast<int16_t>(slot < 0 ? -1 : up);
+    u_s[tid] = u;
   }
   __syncthreads();
 
-  // ---- the walk: lanes 0 .. 15 a candidate each (16 .. 31 do the same) ----
+  // ---- the walk: lanes 0 .. 15 a candidate each ----
   if (warp == 0) {
-    int par[kMaxTree / 32];
-#pragma unroll
-    for (int j = 0; j < kMaxTree / 32; ++j) {
-      const int i = lane + 32 * j;
-      par[j] = i < n && slot_s[i] >= 0 ? a.parents[at + i] : -1;
-    }
     const int k = lane & 15;
+    // Lanes 0 .. 15 hold r, 16 .. 31 d, so that one reduction sums both.  Nothing is
+    // divided: r/|r| - d/|d| is r |d| - d |r| but for a factor, which g keeps (what r off
+    // the candidates is, relative to p).  |r| and |d| are held in [1, 2) by powers of two.
+    const bool low = lane < kCand;
     int cur = 0, len = 0;
-    double r = 0., g = 1.;
+    Pair x = {0.f, 0.f}, g = {1.f, 0.f};
     while (n > 0) {
       if (rank == 0 && lane == 0) a.path[at + len] = cur;
       ++len;
-      const double p = r_s[cur][k];
-      double d = d_s[cur][k];
-      r = p;
-      g = 1.;
-      const double whole = fmax(0., 1. - sum16(p));
-      double rest = whole;
+      const Pair p = {r_s[cur][k], 0.f};
+      x = low ? p : Pair{d_s[cur][k], 0.f};
+      g = {1.f, 0.f};
+      Pair sum = sum16(x);
+      const Pair P = shfl(sum, 0);
+      Pair rest = Pair{1.f, 0.f} - P;
+      if (rest.hi < 0.f) rest = {0.f, 0.f};
+      const Pair whole = rest;
+      Pair R = rest + P, D = shfl(sum, 16);
+      if (!low) x = scaled(x, to_one(D.hi));
+      D = scaled(D, to_one(D.hi));
       int took = -1;
       bool over = false;
-#pragma unroll
-      for (int j = 0; j < kMaxTree / 32; ++j) {
-        unsigned kids = __ballot_sync(kAll, par[j] == cur);
-        while (kids && took < 0 && !over) {
+#pragma unroll 1
+      for (int j = cur >> 5; j <= (n - 1) >> 5 && took < 0 && !over; ++j) {
+        unsigned kids = __ballot_sync(kAll, up_s[32 * j + lane] == cur);
+#pragma unroll 1
+        while (kids && !over) {
           const int i = 32 * j + __ffs(kids) - 1;
           kids &= kids - 1;
           const int s = slot_s[i];
-          const double dk = __shfl_sync(kAll, d, s);
-          if (!(dk > 0.)) continue;  // (its mass was taken by a sibling before)
-          const double R = rest + sum16(r), D = sum16(d), rk = __shfl_sync(kAll, r, s);
-          const double u = u_s[i];
-          if (u * dk * R < rk * D) {
+          const Pair dk = shfl(x, 16 + s);
+          if (!(dk.hi > 0.f)) continue;  // (its mass was taken by a sibling before)
+          const Pair rk = shfl(x, s);
+          if (dk * u_s[i] * R < rk * D) {
             took = i;
             break;
           }
-          const double ir = 1. / R, id = 1. / D;
-          r = fmax(0., r * ir - d * id);
-          rest *= ir;
-          g *= ir;
-          if (!a.replace && k == s) d = 0.;
-          if (!(rest + sum16(r) > 0.)) {  // p never exceeds q: p itself
-            r = p;
-            rest = whole;
-            g = 1.;
+          const Pair d = shfl_xor(x, 16);
+          if (low) {
+            x = x * D - d * R;
+            if (x.hi < 0.f) x = {0.f, 0.f};
+          } else if (!a.replace && k == s) {
+            x = {0.f, 0.f};
+          }
+          rest = rest * D;
+          g = g * D;
+          sum = sum16(x);
+          R = rest + shfl(sum, 0);
+          D = shfl(sum, 16);
+          if (!(R.hi > 0.f)) {  // p never exceeds q: p itself
+            x = p;
+            g = {1.f, 0.f};
             over = true;
+          } else {
+            const float e = to_one(R.hi), f = to_one(D.hi);
+            x = scaled(x, low ? e : f);
+            rest = scaled(rest, e);
+            g = scaled(g, e);
+            R = scaled(R, e);
+            D = scaled(D, f);
           }
         }
       }
@@ -314,8 +417,8 @@ __global__ void __launch_bounds__(kThreads)
         const int y = __shfl_up_sync(0xffffu, c, z, kCand);
         again |= k >= z && y == c;
       }
-      vec_s[k] = again || static_cast<unsigned>(c) >= static_cast<unsigned>(V) ? -1 : c;
-      val_s[k] = r / g;
+      at_s[k] = again || static_cast<unsigned>(c) >= static_cast<unsigned>(V) ? -1 : c;
+      val_s[k] = x / g;
     }
     if (lane == 0) node_s = cur;
   }
@@ -328,10 +431,8 @@ __global__ void __launch_bounds__(kThreads)
   left.row.base = reinterpret_cast<const float4*>(a.p + (start - left.row.off));
   left.row.V = V;
   left.row.vecs = (V + left.row.off + 3) / 4;
-  const int c = lane < kCand ? vec_s[lane] : -1;
-  left.vec = c < 0 ? -1 : (c + left.row.off) >> 2;
-  left.place = (c + left.row.off) & 3;
-  left.val = lane < kCand ? val_s[lane] : 0.;
+  left.at = at_s;
+  left.val = val_s;
   const int total_warps = ranks * kWarps;
   cluster_wait();
   auto range_at = [&](int w) {
@@ -339,51 +440,39 @@ __global__ void __launch_bounds__(kThreads)
   };
   for (int pass = 0; pass < 2 && n > 0; ++pass) {
     const int w = rank * kWarps + warp;
-    const double s = range_sum(left, range_at(w), range_at(w + 1), lane);
+    const int v0 = range_at(w), v1 = range_at(w + 1);
+    const unsigned cand = left.among(v0, v1);
+    Pair s = left.sum(v0 + lane, v1, 32, cand);
+    if (cand >> lane & 1) s = s + val_s[lane];
+#pragma unroll
+    for (int off = 16; off; off >>= 1) s = s + shfl_xor(s, off);
     if (lane < ranks) {  // to every block of the cluster
       const uint32_t to = dsmem_addr(&sums_s[w], lane);
-      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(s) : "memory");
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(s.hi), "f"(s.lo)
+                   : "memory");
     }
     cluster_sync_all();
     if (warp == 0) {
       constexpr int kEach = kMaxCluster * kWarps / 32;
-      double x[kEach], sum = 0.;
+      Pair sum = {0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < kEach; ++j) {
         const int i = lane * kEach + j;
-        x[j] = i < total_warps ? sums_s[i] : 0.;
-        sum += x[j];
+        if (i < total_warps) sum = sum + *reinterpret_cast<const Pair*>(&sums_s[i]);
       }
-      const double to = scan32(sum);
-      const double total = __shfl_sync(kAll, to, 31), t = u_s[0] * total;
-      double run = to - sum;
-      int mine = -1, last = -1;
-      double rel = 0., rel_last = 0.;
-#pragma unroll
-      for (int j = 0; j < kEach; ++j) {
-        if (x[j] > 0.) {
-          last = lane * kEach + j;
-          rel_last = t - run;
-          if (mine < 0 && run + x[j] > t) {
-            mine = last;
-            rel = rel_last;
-          }
-        }
-        run += x[j];
+      const Pair total = shfl(scan32(sum), 31);
+      Pair t = total * u_s[0];
+      const int group = find32(sum, t, sum.hi > 0.f);
+      int owner = -1;
+      if (group >= 0) {
+        const Pair y = lane < kEach && group * kEach + lane < total_warps
+                           ? *reinterpret_cast<const Pair*>(&sums_s[group * kEach + lane])
+                           : Pair{0.f, 0.f};
+        owner = group * kEach + find32(y, t, y.hi > 0.f);
       }
-      unsigned hit = __ballot_sync(kAll, mine >= 0);
-      int src = hit ? __ffs(hit) - 1 : 0;
-      if (!hit) {  // rounding left none: the last range with mass
-        hit = __ballot_sync(kAll, last >= 0);
-        src = hit ? 31 - __clz(hit) : 0;
-        mine = last;
-        rel = rel_last;
-      }
-      const int owner = hit ? __shfl_sync(kAll, mine, src) : -1;
-      rel = __shfl_sync(kAll, rel, src);
       int got = -1;
       if (owner >= 0 && owner / kWarps == rank)
-        got = range_find(left, range_at(owner), range_at(owner + 1), rel, lane);
+        got = find(left, range_at(owner), range_at(owner + 1), t, lane);
       if (lane == 0) {
         owner_s = owner;
         got_s = got;
@@ -391,7 +480,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     __syncthreads();
     if (owner_s >= 0) break;
-    left.vec = -1;  // what is left sums to nothing: the row itself
+    if (tid < kCand) at_s[tid] = -1;  // what is left sums to nothing: the row itself
     cluster_sync_all();
   }
   if (tid == 0) {
@@ -430,8 +519,8 @@ extern "C" dfl2_status dfl2_tree_verify(const float* p, int B, int T, int V, con
   const dfl2::TreeVerifyArgs a{p,    tokens, parents, count,      cand_idx, q, u,
                                path, n_path, next_token, T, V, replace != 0,
                                dfl2::device_error_word()};
-  // as many blocks a sequence as are resident at once (four an SM), and have 4096 elements
-  const int most = 4 * dfl2::device_info().sms;
+  // as many blocks a sequence as are resident at once, and have 4096 elements each
+  const int most = dfl2::kCtas * dfl2::device_info().sms;
   int ranks = dfl2::kMaxCluster;
   while (ranks > 1 && (int64_t(ranks) * B > most || V / ranks < 4096)) ranks /= 2;
   const cudaError_t e =
