@@ -16,9 +16,14 @@
 // Numbers are unevaluated sums of two floats (about 46 bits): decisions and the drawn index
 // have to be those of the exact sums, and this GPU's doubles are slow (two additions a cycle
 // and SM, 60 cycles each).
+//
+// One tree is bound by the latency of its dependent steps: a candidate's number and its p,
+// the tests of the walk (about 1000 cycles each), the row's elements, and the search for the
+// drawn one, in two scans.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "cache.cuh"
 
@@ -26,7 +31,7 @@ namespace dfl2 {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kThreads = 512, kWarps = kThreads / 32, kCtas = 2, kMaxCluster = 8;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kCtas = 2, kMaxCluster = 16;
 
 struct TreeVerifyArgs {
   const float* p;
@@ -68,11 +73,6 @@ __device__ __forceinline__ Pair operator*(Pair a, Pair b) {
 }
 __device__ __forceinline__ Pair operator*(Pair a, float b) { return a * Pair{b, 0.f}; }
 __device__ __forceinline__ Pair scaled(Pair a, float f) { return {a.hi * f, a.lo * f}; }  // f = 2^n
-__device__ __forceinline__ Pair operator/(Pair a, Pair b) {
-  const float q = __fdiv_rn(a.hi, b.hi);
-  const Pair r = a - b * q;
-  return quick(q, __fdiv_rn(r.hi, b.hi));
-}
 __device__ __forceinline__ bool operator<(Pair a, Pair b) {
   return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo);
 }
@@ -102,30 +102,16 @@ __device__ __forceinline__ float to_one(float x) {
   return e < 2 || e > 252 ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
 }
 
-// The row of the last draw.  Rows need not begin on 16 bytes: elements are numbered from
+// The row of the last draw.  Rows need not begin on 16 bytes: its vectors are numbered from
 // the 16-byte boundary at or before the row, `off` elements early.
 struct Row {
-  const float4* base;
+  const float* p;  // element 0
   int off, V, vecs;
-  // Elements 4 v - off .. + 3 of a row, 0 where v is past `end` or not wholly inside.
-  __device__ __forceinline__ float4 inner(int v, int end) const {
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int e = 4 * v - off;
-    if (v < end && e >= 0 && e + 3 < V) x = __ldg(base + v);
-    return x;
+  __device__ __forceinline__ float4 vec(int v) const {
+    return __ldg(reinterpret_cast<const float4*>(p - off) + v);
   }
-  // The row's first and last vectors where they are cut, else x.
-  __device__ __forceinline__ float4 ends(float4 x, int v) const {
-    const int e = 4 * v - off;
-    if (e < 0 || (e < V && e + 3 >= V)) {
-      const float* f = reinterpret_cast<const float*>(base + v);
-      x.x = e >= 0 ? f[0] : 0.f;
-      x.y = e + 1 >= 0 && e + 1 < V ? f[1] : 0.f;
-      x.z = e + 2 >= 0 && e + 2 < V ? f[2] : 0.f;
-      x.w = e + 3 < V ? f[3] : 0.f;
-    }
-    return x;
-  }
+  // Whether vector v holds elements of other rows (and may lie outside the tensor).
+  __device__ __forceinline__ bool cut(int v) const { return 4 * v < off || 4 * v + 4 - off > V; }
 };
 
 // Two floats in one register pair, for the two-sums of the row.
@@ -147,72 +133,93 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {  // a - b, as
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(b), "l"(0xBF800000BF800000ull), "l"(a));
   return r;
 }
-// hi + lo += x, twice.
+// hi + lo += x, twice: hi takes x to the nearest multiple of 2^-24 (what is left of x + 0.5
+// - 0.5), so it stays exact while it is below 1, and lo the rest, at most 2^-25 of each.
 __device__ __forceinline__ void add_exact2(uint64_t& hi, uint64_t& lo, uint64_t x) {
-  const uint64_t s = add2(hi, x), c = sub2(s, hi);
-  lo = add2(lo, add2(sub2(hi, sub2(s, c)), sub2(x, c)));
-  hi = s;
+  const uint64_t h = add2(add2(x, 0x3F0000003F000000ull), 0xBF000000BF000000ull);
+  hi = add2(hi, h);
+  lo = add2(lo, sub2(x, h));
 }
 
-// What is drawn from: the row with the candidates' values replaced.  These are pairs (their
-// rounding to a float would move the borders of all later elements by 2^-25 of them), so
-// they are added beside the row's, whose own values there count as 0.
+// The sum of vectors v, v + step, .. below v1, without those that are cut.
+__device__ __noinline__ Pair row_sum(const Row row, int v, int v1, int step) {
+  constexpr int kBatch = 10;  // (a lane's vectors of 151,936 elements in 8 blocks)
+  uint64_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll 1
+  for (; v < v1; v += step * kBatch) {
+    float4 x[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = v + step * j;
+      x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < v1 && !row.cut(i)) x[j] = row.vec(i);
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (v + step * j >= v1) break;
+      add_exact2(hi[0], lo[0], pack(x[j].x, x[j].y));
+      add_exact2(hi[1], lo[1], pack(x[j].z, x[j].w));
+    }
+  }
+  float h[4], l[4];
+  unpack(hi[0], h[0], h[1]);
+  unpack(hi[1], h[2], h[3]);
+  unpack(lo[0], l[0], l[1]);
+  unpack(lo[1], l[2], l[3]);
+  return (quick(h[0], l[0]) + quick(h[1], l[1])) + (quick(h[2], l[2]) + quick(h[3], l[3]));
+}
+
+// What is drawn from: the row times g, and in the candidates' places other values.  In a
+// sum over vectors a candidate's own p is taken out again (the sums are exact enough).
 struct Left {
   Row row;
-  const int* at;    // [16], the candidates' elements; -1: none
-  const Pair* val;
+  Pair g;
+  const int* at;     // [16], the candidates' elements; -1: none
+  const float* p;    // [16] their p
+  const Pair* val;   // [16]
   // The candidates in vectors [v0, v1), by a warp.
   __device__ __forceinline__ unsigned among(int v0, int v1) const {
     const int lane = threadIdx.x & 31, c = lane < kCand ? at[lane] : -1;
     const int v = (c + row.off) >> 2;
     return __ballot_sync(kAll, c >= 0 && v >= v0 && v < v1);
   }
-  // The sum of vectors v, v + step, .. below v1; cand: the candidates that may be there.
+  // This lane's sum of vectors v, v + step, .. below v1; cand: the candidates that may be
+  // among them.
   __device__ __forceinline__ Pair sum(int v, int v1, int step, unsigned cand) const {
-    constexpr int kBatch = 8;
-    uint64_t hi[2] = {0, 0}, lo[2] = {0, 0};
+    Pair s = row_sum(row, v, v1, step);
+    const int last = row.vecs - 1;
+    if (v < v1 && (v == 0 || v1 > last)) {  // the elements of the cut vectors
 #pragma unroll 1
-    for (; v < v1; v += step * kBatch) {
-      float4 x[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) x[j] = row.inner(v + step * j, v1);
-      if (cand || v < step || v + step * kBatch >= row.vecs)
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          if (v + step * j < v1) x[j] = odd(x[j], v + step * j, cand);
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        if (v + step * j >= v1) break;
-        add_exact2(hi[0], lo[0], pack(x[j].x, x[j].y));
-        add_exact2(hi[1], lo[1], pack(x[j].z, x[j].w));
+      for (int j = 0; j < (last ? 8 : 4); ++j) {
+        const int i = j < 4 ? 0 : last, e = 4 * i + (j & 3) - row.off;
+        if (row.cut(i) && e >= 0 && e < row.V && i >= v && i < v1 && (i - v) % step == 0)
+          s = s + Pair{row.p[e], 0.f};
       }
     }
-    float h[4], l[4];
-    unpack(hi[0], h[0], h[1]);
-    unpack(hi[1], h[2], h[3]);
-    unpack(lo[0], l[0], l[1]);
-    unpack(lo[1], l[2], l[3]);
-    return (quick(h[0], l[0]) + quick(h[1], l[1])) + (quick(h[2], l[2]) + quick(h[3], l[3]));
-  }
-  // Vector v where the row is cut, and without the candidates among `which`.
-  __device__ __noinline__ float4 odd(float4 x, int v, unsigned which) const {
-    x = row.ends(x, v);
-    for (; which; which &= which - 1) {
-      const int c = at[__ffs(which) - 1] + row.off;
-      if (c >> 2 != v) continue;
-      if ((c & 3) == 0) x.x = 0.f;
-      if ((c & 3) == 1) x.y = 0.f;
-      if ((c & 3) == 2) x.z = 0.f;
-      if ((c & 3) == 3) x.w = 0.f;
+    Pair c = {0.f, 0.f};
+#pragma unroll 1
+    for (; cand; cand &= cand - 1) {
+      const int k = __ffs(cand) - 1, i = (at[k] + row.off) >> 2;
+      if (i >= v && i < v1 && (i - v) % step == 0) {
+        s = s - Pair{p[k], 0.f};
+        c = c + val[k];
+      }
     }
+    return s * g + c;
+  }
+  __device__ __forceinline__ Pair element(int e, unsigned cand) const {
+    Pair x = g * row.p[e];
+#pragma unroll 1
+    for (; cand; cand &= cand - 1)
+      if (at[__ffs(cand) - 1] == e) x = val[__ffs(cand) - 1];
     return x;
   }
 };
 
-// By a warp: which of the lanes' values, in order, the running sum first exceeds t at (the
-// last one above 0 if none, -1 if that is none either), and t less what comes before it.
-__device__ __forceinline__ int find32(Pair x, Pair& t, bool above) {
-  const Pair to = scan32(x);
+// By a warp: which of the lanes' values x, in order, the running sum `to` first exceeds t at
+// (the last one above 0 if none, -1 if that is none either), and t less what comes before it.
+__device__ __forceinline__ int find32(Pair x, Pair to, Pair& t) {
+  const bool above = x.hi > 0.f;
   unsigned hit = __ballot_sync(kAll, above && t < to);
   if (!hit) {
     hit = __ballot_sync(kAll, above);
@@ -224,38 +231,6 @@ __device__ __forceinline__ int find32(Pair x, Pair& t, bool above) {
   return w;
 }
 
-// The element of vectors [v0, v1) at which the running sum first exceeds t, by a warp:
-// 32 parts a step, down to a vector a lane.
-__device__ __noinline__ int find(const Left& a, int v0, int v1, Pair t, int lane) {
-  while (true) {
-    const int each = (v1 - v0 + 31) / 32;
-    const int w0 = min(v1, v0 + lane * each), w1 = min(v1, w0 + each);
-    const unsigned cand = a.among(v0, v1);
-    Pair s = a.sum(w0, w1, 1, cand);
-    for (unsigned c = cand; c; c &= c - 1) {
-      const int k = __ffs(c) - 1, v = (a.at[k] + a.row.off) >> 2;
-      if (v >= w0 && v < w1) s = s + a.val[k];
-    }
-    const int w = find32(s, t, s.hi > 0.f);
-    if (w < 0) return -1;
-    if (each > 1) {
-      v1 = __shfl_sync(kAll, w1, w);
-      v0 = __shfl_sync(kAll, w0, w);
-      continue;
-    }
-    // an element a lane
-    const int e = 4 * (v0 + w) - a.row.off + lane;
-    Pair x = {0.f, 0.f};
-    if (lane < 4 && e >= 0 && e < a.row.V) {
-      x.hi = __ldg(reinterpret_cast<const float*>(a.row.base) + a.row.off + e);
-      for (unsigned c = cand; c; c &= c - 1)
-        if (a.at[__ffs(c) - 1] == e) x = a.val[__ffs(c) - 1];
-    }
-    const int z = find32(x, t, x.hi > 0.f);
-    return z < 0 ? -1 : __shfl_sync(kAll, e, z);
-  }
-}
-
 __global__ void __launch_bounds__(kThreads, kCtas)
     tree_verify_kernel(const __grid_constant__ TreeVerifyArgs a) {
   __shared__ float r_s[kMaxTree][kCand], d_s[kMaxTree][kCand];
@@ -263,8 +238,9 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   __shared__ int16_t up_s[kMaxTree];   // its parent; -1: no child
   __shared__ float u_s[kMaxTree];
   __shared__ int at_s[kCand];          // the last node's candidates, and their part of what
-  __shared__ Pair val_s[kCand];        // is left
-  __shared__ int node_s, got_s, owner_s;
+  __shared__ Pair val_s[kCand], g_s;   // is left, and of the row's other elements
+  __shared__ int node_s, owner_s, who_s, last_s;
+  __shared__ Pair t_s, warp_s[kWarps];
   __shared__ uint64_t sums_s[kMaxCluster * kWarps];  // every warp of the cluster's (a Pair)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.y, rank = blockIdx.x, ranks = gridDim.x;
@@ -305,12 +281,9 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
     for (int z = 0; z < kBatch; ++z) {
       const int x = x0 + z * kThreads;
-      bool again = false;
-#pragma unroll
-      for (int k = 1; k < kCand; ++k) {
-        const int y = __shfl_up_sync(kAll, c[z], k, kCand);
-        again |= (lane & 15) >= k && y == c[z];
-      }
+      // (c is below 2^30; the halves of a warp are different nodes)
+      const unsigned same = __match_any_sync(kAll, c[z] ^ (lane >> 4 << 30));
+      const bool again = same >> (lane & 16) & ((1u << (lane & 15)) - 1);
       if (x < n * kCand) {
         r_s[x / kCand][x % kCand] = again ? 0.f : p[z];
         d_s[x / kCand][x % kCand] = again ? 0.f : q[z];
@@ -343,9 +316,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     // divided: r/|r| - d/|d| is r |d| - d |r| but for a factor, which g keeps (what r off
     // the candidates is, relative to p).  |r| and |d| are held in [1, 2) by powers of two.
     const bool low = lane < kCand;
-    int cur = 0, len = 0;
+    int cur = 0, len = 0, cand = -1;
     Pair x = {0.f, 0.f}, g = {1.f, 0.f};
     while (n > 0) {
+      cand = a.cand[(at + cur) * kCand + k];  // (looked at after the walk)
       if (rank == 0 && lane == 0) a.path[at + len] = cur;
       ++len;
       const Pair p = {r_s[cur][k], 0.f};
@@ -409,17 +383,13 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       for (int i = len + lane; i < T; i += 32) a.path[at + i] = -1;
       if (lane == 0) a.n_path[b] = len;
     }
-    if (lane < kCand) {
-      const int c = n > 0 ? a.cand[(at + cur) * kCand + k] : -1;
-      bool again = false;
-#pragma unroll
-      for (int z = 1; z < kCand; ++z) {
-        const int y = __shfl_up_sync(0xffffu, c, z, kCand);
-        again |= k >= z && y == c;
-      }
-      at_s[k] = again || static_cast<unsigned>(c) >= static_cast<unsigned>(V) ? -1 : c;
-      val_s[k] = x / g;
+    bool again = static_cast<unsigned>(cand) >= static_cast<unsigned>(V);
+    again |= (__match_any_sync(kAll, cand) & ((1u << k) - 1)) != 0;
+    if (low) {
+      at_s[k] = again ? -1 : cand;
+      val_s[k] = x;
     }
+    if (lane == 0) g_s = g.hi < 0x1p100f ? g : Pair{0x1p100f, 0.f};
     if (lane == 0) node_s = cur;
   }
   __syncthreads();
@@ -427,24 +397,23 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   // ---- the last draw ----
   Left left;
   const int64_t start = (at + node_s) * V;
+  left.row.p = a.p + start;
   left.row.off = static_cast<int>(start & 3);
-  left.row.base = reinterpret_cast<const float4*>(a.p + (start - left.row.off));
   left.row.V = V;
   left.row.vecs = (V + left.row.off + 3) / 4;
+  left.g = g_s;
   left.at = at_s;
+  left.p = r_s[node_s];
   left.val = val_s;
   const int total_warps = ranks * kWarps;
+  const int each = (left.row.vecs + total_warps - 1) / total_warps;
   cluster_wait();
-  auto range_at = [&](int w) {
-    return static_cast<int>(static_cast<int64_t>(left.row.vecs) * w / total_warps);
-  };
+  auto range_at = [&](int w) { return min(left.row.vecs, w * each); };
   for (int pass = 0; pass < 2 && n > 0; ++pass) {
     const int w = rank * kWarps + warp;
     const int v0 = range_at(w), v1 = range_at(w + 1);
-    const unsigned cand = left.among(v0, v1);
-    Pair s = left.sum(v0 + lane, v1, 32, cand);
-    if (cand >> lane & 1) s = s + val_s[lane];
-#pragma unroll
+    Pair s = left.sum(v0 + lane, v1, 32, left.among(v0, v1));
+#pragma unroll 1
     for (int off = 16; off; off >>= 1) s = s + shfl_xor(s, off);
     if (lane < ranks) {  // to every block of the cluster
       const uint32_t to = dsmem_addr(&sums_s[w], lane);
@@ -454,40 +423,113 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     cluster_sync_all();
     if (warp == 0) {
       constexpr int kEach = kMaxCluster * kWarps / 32;
-      Pair sum = {0.f, 0.f};
+      Pair x[kEach], sum = {0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < kEach; ++j) {
         const int i = lane * kEach + j;
-        if (i < total_warps) sum = sum + *reinterpret_cast<const Pair*>(&sums_s[i]);
+        x[j] = i < total_warps ? *reinterpret_cast<const Pair*>(&sums_s[i]) : Pair{0.f, 0.f};
+        sum = sum + x[j];
       }
-      const Pair total = shfl(scan32(sum), 31);
-      Pair t = total * u_s[0];
-      const int group = find32(sum, t, sum.hi > 0.f);
-      int owner = -1;
-      if (group >= 0) {
-        const Pair y = lane < kEach && group * kEach + lane < total_warps
-                           ? *reinterpret_cast<const Pair*>(&sums_s[group * kEach + lane])
-                           : Pair{0.f, 0.f};
-        owner = group * kEach + find32(y, t, y.hi > 0.f);
+      const Pair to = scan32(sum);
+      Pair t = shfl(to, 31) * u_s[0];
+      int owner = find32(sum, to, t);
+      if (owner >= 0) {  // every lane looks in its own four
+        int mine = 0;
+        Pair before = {0.f, 0.f}, run = {0.f, 0.f};
+        bool found = false;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+          if (!found && x[j].hi > 0.f) {
+            mine = j;
+            before = run;
+            run = run + x[j];
+            found = t < run;
+          }
+        t = shfl(t - before, owner);
+        owner = owner * kEach + __shfl_sync(kAll, mine, owner);
       }
-      int got = -1;
-      if (owner >= 0 && owner / kWarps == rank)
-        got = find(left, range_at(owner), range_at(owner + 1), t, lane);
       if (lane == 0) {
         owner_s = owner;
-        got_s = got;
+        t_s = t;
+        who_s = kThreads;
+        last_s = -1;
       }
     }
     __syncthreads();
     if (owner_s >= 0) break;
     if (tid < kCand) at_s[tid] = -1;  // what is left sums to nothing: the row itself
+    left.g = {1.f, 0.f};
     cluster_sync_all();
   }
-  if (tid == 0) {
-    const int owner = n > 0 ? owner_s : -1;
-    if (owner < 0 ? rank == 0 : owner / kWarps == rank) a.next[b] = owner < 0 ? -1 : got_s;
+
+  // ---- the element, by the block that has its range: a run of vectors a thread ----
+  const int owner = n > 0 ? owner_s : -1;
+  if (owner >= 0 && owner / kWarps == rank) {
+    const int v0 = range_at(owner), v1 = range_at(owner + 1);
+    const int run = (v1 - v0 + kThreads - 1) / kThreads;
+    const int w0 = min(v1, v0 + tid * run), w1 = min(v1, w0 + run);
+    const unsigned cand = left.among(v0, v1);
+    const Pair x = left.sum(w0, w1, 1, cand);
+    const Pair to = scan32(x);
+    if (lane == 31) warp_s[warp] = to;
+    __syncthreads();
+    const Pair sums = scan32(lane < kWarps ? warp_s[lane] : Pair{0.f, 0.f});
+    Pair before = shfl(sums, max(0, warp - 1));
+    if (warp == 0) before = {0.f, 0.f};
+    const unsigned hit = __ballot_sync(kAll, x.hi > 0.f && t_s < before + to);
+    const unsigned some = __ballot_sync(kAll, x.hi > 0.f);
+    if (lane == 0) {
+      if (hit) atomicMin(&who_s, tid + __ffs(hit) - 1);
+      if (some) atomicMax(&last_s, tid + 31 - __clz(some));
+    }
+    __syncthreads();
+    if (tid == (who_s < kThreads ? who_s : last_s)) {
+      const int e0 = max(0, 4 * w0 - left.row.off), e1 = min(V, 4 * w1 - left.row.off);
+      const Pair t = t_s - (before + (to - x));
+      Pair c = {0.f, 0.f};
+      int got = -1;
+#pragma unroll 1
+      for (int e = e0; e < e1; ++e) {
+        const Pair y = left.element(e, cand);
+        if (!(y.hi > 0.f)) continue;
+        c = c + y;
+        got = e;
+        if (t < c) break;
+      }
+      a.next[b] = got;
+    }
+  } else if (owner < 0 && rank == 0 && tid == 0) {
+    a.next[b] = -1;
   }
   cluster_sync_all();  // no block ends while another may still write to it
+}
+
+// Whether the current device can hold a cluster of 16 blocks of the kernel.
+bool wide_clusters() {
+  static std::atomic<int> known[64];  // (ordinals are below 64: ensured with the device's state)
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  int k = known[dev].load();
+  if (k == 0) {
+    int n = 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kMaxCluster);
+    cfg.blockDim = dim3(kThreads);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kMaxCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const bool ok =
+        cudaFuncSetAttribute(tree_verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                             1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, tree_verify_kernel, &cfg) == cudaSuccess && n > 0;
+    if (!ok) cudaGetLastError();
+    k = ok ? 2 : 1;
+    known[dev].store(k);
+  }
+  return k == 2;
 }
 
 }  // namespace
@@ -519,9 +561,10 @@ extern "C" dfl2_status dfl2_tree_verify(const float* p, int B, int T, int V, con
   const dfl2::TreeVerifyArgs a{p,    tokens, parents, count,      cand_idx, q, u,
                                path, n_path, next_token, T, V, replace != 0,
                                dfl2::device_error_word()};
-  // as many blocks a sequence as are resident at once, and have 4096 elements each
+  // As many blocks a sequence as are resident at once, and have 4096 elements each; 16, which
+  // a device may refuse, where it takes them.
   const int most = dfl2::kCtas * dfl2::device_info().sms;
-  int ranks = dfl2::kMaxCluster;
+  int ranks = dfl2::wide_clusters() ? dfl2::kMaxCluster : 8;
   while (ranks > 1 && (int64_t(ranks) * B > most || V / ranks < 4096)) ranks /= 2;
   const cudaError_t e =
       dfl2::launch_kc(dfl2::tree_verify_kernel, dim3(ranks, B), dim3(dfl2::kThreads), 0,
