@@ -112,10 +112,11 @@ def load():
     L.dfl2_tree_attn_workspace_size.argtypes = [I, I, I, I, I, I]
     L.dfl2_tree_attn_workspace_size.restype = SZ
     L.dfl2_tree_attn.argtypes = [P, S, C, I, I, I, I, P, P, P, P, F, P, S, P, P, SZ, P]
+    L.dfl2_window_attn.argtypes = [P, S, C, I, I, I, I, P, P, P, P, P, I, I, F, P, S, P, P, SZ, P]
     L.dfl2_tree_verify.argtypes = [P, I, I, I, P, P, P, P, P, P, I, P, P, P, P]
     for name in ("dfl2_cache_reserve", "dfl2_cache_write", "dfl2_cache_compact",
                  "dfl2_cache_fork", "dfl2_cache_free", "dfl2_tree_mask", "dfl2_tree_accept",
-                 "dfl2_tree_verify", "dfl2_tree_attn"):
+                 "dfl2_tree_verify", "dfl2_tree_attn", "dfl2_window_attn"):
         getattr(L, name).restype = I
     for name in ("dfl2_workspace_init", "dfl2_device_error", "dfl2_topk", "dfl2_select",
                  "dfl2_walk", "dfl2_conv2", "dfl2_conv2_ws", "dfl2_tail", "dfl2_verify", "dfl2_tables_build",
@@ -538,3 +539,12 @@ def dfl2_tree_attn(q, cache, layer: int, length, mask, out, ws, rows=None, count
     [B,T,q_heads].  mask int32 [B,T,ceil(T/32)], None for a chain; scale: head_dim ** -0.5."""
     _check(_native.tree_attn(q, cache, layer, length, mask, out, ws, rows, count, lse, scale,
                              stream))
+
+
+def dfl2_window_attn(q, cache, layer: int, length, mask, depth, sinks: int, window: int, out, ws,
+                     rows=None, count=None, lse=None, scale=None, stream=None) -> None:
+    """dfl2_tree_attn in a layer whose tokens see the last `window` positions, their own
+    included, and the first `sinks`; depth int32 [B,T] as dfl2_tree_mask gives it (None for a
+    chain); ws: dfl2_tree_attn_workspace_size bytes."""
+    _check(_native.window_attn(q, cache, layer, length, mask, out, ws, rows, count, lse, scale,
+                               stream, depth, sinks, window))

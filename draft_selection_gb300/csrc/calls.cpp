@@ -245,8 +245,9 @@ PyObject* tree_verify(PyObject* const* a) {
   });
 }
 
-PyObject* tree_attn(PyObject* const* a) {
-  // q, cache, layer, length, mask, out, ws, rows, count, lse, scale, stream
+// q, cache, layer, length, mask, out, ws, rows, count, lse, scale, stream; win: then depth,
+// sinks, window
+PyObject* attn(PyObject* const* a, bool win) {
   const dfl2_cache* c = cache_of(a[1]);
   const at::Tensor &q = tensor(a[0], "q", 4), &out = tensor(a[5], "out", 4),
                    &ws = tensor(a[6], "ws");
@@ -277,13 +278,20 @@ PyObject* tree_attn(PyObject* const* a) {
   const void* qp = q.data_ptr();
   void *op = out.data_ptr(), *wp = ws.data_ptr();
   const size_t bytes = ws.nbytes();
+  const int32_t* depth = win ? i32(a[12], "depth", {B, T}) : nullptr;
+  const int sinks = win ? whole(a[13], "sinks") : 0, window = win ? whole(a[14], "window") : 0;
   const dfl2_stream s = stream_of(a[11]);
   return run([&] {
-    return dfl2_tree_attn(qp, qs, c, layer, B, T, H, rows, length, n,
-                          reinterpret_cast<const uint32_t*>(mask), static_cast<float>(scale), op,
+    const uint32_t* m = reinterpret_cast<const uint32_t*>(mask);
+    if (win)
+      return dfl2_window_attn(qp, qs, c, layer, B, T, H, rows, length, n, m, depth, sinks, window,
+                              static_cast<float>(scale), op, os, lse, wp, bytes, s);
+    return dfl2_tree_attn(qp, qs, c, layer, B, T, H, rows, length, n, m, static_cast<float>(scale), op,
                           os, lse, wp, bytes, s);
   });
 }
+PyObject* tree_attn(PyObject* const* a) { return attn(a, false); }
+PyObject* window_attn(PyObject* const* a) { return attn(a, true); }
 
 // A function of N positional arguments; no C++ exception leaves it.
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -313,6 +321,7 @@ PyMethodDef methods[] = {method<cache_reserve, 6>("cache_reserve"),
                          method<tree_accept, 8>("tree_accept"),
                          method<tree_verify, 12>("tree_verify"),
                          method<tree_attn, 12>("tree_attn"),
+                         method<window_attn, 15>("window_attn"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,
                       nullptr,               nullptr,  nullptr, nullptr};

@@ -53,7 +53,12 @@ struct AttnArgs {
   int stream_rows; // rows of a stream: whole nodes, at most 128
   int rows;        // rows of a row tile
   int row_tiles;   // ceil(T G / rows)
+  // with a window (kernels with kWin): a node sees, of what it would see without, the first
+  // `sinks` positions and those less than `window` before its own
+  int sinks, window;
+  const int32_t* depth;  // [B][T] a node's own position behind the length, or NULL: its number
 };
+cudaError_t launch_window_attn(const AttnArgs& a, const dfl2_cache* c, cudaStream_t s);
 
 namespace {
 
@@ -61,6 +66,34 @@ namespace {
 struct Seq {
   int row, len, n, tiles;
 };
+// With a window the units are the tiles that a node may see something of: those of the
+// sinks, and those from the first one that reaches into the first node's window on.
+struct Gap {
+  int at, size;  // tiles at, .. at + size - 1 are left out
+};
+__device__ __forceinline__ Gap gap_of(const AttnArgs& a, int len, int tiles) {
+  Gap g;
+  g.at = min(tiles, (a.sinks + kKeys - 1) / kKeys);
+  g.size = max(0, max(0, len - a.window + 1) / kKeys - g.at);
+  return g;
+}
+// The tile of keys that a sequence's unit is.
+template <bool kWin>
+__device__ __forceinline__ int key_tile(const AttnArgs& a, const Seq& s, int tile) {
+  if (!kWin) return tile;
+  const Gap g = gap_of(a, s.len, (s.len + s.n + kKeys - 1) / kKeys);
+  return tile < g.at ? tile : tile + g.size;
+}
+// Whether a node may miss something of a tile of keys (that of position p0 on): it has nodes,
+// or positions past the end, or reaches out of the sinks or a node's window.
+template <bool kWin>
+__device__ __forceinline__ bool is_edge(const AttnArgs& a, const Seq& s, int key) {
+  if (!kWin) return key >= s.len / kKeys;
+  const int p0 = key * kKeys;
+  return p0 + kKeys > s.len ||
+         (p0 + kKeys > a.sinks && p0 < s.len + a.t.T - a.window);  // (depths are below T)
+}
+template <bool kWin>
 __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
   Seq s;
   s.len = a.t.length[b];
@@ -71,6 +104,7 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b) {
     s.n = 0;
   }
   s.tiles = s.n > 0 ? (s.len + s.n + kKeys - 1) / kKeys : 0;
+  if (kWin && s.n > 0) s.tiles -= gap_of(a, s.len, s.tiles).size;
   return s;
 }
 
@@ -89,6 +123,7 @@ __device__ __forceinline__ int range_of(int64_t units, int n, int64_t u) {
 }
 
 // A place in a range of units.
+template <bool kWin>
 struct Cursor {
   int64_t u;
   int b, h, tile;  // sequence, key head, tile
@@ -107,7 +142,7 @@ struct Cursor {
     h = 0;
     do {
       if (++b >= a.B) return;
-      s = load_seq(a, b);
+      s = load_seq<kWin>(a, b);
     } while (s.tiles == 0);
   }
 };
@@ -120,18 +155,20 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // Range `cta` [u0, u1) of the units in n_cta ranges, and the place where it begins, by a
 // warp together.  Up to 32 sequences need one load of their lengths.
+template <bool kWin>
 struct Range {
   int64_t units, u0, u1;
   int n_cta;
-  Cursor first;  // if u0 < u1
+  Cursor<kWin> first;  // if u0 < u1
 };
-__device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
+template <bool kWin>
+__device__ __forceinline__ Range<kWin> find_range(const AttnArgs& a, int cta) {
   const int lane = threadIdx.x & 31;
-  Range g;
+  Range<kWin> g;
   Seq own;
   int sum;  // tiles of the sequences up to this lane's: 32 times 2^24 at most
   auto load = [&](int b0) {
-    own = b0 + lane < a.B ? load_seq(a, b0 + lane) : Seq{0, 0, 0, 0};
+    own = b0 + lane < a.B ? load_seq<kWin>(a, b0 + lane) : Seq{0, 0, 0, 0};
     sum = own.tiles;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -143,7 +180,7 @@ __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
   g.units = static_cast<int64_t>(__shfl_sync(kAll, sum, 31)) * a.H;
   if (a.B > 32) {
     int64_t x = 0;
-    for (int b = lane + 32; b < a.B; b += 32) x += load_seq(a, b).tiles;
+    for (int b = lane + 32; b < a.B; b += 32) x += load_seq<kWin>(a, b).tiles;
 #pragma unroll
     for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(kAll, x, off);
     g.units += x * a.H;
@@ -182,7 +219,8 @@ __device__ __forceinline__ Range find_range(const AttnArgs& a, int cta) {
 }
 
 // Of the head whose first unit is v0.
-__device__ __forceinline__ Cut make_cut(const Range& g, int64_t v0, int b, int h, const Seq& s) {
+template <bool kWin>
+__device__ __forceinline__ Cut make_cut(const Range<kWin>& g, int64_t v0, int b, int h, const Seq& s) {
   const int c0 = range_of(g.units, g.n_cta, v0), c1 = range_of(g.units, g.n_cta, v0 + s.tiles - 1);
   return Cut{b, h * 1024 + s.n, c0, c1 * 2 + (range_start(g.units, g.n_cta, c0) < v0 ? 1 : 0)};
 }

@@ -546,6 +546,22 @@ dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_c
                            float scale, void* out, const int64_t* out_strides, float* lse,
                            void* ws, size_t ws_bytes, dfl2_stream stream);
 
+/* The same in a layer whose tokens see a window and the first few positions (sinks): of
+ * the positions that dfl2_tree_attn lets node i see, those at or past `sinks` only count
+ * if they are less than `window` positions before it.  Node i stands at position
+ * length + depth[b,i] (int32 [B,T], as dfl2_tree_mask gives it; other values than
+ * 0 .. T-1 are taken to the nearer end; NULL: length + i, only without a mask), and so does
+ * a node that it sees.  Only the sinks and what the first node's window reaches are read,
+ * and pages that lie wholly between the two need not be there.
+ *   sinks 0 .. 2^30; window 1 .. 2^30 (1: itself).
+ * All else, the workspace included, as for dfl2_tree_attn. */
+dfl2_status dfl2_window_attn(const void* q, const int64_t* q_strides, const dfl2_cache* cache,
+                             int layer, int B, int T, int q_heads, const int32_t* table_rows,
+                             const int32_t* length, const int32_t* count, const uint32_t* mask,
+                             const int32_t* depth, int sinks, int window, float scale, void* out,
+                             const int64_t* out_strides, float* lse, void* ws, size_t ws_bytes,
+                             dfl2_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
