@@ -308,11 +308,20 @@ __device__ __forceinline__ int depth_of(const AttnArgs& a, int b, int i) {
 // Only needed where the window is shorter than the tree.
 __device__ __noinline__ uint64_t near_nodes(const AttnArgs& a, int b, int len, int deep,
                                             uint64_t nodes, int j0) {
-  for (uint64_t left = nodes; left; left &= left - 1) {
-    const int z = __ffsll(left) - 1, d = depth_of(a, b, j0 + z);
-    if (deep - d >= a.window && len + d >= a.sinks) nodes &= ~(1ull << z);
+  if (!a.depth)
+    return nodes & (~low_bits(deep - a.window + 1 - j0) | low_bits(a.sinks - len - j0));
+  uint64_t gone = 0;
+#pragma unroll 1
+  for (int z0 = 0; z0 < 64; z0 += 8) {  // (eight loads at once)
+    if (!(nodes >> z0 & 0xFF)) continue;
+    int d[8];
+#pragma unroll
+    for (int z = 0; z < 8; ++z) d[z] = depth_of(a, b, min(a.t.T - 1, j0 + z0 + z));
+#pragma unroll
+    for (int z = 0; z < 8; ++z)
+      if (deep - d[z] >= a.window && len + d[z] >= a.sinks) gone |= 1ull << (z0 + z);
   }
-  return nodes;
+  return nodes & ~gone;
 }
 
 // Which of the 64 positions from p0 on node i of sequence b sees (0 past the end).
