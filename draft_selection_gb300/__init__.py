@@ -112,11 +112,14 @@ def load():
     L.dfl2_tree_attn_workspace_size.argtypes = [I, I, I, I, I, I]
     L.dfl2_tree_attn_workspace_size.restype = SZ
     L.dfl2_tree_attn.argtypes = [P, S, C, I, I, I, I, P, P, P, P, F, P, S, P, P, SZ, P]
+    L.dfl2_cache_evict_workspace_size.argtypes = [I, I]
+    L.dfl2_cache_evict_workspace_size.restype = SZ
+    L.dfl2_cache_evict.argtypes = [C, I, P, P, I, I, I, P, P, P, P, P, SZ, P]
     L.dfl2_window_attn.argtypes = [P, S, C, I, I, I, I, P, P, P, P, P, I, I, F, P, S, P, P, SZ, P]
     L.dfl2_tree_verify.argtypes = [P, I, I, I, P, P, P, P, P, P, I, P, P, P, P]
     for name in ("dfl2_cache_reserve", "dfl2_cache_write", "dfl2_cache_compact",
                  "dfl2_cache_fork", "dfl2_cache_free", "dfl2_tree_mask", "dfl2_tree_accept",
-                 "dfl2_tree_verify", "dfl2_tree_attn", "dfl2_window_attn"):
+                 "dfl2_tree_verify", "dfl2_tree_attn", "dfl2_window_attn", "dfl2_cache_evict"):
         getattr(L, name).restype = I
     for name in ("dfl2_workspace_init", "dfl2_device_error", "dfl2_topk", "dfl2_select",
                  "dfl2_walk", "dfl2_conv2", "dfl2_conv2_ws", "dfl2_tail", "dfl2_verify", "dfl2_tables_build",
@@ -503,6 +506,19 @@ def dfl2_cache_fork(cache, src, dst, length, served, stream=None) -> None:
 def dfl2_cache_free(cache, rows, stream=None) -> None:
     """Every page of the table rows given back."""
     _check(_native.cache_free(cache, rows, stream))
+
+
+def dfl2_cache_evict_workspace_size(B: int, keep: int) -> int:
+    return int(load().dfl2_cache_evict_workspace_size(B, keep))
+
+
+def dfl2_cache_evict(cache, length, keep: int, sinks: int, recent: int, weight, kept, new_length,
+                     served, ws, rows=None, stream=None) -> None:
+    """Sequences longer than keep positions give up those of least weight (float32
+    [rows, cols*page_size]) but for the first `sinks` and the last `recent`; kept int32
+    [B,keep] the positions that stay, new_length (may be length) and served int32 [B] out."""
+    _check(_native.cache_evict(cache, length, keep, sinks, recent, weight, kept, new_length, served,
+                               ws, rows, stream))
 
 
 def dfl2_tree_mask(parents, mask, depth=None, count=None, stream=None) -> None:

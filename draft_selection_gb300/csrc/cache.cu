@@ -223,21 +223,6 @@ __global__ void __launch_bounds__(kBookThreads) take_kernel(const __grid_constan
   }
 }
 
-// One holder of page p fewer.
-__device__ __forceinline__ void drop_page(const TableView& t, int p) {
-  if (static_cast<unsigned>(p) >= static_cast<unsigned>(t.pages)) {
-    record_error(t.err, kDevErrBadIndex);
-    return;
-  }
-  const int old = atomicSub(&t.refs[p], 1);
-  if (old == 1) {
-    atomicOr(&t.free_bits[p >> 5], 1u << (p & 31));
-  } else if (old < 1) {  // nobody held it: the state is not a cache's
-    atomicAdd(&t.refs[p], 1);
-    record_error(t.err, kDevErrBadIndex);
-  }
-}
-
 __global__ void __launch_bounds__(256) free_kernel(const __grid_constant__ TableView t) {
   pdl_wait();
   pdl_launch_dependents();

@@ -89,6 +89,21 @@ struct TableView {
   }
 };
 
+// One holder of page p fewer.
+__device__ __forceinline__ void drop_page(const TableView& t, int p) {
+  if (static_cast<unsigned>(p) >= static_cast<unsigned>(t.pages)) {
+    record_error(t.err, kDevErrBadIndex);
+    return;
+  }
+  const int old = atomicSub(&t.refs[p], 1);
+  if (old == 1) {
+    atomicOr(&t.free_bits[p >> 5], 1u << (p & 31));
+  } else if (old < 1) {  // nobody held it: the state is not a cache's
+    atomicAdd(&t.refs[p], 1);
+    record_error(t.err, kDevErrBadIndex);
+  }
+}
+
 inline TableView table_view(const dfl2_cache* c, const int32_t* seq, const int32_t* length,
                             const int32_t* count, int T) {
   return TableView{c->table, c->rows, c->cols,  c->pages, log2_of(c->page_size), c->refs,

@@ -226,6 +226,25 @@ float* f32(PyObject* o, const char* name, Sizes shape) {
   return static_cast<float*>(t.data_ptr());
 }
 
+PyObject* cache_evict(PyObject* const* a) {
+  // cache, length, keep, sinks, recent, weight, kept, new_length, served, ws, rows, stream
+  const dfl2_cache* c = cache_of(a[0]);
+  const int B = size(tensor(a[1], "length", 1), 0, "length");
+  const int keep = whole(a[2], "keep"), sinks = whole(a[3], "sinks"), recent = whole(a[4], "recent");
+  const at::Tensor& ws = tensor(a[9], "ws");
+  float* w = f32(a[5], "weight", {c->rows, int64_t(c->cols) * c->page_size});
+  const int32_t *length = i32(a[1], "length", {B}), *rows = i32(a[10], "rows", {B});
+  int32_t *kept = i32(a[6], "kept", {B, keep}), *new_length = i32(a[7], "new_length", {B}),
+          *served = i32(a[8], "served", {B});
+  void* wp = ws.data_ptr();
+  const size_t bytes = ws.nbytes();
+  const dfl2_stream s = stream_of(a[11]);
+  return run([&] {
+    return dfl2_cache_evict(c, B, rows, length, keep, sinks, recent, w, kept, new_length, served,
+                            wp, bytes, s);
+  });
+}
+
 PyObject* tree_verify(PyObject* const* a) {
   // p, tokens, parents, cand_idx, q, u, path, n_path, next_token, count, replace, stream
   const at::Tensor& p = tensor(a[0], "p", 3);
@@ -319,6 +338,7 @@ PyMethodDef methods[] = {method<cache_reserve, 6>("cache_reserve"),
                          method<cache_free, 3>("cache_free"),
                          method<tree_mask, 5>("tree_mask"),
                          method<tree_accept, 8>("tree_accept"),
+                         method<cache_evict, 12>("cache_evict"),
                          method<tree_verify, 12>("tree_verify"),
                          method<tree_attn, 12>("tree_attn"),
                          method<window_attn, 15>("window_attn"),

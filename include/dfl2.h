@@ -458,6 +458,29 @@ dfl2_status dfl2_cache_fork(const dfl2_cache* cache, int n, const int32_t* src,
 dfl2_status dfl2_cache_free(const dfl2_cache* cache, int n, const int32_t* table_rows,
                             dfl2_stream stream);
 
+/* A sequence longer than `keep` positions gives up those of least weight: its first
+ * `sinks` and last `recent` positions stay, and of the others as many of the largest
+ * weights as make `keep` (equal ones: the lower positions; NaN counts as -inf).  In every
+ * layer the rows that stay move together, in order, to positions 0 .. keep-1, their weights
+ * with them, and the pages of the positions behind are given back.  One no longer than
+ * `keep` stays as it is.
+ *   weight      float32 [rows, cols*page_size]: of position j of table row r (as
+ *               dfl2_cache_weigh leaves it); what lies behind the new length stays.
+ *   kept        int32 [B,keep]: the old positions of the ones that stay, in order (for what
+ *               else the caller keeps by position), then -1.
+ *   new_length  int32 [B]: min(length, keep) (may be the same array as length).
+ *   served      int32 [B]: 1, or 0 where a page of the sequence is missing, where one that
+ *               would be written is shared with another sequence (dfl2_cache_fork), or where
+ *               the sequence cannot be that long; it is then left as it was, with kept -1.
+ *   ws          dfl2_cache_evict_workspace_size bytes of scratch (not zero-filled, and not
+ *               shared with an entry point whose workspace holds counters).
+ * 1 <= keep <= 2^30; sinks, recent >= 0, together at most keep.  Two kernel launches. */
+size_t dfl2_cache_evict_workspace_size(int B, int keep);
+dfl2_status dfl2_cache_evict(const dfl2_cache* cache, int B, const int32_t* table_rows,
+                             const int32_t* length, int keep, int sinks, int recent, float* weight,
+                             int32_t* kept, int32_t* new_length, int32_t* served, void* ws,
+                             size_t ws_bytes, dfl2_stream stream);
+
 /* parents int32 [B,T]: parents[b,i] < i is the node that node i follows, -1
  * none (node 0).  mask uint32 [B,T,ceil(T/32)]: bit j of row i is set iff j is i
  * or an ancestor of i.  depth int32 [B,T] (nullable): the number of ancestors.
