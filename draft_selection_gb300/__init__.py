@@ -112,6 +112,9 @@ def load():
     L.dfl2_tree_attn_workspace_size.argtypes = [I, I, I, I, I, I]
     L.dfl2_tree_attn_workspace_size.restype = SZ
     L.dfl2_tree_attn.argtypes = [P, S, C, I, I, I, I, P, P, P, P, F, P, S, P, P, SZ, P]
+    L.dfl2_cache_weigh_workspace_size.argtypes = []
+    L.dfl2_cache_weigh_workspace_size.restype = SZ
+    L.dfl2_cache_weigh.argtypes = [P, S, P, C, I, I, I, I, P, P, P, P, F, I, P, P, SZ, P]
     L.dfl2_cache_evict_workspace_size.argtypes = [I, I]
     L.dfl2_cache_evict_workspace_size.restype = SZ
     L.dfl2_cache_evict.argtypes = [C, I, P, P, I, I, I, P, P, P, P, P, SZ, P]
@@ -119,7 +122,8 @@ def load():
     L.dfl2_tree_verify.argtypes = [P, I, I, I, P, P, P, P, P, P, I, P, P, P, P]
     for name in ("dfl2_cache_reserve", "dfl2_cache_write", "dfl2_cache_compact",
                  "dfl2_cache_fork", "dfl2_cache_free", "dfl2_tree_mask", "dfl2_tree_accept",
-                 "dfl2_tree_verify", "dfl2_tree_attn", "dfl2_window_attn", "dfl2_cache_evict"):
+                 "dfl2_tree_verify", "dfl2_tree_attn", "dfl2_window_attn", "dfl2_cache_weigh",
+                 "dfl2_cache_evict"):
         getattr(L, name).restype = I
     for name in ("dfl2_workspace_init", "dfl2_device_error", "dfl2_topk", "dfl2_select",
                  "dfl2_walk", "dfl2_conv2", "dfl2_conv2_ws", "dfl2_tail", "dfl2_verify", "dfl2_tables_build",
@@ -564,3 +568,17 @@ def dfl2_window_attn(q, cache, layer: int, length, mask, depth, sinks: int, wind
     chain); ws: dfl2_tree_attn_workspace_size bytes."""
     _check(_native.window_attn(q, cache, layer, length, mask, out, ws, rows, count, lse, scale,
                                stream, depth, sinks, window))
+
+
+def dfl2_cache_weigh_workspace_size() -> int:
+    return int(load().dfl2_cache_weigh_workspace_size())
+
+
+def dfl2_cache_weigh(q, lse, cache, layer: int, length, weight, ws, path=None, n_path=None,
+                     first=False, rows=None, scale=None, stream=None) -> None:
+    """The attention weight that each position received from the kept queries (nodes
+    path[b,:n_path] of q [B,T,q_heads,head_dim] and lse [B,T,q_heads], at positions length ..)
+    in layer `layer`, added to weight float32 [rows, cols*page_size]; first: the kept
+    queries' own positions are set."""
+    _check(_native.cache_weigh(q, lse, cache, layer, length, weight, ws, path, n_path, first, rows,
+                               scale, stream))

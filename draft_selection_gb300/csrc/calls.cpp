@@ -264,6 +264,13 @@ PyObject* tree_verify(PyObject* const* a) {
   });
 }
 
+double scale_of(PyObject* o, const dfl2_cache* c) {
+  if (o == Py_None) return std::pow(static_cast<double>(c->head_dim), -0.5);
+  const double scale = PyFloat_AsDouble(o);
+  if (scale == -1. && PyErr_Occurred()) throw Raised();
+  return scale;
+}
+
 // q, cache, layer, length, mask, out, ws, rows, count, lse, scale, stream; win: then depth,
 // sinks, window
 PyObject* attn(PyObject* const* a, bool win) {
@@ -285,11 +292,7 @@ PyObject* attn(PyObject* const* a, bool win) {
       REFUSE(PyExc_ValueError, "lse must be contiguous float32 [B, T, q_heads]");
     lse = static_cast<float*>(t.data_ptr());
   }
-  double scale = std::pow(static_cast<double>(c->head_dim), -0.5);
-  if (a[10] != Py_None) {
-    scale = PyFloat_AsDouble(a[10]);
-    if (scale == -1. && PyErr_Occurred()) throw Raised();
-  }
+  const double scale = scale_of(a[10], c);
   const int layer = whole(a[2], "layer");
   const int32_t *length = i32(a[3], "length", {B}),
                 *mask = i32(a[4], "mask", {B, T, (T + 31ll) / 32}),
@@ -311,6 +314,34 @@ PyObject* attn(PyObject* const* a, bool win) {
 }
 PyObject* tree_attn(PyObject* const* a) { return attn(a, false); }
 PyObject* window_attn(PyObject* const* a) { return attn(a, true); }
+
+PyObject* cache_weigh(PyObject* const* a) {
+  // q, lse, cache, layer, length, weight, ws, path, n_path, first, rows, scale, stream
+  const dfl2_cache* c = cache_of(a[2]);
+  const at::Tensor &q = tensor(a[0], "q", 4), &ws = tensor(a[6], "ws");
+  if (q.scalar_type() != type_of(c))
+    REFUSE(PyExc_ValueError, "q must be [B, T, q_heads, head_dim] of the cache's type");
+  if (q.size(3) != c->head_dim || q.stride(3) != 1)
+    REFUSE(PyExc_ValueError, "q must have the cache's head_dim (%d, not %lld), stride 1",
+           (int)c->head_dim, (long long)q.size(3));
+  const int B = size(q, 0, "q"), T = size(q, 1, "q"), H = size(q, 2, "q");
+  const int64_t qs[3] = {q.stride(0), q.stride(1), q.stride(2)};
+  const float* lse = f32(a[1], "lse", {B, T, H});
+  float* weight = f32(a[5], "weight", {c->rows, int64_t(c->cols) * c->page_size});
+  const double scale = scale_of(a[11], c);
+  const int layer = whole(a[3], "layer"), first = PyObject_IsTrue(a[9]);
+  if (first < 0) throw Raised();
+  const int32_t *length = i32(a[4], "length", {B}), *path = i32(a[7], "path", {B, T}),
+                *n_path = i32(a[8], "n_path", {B}), *rows = i32(a[10], "rows", {B});
+  const void* qp = q.data_ptr();
+  void* wp = ws.data_ptr();
+  const size_t bytes = ws.nbytes();
+  const dfl2_stream s = stream_of(a[12]);
+  return run([&] {
+    return dfl2_cache_weigh(qp, qs, lse, c, layer, B, T, H, rows, length, path, n_path,
+                            static_cast<float>(scale), first, weight, wp, bytes, s);
+  });
+}
 
 // A function of N positional arguments; no C++ exception leaves it.
 template <PyObject* (*F)(PyObject* const*), int N>
@@ -342,6 +373,7 @@ PyMethodDef methods[] = {method<cache_reserve, 6>("cache_reserve"),
                          method<tree_verify, 12>("tree_verify"),
                          method<tree_attn, 12>("tree_attn"),
                          method<window_attn, 15>("window_attn"),
+                         method<cache_weigh, 13>("cache_weigh"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,
                       nullptr,               nullptr,  nullptr, nullptr};

@@ -12,6 +12,26 @@
   } while (0)
 
 namespace dfl2 {
+
+dfl2_status check_attn_shapes(int B, int T, int q_heads, int kv_heads, int head_dim, int dtype) {
+  if (B < 1 || T < 1 || q_heads < 1 || kv_heads < 1)
+    return report_errorf(DFL2_ERR_INVALID_ARG, "B=%d, T=%d, q_heads=%d, kv_heads=%d must be >= 1",
+                         B, T, q_heads, kv_heads);
+  if (q_heads % kv_heads)
+    return report_errorf(DFL2_ERR_INVALID_ARG, "q_heads=%d is no multiple of kv_heads=%d", q_heads,
+                         kv_heads);
+  if (B > kMaxBatch || T > kMaxTree || q_heads / kv_heads > kLanes)
+    return report_errorf(DFL2_ERR_UNSUPPORTED,
+                         "B=%d, T=%d, q_heads/kv_heads=%d: at most %d, %d, %d", B, T,
+                         q_heads / kv_heads, kMaxBatch, kMaxTree, kLanes);
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return report_errorf(DFL2_ERR_UNSUPPORTED, "head_dim=%d: 64, 128 or 256", head_dim);
+  if (dtype != DFL2_BF16 && dtype != DFL2_F16)
+    return report_errorf(DFL2_ERR_UNSUPPORTED, "dtype %d: the attention takes bf16 and fp16",
+                         dtype);
+  return DFL2_OK;
+}
+
 namespace {
 
 // ---- plan ---------------------------------------------------------------------
@@ -41,25 +61,6 @@ AttnPlan attn_plan(int T, int G, int D, int sms) {
   return p;
 }
 
-dfl2_status check_shapes(int B, int T, int q_heads, int kv_heads, int head_dim, int dtype) {
-  if (B < 1 || T < 1 || q_heads < 1 || kv_heads < 1)
-    return report_errorf(DFL2_ERR_INVALID_ARG, "B=%d, T=%d, q_heads=%d, kv_heads=%d must be >= 1",
-                         B, T, q_heads, kv_heads);
-  if (q_heads % kv_heads)
-    return report_errorf(DFL2_ERR_INVALID_ARG, "q_heads=%d is no multiple of kv_heads=%d", q_heads,
-                         kv_heads);
-  if (B > kMaxBatch || T > kMaxTree || q_heads / kv_heads > kLanes)
-    return report_errorf(DFL2_ERR_UNSUPPORTED,
-                         "B=%d, T=%d, q_heads/kv_heads=%d: at most %d, %d, %d", B, T,
-                         q_heads / kv_heads, kMaxBatch, kMaxTree, kLanes);
-  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
-    return report_errorf(DFL2_ERR_UNSUPPORTED, "head_dim=%d: 64, 128 or 256", head_dim);
-  if (dtype != DFL2_BF16 && dtype != DFL2_F16)
-    return report_errorf(DFL2_ERR_UNSUPPORTED, "dtype %d: the attention takes bf16 and fp16",
-                         dtype);
-  return DFL2_OK;
-}
-
 // Both entry points; `windowed`: with sinks, window and depth.
 dfl2_status attend(const void* q, const int64_t* q_strides, const dfl2_cache* cache, int layer,
                    int B, int T, int q_heads, const int32_t* table_rows, const int32_t* length,
@@ -71,7 +72,7 @@ dfl2_status attend(const void* q, const int64_t* q_strides, const dfl2_cache* ca
                                {mask, "mask", 4, true}, {out, "out", 16}, {lse, "lse", 4, true},
                           {depth, "depth", 4, true}};
   DFL2_TRY(check_cache_host(cache));
-  DFL2_TRY(check_shapes(B, T, q_heads, cache->kv_heads, cache->head_dim, cache->dtype));
+  DFL2_TRY(check_attn_shapes(B, T, q_heads, cache->kv_heads, cache->head_dim, cache->dtype));
   DFL2_TRY(check_args_host(ptrs, 8));
   if (layer < 0 || layer >= cache->layers)
     return report_errorf(DFL2_ERR_INVALID_ARG, "layer %d of %d", layer, cache->layers);
@@ -164,7 +165,7 @@ extern "C" {
 
 size_t dfl2_tree_attn_workspace_size(int B, int T, int q_heads, int kv_heads, int head_dim,
                                      dfl2_dtype dtype) {
-  if (dfl2::check_shapes(B, T, q_heads, kv_heads, head_dim, dtype) != DFL2_OK) return 0;
+  if (dfl2::check_attn_shapes(B, T, q_heads, kv_heads, head_dim, dtype) != DFL2_OK) return 0;
   if (dfl2::check_args_device(nullptr, 0) != DFL2_OK) return 0;
   return dfl2::attn_plan(T, q_heads / kv_heads, head_dim, dfl2::device_info().sms).ws_bytes;
 }

@@ -58,6 +58,8 @@ struct AttnArgs {
   int sinks, window;
   const int32_t* depth;  // [B][T] a node's own position behind the length, or NULL: its number
 };
+// What the attention's entry points and dfl2_cache_weigh take.
+dfl2_status check_attn_shapes(int B, int T, int q_heads, int kv_heads, int head_dim, int dtype);
 cudaError_t launch_window_attn(const AttnArgs& a, const dfl2_cache* c, cudaStream_t s);
 
 namespace {

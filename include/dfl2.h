@@ -585,6 +585,34 @@ dfl2_status dfl2_window_attn(const void* q, const int64_t* q_strides, const dfl2
                              const int64_t* out_strides, float* lse, void* ws, size_t ws_bytes,
                              dfl2_stream stream);
 
+/* What each position received of the attention of the tokens that a turn kept, added to its
+ * weight (for dfl2_cache_evict): called for a layer after acceptance and compaction, with
+ * the q and lse of that layer's attention call.
+ *   weight[r,j] += sum over i, h of exp(scale <q[b,path[b,i],h], K[b,j]> - lse[b,path[b,i],h])
+ * for the kept queries i = 0 .. n_path-1, which stand at positions length + i now, over the
+ * positions j <= length + i that each sees; r is the sequence's table row.
+ *   q           as for dfl2_tree_attn (strides: non-negative multiples of 8).
+ *   lse         float32 [B,T,q_heads], as that call left it; a query and head whose lse is
+ *               not finite adds nothing.
+ *   length      int32 [B]: committed positions before this turn's.
+ *   path        int32 [B,T]: node numbers (dfl2_tree_accept's); NULL: 0, 1, ..  One out of
+ *               0 .. T-1 is recorded and left out.  n_path int32 [B], taken to 0 .. T;
+ *               NULL: T.  So a prompt's chunk, or a token, needs neither.
+ *   weight      float32 [rows, cols*page_size] (rows and cols: the table's).
+ *   first       non-zero: the weights of positions length .. length+n_path-1 are set instead
+ *               (the first layer's call of a turn).
+ * A position without a page is recorded, and its weight left as it was; a sequence whose
+ * positions its table row cannot hold is recorded and left out.
+ * Shapes and types as for dfl2_tree_attn.  ws: dfl2_cache_weigh_workspace_size bytes of scratch
+ * (not zero-filled, and not shared with an entry point whose workspace holds counters).
+ * Each weight is a sum in a fixed order: the same call gives the same bits. */
+size_t dfl2_cache_weigh_workspace_size(void);
+dfl2_status dfl2_cache_weigh(const void* q, const int64_t* q_strides, const float* lse,
+                             const dfl2_cache* cache, int layer, int B, int T, int q_heads,
+                             const int32_t* table_rows, const int32_t* length, const int32_t* path,
+                             const int32_t* n_path, float scale, int first, float* weight, void* ws,
+                             size_t ws_bytes, dfl2_stream stream);
+
 #ifdef __cplusplus
 }
 #endif
