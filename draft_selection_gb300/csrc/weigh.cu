@@ -6,17 +6,22 @@
 // other way round, S^T = K Q^T, 128 keys by the (query, head) columns, so that a key is a
 // lane of TMEM, and a thread adds up its key's columns.
 //
-// Split.  A step is 128 keys of one key head against up to NC columns; the steps of all
-// sequences (lengths are on the device) are cut into equal, contiguous ranges, one a CTA.
-// A tile of keys whose steps (all heads, all columns) lie in one range is added to the
-// weights by it; of one that several ranges share each leaves its part in the workspace,
-// and weigh_add_kernel adds the parts in order.  So the result does not depend on timing.
+// Split.  A step is a group of up to kt tiles of 128 keys of one key head against up to
+// kCols columns; the steps of all sequences (lengths are on the device) are cut into equal,
+// contiguous ranges, one a CTA.  A group whose steps (all heads, all columns) lie in one range
+// is added to the weights by it; of one that several ranges share each leaves its part in
+// the workspace, and weigh_add_kernel adds the parts in order.  So the result does not depend
+// on timing.  A group's tiles stay in shared memory while all columns pass by: an SM takes in
+// about 26 bytes a cycle from L2, and with the 32 KB of 128 columns (128 channels) brought
+// again for every 128 keys the gather of Q bounded everything (2700 cycles a tile).  kt is the
+// largest of 4, 2 and 1 that leaves every CTA eight steps.
 //
 // Roles: warp 0 loads K (TMA boxes of one page, 128-byte swizzle); warp 1 issues the MMAs; four
 // warps gather the columns' rows of Q, which path may order anyhow, with 16-byte cp.async; and
-// two groups of four take turns with the two accumulators.
+// two groups of four warps add up the even and the odd tiles of a group.  Four accumulators
+// take turns, so MMAs, exponentials and gather overlap.
 //
-// Bounds.  A step reads 32 KB of K (128 channels): 1400 cycles of an SM's share of HBM.  With
+// Bounds.  A tile of K is 32 KB (128 channels): 1400 cycles of an SM's share of HBM.  With
 // 128 columns its MMAs take 512 cycles, and its 16,384 exponentials as many.  So HBM bounds
 // up to some 300 columns a key head, and beyond that the tensor cores and the exponentials.
 #include "tree_attn_kernel.cuh"
@@ -26,9 +31,12 @@ namespace {
 
 constexpr int kTile = 128;   // keys of a tile: lanes of TMEM
 constexpr int kInfos = 4;    // steps whose columns' numbers are held
+constexpr int kAccs = 4;     // accumulators
+constexpr int kMaxGroup = 4; // tiles of a group
 
-struct alignas(16) WeighCut {  // a tile that range c0 begins and c1 ends; b < 0: none
-  int b, tile, c0, c1;
+struct alignas(16) WeighCut {  // a group that range c0 begins and c1 ends; b < 0: none
+  int b, group, c0, c1;
+  int kt;
 };
 
 struct WeighArgs {
@@ -41,7 +49,7 @@ struct WeighArgs {
   int first;
   int B, H, G;
   float scale_log2;
-  float* parts;        // [grid][2][kTile]
+  float* parts;        // [grid][2][kMaxGroup][kTile]
   WeighCut* cuts;      // [grid]
   int grid;
 };
@@ -50,19 +58,21 @@ template <int D>
 struct WeighCfg {
   static constexpr int kCols = D == 256 ? 64 : 128;  // columns of a step
   static constexpr int kSlotK = kTile * D * 2, kSlotQ = kCols * D * 2;
-  static constexpr int kSlotsK = D == 64 ? 6 : D == 128 ? 3 : 2;
-  static constexpr int kSlotsQ = D == 64 ? 4 : D == 128 ? 3 : 2;
-  static constexpr int kBars = 2 * (kSlotsK + kSlotsQ + kInfos + 2 + 2) + 1;
+  static constexpr int kSlotsK = D == 64 ? 8 : D == 128 ? 4 : 2;
+  static constexpr int kSlotsQ = D == 64 ? 4 : 2;
+  static constexpr int kGroup = kSlotsK < kMaxGroup ? kSlotsK : kMaxGroup;  // most tiles of a group
+  static constexpr int kBars = 2 * (kSlotsK + kSlotsQ + kInfos + kAccs) + 1;
   static constexpr int kThreads = 14 * 32;
   static constexpr size_t kSmem = size_t(kSlotsK) * kSlotK + size_t(kSlotsQ) * kSlotQ +
-                                  kInfos * kCols * 8 + 2 * kTile * 4 + kBars * 8 + 8;
+                                  kInfos * kCols * 8 + kCols * 8 + kBars * 8 + 8;
   static_assert(kSmem + 1024 <= 232448, "shared memory");
 };
 
 struct WSeq {
   int row, len, n, tiles, chunks;
-  __device__ __forceinline__ int64_t steps(int H) const {
-    return static_cast<int64_t>(tiles) * H * chunks;
+  __device__ __forceinline__ int groups(int kt) const { return (tiles + kt - 1) / kt; }
+  __device__ __forceinline__ int64_t steps(int H, int kt) const {
+    return static_cast<int64_t>(groups(kt)) * H * chunks;
   }
 };
 template <int kCols>
@@ -71,13 +81,9 @@ __device__ __forceinline__ WSeq load_wseq(const WeighArgs& a, int b) {
   s.len = a.t.length[b];
   s.n = a.t.count_of(b);
   s.row = a.t.seq ? a.t.seq[b] : b;
-  // (and the weights of a row hold no more than its entries' positions)
-  if (!a.t.in_range(s.row, s.len)) {
-    record_error(a.t.err, kDevErrBadIndex);
-    s.n = 0;
-  }
   const int64_t room = static_cast<int64_t>(a.t.cols) << a.t.page_shift;
-  if (s.n > 0 && s.len + s.n > room) {  // positions that can have no page
+  // (the weights of a row hold no more than its entries' positions)
+  if (!a.t.in_range(s.row, s.len) || (s.n > 0 && s.len + s.n > room)) {
     record_error(a.t.err, kDevErrBadIndex);
     s.n = 0;
   }
@@ -88,53 +94,52 @@ __device__ __forceinline__ WSeq load_wseq(const WeighArgs& a, int b) {
 
 template <int kCols>
 struct WCursor {
-  int b, tile, h, chunk;
+  int b, group, h, chunk;
   WSeq s;
-  __device__ __forceinline__ void next(const WeighArgs& a) {
+  __device__ __forceinline__ void next(const WeighArgs& a, int kt) {
     if (++chunk < s.chunks) return;
     chunk = 0;
     if (++h < a.H) return;
     h = 0;
-    if (++tile < s.tiles) return;
-    tile = 0;
+    if (++group < s.groups(kt)) return;
+    group = 0;
     do {
       if (++b >= a.B) return;
       s = load_wseq<kCols>(a, b);
     } while (s.tiles == 0);
   }
+  // Tiles of this group.
+  __device__ __forceinline__ int here(int kt) const { return min(kt, s.tiles - group * kt); }
 };
 
 // Range `cta` [u0, u1) of the steps, and where it begins, by a warp.
 template <int kCols>
 struct WRange {
   int64_t units, u0, u1;
-  int n_cta;
+  int n_cta, kt;
   WCursor<kCols> first;  // if u0 < u1
 };
-template <int kCols>
+template <int kCols, int kGroup>
 __device__ __forceinline__ WRange<kCols> find_wrange(const WeighArgs& a, int cta) {
   const int lane = threadIdx.x & 31;
   WRange<kCols> g;
-  WSeq own;
-  int64_t sum;
-  auto load = [&](int b0) {
-    own = b0 + lane < a.B ? load_wseq<kCols>(a, b0 + lane) : WSeq{0, 0, 0, 0, 0};
-    sum = own.steps(a.H);
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t y = __shfl_up_sync(kAll, sum, off);
-      if (lane >= off) sum += y;
-    }
-  };
-  load(0);
-  g.units = __shfl_sync(kAll, sum, 31);
-  if (a.B > 32) {
-    int64_t x = 0;
-    for (int b = lane + 32; b < a.B; b += 32) x += load_wseq<kCols>(a, b).steps(a.H);
-#pragma unroll
-    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(kAll, x, off);
-    g.units += x;
+  // each lane's sequences' steps for groups of 4, 2 and 1
+  WSeq own = lane < a.B ? load_wseq<kCols>(a, lane) : WSeq{0, 0, 0, 0, 0};
+  int64_t x[3] = {own.steps(a.H, 4), own.steps(a.H, 2), own.steps(a.H, 1)};
+  for (int b = lane + 32; b < a.B; b += 32) {
+    const WSeq s = load_wseq<kCols>(a, b);
+    x[0] += s.steps(a.H, 4);
+    x[1] += s.steps(a.H, 2);
+    x[2] += s.steps(a.H, 1);
   }
+#pragma unroll
+  for (int off = 16; off; off >>= 1)
+#pragma unroll
+    for (int z = 0; z < 3; ++z) x[z] += __shfl_xor_sync(kAll, x[z], off);
+  const int64_t enough = 8ll * a.grid;
+  const int pick = kGroup >= 4 && x[0] >= enough ? 0 : x[1] >= enough ? 1 : 2;
+  g.kt = 4 >> pick;
+  g.units = x[pick];
   g.n_cta = static_cast<int>(min(static_cast<int64_t>(a.grid), g.units));
   g.u0 = g.u1 = 0;
   if (cta >= g.n_cta) return g;
@@ -142,11 +147,18 @@ __device__ __forceinline__ WRange<kCols> find_wrange(const WeighArgs& a, int cta
   g.u1 = range_start(g.units, g.n_cta, cta + 1);
   int64_t base = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    if (b0 > 0) load(b0);
+    if (b0 > 0) own = b0 + lane < a.B ? load_wseq<kCols>(a, b0 + lane) : WSeq{0, 0, 0, 0, 0};
+    const int64_t mine = own.steps(a.H, g.kt);
+    int64_t sum = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(kAll, sum, off);
+      if (lane >= off) sum += y;
+    }
     const unsigned hit = __ballot_sync(kAll, g.u0 < base + sum);
     if (hit) {
       const int w = __ffs(hit) - 1;
-      const int64_t in = g.u0 - base - __shfl_sync(kAll, sum - own.steps(a.H), w);
+      const int64_t in = g.u0 - base - __shfl_sync(kAll, sum - mine, w);
       WCursor<kCols>& c = g.first;
       c.b = b0 + w;
       c.s = WSeq{__shfl_sync(kAll, own.row, w), __shfl_sync(kAll, own.len, w),
@@ -154,8 +166,8 @@ __device__ __forceinline__ WRange<kCols> find_wrange(const WeighArgs& a, int cta
                  __shfl_sync(kAll, own.chunks, w)};
       const int64_t hc = in / c.s.chunks;
       c.chunk = static_cast<int>(in - hc * c.s.chunks);
-      c.tile = static_cast<int>(hc / a.H);
-      c.h = static_cast<int>(hc - static_cast<int64_t>(c.tile) * a.H);
+      c.group = static_cast<int>(hc / a.H);
+      c.h = static_cast<int>(hc - static_cast<int64_t>(c.group) * a.H);
       return g;
     }
     base += __shfl_sync(kAll, sum, 31);
@@ -179,20 +191,18 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ks = smem;                             // [slots][kBlk][128 keys][128 B]
   uint8_t* qs = ks + C::kSlotsK * C::kSlotK;      // [slots][kBlk][kCols][128 B]
-  float* lse_s = reinterpret_cast<float*>(qs + C::kSlotsQ * C::kSlotQ);  // [kInfos][kCols], negated
+  int64_t* from_s = reinterpret_cast<int64_t*>(qs + C::kSlotsQ * C::kSlotQ);  // [kCols] rows of Q
+  float* lse_s = reinterpret_cast<float*>(from_s + kCols);      // [kInfos][kCols], negated
   int* pos_s = reinterpret_cast<int*>(lse_s + kInfos * kCols);  // [kInfos][kCols]
-  float* acc_s = reinterpret_cast<float*>(pos_s + kInfos * kCols);  // [2][kTile]
-  uint64_t* k_full = reinterpret_cast<uint64_t*>(acc_s + 2 * kTile);
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(pos_s + kInfos * kCols);
   uint64_t* k_empty = k_full + C::kSlotsK;
   uint64_t* q_full = k_empty + C::kSlotsK;
   uint64_t* q_empty = q_full + C::kSlotsQ;
   uint64_t* i_full = q_empty + C::kSlotsQ;   // a step's columns are described
   uint64_t* i_empty = i_full + kInfos;
-  uint64_t* s_full = i_empty + kInfos;       // [2] scores are in TMEM
-  uint64_t* s_empty = s_full + 2;
-  uint64_t* acc_full = s_empty + 2;          // [2] the second group's sums are in place
-  uint64_t* acc_empty = acc_full + 2;
-  uint64_t* all_done = acc_empty + 2;
+  uint64_t* s_full = i_empty + kInfos;       // [kAccs] scores are in TMEM
+  uint64_t* s_empty = s_full + kAccs;
+  uint64_t* all_done = s_empty + kAccs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(all_done + 1);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -207,19 +217,17 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
     }
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(&i_full[i], 4);
-      mbar_init(&i_empty[i], 4);
+      mbar_init(&i_empty[i], 8);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kAccs; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], 4);
-      mbar_init(&acc_full[i], 4);
-      mbar_init(&acc_empty[i], 4);
     }
     mbar_init(all_done, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
   }
-  if (warp == 1) tmem_alloc(tmem_slot, 2 * kCols);
+  if (warp == 1) tmem_alloc(tmem_slot, kAccs * kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -227,7 +235,8 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  const WRange<kCols> g = find_wrange<kCols>(a, blockIdx.x);
+  const WRange<kCols> g = find_wrange<kCols, C::kGroup>(a, blockIdx.x);
+  const int kt = g.kt;
   WCursor<kCols> cur = g.first;
   int64_t N = g.u1 - g.u0;
   if (smem_u32(smem) & 1023u) {  // the swizzle counts on it
@@ -238,26 +247,29 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
   // A wait that ran out (ok false) is the last one of its warp: what follows is only counted.
   bool ok = true;
   if (warp == 0) {
-    // ---- K: a tile of a head at a time ----
+    // ---- K: the tiles of a group, a head at a time ----
     const int ps = 1 << a.t.page_shift, box = min(ps, kTile);
     const int boxes = kTile / box * kBlk;  // at most 64
-    int slot = 0, ph = 0, issued = 0, page[2] = {0, 0};
-    bool fresh = true;
+    int slot = 0, ph = 0, issued = 0;
     for (int64_t i = 0; i < N && ok;) {
       const WSeq s = cur.s;
-      if (fresh)
+      const int here = cur.here(kt);
+#pragma unroll 1
+      for (int t = 0; t < here && ok; ++t) {
+        const int tile = cur.group * kt + t;
+        int page[2];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {  // this lane's pages of the tile; one too far for none
-          const int x = lane + 32 * z, pos = cur.tile * kTile + x / kBlk * box;
+          const int x = lane + 32 * z, pos = tile * kTile + x / kBlk * box;
           page[z] = a.t.pages;
           if (x < boxes && pos < s.len + s.n) {
             const int p = a.t.page_at(s.row, pos >> a.t.page_shift);
             if (p >= 0) page[z] = p;
           }
         }
-      if (issued >= C::kSlotsK) ok = wait(&k_empty[slot], ph ^ 1, a.t.err);
-      ok = __all_sync(kAll, ok);
-      if (ok) {
+        if (issued >= C::kSlotsK) ok = wait(&k_empty[slot], ph ^ 1, a.t.err);
+        ok = __all_sync(kAll, ok);
+        if (!ok) break;
         if (lane == 0) mbar_arrive_expect_tx(&k_full[slot], C::kSlotK);
         __syncwarp();
 #pragma unroll
@@ -265,7 +277,7 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
           const int x = lane + 32 * z;
           if (x < boxes)
             tma_load_4d(ks + slot * C::kSlotK + x % kBlk * (kTile * 128) + x / kBlk * box * 128, &tmK,
-                        x % kBlk * 64, cur.tile * kTile & (ps - 1), cur.h, page[z], &k_full[slot]);
+                        x % kBlk * 64, tile * kTile & (ps - 1), cur.h, page[z], &k_full[slot]);
         }
         ++issued;
         if (++slot == C::kSlotsK) {
@@ -273,12 +285,9 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
           ph ^= 1;
         }
       }
-      const int tile = cur.tile, b = cur.b;
-      const int64_t here = min(N - i, static_cast<int64_t>(s.chunks - cur.chunk));
-      i += here;
-      cur.chunk = s.chunks - 1;  // (on to the next head's tile)
-      cur.next(a);
-      fresh = cur.tile != tile || cur.b != b;
+      i += min(N - i, static_cast<int64_t>(s.chunks - cur.chunk));
+      cur.chunk = s.chunks - 1;  // (on to the next head's tiles)
+      cur.next(a, kt);
     }
     // the copies still in flight land before the CTA ends
     for (int j = max(0, issued - C::kSlotsK); j < issued; ++j)
@@ -287,229 +296,255 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
     // ---- MMAs (the whole warp walks, one elected lane issues: descriptors stay uniform) ----
     const uint32_t tb = __shfl_sync(kAll, tmem, 0);
     const uint64_t ad = umma_desc_sw128(ks), bd = umma_desc_sw128(qs);
-    int k_slot = 0, k_ph = 0, q_slot = 0, q_ph = 0;
+    int k_slot = 0, k_ph = 0, q_slot = 0, q_ph = 0;  // (of a group's first tile)
+    uint32_t m = 0;                                  // MMAs so far
     for (int64_t i = 0; i < N && ok; ++i) {
-      const int buf = static_cast<int>(i & 1);
       const int cols = min(kCols, cur.s.n * a.G - cur.chunk * kCols);
-      if (i == 0 || cur.chunk == 0) ok = wait(&k_full[k_slot], k_ph, a.t.err);
-      ok = ok && wait(&q_full[q_slot], q_ph, a.t.err);
-      if (i > 1) ok = ok && wait(&s_empty[buf], ((i >> 1) - 1) & 1, a.t.err);
-      ok = __all_sync(kAll, ok);
-      if (!ok) break;
-      tc_fence_after();
+      const int here = cur.here(kt);
+      const bool fresh = i == 0 || cur.chunk == 0;
       const bool last = cur.chunk == cur.s.chunks - 1 || i == N - 1;
-      if (elect_one()) {
-        const uint32_t id = idesc_f16<E>(kTile, (cols + 15) & ~15, false);
-        const uint64_t ak = ad + k_slot * (C::kSlotK >> 4), bq = bd + q_slot * (C::kSlotQ >> 4);
+      const uint32_t id = idesc_f16<E>(kTile, (cols + 15) & ~15, false);
+      const uint64_t bq = bd + q_slot * (C::kSlotQ >> 4);
+      ok = wait(&q_full[q_slot], q_ph, a.t.err);
+      int slot = k_slot, ph = k_ph;
+#pragma unroll 1
+      for (int t = 0; t < here && ok; ++t, ++m) {
+        const uint32_t acc = m % kAccs;
+        if (fresh) ok = wait(&k_full[slot], ph, a.t.err);
+        if (m >= kAccs) ok = ok && wait(&s_empty[acc], (m / kAccs - 1) & 1, a.t.err);
+        ok = __all_sync(kAll, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t ak = ad + slot * (C::kSlotK >> 4);
 #pragma unroll
-        for (int kb = 0; kb < kBlk; ++kb)
+          for (int kb = 0; kb < kBlk; ++kb)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_bf16(tb + buf * kCols, ak + kb * (kTile * 128 >> 4) + 2 * k,
-                      bq + kb * (kCols * 128 >> 4) + 2 * k, id, kb > 0 || k > 0);
-        umma_commit(&s_full[buf]);
-        umma_commit(&q_empty[q_slot]);
-        if (last) umma_commit(&k_empty[k_slot]);
+            for (int k = 0; k < 4; ++k)
+              umma_bf16(tb + acc * kCols, ak + kb * (kTile * 128 >> 4) + 2 * k,
+                        bq + kb * (kCols * 128 >> 4) + 2 * k, id, kb > 0 || k > 0);
+          umma_commit(&s_full[acc]);
+          if (t == here - 1) umma_commit(&q_empty[q_slot]);
+          if (last) umma_commit(&k_empty[slot]);
+        }
+        __syncwarp();
+        if (++slot == C::kSlotsK) {
+          slot = 0;
+          ph ^= 1;
+        }
       }
-      __syncwarp();
+      if (last) {
+        k_slot = slot;
+        k_ph = ph;
+      }
       if (++q_slot == C::kSlotsQ) {
         q_slot = 0;
         q_ph ^= 1;
       }
-      if (last && ++k_slot == C::kSlotsK) {
-        k_slot = 0;
-        k_ph ^= 1;
-      }
-      cur.next(a);
+      cur.next(a, kt);
     }
     if (elect_one()) umma_commit(all_done);  // every MMA complete before TMEM is freed
     mbar_wait(all_done, 0, a.t.err);
     __syncwarp();
   } else if (warp < 6) {
     // ---- Q: a warp a quarter of the columns, a lane to a column's numbers ----
+    // A step's numbers are looked up a step before its rows are asked for, and its rows are
+    // waited for kLag steps after that (fewer than there are slots).
+    constexpr int kLag = C::kSlotsQ > 2 ? 2 : 1;
     const int w = warp - 2;
-    constexpr int kMine = kCols / 4, kPieces = D / 8;  // columns of a warp, 16-byte pieces
-    int slot = 0, ph = 0, before = 0;
-    int64_t i = 0;
-    for (; i < N && ok; ++i) {
-      const WSeq s = cur.s;
-      const int info = static_cast<int>(i & (kInfos - 1));
-      const int col = cur.chunk * kCols + w * kMine + lane;  // (of kMine lanes)
-      int64_t from = -1;
-      float l = 0.f;
-      int pos = INT32_MIN;  // seen by no key
-      if (lane < kMine && col < s.n * a.G) {
-        const int x = col / a.G, head = cur.h * a.G + col - x * a.G;
-        const int node = a.path ? a.path[static_cast<int64_t>(cur.b) * a.t.T + x] : x;
+    constexpr int kMine = kCols / 4;       // columns of a warp
+    constexpr int kPieces = D / 8;         // 16-byte pieces of a row
+    constexpr int kAtOnce = 32 / kPieces;  // columns that a warp's lanes copy a piece each of
+    struct Column {
+      int64_t from;  // of q; -1: none
+      float l;
+      int pos;  // of the positions behind the length, the last one that it sees
+    };
+    auto look = [&](const WCursor<kCols>& c) {
+      Column x{-1, 0.f, INT32_MIN};
+      const int col = c.chunk * kCols + w * kMine + lane;
+      if (lane < kMine && col < c.s.n * a.G) {
+        const int i = col / a.G, head = c.h * a.G + col - i * a.G;
+        const int node = a.path ? a.path[static_cast<int64_t>(c.b) * a.t.T + i] : i;
         if (static_cast<unsigned>(node) < static_cast<unsigned>(a.t.T)) {
-          l = a.lse[(static_cast<int64_t>(cur.b) * a.t.T + node) * (a.H * a.G) + head];
-          if (isfinite(l)) pos = x;
-          from = cur.b * a.qb + node * a.qt + head * a.qh;
+          x.l = a.lse[(static_cast<int64_t>(c.b) * a.t.T + node) * (a.H * a.G) + head];
+          x.pos = i;
+          x.from = c.b * a.qb + node * a.qt + head * a.qh;
         } else {
           record_error(a.t.err, kDevErrBadIndex);
         }
       }
+      return x;
+    };
+    int64_t* from = from_s + w * kMine;
+    const int piece = lane % kPieces, c0 = lane / kPieces;  // this lane's, of kAtOnce columns
+    // a row's piece p lies at p ^ (row % 8) of its 128 bytes; 8 rows are 1024 bytes
+    const int dst0 = (piece >> 3) * (kCols * 128) + w * kMine * 128;
+    int slot = 0, ph = 0, before[2] = {0, 0};  // the slots of the steps before
+    int64_t i = 0;
+    Column next{};
+    if (N > 0) next = look(cur);
+    for (; i < N; ++i) {
+      const Column x = next;
+      const int mine = min(kMine, cur.s.n * a.G - cur.chunk * kCols - w * kMine);
+      if (i + 1 < N) {
+        cur.next(a, kt);
+        next = look(cur);
+      }
+      const int info = static_cast<int>(i & (kInfos - 1));
       if (i >= kInfos) ok = wait(&i_empty[info], ((i / kInfos) - 1) & 1, a.t.err);
       if (i >= C::kSlotsQ) ok = ok && wait(&q_empty[slot], ph ^ 1, a.t.err);
       ok = __all_sync(kAll, ok);
       if (!ok) break;
       if (lane < kMine) {
-        lse_s[info * kCols + w * kMine + lane] = -l * kLog2e;
-        pos_s[info * kCols + w * kMine + lane] = pos;
+        lse_s[info * kCols + w * kMine + lane] = -x.l * kLog2e;
+        pos_s[info * kCols + w * kMine + lane] = isfinite(x.l) ? x.pos : INT32_MIN;
+        from[lane] = x.from;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&i_full[info]);
-      // 32 / kPieces columns at a time
-      uint8_t* dst = qs + slot * C::kSlotQ;
-      const int mine = min(kMine, s.n * a.G - cur.chunk * kCols - w * kMine);
+      uint8_t* dst = qs + slot * C::kSlotQ + dst0;
 #pragma unroll 4
-      for (int z = 0; z < mine * kPieces; z += 32) {
-        const int c = (z + lane) / kPieces, p = (z + lane) % kPieces, at = w * kMine + c;
-        const int64_t f = __shfl_sync(kAll, from, c & 31);
-        if (c < mine)
-          cp_async16(dst + (p >> 3) * (kCols * 128) + at * 128 + (((p & 7) ^ (at & 7)) << 4),
-                     static_cast<const E*>(a.q) + (f < 0 ? 0 : f) + p * 8, f >= 0);
+      for (int c = c0; c < mine; c += kAtOnce) {
+        const int64_t f = from[c];
+        cp_async16(dst + c * 128 + (((piece & 7) ^ (c & 7)) << 4),
+                   static_cast<const E*>(a.q) + (f < 0 ? 0 : f) + piece * 8, f >= 0);
       }
       cp_async_commit();
-      if (i > 0) {
-        cp_async_wait<1>();
+      __syncwarp();  // (the next step's numbers replace these)
+      if (i >= kLag) {
+        cp_async_wait<kLag>();
         fence_proxy_async_smem();
-        mbar_arrive(&q_full[before]);
+        mbar_arrive(&q_full[before[kLag - 1]]);
       }
-      before = slot;
+      before[1] = before[0];
+      before[0] = slot;
       if (++slot == C::kSlotsQ) {
         slot = 0;
         ph ^= 1;
       }
-      cur.next(a);
     }
     cp_async_wait<0>();
     fence_proxy_async_smem();
-    if (i > 0) mbar_arrive(&q_full[before]);
+    if (kLag > 1 && i > 1) mbar_arrive(&q_full[before[1]]);
+    if (i > 0) mbar_arrive(&q_full[before[0]]);
   } else {
-    // ---- sums: a thread to a key, two groups by turns ----
-    const int group = (warp - 6) >> 2, quarter = warp & 3, key = quarter * 32 + lane;
-    const uint32_t tbase =
-        tmem + group * kCols + (static_cast<uint32_t>(quarter * 32) << 16);
+    // ---- sums: a thread to a key of every second tile ----
+    const int odd = (warp - 6) >> 2, quarter = warp & 3, key = quarter * 32 + lane;
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint64_t sl2 = pack_f32x2(a.scale_log2, a.scale_log2);
-    if (group == 0 && key == 0) a.cuts[blockIdx.x].b = -1;
-    int seg = 0;
-    for (int64_t i = 0; i < N && ok; ++seg) {
-      // this CTA's steps of a tile
+    if (odd == 0 && key == 0) a.cuts[blockIdx.x].b = -1;
+    uint32_t m = 0;  // MMAs before this step's
+    for (int64_t i = 0; i < N && ok;) {
+      // this CTA's steps of a group
       const WSeq s = cur.s;
-      const int b = cur.b, tile = cur.tile;
+      const int here = cur.here(kt), tile0 = cur.group * kt;
       const int per = a.H * s.chunks, at0 = cur.h * s.chunks + cur.chunk;
       const int64_t i1 = min(N, i + per - at0);
-      const int64_t v0 = g.u0 + i - at0;  // the tile's first step
-      const int rel = tile * kTile + key - s.len;  // < 0: committed
-      const bool plain = (tile + 1) * kTile <= s.len;
-      uint64_t sum[2] = {0, 0};
-      float more = 0.f;
+      const int64_t v0 = g.u0 + i - at0;  // the group's first step
       int chunk = cur.chunk;
-      for (; i < i1; ++i) {
-        if ((i & 1) == group && ok) {
-          const int info = static_cast<int>(i & (kInfos - 1));
-          const int cols = min(kCols, s.n * a.G - chunk * kCols);
-          ok = wait(&i_full[info], (i / kInfos) & 1, a.t.err) &&
-               wait(&s_full[group], (i >> 1) & 1, a.t.err);
+      float all[2] = {0.f, 0.f};  // of tiles `odd` and odd + 2
+      for (; i < i1; ++i, m += here) {
+        const int info = static_cast<int>(i & (kInfos - 1));
+        const int cols = min(kCols, s.n * a.G - chunk * kCols);
+        const float* l = lse_s + info * kCols;
+        const int* p = pos_s + info * kCols;
+        if (ok) ok = wait(&i_full[info], (i / kInfos) & 1, a.t.err);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const int t = odd + 2 * z;
+          if (t >= here) break;
+          const uint32_t acc = (m + t) % kAccs;
+          if (ok) ok = wait(&s_full[acc], (m + t) / kAccs & 1, a.t.err);
           ok = __all_sync(kAll, ok);
-          if (ok) {
-            tc_fence_after();
-            const float* l = lse_s + info * kCols;
-            const int* p = pos_s + info * kCols;
+          if (!ok) break;
+          tc_fence_after();
+          const int rel = (tile0 + t) * kTile + key - s.len;  // < 0: committed
+          const bool plain = (tile0 + t + 1) * kTile <= s.len;
+          uint64_t sum[2] = {0, 0};
+          float more = 0.f;
 #pragma unroll 1
-            for (int c = 0; c < cols; c += 32) {
-              uint32_t x[32];
-              tmem_ld32_issue(tbase + c, x);
-              // (a column that is left out, or past the last, is seen by no key)
-              const bool whole = plain && __all_sync(kAll, p[c + lane] >= 0);
-              tmem_ld32_wait(x);
-              if (whole) {
+          for (int c = 0; c < cols; c += 32) {
+            uint32_t x[32];
+            tmem_ld32_issue(tbase + acc * kCols + c, x);
+            // (a column that is left out, or past the last, is seen by no key)
+            const bool whole = plain && __all_sync(kAll, p[c + lane] >= 0);
+            tmem_ld32_wait(x);
+            if (whole) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                  const float4 y = *reinterpret_cast<const float4*>(l + c + j);
-                  float e0, e1, e2, e3;
-                  unpack_f32x2(fma_f32x2(pack_u32x2(x[j], x[j + 1]), sl2, pack_f32x2(y.x, y.y)), e0,
-                               e1);
-                  unpack_f32x2(fma_f32x2(pack_u32x2(x[j + 2], x[j + 3]), sl2, pack_f32x2(y.z, y.w)),
-                               e2, e3);
-                  sum[0] = add_f32x2(sum[0], pack_f32x2(ex2(e0), ex2(e1)));
-                  sum[1] = add_f32x2(sum[1], pack_f32x2(ex2(e2), ex2(e3)));
-                }
-              } else {
+              for (int j = 0; j < 32; j += 4) {
+                const float4 y = *reinterpret_cast<const float4*>(l + c + j);
+                float e0, e1, e2, e3;
+                unpack_f32x2(fma_f32x2(pack_u32x2(x[j], x[j + 1]), sl2, pack_f32x2(y.x, y.y)), e0, e1);
+                unpack_f32x2(fma_f32x2(pack_u32x2(x[j + 2], x[j + 3]), sl2, pack_f32x2(y.z, y.w)), e2,
+                             e3);
+                sum[0] = add_f32x2(sum[0], pack_f32x2(ex2(e0), ex2(e1)));
+                sum[1] = add_f32x2(sum[1], pack_f32x2(ex2(e2), ex2(e3)));
+              }
+            } else {
+              const int left = min(32, cols - c);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                  const float e = ex2(fmaf(__uint_as_float(x[j]), a.scale_log2, l[c + j]));
-                  if (rel <= p[c + j]) more += e;
-                }
+              for (int j = 0; j < 32; ++j) {
+                if (j >= left) break;
+                const float e = ex2(fmaf(__uint_as_float(x[j]), a.scale_log2, l[c + j]));
+                if (rel <= p[c + j]) more += e;
               }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&s_empty[group]);
-              mbar_arrive(&i_empty[info]);
-            }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_empty[acc]);
+          float s0, s1;
+          unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
+          all[z] += (s0 + s1) + more;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&i_empty[info]);
         if (++chunk == s.chunks) chunk = 0;
       }
-      // ---- the end of this CTA's part of the tile ----
-      float s0, s1;
-      unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
-      float all = (s0 + s1) + more;
-      const int half = seg & 1;
-      if (group == 1) {
-        if (seg > 1 && ok) ok = wait(&acc_empty[half], ((seg >> 1) - 1) & 1, a.t.err);
-        ok = __all_sync(kAll, ok);
-        if (ok) {
-          acc_s[half * kTile + key] = all;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_full[half]);
-        }
-      } else {
-        if (ok) ok = wait(&acc_full[half], (seg >> 1) & 1, a.t.err);
-        ok = __all_sync(kAll, ok);
-        if (ok) {
-          all += acc_s[half * kTile + key];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[half]);
-          const bool begins = at0 == 0, ends = g.u0 + i == v0 + per;
-          if (begins && ends) {
-            put(a, s, tile * kTile + key, all);
-          } else {
-            a.parts[(static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * kTile + key] = all;
-            if (begins && key == 0)
-              a.cuts[blockIdx.x] = WeighCut{b, tile, static_cast<int>(blockIdx.x),
-                                            range_of(g.units, g.n_cta, v0 + per - 1)};
-          }
-        }
+      // ---- the end of this CTA's part of the group ----
+      const bool begins = at0 == 0, ends = g.u0 + i == v0 + per;
+      float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) *
+                                  (kMaxGroup * kTile);
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int t = odd + 2 * z;
+        if (t >= here || !ok) break;
+        if (begins && ends)
+          put(a, s, (tile0 + t) * kTile + key, all[z]);
+        else
+          part[t * kTile + key] = all[z];
       }
-      cur.h = a.H - 1;  // on to the next tile
+      if (begins && !ends && odd == 0 && key == 0)
+        a.cuts[blockIdx.x] = WeighCut{cur.b, cur.group, static_cast<int>(blockIdx.x),
+                                      range_of(g.units, g.n_cta, v0 + per - 1), kt};
+      cur.h = a.H - 1;  // on to the next group
       cur.chunk = s.chunks - 1;
-      cur.next(a);
+      cur.next(a, kt);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 2 * kCols);
+  if (warp == 1) tmem_dealloc(tmem, kAccs * kCols);
 }
 
-// The parts of the tiles that several ranges share, in order.
+// The parts of the groups that several ranges share, in order.
 template <int kCols>
-__global__ void __launch_bounds__(kTile) weigh_add_kernel(const __grid_constant__ WeighArgs a) {
+__global__ void __launch_bounds__(kMaxGroup * kTile)
+    weigh_add_kernel(const __grid_constant__ WeighArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const WeighCut cut = a.cuts[blockIdx.x];
-  if (cut.b < 0) return;
-  const int key = threadIdx.x;
+  const int x = threadIdx.x;
+  if (cut.b < 0 || x >= cut.kt * kTile) return;
   const WSeq s = load_wseq<kCols>(a, cut.b);
-  float sum = a.parts[(static_cast<int64_t>(cut.c0) * 2 + 1) * kTile + key];
+  constexpr int kPart = kMaxGroup * kTile;
+  if (cut.group * cut.kt * kTile + x >= s.len + s.n) return;
+  float sum = a.parts[(static_cast<int64_t>(cut.c0) * 2 + 1) * kPart + x];
 #pragma unroll 8
-  for (int c = cut.c0 + 1; c <= cut.c1; ++c)
-    sum += a.parts[static_cast<int64_t>(c) * 2 * kTile + key];
-  put(a, s, cut.tile * kTile + key, sum);
+  for (int c = cut.c0 + 1; c <= cut.c1; ++c) sum += a.parts[static_cast<int64_t>(c) * 2 * kPart + x];
+  put(a, s, cut.group * cut.kt * kTile + x, sum);
 }
 
 struct WeighPlan {
@@ -519,7 +554,7 @@ struct WeighPlan {
 WeighPlan weigh_plan() {
   WeighPlan p;
   p.grid = device_info().sms;
-  p.cut_off = align_up(size_t(p.grid) * 2 * kTile * sizeof(float), 256);
+  p.cut_off = align_up(size_t(p.grid) * 2 * kMaxGroup * kTile * sizeof(float), 256);
   p.ws_bytes = p.cut_off + p.grid * sizeof(WeighCut) + 256;  // (to align the base)
   return p;
 }
@@ -545,7 +580,7 @@ cudaError_t launch_weigh(const WeighArgs& a, const dfl2_cache* c, const void* k,
   }
   e = launch_k(kernel, dim3(a.grid), dim3(C::kThreads), C::kSmem, s, true, a, tk);
   if (e != cudaSuccess) return e;
-  return launch_k(weigh_add_kernel<C::kCols>, dim3(a.grid), dim3(kTile), 0, s, true, a);
+  return launch_k(weigh_add_kernel<C::kCols>, dim3(a.grid), dim3(kMaxGroup * kTile), 0, s, true, a);
 }
 template <typename E>
 cudaError_t launch_weigh_d(const WeighArgs& a, const dfl2_cache* c, const void* k, cudaStream_t s) {
