@@ -18,8 +18,9 @@
 //
 // Roles: warp 0 loads K (TMA boxes of one page, 128-byte swizzle); warp 1 issues the MMAs; four
 // warps gather the columns' rows of Q, which path may order anyhow, with 16-byte cp.async; and
-// two groups of four warps add up the even and the odd tiles of a group.  Four accumulators
-// take turns, so MMAs, exponentials and gather overlap.
+// four warps for each tile of a group add up (a warp's 128 columns take 2,000 cycles, most of
+// them latency, so a scheduler wants four of them).  Four accumulators take turns, so MMAs,
+// exponentials and gather overlap.
 //
 // Bounds.  A tile of K is 32 KB (128 channels): 1400 cycles of an SM's share of HBM.  With
 // 128 columns its MMAs take 512 cycles, and its 16,384 exponentials as many.  So HBM bounds
@@ -34,9 +35,11 @@ constexpr int kInfos = 4;    // steps whose columns' numbers are held
 constexpr int kAccs = 4;     // accumulators
 constexpr int kMaxGroup = 4; // tiles of a group
 
-struct alignas(16) WeighCut {  // a group that range c0 begins and c1 ends; b < 0: none
-  int b, group, c0, c1;
-  int kt;
+struct alignas(32) WeighCut {  // a group that range c0 begins and c1 ends; b < 0: none
+  int b, c0, c1;
+  int pos;       // the group's first position
+  int row, len, n;
+  int keys;      // positions of the group
 };
 
 struct WeighArgs {
@@ -62,7 +65,7 @@ struct WeighCfg {
   static constexpr int kSlotsQ = D == 64 ? 4 : 2;
   static constexpr int kGroup = kSlotsK < kMaxGroup ? kSlotsK : kMaxGroup;  // most tiles of a group
   static constexpr int kBars = 2 * (kSlotsK + kSlotsQ + kInfos + kAccs) + 1;
-  static constexpr int kThreads = 14 * 32;
+  static constexpr int kThreads = (6 + 4 * kMaxGroup) * 32;
   static constexpr size_t kSmem = size_t(kSlotsK) * kSlotK + size_t(kSlotsQ) * kSlotQ +
                                   kInfos * kCols * 8 + kCols * 8 + kBars * 8 + 8;
   static_assert(kSmem + 1024 <= 232448, "shared memory");
@@ -217,7 +220,7 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
     }
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(&i_full[i], 4);
-      mbar_init(&i_empty[i], 8);
+      mbar_init(&i_empty[i], 4 * kMaxGroup);
     }
     for (int i = 0; i < kAccs; ++i) {
       mbar_init(&s_full[i], 1);
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
     const uint32_t tb = __shfl_sync(kAll, tmem, 0);
     const uint64_t ad = umma_desc_sw128(ks), bd = umma_desc_sw128(qs);
     int k_slot = 0, k_ph = 0, q_slot = 0, q_ph = 0;  // (of a group's first tile)
-    uint32_t m = 0;                                  // MMAs so far
+    uint32_t m = 0;  // rounds so far: kt a step, so that an accumulator is always the same warps'
     for (int64_t i = 0; i < N && ok; ++i) {
       const int cols = min(kCols, cur.s.n * a.G - cur.chunk * kCols);
       const int here = cur.here(kt);
@@ -308,27 +311,29 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
       ok = wait(&q_full[q_slot], q_ph, a.t.err);
       int slot = k_slot, ph = k_ph;
 #pragma unroll 1
-      for (int t = 0; t < here && ok; ++t, ++m) {
+      for (int t = 0; t < kt && ok; ++t, ++m) {
         const uint32_t acc = m % kAccs;
-        if (fresh) ok = wait(&k_full[slot], ph, a.t.err);
+        if (fresh && t < here) ok = wait(&k_full[slot], ph, a.t.err);
         if (m >= kAccs) ok = ok && wait(&s_empty[acc], (m / kAccs - 1) & 1, a.t.err);
         ok = __all_sync(kAll, ok);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t ak = ad + slot * (C::kSlotK >> 4);
+          if (t < here) {
+            const uint64_t ak = ad + slot * (C::kSlotK >> 4);
 #pragma unroll
-          for (int kb = 0; kb < kBlk; ++kb)
+            for (int kb = 0; kb < kBlk; ++kb)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_bf16(tb + acc * kCols, ak + kb * (kTile * 128 >> 4) + 2 * k,
-                        bq + kb * (kCols * 128 >> 4) + 2 * k, id, kb > 0 || k > 0);
+              for (int k = 0; k < 4; ++k)
+                umma_bf16(tb + acc * kCols, ak + kb * (kTile * 128 >> 4) + 2 * k,
+                          bq + kb * (kCols * 128 >> 4) + 2 * k, id, kb > 0 || k > 0);
+          }
           umma_commit(&s_full[acc]);
           if (t == here - 1) umma_commit(&q_empty[q_slot]);
-          if (last) umma_commit(&k_empty[slot]);
+          if (last && t < here) umma_commit(&k_empty[slot]);
         }
         __syncwarp();
-        if (++slot == C::kSlotsK) {
+        if (t < here && ++slot == C::kSlotsK) {
           slot = 0;
           ph ^= 1;
         }
@@ -348,9 +353,10 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
     __syncwarp();
   } else if (warp < 6) {
     // ---- Q: a warp a quarter of the columns, a lane to a column's numbers ----
-    // A step's numbers are looked up a step before its rows are asked for, and its rows are
-    // waited for kLag steps after that (fewer than there are slots).
-    constexpr int kLag = C::kSlotsQ > 2 ? 2 : 1;
+    // A step's numbers are looked up a step before its rows are asked for.  With four slots
+    // its rows are waited for two steps later; with two at once, since the next step's slot
+    // is only free when the MMAs that wait for these rows are next.
+    constexpr int kLag = C::kSlotsQ > 2 ? 2 : 0;
     const int w = warp - 2;
     constexpr int kMine = kCols / 4;       // columns of a warp
     constexpr int kPieces = D / 8;         // 16-byte pieces of a row
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
       if (i >= kLag) {
         cp_async_wait<kLag>();
         fence_proxy_async_smem();
-        mbar_arrive(&q_full[before[kLag - 1]]);
+        mbar_arrive(&q_full[kLag ? before[1] : slot]);
       }
       before[1] = before[0];
       before[0] = slot;
@@ -426,77 +432,83 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
     }
     cp_async_wait<0>();
     fence_proxy_async_smem();
-    if (kLag > 1 && i > 1) mbar_arrive(&q_full[before[1]]);
-    if (i > 0) mbar_arrive(&q_full[before[0]]);
+    if (kLag && i > 1) mbar_arrive(&q_full[before[1]]);
+    if (kLag && i > 0) mbar_arrive(&q_full[before[0]]);
   } else {
-    // ---- sums: a thread to a key of every second tile ----
-    const int odd = (warp - 6) >> 2, quarter = warp & 3, key = quarter * 32 + lane;
+    // ---- sums: a thread to a key, four warps to a tile of the group ----
+    const int t = (warp - 6) >> 2, quarter = warp & 3, key = quarter * 32 + lane;
     const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint64_t sl2 = pack_f32x2(a.scale_log2, a.scale_log2);
-    if (odd == 0 && key == 0) a.cuts[blockIdx.x].b = -1;
-    uint32_t m = 0;  // MMAs before this step's
+    if (t == 0 && key == 0) a.cuts[blockIdx.x].b = -1;
+    uint32_t m = t;  // the round of this tile in this step
     for (int64_t i = 0; i < N && ok;) {
       // this CTA's steps of a group
       const WSeq s = cur.s;
-      const int here = cur.here(kt), tile0 = cur.group * kt;
+      const int here = cur.here(kt), tile = cur.group * kt + t;
       const int per = a.H * s.chunks, at0 = cur.h * s.chunks + cur.chunk;
       const int64_t i1 = min(N, i + per - at0);
       const int64_t v0 = g.u0 + i - at0;  // the group's first step
+      const int rel = tile * kTile + key - s.len;  // < 0: committed
+      const bool plain = (tile + 1) * kTile <= s.len;
       int chunk = cur.chunk;
-      float all[2] = {0.f, 0.f};  // of tiles `odd` and odd + 2
-      for (; i < i1; ++i, m += here) {
+      uint64_t sum[2] = {0, 0};
+      for (; i < i1; ++i, m += kt) {
         const int info = static_cast<int>(i & (kInfos - 1));
-        const int cols = min(kCols, s.n * a.G - chunk * kCols);
-        const float* l = lse_s + info * kCols;
-        const int* p = pos_s + info * kCols;
-        if (ok) ok = wait(&i_full[info], (i / kInfos) & 1, a.t.err);
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const int t = odd + 2 * z;
-          if (t >= here) break;
-          const uint32_t acc = (m + t) % kAccs;
-          if (ok) ok = wait(&s_full[acc], (m + t) / kAccs & 1, a.t.err);
+        if (ok) ok = wait(&i_full[info], (i / kInfos) & 1, a.t.err);  // (an idle warp keeps in step)
+        ok = __all_sync(kAll, ok);
+        if (t < kt) {
+          const int cols = t < here ? min(kCols, s.n * a.G - chunk * kCols) : 0;
+          const float* l = lse_s + info * kCols;
+          const int* p = pos_s + info * kCols;
+          const uint32_t acc = m % kAccs;
+          if (ok) ok = wait(&s_full[acc], m / kAccs & 1, a.t.err);
           ok = __all_sync(kAll, ok);
-          if (!ok) break;
-          tc_fence_after();
-          const int rel = (tile0 + t) * kTile + key - s.len;  // < 0: committed
-          const bool plain = (tile0 + t + 1) * kTile <= s.len;
-          uint64_t sum[2] = {0, 0};
-          float more = 0.f;
+          if (ok) {
+            tc_fence_after();
+            uint64_t step[2] = {0, 0};
 #pragma unroll 1
-          for (int c = 0; c < cols; c += 32) {
-            uint32_t x[32];
-            tmem_ld32_issue(tbase + acc * kCols + c, x);
-            // (a column that is left out, or past the last, is seen by no key)
-            const bool whole = plain && __all_sync(kAll, p[c + lane] >= 0);
-            tmem_ld32_wait(x);
-            if (whole) {
+            for (int c = 0; c < cols; c += 32) {
+              uint32_t x[32];
+              tmem_ld32_issue(tbase + acc * kCols + c, x);
+              // (a column that is left out, or past the last, is seen by no key)
+              const bool whole = plain && __all_sync(kAll, p[c + lane] >= 0);
+              tmem_ld32_wait(x);
+              if (whole) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 y = *reinterpret_cast<const float4*>(l + c + j);
-                float e0, e1, e2, e3;
-                unpack_f32x2(fma_f32x2(pack_u32x2(x[j], x[j + 1]), sl2, pack_f32x2(y.x, y.y)), e0, e1);
-                unpack_f32x2(fma_f32x2(pack_u32x2(x[j + 2], x[j + 3]), sl2, pack_f32x2(y.z, y.w)), e2,
-                             e3);
-                sum[0] = add_f32x2(sum[0], pack_f32x2(ex2(e0), ex2(e1)));
-                sum[1] = add_f32x2(sum[1], pack_f32x2(ex2(e2), ex2(e3)));
-              }
-            } else {
-              const int left = min(32, cols - c);
+                for (int j = 0; j < 32; j += 4) {
+                  const float4 y = *reinterpret_cast<const float4*>(l + c + j);
+                  float e[4];
+                  unpack_f32x2(fma_f32x2(pack_u32x2(x[j], x[j + 1]), sl2, pack_f32x2(y.x, y.y)), e[0],
+                               e[1]);
+                  unpack_f32x2(fma_f32x2(pack_u32x2(x[j + 2], x[j + 3]), sl2, pack_f32x2(y.z, y.w)),
+                               e[2], e[3]);
+                  step[0] = add_f32x2(step[0], pack_f32x2(ex2(e[0]), ex2(e[1])));
+                  step[1] = add_f32x2(step[1], pack_f32x2(ex2(e[2]), ex2(e[3])));
+                }
+              } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                if (j >= left) break;
-                const float e = ex2(fmaf(__uint_as_float(x[j]), a.scale_log2, l[c + j]));
-                if (rel <= p[c + j]) more += e;
+                for (int j = 0; j < 32; j += 4) {
+                  const float4 y = *reinterpret_cast<const float4*>(l + c + j);
+                  const int4 at = *reinterpret_cast<const int4*>(p + c + j);
+                  float e[4] = {ex2(fmaf(__uint_as_float(x[j]), a.scale_log2, y.x)),
+                                ex2(fmaf(__uint_as_float(x[j + 1]), a.scale_log2, y.y)),
+                                ex2(fmaf(__uint_as_float(x[j + 2]), a.scale_log2, y.z)),
+                                ex2(fmaf(__uint_as_float(x[j + 3]), a.scale_log2, y.w))};
+                  e[0] = rel <= at.x ? e[0] : 0.f;
+                  e[1] = rel <= at.y ? e[1] : 0.f;
+                  e[2] = rel <= at.z ? e[2] : 0.f;
+                  e[3] = rel <= at.w ? e[3] : 0.f;
+                  step[0] = add_f32x2(step[0], pack_f32x2(e[0], e[1]));
+                  step[1] = add_f32x2(step[1], pack_f32x2(e[2], e[3]));
+                }
               }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[acc]);
+            sum[0] = add_f32x2(sum[0], step[0]);
+            sum[1] = add_f32x2(sum[1], step[1]);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_empty[acc]);
-          float s0, s1;
-          unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
-          all[z] += (s0 + s1) + more;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&i_empty[info]);
@@ -504,20 +516,19 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
       }
       // ---- the end of this CTA's part of the group ----
       const bool begins = at0 == 0, ends = g.u0 + i == v0 + per;
-      float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) *
-                                  (kMaxGroup * kTile);
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const int t = odd + 2 * z;
-        if (t >= here || !ok) break;
+      if (t < here && ok) {
+        float s0, s1;
+        unpack_f32x2(add_f32x2(sum[0], sum[1]), s0, s1);
         if (begins && ends)
-          put(a, s, (tile0 + t) * kTile + key, all[z]);
+          put(a, s, tile * kTile + key, s0 + s1);
         else
-          part[t * kTile + key] = all[z];
+          a.parts[((static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * kMaxGroup + t) * kTile +
+                  key] = s0 + s1;
       }
-      if (begins && !ends && odd == 0 && key == 0)
-        a.cuts[blockIdx.x] = WeighCut{cur.b, cur.group, static_cast<int>(blockIdx.x),
-                                      range_of(g.units, g.n_cta, v0 + per - 1), kt};
+      if (begins && !ends && t == 0 && key == 0)
+        a.cuts[blockIdx.x] = WeighCut{cur.b, static_cast<int>(blockIdx.x),
+                                      range_of(g.units, g.n_cta, v0 + per - 1), tile * kTile, s.row,
+                                      s.len, s.n, min(here * kTile, s.len + s.n - tile * kTile)};
       cur.h = a.H - 1;  // on to the next group
       cur.chunk = s.chunks - 1;
       cur.next(a, kt);
@@ -530,21 +541,22 @@ __global__ void __launch_bounds__(WeighCfg<D>::kThreads, 1)
 }
 
 // The parts of the groups that several ranges share, in order.
-template <int kCols>
 __global__ void __launch_bounds__(kMaxGroup * kTile)
     weigh_add_kernel(const __grid_constant__ WeighArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const WeighCut cut = a.cuts[blockIdx.x];
   const int x = threadIdx.x;
-  if (cut.b < 0 || x >= cut.kt * kTile) return;
-  const WSeq s = load_wseq<kCols>(a, cut.b);
+  if (cut.b < 0 || x >= cut.keys) return;
   constexpr int kPart = kMaxGroup * kTile;
-  if (cut.group * cut.kt * kTile + x >= s.len + s.n) return;
+  const int pos = cut.pos + x;
+  float* w = a.weight + (static_cast<int64_t>(cut.row) * a.t.cols << a.t.page_shift) + pos;
+  const float old = *w;  // (beside the parts and the page's number)
+  const int page = a.t.entry(cut.row, pos >> a.t.page_shift);
   float sum = a.parts[(static_cast<int64_t>(cut.c0) * 2 + 1) * kPart + x];
 #pragma unroll 8
   for (int c = cut.c0 + 1; c <= cut.c1; ++c) sum += a.parts[static_cast<int64_t>(c) * 2 * kPart + x];
-  put(a, s, cut.group * cut.kt * kTile + x, sum);
+  if (a.t.checked(page) >= 0) *w = (a.first && pos >= cut.len ? 0.f : old) + sum;
 }
 
 struct WeighPlan {
@@ -580,7 +592,7 @@ cudaError_t launch_weigh(const WeighArgs& a, const dfl2_cache* c, const void* k,
   }
   e = launch_k(kernel, dim3(a.grid), dim3(C::kThreads), C::kSmem, s, true, a, tk);
   if (e != cudaSuccess) return e;
-  return launch_k(weigh_add_kernel<C::kCols>, dim3(a.grid), dim3(kMaxGroup * kTile), 0, s, true, a);
+  return launch_k(weigh_add_kernel, dim3(a.grid), dim3(kMaxGroup * kTile), 0, s, true, a);
 }
 template <typename E>
 cudaError_t launch_weigh_d(const WeighArgs& a, const dfl2_cache* c, const void* k, cudaStream_t s) {

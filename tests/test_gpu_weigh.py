@@ -121,6 +121,15 @@ def test_many_and_long_sequences():
     Weighed([20011, 3], 2, 4, 2, 64, 64, seed=2).check()
 
 
+@pytest.mark.parametrize("H,D,B", [(8, 64, 100), (8, 128, 100), (16, 256, 60), (4, 64, 90)])
+def test_groups_of_tiles(H, D, B):
+    """Enough work for groups of two and four tiles, the last of them with fewer, several heads
+    and sequences to a range."""
+    rng = np.random.default_rng(H + D)
+    lens = [int(x) for x in rng.integers(100, 900, B)]
+    Weighed(lens, 3, H, H, D, 32, seed=D, kept=[int(x) for x in rng.integers(1, 4, B)], path=True).check()
+
+
 def test_layouts():
     """Another layer, pages as [page_size, kv_heads, head_dim], q a part of wider rows."""
     c = Weighed([100, 37], 4, 8, 2, 128, 16, nhd=True, layers=3, layer=1, rows=True, seed=5)
