@@ -121,7 +121,7 @@ def test_many_and_long_sequences():
     Weighed([20011, 3], 2, 4, 2, 64, 64, seed=2).check()
 
 
-@pytest.mark.parametrize("H,D,B", [(8, 64, 100), (8, 128, 100), (16, 256, 60), (4, 64, 90)])
+@pytest.mark.parametrize("H,D,B", [(8, 64, 100), (8, 128, 170), (16, 256, 60), (4, 64, 90)])
 def test_groups_of_tiles(H, D, B):
     """Enough work for groups of two and four tiles, the last of them with fewer, several heads
     and sequences to a range."""
