@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kSelThreads)
     evict_select_kernel(const __grid_constant__ EvictArgs a) {
   __shared__ int hist[kBins];
   __shared__ uint32_t sums[2][kSelWarps];
-  __shared__ int digit_s, left_s, first_s;
+  __shared__ int digit_s, left_s, all_s, first_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
   pdl_wait();
   pdl_launch_dependents();
@@ -130,20 +130,26 @@ __global__ void __launch_bounds__(kSelThreads)
       if (before < m && m <= before + x0) {
         digit_s = 2 * tid;
         left_s = m - before;
+        all_s = x0;
       } else if (before + x0 < m && m <= before + x0 + x1) {
         digit_s = 2 * tid + 1;
         left_s = m - before - x0;
+        all_s = x1;
       }
       __syncthreads();
       key |= (mask - static_cast<uint32_t>(digit_s)) << shift;
       m = left_s;
+      if (m == all_s) break;  // every weight of these digits stays: they need no further ones
     }
   }
 
-  // The positions of chunk c that stay: a bit for each of a thread's, and the number of those
-  // that stay before the warp's first; larger / equal: of the chunks before.
+  // The positions of chunk c that stay: a bit for each of a warp's (gt: of larger weights, eq:
+  // of equal ones), and the numbers of both (g, e) before the warp's first; larger, equal: in
+  // the chunks before.
   int larger = 0, equal = 0;
-  auto stay = [&](int c, unsigned (&gt)[kPer], unsigned (&eq)[kPer], int& gt0, int& eq0) {
+  unsigned gt[kPer], eq[kPer];
+  int g = 0, e = 0;
+  auto stay = [&](int c) {
     uint32_t n = 0;  // larger ones, and equal ones << 16
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -158,8 +164,8 @@ __global__ void __launch_bounds__(kSelThreads)
     const uint32_t x = sums[c & 1][lane];
     const uint32_t before = __reduce_add_sync(kAll, lane < warp ? x : 0u);
     const uint32_t all = __reduce_add_sync(kAll, x);
-    gt0 = larger + static_cast<int>(before & 0xFFFF);
-    eq0 = equal + static_cast<int>(before >> 16);
+    g = larger + static_cast<int>(before & 0xFFFF);
+    e = equal + static_cast<int>(before >> 16);
     larger += static_cast<int>(all & 0xFFFF);
     equal += static_cast<int>(all >> 16);
   };
@@ -170,9 +176,7 @@ __global__ void __launch_bounds__(kSelThreads)
   int first = len;
   for (int c = 0; c < chunks && first == len; ++c) {
     if (chunks > 1) load(c);
-    unsigned gt[kPer], eq[kPer];
-    int g, e;
-    stay(c, gt, eq, g, e);
+    stay(c);
     int gone = len;
 #pragma unroll
     for (int j = kPer - 1; j >= 0; --j) {
@@ -222,10 +226,10 @@ __global__ void __launch_bounds__(kSelThreads)
     return table[p >> a.t.page_shift] * a.page_stride + (p & (ps - 1)) * a.slot_stride;
   };
   for (int c = 0; c < chunks; ++c) {
-    if (chunks > 1) load(c);
-    unsigned gt[kPer], eq[kPer];
-    int g, e;
-    stay(c, gt, eq, g, e);  // (its barrier: every weight of the chunk has been read)
+    if (chunks > 1) {
+      load(c);
+      stay(c);  // (its barrier: every weight of the chunk has been read)
+    }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int p = pos_of(c, j);
