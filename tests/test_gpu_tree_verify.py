@@ -82,6 +82,12 @@ def test_paths_and_draws(B, T, V, replace):
     assert dfl2.dfl2_device_error(clear=True) == 0
 
 
+@pytest.mark.parametrize("V", [1, 2, 3, 4, 5, 9])
+def test_vocabularies_smaller_than_the_candidates(V):
+    x = make(6, 5, V, False, seed=V)
+    check(x, False, call(x, False))
+
+
 def test_counts():
     x = make(8, 12, 300, False, seed=3)
     count = [0, 1, 2, 5, 12, 40, -3, 11]
