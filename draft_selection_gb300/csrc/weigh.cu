@@ -25,6 +25,11 @@
 // Bounds.  A tile of K is 32 KB (128 channels): 1400 cycles of an SM's share of HBM.  With
 // 128 columns its MMAs take 512 cycles, and its 16,384 exponentials as many.  So HBM bounds
 // up to some 300 columns a key head, and beyond that the tensor cores and the exponentials.
+// Measured: 64 sequences of 900 to 4100 positions, 8 key heads, one to 15 kept tokens: 62 us,
+// 76% of measured HBM.  A chunk of 256 tokens, 7 heads a key head, behind 3000 to 12,345
+// positions, 4 sequences: 71 us, 43% of the tensor cores' rate: a step of four tiles takes 4900
+// cycles, 640 for each tile's MMAs and 3300 for its sums, which the next step's MMAs into the
+// same accumulator wait for.
 #include "tree_attn_kernel.cuh"
 
 namespace dfl2 {

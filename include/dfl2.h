@@ -53,7 +53,8 @@
  *     replaces it in the word.)
  *   - Workspaces must be zero-filled once before their first use (for example
  *     with dfl2_workspace_init); the library keeps them valid afterwards.
- *     dfl2_tree_attn's is the exception: scratch of that call, which overwrites
+ *     Those of dfl2_tree_attn, dfl2_window_attn, dfl2_cache_weigh and
+ *     dfl2_cache_evict are the exception: scratch of one call, which overwrites
  *     it, so it must not be a workspace that another entry point uses.
  */
 #ifndef DFL2_H
@@ -362,7 +363,9 @@ dfl2_status dfl2_verify(const float* p, const int32_t* tokens, const int32_t* sl
  *   per layer: dfl2_cache_write (the nodes' keys and values), dfl2_tree_attn
  *   dfl2_tree_accept     the target's choice at each node -> the kept path
  *   dfl2_cache_compact   the kept nodes' rows moved together, pages given back
- * dfl2_cache_fork and dfl2_cache_free begin and end sequences.
+ * dfl2_cache_fork and dfl2_cache_free begin and end sequences.  Layers with a window take
+ * dfl2_window_attn, sampled trees dfl2_tree_verify; dfl2_cache_weigh and dfl2_cache_evict,
+ * after the compaction, hold a sequence at a number of positions.
  *
  * The cache.  Element c of position `slot` in page `page`, key head h, layer l
  * of K is k[l*layer_stride + page*page_stride + h*head_stride +
@@ -528,9 +531,9 @@ dfl2_status dfl2_tree_accept(const int32_t* tokens, const int32_t* parents,
  * passed over.  When no child is kept: next_token = the first index, in order, at which
  * the running sum of r exceeds u[b,0] times its total (the last one with r > 0 if
  * rounding leaves none; of p if r sums to 0, -1 if that does too).
- * path, n_path, next_token: as dfl2_tree_accept's.  Decisions are taken in double
- * precision; the running sums are those of exact addition to about 2^-48.  Rows with
- * NaN, Inf or values below 0 are not supported.
+ * path, n_path, next_token: as dfl2_tree_accept's.  Decisions are taken in
+ * arithmetic of about 46 bits, and so are the running sums.  Rows with NaN, Inf or values
+ * below 0 are not supported.
  * 1 <= T <= 256, 1 <= V <= 2^30; p, cand_idx 16-byte aligned (rows of p need not be). */
 dfl2_status dfl2_tree_verify(const float* p, int B, int T, int V, const int32_t* tokens,
                              const int32_t* parents, const int32_t* count,
