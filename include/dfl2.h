@@ -55,7 +55,8 @@
  *     with dfl2_workspace_init); the library keeps them valid afterwards.
  *     Those of dfl2_tree_attn, dfl2_window_attn, dfl2_cache_weigh and
  *     dfl2_cache_evict are the exception: scratch of one call, which overwrites
- *     it, so it must not be a workspace that another entry point uses.
+ *     it, so it must not be a workspace that another entry point uses; calls that may
+ *     run at the same time need one each.
  */
 #ifndef DFL2_H
 #define DFL2_H
@@ -518,7 +519,7 @@ dfl2_status dfl2_tree_accept(const int32_t* tokens, const int32_t* parents,
  *               below its node makes the node no child).
  *   cand_idx, q int32 and float32 [B,T,16]: the children of node i were drawn from the
  *               candidates cand_idx[b,i] with weights q[b,i] (dfl2_walk's; they need
- *               not sum to 1), in the order of their numbers.  A candidate named twice
+ *               not sum to 1, but to a finite number), in the order of their numbers.  A candidate named twice
  *               counts at its lowest slot; one outside [0, V) is recorded and, as a
  *               weight that is not above 0, counts as 0.
  *   replace     0: children drawn without replacement (distinct); else independently.

@@ -240,3 +240,18 @@ def test_same_bits_again_and_in_a_graph_on_another_stream(T):
         torch.cuda.synchronize()
         want, wl = c.run()
         assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_layouts(T):
+    """Pages as [page_size, kv_heads, head_dim], another layer, q and out parts of wider rows."""
+    c = Windowed([100, 337], T, 8, 2, 128, 16, nhd=True, layers=3, layer=1, rows=True, sinks=5,
+                 window=70, seed=5)
+    wide = torch.randn(2, T, 12, 128, device="cuda").to(torch.bfloat16)
+    wide[:, :, :8] = c.q.cuda()
+    hold = torch.full((2, 8, T, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    out, lse = c.run(q=wide[:, :, :8], out=hold.transpose(1, 2))
+    c.check(out, lse)
+    part = torch.full((2, T, 8, 136), float("nan"), dtype=torch.bfloat16, device="cuda")
+    c.run(out=part[..., 8:])  # rows that begin on 16 bytes and not on 32
+    assert torch.equal(part[..., 8:], out) and torch.isnan(part[..., :8]).all()
