@@ -18,7 +18,7 @@
 // Bound by HBM: each row that moves is read and written once (16 sequences of up to 4000
 // positions at 2000, 16 layers, 8 heads x 128 channels, 2.6 GB: 419 us, 6.3 TB/s).  One
 // sequence at 1024 positions, 32 layers: 44 us, 6.1 TB/s, with 16 warps a block (8: 50), after
-// 11 us of selection: a chain of two or three histograms, a scan and a look at the pages.
+// 10 us of selection: a chain of two or three histograms, a scan and a look at the pages.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -30,8 +30,7 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
-constexpr int kPer = 8;                          // positions a thread holds
-constexpr int kChunk = kSelThreads * kPer;       // positions of a block at a time
+constexpr int kPer = 8;                          // positions a thread holds at most
 constexpr int kBins = 2048;
 
 struct Move {
@@ -82,16 +81,19 @@ __global__ void __launch_bounds__(kSelThreads)
   }
   float* weight = a.weight + (static_cast<int64_t>(row) * a.t.cols << a.t.page_shift);
   const int recent0 = len - a.recent;  // the first recent position
-  const int chunks = (len - a.sinks - 1) / kChunk + 1;
+  // A block holds kSelThreads times `per` positions at a time, so that short sequences too
+  // are spread over all warps (1041 positions: 11 us with eight to a thread in any case).
+  const int per = min(kPer, (len - a.sinks - 1) / kSelThreads + 1);
+  const int chunk = kSelThreads * per, chunks = (len - a.sinks - 1) / chunk + 1;
 
   // A thread's positions of a chunk: a warp's are contiguous, so that ballots give their order.
   float w[kPer];
-  auto pos_of = [&](int c, int j) { return a.sinks + c * kChunk + (warp * kPer + j) * 32 + lane; };
+  auto pos_of = [&](int c, int j) { return a.sinks + c * chunk + (warp * per + j) * 32 + lane; };
   auto load = [&](int c) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int p = pos_of(c, j);
-      w[j] = p < len ? weight[p] : 0.f;
+      w[j] = j < per && p < len ? weight[p] : 0.f;
     }
   };
   load(0);
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(kSelThreads)
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
           const uint32_t k = weight_key(w[j]);
-          if (pos_of(c, j) < recent0 && (k & above) == key)
+          if (j < per && pos_of(c, j) < recent0 && (k & above) == key)
             atomicAdd(&hist[mask - (k >> shift & mask)], 1);
         }
       }
@@ -156,6 +158,8 @@ __global__ void __launch_bounds__(kSelThreads)
     uint32_t n = 0;  // larger ones, and equal ones << 16
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
+      gt[j] = eq[j] = 0;
+      if (j >= per) continue;
       const int p = pos_of(c, j);
       const uint32_t k = p >= recent0 ? 0xFFFFFFFFu : weight_key(w[j]);
       gt[j] = __ballot_sync(kAll, p < len && k > key);
@@ -190,7 +194,7 @@ __global__ void __launch_bounds__(kSelThreads)
         if (z < j) eb += __popc(eq[z]);
       const bool stays = gt[j] >> lane & 1 ||
                          (eq[j] >> lane & 1 && eb + __popc(eq[j] & lower) < m);
-      if (p < len && !stays) gone = p;
+      if (j < per && p < len && !stays) gone = p;
     }
     gone = __reduce_min_sync(kAll, gone);
     if (lane == 0 && gone < len) atomicMin(&first_s, gone);
@@ -235,6 +239,7 @@ __global__ void __launch_bounds__(kSelThreads)
     }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
+      if (j >= per) break;
       const int p = pos_of(c, j);
       const int eb = e + __popc(eq[j] & lower);
       const bool is_eq = eq[j] >> lane & 1;
