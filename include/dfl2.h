@@ -590,14 +590,15 @@ dfl2_status dfl2_window_attn(const void* q, const int64_t* q_strides, const dfl2
                              dfl2_stream stream);
 
 /* What each position received of the attention of the tokens that a turn kept, added to its
- * weight (for dfl2_cache_evict): called for a layer after acceptance and compaction, with
- * the q and lse of that layer's attention call.
+ * weight (for dfl2_cache_evict): called for a layer without a window, after acceptance and
+ * compaction, with the q and lse of that layer's attention call.
  *   weight[r,j] += sum over i, h of exp(scale <q[b,path[b,i],h], K[b,j]> - lse[b,path[b,i],h])
  * for the kept queries i = 0 .. n_path-1, which stand at positions length + i now, over the
  * positions j <= length + i that each sees; r is the sequence's table row.
  *   q           as for dfl2_tree_attn (strides: non-negative multiples of 8).
- *   lse         float32 [B,T,q_heads], as that call left it; a query and head whose lse is
- *               not finite adds nothing.
+ *   lse         float32 [B,T,q_heads], as dfl2_tree_attn left it (not dfl2_window_attn, whose
+ *               sums leave positions out that are counted here); a query and head whose lse
+ *               is not finite adds nothing.
  *   length      int32 [B]: committed positions before this turn's.
  *   path        int32 [B,T]: node numbers (dfl2_tree_accept's); NULL: 0, 1, ..  One out of
  *               0 .. T-1 is recorded and left out.  n_path int32 [B], taken to 0 .. T;
