@@ -574,11 +574,12 @@ def dfl2_cache_weigh_workspace_size() -> int:
     return int(load().dfl2_cache_weigh_workspace_size())
 
 
-def dfl2_cache_weigh(q, lse, cache, layer: int, length, weight, ws, path=None, n_path=None,
+def dfl2_cache_weigh(q, lse, cache, layer: int, length, weight, ws=..., path=None, n_path=None,
                      first=False, rows=None, scale=None, stream=None) -> None:
     """The attention weight that each position received from the kept queries (nodes
     path[b,:n_path] of q [B,T,q_heads,head_dim] and lse [B,T,q_heads], at positions length ..)
     in layer `layer`, added to weight float32 [rows, cols*page_size]; first: the kept
-    queries' own positions are set."""
+    queries' own positions are set.  ws: dfl2_cache_weigh_workspace_size() bytes; where it is
+    left out, scratch of torch's allocator for this call."""
     _check(_native.cache_weigh(q, lse, cache, layer, length, weight, ws, path, n_path, first, rows,
                                scale, stream))

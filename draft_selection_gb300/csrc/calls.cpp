@@ -6,6 +6,7 @@
 // the package name them.
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <algorithm>
@@ -315,10 +316,30 @@ PyObject* attn(PyObject* const* a, bool win) {
 PyObject* tree_attn(PyObject* const* a) { return attn(a, false); }
 PyObject* window_attn(PyObject* const* a) { return attn(a, true); }
 
+// Scratch of one call from torch's allocator, given back when the call has been issued: what
+// the stream does next with the memory comes after it.
+struct Scratch {
+  void* p = nullptr;
+  size_t bytes = 0;
+  Scratch(size_t n, dfl2_stream s) : bytes(n) {
+    if (n)
+      p = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(n,
+                                                                 reinterpret_cast<cudaStream_t>(s));
+  }
+  ~Scratch() {
+    if (p) c10::cuda::CUDACachingAllocator::raw_delete(p);
+  }
+  Scratch(const Scratch&) = delete;
+  Scratch& operator=(const Scratch&) = delete;
+};
+
 PyObject* cache_weigh(PyObject* const* a) {
-  // q, lse, cache, layer, length, weight, ws, path, n_path, first, rows, scale, stream
+  // q, lse, cache, layer, length, weight, ws (... where it is left out), path, n_path, first,
+  // rows, scale, stream
   const dfl2_cache* c = cache_of(a[2]);
-  const at::Tensor &q = tensor(a[0], "q", 4), &ws = tensor(a[6], "ws");
+  const at::Tensor& q = tensor(a[0], "q", 4);
+  const bool own = a[6] == Py_Ellipsis;
+  const at::Tensor* ws = own ? nullptr : &tensor(a[6], "ws");
   if (q.scalar_type() != type_of(c))
     REFUSE(PyExc_ValueError, "q must be [B, T, q_heads, head_dim] of the cache's type");
   if (q.size(3) != c->head_dim || q.stride(3) != 1)
@@ -334,9 +355,11 @@ PyObject* cache_weigh(PyObject* const* a) {
   const int32_t *length = i32(a[4], "length", {B}), *path = i32(a[7], "path", {B, T}),
                 *n_path = i32(a[8], "n_path", {B}), *rows = i32(a[10], "rows", {B});
   const void* qp = q.data_ptr();
-  void* wp = ws.data_ptr();
-  const size_t bytes = ws.nbytes();
   const dfl2_stream s = stream_of(a[12]);
+  // (host memory is refused by the call)
+  const Scratch scratch(own && q.is_cuda() ? dfl2_cache_weigh_workspace_size() : 0, s);
+  void* wp = own ? scratch.p : ws->data_ptr();
+  const size_t bytes = own ? scratch.bytes : ws->nbytes();
   return run([&] {
     return dfl2_cache_weigh(qp, qs, lse, c, layer, B, T, H, rows, length, path, n_path,
                             static_cast<float>(scale), first, weight, wp, bytes, s);
