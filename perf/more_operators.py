@@ -307,8 +307,6 @@ def prepare(case, seed):
         s["cache"] = dfl2.Cache(s["k"], s["v"], s["table"], s["refs"], s["bits"])
         if c["op"] == "window":
             s["ws"] = dfl2.workspace(dfl2.dfl2_tree_attn_workspace_size(B, T, Hq, H, D, dt))
-        if c["op"] == "weigh":
-            s["ws"] = dfl2.workspace(dfl2.dfl2_cache_weigh_workspace_size())
         if c["op"] == "evict":
             s["ws"] = dfl2.workspace(dfl2.dfl2_cache_evict_workspace_size(B, c["keep"]))
     return s
@@ -519,7 +517,7 @@ def run(s):
                               c["window"], s["out"], s["ws"], lse=s["lse"])
     elif op == "weigh":
         dfl2.dfl2_cache_weigh(s["q"], s["lse"], s["cache"], 0, s["length"], s["weight"],
-                              s["ws"], path=s["path"], n_path=s["n_path"], first=s["first"])
+                              path=s["path"], n_path=s["n_path"], first=s["first"])
     elif op == "evict":
         new = s["new"]
         dfl2.dfl2_cache_reserve(s["cache"], s["base"], s["more"], s["got"])
