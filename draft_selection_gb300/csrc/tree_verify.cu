@@ -142,22 +142,41 @@ __device__ __forceinline__ void add_exact2(uint64_t& hi, uint64_t& lo, uint64_t 
   lo = add2(lo, sub2(x, h));
 }
 
-// The sum of vectors v, v + step, .. below v1, without those that are cut.
-__device__ __noinline__ Pair row_sum(const Row row, int v, int v1, int step) {
+// The sum of vectors v, v + step, .. below v1 (step = 2^lg), without those that are cut and
+// without the elements at[k] of the bits k of `cand`.  Nothing that was added is taken out
+// again: a sum is 0 if and only if every element in it is.
+__device__ __noinline__ Pair row_sum(const Row row, int v, int v1, int lg, const int* at,
+                                     unsigned cand) {
   constexpr int kBatch = 10;  // (a lane's vectors of 151,936 elements in 8 blocks)
   uint64_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll 1
-  for (; v < v1; v += step * kBatch) {
+  for (; v < v1; v += kBatch << lg) {
+    uint64_t gone = 0;  // bit 4 j + z: element z of vector j
+#pragma unroll 1
+    for (unsigned c = cand; c; c &= c - 1) {
+      const int e = at[__ffs(c) - 1] + row.off, d = (e >> 2) - v;
+      if (d >= 0 && d < kBatch << lg && (d & ((1 << lg) - 1)) == 0)
+        gone |= 1ull << (4 * (d >> lg) + (e & 3));
+    }
     float4 x[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      const int i = v + step * j;
+      const int i = v + (j << lg);
       x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < v1 && !row.cut(i)) x[j] = row.vec(i);
     }
+    if (gone) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (gone >> (4 * j) & 1) x[j].x = 0.f;
+        if (gone >> (4 * j + 1) & 1) x[j].y = 0.f;
+        if (gone >> (4 * j + 2) & 1) x[j].z = 0.f;
+        if (gone >> (4 * j + 3) & 1) x[j].w = 0.f;
+      }
+    }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      if (v + step * j >= v1) break;
+      if (v + (j << lg) >= v1) break;
       add_exact2(hi[0], lo[0], pack(x[j].x, x[j].y));
       add_exact2(hi[1], lo[1], pack(x[j].z, x[j].w));
     }
@@ -170,50 +189,50 @@ __device__ __noinline__ Pair row_sum(const Row row, int v, int v1, int step) {
   return (quick(h[0], l[0]) + quick(h[1], l[1])) + (quick(h[2], l[2]) + quick(h[3], l[3]));
 }
 
-// What is drawn from: the row times g, and in the candidates' places other values.  In a
-// sum over vectors a candidate's own p is taken out again (the sums are exact enough).
+// What is drawn from: the row times g, and in the candidates' places other values.
 struct Left {
   Row row;
   Pair g;
-  const int* at;     // [16], the candidates' elements; -1: none
-  const float* p;    // [16] their p
-  const Pair* val;   // [16]
+  const int* at;    // [16], the candidates' elements; -1: none
+  const Pair* val;  // [16]
   // The candidates in vectors [v0, v1), by a warp.
   __device__ __forceinline__ unsigned among(int v0, int v1) const {
     const int lane = threadIdx.x & 31, c = lane < kCand ? at[lane] : -1;
     const int v = (c + row.off) >> 2;
     return __ballot_sync(kAll, c >= 0 && v >= v0 && v < v1);
   }
-  // This lane's sum of vectors v, v + step, .. below v1; cand: the candidates that may be
+  // This lane's sum of vectors v, v + 2^lg, .. below v1; cand: the candidates that may be
   // among them.
-  __device__ __forceinline__ Pair sum(int v, int v1, int step, unsigned cand) const {
-    Pair s = row_sum(row, v, v1, step);
+  __device__ __forceinline__ Pair sum(int v, int v1, int lg, unsigned cand) const {
+    auto mine = [&](int i) { return i >= v && i < v1 && ((i - v) & ((1 << lg) - 1)) == 0; };
+    Pair s = row_sum(row, v, v1, lg, at, cand) * g;
     const int last = row.vecs - 1;
     if (v < v1 && (v == 0 || v1 > last)) {  // the elements of the cut vectors
 #pragma unroll 1
       for (int j = 0; j < (last ? 8 : 4); ++j) {
         const int i = j < 4 ? 0 : last, e = 4 * i + (j & 3) - row.off;
-        if (row.cut(i) && e >= 0 && e < row.V && i >= v && i < v1 && (i - v) % step == 0)
-          s = s + Pair{row.p[e], 0.f};
+        if (row.cut(i) && e >= 0 && e < row.V && mine(i) && slot(e, cand) < 0)
+          s = s + g * row.p[e];
       }
     }
-    Pair c = {0.f, 0.f};
 #pragma unroll 1
     for (; cand; cand &= cand - 1) {
-      const int k = __ffs(cand) - 1, i = (at[k] + row.off) >> 2;
-      if (i >= v && i < v1 && (i - v) % step == 0) {
-        s = s - Pair{p[k], 0.f};
-        c = c + val[k];
-      }
+      const int k = __ffs(cand) - 1;
+      if (mine((at[k] + row.off) >> 2)) s = s + val[k];
     }
-    return s * g + c;
+    return s;
   }
-  __device__ __forceinline__ Pair element(int e, unsigned cand) const {
-    Pair x = g * row.p[e];
+  // Which of the candidates in `cand` element e is; -1: none.
+  __device__ __forceinline__ int slot(int e, unsigned cand) const {
+    int k = -1;
 #pragma unroll 1
     for (; cand; cand &= cand - 1)
-      if (at[__ffs(cand) - 1] == e) x = val[__ffs(cand) - 1];
-    return x;
+      if (at[__ffs(cand) - 1] == e) k = __ffs(cand) - 1;
+    return k;
+  }
+  __device__ __forceinline__ Pair element(int e, unsigned cand) const {
+    const int k = slot(e, cand);
+    return k < 0 ? g * row.p[e] : val[k];
   }
 };
 
@@ -404,7 +423,6 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   left.row.vecs = (V + left.row.off + 3) / 4;
   left.g = g_s;
   left.at = at_s;
-  left.p = r_s[node_s];
   left.val = val_s;
   const int total_warps = ranks * kWarps;
   const int each = (left.row.vecs + total_warps - 1) / total_warps;
@@ -413,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   for (int pass = 0; pass < 2 && n > 0; ++pass) {
     const int w = rank * kWarps + warp;
     const int v0 = range_at(w), v1 = range_at(w + 1);
-    Pair s = left.sum(v0 + lane, v1, 32, left.among(v0, v1));
+    Pair s = left.sum(v0 + lane, v1, 5, left.among(v0, v1));
 #pragma unroll 1
     for (int off = 16; off; off >>= 1) s = s + shfl_xor(s, off);
     if (lane < ranks) {  // to every block of the cluster
@@ -470,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     const int run = (v1 - v0 + kThreads - 1) / kThreads;
     const int w0 = min(v1, v0 + tid * run), w1 = min(v1, w0 + run);
     const unsigned cand = left.among(v0, v1);
-    const Pair x = left.sum(w0, w1, 1, cand);
+    const Pair x = left.sum(w0, w1, 0, cand);
     const Pair to = scan32(x);
     if (lane == 31) warp_s[warp] = to;
     __syncthreads();
