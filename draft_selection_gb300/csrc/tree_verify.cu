@@ -103,6 +103,12 @@ __device__ __forceinline__ float to_one(float x) {
   return e < 2 || e > 252 ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
 }
 
+// a times g, g > 0: not 0 if a is not.
+__device__ __forceinline__ Pair times(Pair a, Pair g) {
+  const Pair x = a * g;
+  return x.hi > 0.f || !(a.hi > 0.f) ? x : Pair{__uint_as_float(1u), 0.f};
+}
+
 // The row of the last draw.  Rows need not begin on 16 bytes: its vectors are numbered from
 // the 16-byte boundary at or before the row, `off` elements early.
 struct Row {
@@ -205,14 +211,14 @@ struct Left {
   // among them.
   __device__ __forceinline__ Pair sum(int v, int v1, int lg, unsigned cand) const {
     auto mine = [&](int i) { return i >= v && i < v1 && ((i - v) & ((1 << lg) - 1)) == 0; };
-    Pair s = row_sum(row, v, v1, lg, at, cand) * g;
+    Pair s = times(row_sum(row, v, v1, lg, at, cand), g);
     const int last = row.vecs - 1;
     if (v < v1 && (v == 0 || v1 > last)) {  // the elements of the cut vectors
 #pragma unroll 1
       for (int j = 0; j < (last ? 8 : 4); ++j) {
         const int i = j < 4 ? 0 : last, e = 4 * i + (j & 3) - row.off;
         if (row.cut(i) && e >= 0 && e < row.V && mine(i) && slot(e, cand) < 0)
-          s = s + g * row.p[e];
+          s = s + times({row.p[e], 0.f}, g);
       }
     }
 #pragma unroll 1
@@ -232,7 +238,7 @@ struct Left {
   }
   __device__ __forceinline__ Pair element(int e, unsigned cand) const {
     const int k = slot(e, cand);
-    return k < 0 ? g * row.p[e] : val[k];
+    return k < 0 ? times({row.p[e], 0.f}, g) : val[k];
   }
 };
 
@@ -502,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       if (some) atomicMax(&last_s, tid + 31 - __clz(some));
     }
     __syncthreads();
-    if (tid == (who_s < kThreads ? who_s : last_s)) {
+    // (the first thread where none has a sum above 0, which rows with values below 0 can do)
+    if (tid == (who_s < kThreads ? who_s : max(0, last_s))) {
       const int e0 = max(0, 4 * w0 - left.row.off), e1 = min(V, 4 * w1 - left.row.off);
       const Pair t = t_s - (before + (to - x));
       Pair c = {0.f, 0.f};

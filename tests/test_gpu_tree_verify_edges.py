@@ -93,3 +93,19 @@ def test_what_is_left_lies_far_from_the_rejected():
         got = call(x, False)
         check(x, False, got)
         assert (got[2] == 150000).all()
+
+
+def test_a_row_of_very_different_sizes():
+    """Candidates of 1e30 beside elements of 1e-17: what is left of these, as floats, is 0 element
+    by element and not 0 in sums.  The first of them is drawn all the same."""
+    x = make(1, 2, 8192, False, seed=6)
+    x["p"][:], x["q"][:] = 0, 0
+    x["cand"][:] = np.arange(8000, 8016)
+    x["p"][:, :, 5:256] = 1e-17
+    x["p"][:, :, 8000:8002] = [1e30, 1e29]
+    x["q"][:, :, 0] = 1
+    x["parents"][:], x["tokens"][:] = [-1, 0], [0, 8000]
+    x["u"][:] = [0, LAST]
+    got = call(x, False)
+    check(x, False, got)
+    assert got[2].tolist() == [5]
