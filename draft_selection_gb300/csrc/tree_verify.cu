@@ -140,59 +140,69 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {  // a - b, as
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(b), "l"(0xBF800000BF800000ull), "l"(a));
   return r;
 }
-// hi + lo += x, twice: hi takes x to the nearest multiple of 2^-24 (what is left of x + 0.5
-// - 0.5), so it stays exact while it is below 1, and lo the rest, at most 2^-25 of each.
+// hi + lo += x, twice: the two-sum, what hi loses of each addition goes into lo.
 __device__ __forceinline__ void add_exact2(uint64_t& hi, uint64_t& lo, uint64_t x) {
-  const uint64_t h = add2(add2(x, 0x3F0000003F000000ull), 0xBF000000BF000000ull);
-  hi = add2(hi, h);
-  lo = add2(lo, sub2(x, h));
+  const uint64_t s = add2(hi, x), c = sub2(s, hi);
+  lo = add2(lo, add2(sub2(hi, sub2(s, c)), sub2(x, c)));
+  hi = s;
 }
 
 // The sum of vectors v, v + step, .. below v1 (step = 2^lg), without those that are cut and
 // without the elements at[k] of the bits k of `cand`.  Nothing that was added is taken out
 // again: a sum is 0 if and only if every element in it is.
+// Off by at most 2^-38 of itself for each of its 32 vectors' sums (32 additions, which leave lo
+// up to 2^-24 of the sum each, and round it as often) and 2^-46 for adding each of these.
 __device__ __noinline__ Pair row_sum(const Row row, int v, int v1, int lg, const int* at,
                                      unsigned cand) {
-  constexpr int kBatch = 10;  // (a lane's vectors of 151,936 elements in 8 blocks)
-  uint64_t hi[2] = {0, 0}, lo[2] = {0, 0};
+  // Vectors on their way at a time: 32 of the 64 registers that two blocks on an SM leave a
+  // thread (64 trees of 151,936 tokens, 19 vectors a lane: 18.7 us with 5, 19.0 with 8, and
+  // with 10 and 12, which spill, 22.5 and 23.3).
+  constexpr int kBatch = 8;
+  constexpr int kFold = 4;  // batches that are added up in floats and their remainders
+  Pair sum = {0.f, 0.f};
 #pragma unroll 1
-  for (; v < v1; v += kBatch << lg) {
-    uint64_t gone = 0;  // bit 4 j + z: element z of vector j
+  while (v < v1) {
+    uint64_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll 1
-    for (unsigned c = cand; c; c &= c - 1) {
-      const int e = at[__ffs(c) - 1] + row.off, d = (e >> 2) - v;
-      if (d >= 0 && d < kBatch << lg && (d & ((1 << lg) - 1)) == 0)
-        gone |= 1ull << (4 * (d >> lg) + (e & 3));
-    }
-    float4 x[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int i = v + (j << lg);
-      x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < v1 && !row.cut(i)) x[j] = row.vec(i);
-    }
-    if (gone) {
+    for (int f = 0; f < kFold && v < v1; ++f, v += kBatch << lg) {
+      uint32_t gone = 0;  // bit 4 j + z: element z of vector j
+#pragma unroll 1
+      for (unsigned c = cand; c; c &= c - 1) {
+        const int e = at[__ffs(c) - 1] + row.off, d = (e >> 2) - v;
+        if (d >= 0 && d < kBatch << lg && (d & ((1 << lg) - 1)) == 0)
+          gone |= 1u << (4 * (d >> lg) + (e & 3));
+      }
+      float4 x[kBatch];
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        if (gone >> (4 * j) & 1) x[j].x = 0.f;
-        if (gone >> (4 * j + 1) & 1) x[j].y = 0.f;
-        if (gone >> (4 * j + 2) & 1) x[j].z = 0.f;
-        if (gone >> (4 * j + 3) & 1) x[j].w = 0.f;
+        const int i = v + (j << lg);
+        x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < v1 && !row.cut(i)) x[j] = row.vec(i);
+      }
+      if (gone) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          if (gone >> (4 * j) & 1) x[j].x = 0.f;
+          if (gone >> (4 * j + 1) & 1) x[j].y = 0.f;
+          if (gone >> (4 * j + 2) & 1) x[j].z = 0.f;
+          if (gone >> (4 * j + 3) & 1) x[j].w = 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (v + (j << lg) >= v1) break;
+        add_exact2(hi[0], lo[0], pack(x[j].x, x[j].y));
+        add_exact2(hi[1], lo[1], pack(x[j].z, x[j].w));
       }
     }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      if (v + (j << lg) >= v1) break;
-      add_exact2(hi[0], lo[0], pack(x[j].x, x[j].y));
-      add_exact2(hi[1], lo[1], pack(x[j].z, x[j].w));
-    }
+    float h[4], l[4];
+    unpack(hi[0], h[0], h[1]);
+    unpack(hi[1], h[2], h[3]);
+    unpack(lo[0], l[0], l[1]);
+    unpack(lo[1], l[2], l[3]);
+    sum = sum + ((quick(h[0], l[0]) + quick(h[1], l[1])) + (quick(h[2], l[2]) + quick(h[3], l[3])));
   }
-  float h[4], l[4];
-  unpack(hi[0], h[0], h[1]);
-  unpack(hi[1], h[2], h[3]);
-  unpack(lo[0], l[0], l[1]);
-  unpack(lo[1], l[2], l[3]);
-  return (quick(h[0], l[0]) + quick(h[1], l[1])) + (quick(h[2], l[2]) + quick(h[3], l[3]));
+  return sum;
 }
 
 // What is drawn from: the row times g, and in the candidates' places other values.

@@ -533,8 +533,8 @@ dfl2_status dfl2_tree_accept(const int32_t* tokens, const int32_t* parents,
  * the running sum of r exceeds u[b,0] times its total (the last one with r > 0 if
  * rounding leaves none; of p if r sums to 0, -1 if that does too).
  * path, n_path, next_token: as dfl2_tree_accept's.  Decisions are taken in
- * arithmetic of about 46 bits, and so are the running sums.  Rows with NaN, Inf or values
- * below 0 are not supported.
+ * arithmetic of about 46 bits; the running sums are off by at most 2^-37 + V 2^-61 of their
+ * total.  Rows with NaN, Inf or values below 0 are not supported.
  * 1 <= T <= 256, 1 <= V <= 2^30; p, cand_idx 16-byte aligned (rows of p need not be). */
 dfl2_status dfl2_tree_verify(const float* p, int B, int T, int V, const int32_t* tokens,
                              const int32_t* parents, const int32_t* count,
