@@ -97,10 +97,11 @@ __device__ __forceinline__ Pair scan32(Pair x) {  // over this lane and those be
   }
   return x;
 }
-// 2^-e for x in [2^e, 2^(e+1)), x normal and e within -125 .. 125; 1 otherwise.
+// 2^-e for x in [2^e, 2^(e+1)), so that x times it is in [1, 2); for x below the smallest normal
+// number 2^127 (then x times it is at least 2^-22), from 2^127 on 2^-126.
 __device__ __forceinline__ float to_one(float x) {
   const int e = static_cast<int>(__float_as_uint(x) >> 23);  // (x >= 0)
-  return e < 2 || e > 252 ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+  return __uint_as_float(static_cast<uint32_t>(254 - min(e, 253)) << 23);
 }
 
 // a times g, g > 0: not 0 if a is not.
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     const int k = lane & 15;
     // Lanes 0 .. 15 hold r, 16 .. 31 d, so that one reduction sums both.  Nothing is
     // divided: r/|r| - d/|d| is r |d| - d |r| but for a factor, which g keeps (what r off
-    // the candidates is, relative to p).  |r| and |d| are held in [1, 2) by powers of two.
+    // the candidates is, relative to p).  |r| and |d| are held near 1 by powers of two.
     const bool low = lane < kCand;
     int cur = 0, len = 0, cand = -1;
     Pair x = {0.f, 0.f}, g = {1.f, 0.f};
