@@ -70,11 +70,28 @@ __global__ void __launch_bounds__(kSelThreads)
   const bool fits = row >= 0 && a.t.checked_length(len) &&
                     len <= static_cast<int64_t>(a.t.cols) << a.t.page_shift;
   int32_t* kept = a.kept + static_cast<int64_t>(b) * a.keep;
-  if (!fits || len <= a.keep) {
-    for (int i = tid; i < a.keep; i += kSelThreads) kept[i] = fits && i < len ? i : -1;
+  const int ps = 1 << a.t.page_shift;
+  const int32_t* table = a.t.table + static_cast<int64_t>(max(0, row)) * a.t.cols;
+  // Whether (for this thread) every page of the sequence is there, and none shared that is
+  // written, which are those of places `first` .. keep - 1.
+  auto pages_good = [&](int first) {
+    bool good = true;
+    for (int c = tid; c < (len + ps - 1) >> a.t.page_shift; c += kSelThreads) {
+      const int p = table[c];
+      if (static_cast<unsigned>(p) >= static_cast<unsigned>(a.t.pages))
+        good = false;
+      else if (first < a.keep && c >= first >> a.t.page_shift &&
+               c <= (a.keep - 1) >> a.t.page_shift)
+        good &= a.t.refs[p] == 1;
+    }
+    return good;
+  };
+  if (!fits || len <= a.keep) {  // (the block as one)
+    const bool good = __syncthreads_and(fits && pages_good(a.keep));
+    for (int i = tid; i < a.keep; i += kSelThreads) kept[i] = good && i < len ? i : -1;
     if (tid == 0) {
       a.plans[b] = Plan{0, -1, len, len};
-      a.served[b] = fits;
+      a.served[b] = good;
       a.new_length[b] = len;
     }
     return;
@@ -203,18 +220,7 @@ __global__ void __launch_bounds__(kSelThreads)
   }
 
   // ---- every page there, and none shared that is written ----
-  const int ps = 1 << a.t.page_shift;
-  const int32_t* table = a.t.table + static_cast<int64_t>(row) * a.t.cols;
-  bool good = true;
-  for (int c = tid; c < (len + ps - 1) >> a.t.page_shift; c += kSelThreads) {
-    const int p = table[c];
-    if (static_cast<unsigned>(p) >= static_cast<unsigned>(a.t.pages))
-      good = false;
-    else if (first < a.keep && c >= first >> a.t.page_shift &&
-             c <= (a.keep - 1) >> a.t.page_shift)
-      good &= a.t.refs[p] == 1;
-  }
-  good = __syncthreads_and(good);
+  const bool good = __syncthreads_and(pages_good(first));
   if (tid == 0) {
     a.plans[b] = Plan{good ? a.keep - min(first, a.keep) : 0, good ? row : -1, len, a.keep};
     a.served[b] = good;
