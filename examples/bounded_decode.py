@@ -11,7 +11,8 @@ stay visible), decodes several texts by sampling.  Every turn
      distribution (dfl2_tree_verify), and keeps the accepted rows (dfl2_cache_compact),
   4. adds up the attention that every cached position received from the accepted tokens
      (dfl2_cache_weigh) and, past the budget, gives up those that received least
-     (dfl2_cache_evict).
+     (dfl2_cache_evict).  The first layer's window and first tokens are among what stays in any
+     case, so that its window is one of the text's positions.
 
   python examples/bounded_decode.py --turns 60 --keep 96
 """
@@ -82,10 +83,13 @@ def draft(target, root, spine, children, ws, g, temperature):
     return tokens, parents, cand, q
 
 
-def decode(batch=4, turns=40, keep=96, spine=5, children=3, page=16, window=32, sinks=4, recent=24,
+def decode(batch=4, turns=40, keep=96, spine=5, children=3, page=16, window=None, sinks=4, recent=24,
            temperature=0.2, seed=0):
-    """Returns the emitted tokens of each text, the cached lengths, the cache, and how many
-    positions each turn gave up."""
+    """window: the first layer's, at most recent + 1, its default.  Returns the emitted tokens of
+    each text, the cached lengths, the cache, and how many positions each turn gave up."""
+    window = recent + 1 if window is None else window
+    if window > recent + 1:  # its last window - 1 cached positions would not be the text's
+        raise ValueError(f"window={window} is more than recent + 1 = {recent + 1}")
     dev = dict(dtype=torch.int32, device="cuda")
     target = Windowed(window, sinks, seed=seed)
     V, T = target.V, 1 + spine * children

@@ -581,6 +581,9 @@ dfl2_status dfl2_tree_attn(const void* q, const int64_t* q_strides, const dfl2_c
  * a node that it sees.  Only the sinks and what the first node's window reaches are read,
  * and pages that lie wholly between the two need not be there.
  *   sinks 0 .. 2^30; window 1 .. 2^30 (1: itself).
+ * Positions are the cache's.  Behind dfl2_cache_evict, which takes some out of the middle, they
+ * are the text's for this layer only if the eviction's `recent` is at least window - 1 and its
+ * `sinks` at least these.
  * All else, the workspace included, as for dfl2_tree_attn. */
 dfl2_status dfl2_window_attn(const void* q, const int64_t* q_strides, const dfl2_cache* cache,
                              int layer, int B, int T, int q_heads, const int32_t* table_rows,
