@@ -466,8 +466,10 @@ dfl2_status dfl2_cache_free(const dfl2_cache* cache, int n, const int32_t* table
  * `sinks` and last `recent` positions stay, and of the others as many of the largest
  * weights as make `keep` (equal ones: the lower positions; NaN counts as -inf).  In every
  * layer the rows that stay move together, in order, to positions 0 .. keep-1, their weights
- * with them, and the pages of the positions behind are given back.  One no longer than
- * `keep` stays as it is.
+ * with them, and the pages that held only positions keep .. length-1 are given back (those
+ * reserved past the length stay).  One no longer than `keep` stays as it is.
+ * dfl2_cache_fork copies no weights: the caller copies the source's row of them before the
+ * fork is weighed or evicted.
  *   weight      float32 [rows, cols*page_size]: of position j of table row r (as
  *               dfl2_cache_weigh leaves it); what lies behind the new length stays.
  *   kept        int32 [B,keep]: the old positions of the ones that stay, in order (for what
