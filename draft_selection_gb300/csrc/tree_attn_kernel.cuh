@@ -925,7 +925,8 @@ __global__ void __launch_bounds__(TcCfg<D, NS>::kThreads, TcCfg<D, NS>::kCtas)
         ++i;
         return true;
       };
-      if (a.mask && r < M && tile_hi * kKeys > s.len)  // read at the head's last tiles
+      if (a.mask && r < M && (key_tile<kWin>(a, s, tile_hi - 1) + 1) * kKeys > s.len)
+        // (read at the head's last tiles)
         prefetch_l1(a.mask + (static_cast<int64_t>(at.b) * a.t.T + node) * a.W);
       const int plain_hi = kWin ? tile_lo : max(tile_lo, min(tile_hi, s.len / kKeys));
       int tile = tile_lo;
