@@ -14,7 +14,10 @@
 // on timing.  A group's tiles stay in shared memory while all columns pass by: an SM takes in
 // about 26 bytes a cycle from L2, and with the 32 KB of 128 columns (128 channels) brought
 // again for every 128 keys the gather of Q bounded everything (2700 cycles a tile).  kt is the
-// largest of 4, 2 and 1 that leaves every CTA eight steps.
+// largest of 4, 2 and 1 that leaves every CTA four steps.  Measured with two, four, eight and
+// sixteen: 8 sequences of 2500 positions, four kept tokens, 17.9, 16.6, 19.3, 19.4 us; 12 of them
+// 21.0, 20.0, 23.9, 23.9; 24 31.3, 31.1, 30.2, 38.4; a chunk of 256 tokens, 7 heads a key head,
+// at 3000 positions 18.7, 19.3, 26.2, 26.3, at 12,000 35.4, 35.4, 35.4, 45.6.
 //
 // Roles: warp 0 loads K (TMA boxes of one page, 128-byte swizzle); warp 1 issues the MMAs; four
 // warps gather the columns' rows of Q, which path may order anyhow, with 16-byte cp.async; and
@@ -144,7 +147,7 @@ __device__ __forceinline__ WRange<kCols> find_wrange(const WeighArgs& a, int cta
   for (int off = 16; off; off >>= 1)
 #pragma unroll
     for (int z = 0; z < 3; ++z) x[z] += __shfl_xor_sync(kAll, x[z], off);
-  const int64_t enough = 8ll * a.grid;
+  const int64_t enough = 4ll * a.grid;
   const int pick = kGroup >= 4 && x[0] >= enough ? 0 : x[1] >= enough ? 1 : 2;
   g.kt = 4 >> pick;
   g.units = x[pick];
