@@ -409,8 +409,11 @@ dfl2_status dfl2_cache_evict(const dfl2_cache* cache, int B, const int32_t* tabl
     m.keep = keep;
     m.moves = a.moves;
     m.plans = a.plans;
-    // few columns: more warps share the rows, so that enough of them are on their way (256
-    // blocks: 44 us with 16 warps, 50 with 8)
+    // Few columns: more warps share the rows, so that enough of them are on their way.  Both
+    // launches, with 8, 16 and 32 warps, 1041 positions at 1024, and 8192 at 4096: 64 blocks 30,
+    // 31, 27 us and 89, 73, 64; 128 blocks 47, 41, 39 and 115, 102, 103; 256 blocks 74, 67, 61
+    // and 184, 194, 184; 384 blocks 99, 87, 88 and 278, 283, 261; 1024 blocks 205, 202, 209.  So
+    // it matters below a block an SM; past two 8 warps are within 12% of the best.
     const dim3 grid((m.columns + 31) / 32, B);
     const int64_t blocks = int64_t(grid.x) * B;
     if (blocks < dfl2::device_info().sms)
