@@ -9,18 +9,18 @@
 //
 // A cluster of blocks to a sequence.  Every block looks the candidates of all nodes up at
 // once (two dependent loads, however deep the tree is) and walks the tree in its first
-// warp, a lane to a candidate, in double precision; so the blocks need not exchange the
-// path.  The row of the last draw is then cut into one range a warp.  The warps' sums are
-// exchanged through distributed shared memory, and the warp whose range the drawn number
-// falls in looks for the element.
+// warp, a lane to a candidate; so the blocks need not exchange the path.  The row of the last
+// draw is then cut into one range a warp.  The warps' sums are exchanged through distributed
+// shared memory, and the block that has the range the drawn number falls in looks for the
+// element with all its threads.
 // Numbers are unevaluated sums of two floats (about 46 bits): decisions and the drawn index
 // have to be those of the exact sums, and this GPU's doubles are slow (two additions a cycle
 // and SM, 60 cycles each).
 //
 // One tree is bound by the latency of its dependent steps: a candidate's number and its p
 // (2 us), the tests of the walk (about 1000 cycles each), the row's elements, and the search for
-// the drawn one (9.3 us for 33 nodes and 151,936 tokens).  64 trees: the longest walk of them,
-// and 39 MB of rows (16 us; 5.7 at HBM's rate).
+// the drawn one (9.8 us a pass for 33 nodes and 151,936 tokens).  64 trees: the longest walk of
+// them, and 39 MB of rows (19.0 us a pass; 5.7 at HBM's rate).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -142,7 +142,7 @@ __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {  // a - b, as
   return r;
 }
 // hi + lo += x, twice: the two-sum, what hi loses of each addition goes into lo.
-__device__ __forceinline__ void add_exact2(uint64_t& hi, uint64_t& lo, uint64_t x) {
+__device__ __forceinline__ void add2_with_rest(uint64_t& hi, uint64_t& lo, uint64_t x) {
   const uint64_t s = add2(hi, x), c = sub2(s, hi);
   lo = add2(lo, add2(sub2(hi, sub2(s, c)), sub2(x, c)));
   hi = s;
@@ -192,8 +192,8 @@ __device__ __noinline__ Pair row_sum(const Row row, int v, int v1, int lg, const
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         if (v + (j << lg) >= v1) break;
-        add_exact2(hi[0], lo[0], pack(x[j].x, x[j].y));
-        add_exact2(hi[1], lo[1], pack(x[j].z, x[j].w));
+        add2_with_rest(hi[0], lo[0], pack(x[j].x, x[j].y));
+        add2_with_rest(hi[1], lo[1], pack(x[j].z, x[j].w));
       }
     }
     float h[4], l[4];
@@ -366,7 +366,6 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       const Pair P = shfl(sum, 0);
       Pair rest = Pair{1.f, 0.f} - P;
       if (rest.hi < 0.f) rest = {0.f, 0.f};
-      const Pair whole = rest;
       Pair R = rest + P, D = shfl(sum, 16);
       if (!low) x = scaled(x, to_one(D.hi));
       D = scaled(D, to_one(D.hi));
@@ -469,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       const Pair to = scan32(sum);
       Pair t = shfl(to, 31) * u_s[0];
       int owner = find32(sum, to, t);
-      if (owner >= 0) {  // every lane looks in its own four
+      if (owner >= 0) {  // every lane looks in its own kEach
         int mine = 0;
         Pair before = {0.f, 0.f}, run = {0.f, 0.f};
         bool found = false;
